@@ -473,6 +473,164 @@ void hmoe_linear_destroy(hmoe_linear* linear);
 hmoe_status hmoe_quantize_act_nvfp4(const void* x, int rows, int K, int act_dtype, float global_scale,
                                     void* codes, void* scales, hmoe_stream_t stream);
 
+/* ------------------------------------------------------------ rows sorted by expert and back
+ * For experts' work that runs outside hmoe_forward (expert adapters, experts
+ * in 16 bits, training): token rows are copied into one buffer sorted by
+ * expert, each expert's rows side by side, and the experts' results are
+ * brought back and summed per token. With s = t*topk + j a routed slot:
+ *   dispatch  rows[r] = (gates[s]) x[s / topk] for the slot s = row_slot[r];
+ *             rows without a slot (padding) are zero
+ *   combine   out[t] = sum_j (gates[t][j]) rows[slot_row[t][j]]
+ * The gates are applied where they are given. Sums are fp32, in ascending j,
+ * rounded once to the row type, so no result depends on the schedule. A slot
+ * without a row contributes nothing, whatever any row holds; a token whose
+ * slots all lack one gets zeros.
+ *   These entry points have no counterpart on the pages; they take the route
+ *   geometry of hmoe_plan_routes.
+ * Conventions as for the layer. All tensors are contiguous. ws: at least
+ * hmoe_dispatch_workspace_size bytes, 256-byte aligned, zeroed once
+ * (hmoe_workspace_init); only its status word is used, so any workspace of
+ * this library serves, and calls may share one. hmoe_check_device_status
+ * reports HMOE_ERR_BAD_ROUTE for inconsistent offsets and out-of-range perm,
+ * slot_row and ids entries, which are skipped (the result is then
+ * undefined). */
+typedef enum { HMOE_ROW_BF16 = 0, HMOE_ROW_F16 = 1, HMOE_ROW_F32 = 2 } hmoe_row_dtype;
+
+typedef struct {
+  int H;         /* row width, 1..2^20 (rows of a multiple of 16 bytes at 16-byte aligned addresses run fastest) */
+  int E;         /* experts, 1..512 */
+  int topk;      /* experts per token, 1..min(E, 32) */
+  int row_dtype; /* hmoe_row_dtype of x, rows, out and their gradients */
+  int align;     /* each expert's rows start at a multiple of align and are padded to it, 1..1024; 1: no padding */
+  int capacity;  /* rows an expert may get; its first slots in ascending order keep theirs. 0: no limit */
+} hmoe_dispatch_desc;
+
+/* Rows of the sorted buffer for T tokens: T*topk with each expert that can
+ * have any padded, at most E padded capacities. Host only.
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG,
+ *   HMOE_ERR_UNSUPPORTED_SHAPE (E, topk, H, align; rows above INT_MAX). */
+hmoe_status hmoe_dispatch_rows(const hmoe_dispatch_desc* desc, int T, int* rows);
+
+/* Workspace bytes for the calls below at up to max_tokens tokens. Host only.
+ *   No page defines it. Errors as hmoe_dispatch_rows. */
+hmoe_status hmoe_dispatch_workspace_size(const hmoe_dispatch_desc* desc, int max_tokens, size_t* bytes);
+
+/* Sort T token rows by expert. perm, offsets: as hmoe_plan_routes wrote them.
+ * x: device [T][H]. gates: device fp32 [T][topk], applied to the rows, or
+ * NULL. With R = hmoe_dispatch_rows(T), all device and fully written:
+ * rows [R][H]; row_slot int32 [R], the slot of each row or -1 for padding;
+ * slot_row int32 [T][topk], the row of each slot or -1 where the capacity
+ * dropped it; row_offsets int32 [E+1], where each expert's rows start. Rows
+ * from row_offsets[E] on are padding too. T = 0 is valid and writes
+ * row_offsets as zeros.
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
+ *   pointer, bad descriptor), HMOE_ERR_UNSUPPORTED_SHAPE,
+ *   HMOE_ERR_WORKSPACE_TOO_SMALL, HMOE_ERR_CUDA. */
+hmoe_status hmoe_dispatch(const hmoe_dispatch_desc* desc, const void* x, int T, const float* gates,
+                          const int32_t* perm, const int32_t* offsets, void* rows, int32_t* row_slot,
+                          int32_t* slot_row, int32_t* row_offsets, void* ws, size_t ws_bytes, hmoe_stream_t stream);
+
+/* The gradient of hmoe_dispatch. drows [R][H] -> dx [T][H] =
+ * sum_j (gates) drows[slot_row]. Where the gates were applied and their
+ * gradient is wanted, give gates and x, and
+ *   dgates  fp32 [T][topk] = <drows[slot_row[t][j]], x[t]>, 0 for a dropped
+ *           slot, and/or
+ *   dlogits fp32 [T][E] = the gradient of the router logits through the
+ *           softmax over the chosen experts (ids as hmoe_plan_routes wrote
+ *           them): gates_j (dgates_j - sum_i gates_i dgates_i) at ids[t][j],
+ *           zero elsewhere.
+ * Either may be NULL. The dot products are fp32, in a fixed order.
+ *   No page defines it. Errors as hmoe_dispatch; dgates or dlogits without
+ *   gates and x, or dlogits without ids, is HMOE_ERR_INVALID_ARG. */
+hmoe_status hmoe_dispatch_backward(const hmoe_dispatch_desc* desc, const void* drows, int T, const int32_t* slot_row,
+                                   const void* x, const float* gates, const int32_t* ids, void* dx, float* dgates,
+                                   float* dlogits, void* ws, size_t ws_bytes, hmoe_stream_t stream);
+
+/* Bring sorted rows back: out [T][H] = sum_j (gates[t][j]) rows[slot_row[t][j]].
+ * gates: device fp32 [T][topk], or NULL for plain sums.
+ *   No page defines it. Errors as hmoe_dispatch. */
+hmoe_status hmoe_combine(const hmoe_dispatch_desc* desc, const void* rows, int T, const int32_t* slot_row,
+                         const float* gates, void* out, void* ws, size_t ws_bytes, hmoe_stream_t stream);
+
+/* The gradient of hmoe_combine. dout [T][H] -> drows [R][H] =
+ * (gates) dout[row_slot / topk], zero on padding, fully written. With gates
+ * and rows (the combine's input), dgates and dlogits as in
+ * hmoe_dispatch_backward, of <rows[slot_row[t][j]], dout[t]>.
+ *   No page defines it. Errors as hmoe_dispatch_backward. */
+hmoe_status hmoe_combine_backward(const hmoe_dispatch_desc* desc, const void* dout, int T, const int32_t* row_slot,
+                                  const int32_t* slot_row, const void* rows, const float* gates, const int32_t* ids,
+                                  void* drows, float* dgates, float* dlogits, void* ws, size_t ws_bytes,
+                                  hmoe_stream_t stream);
+
+/* ------------------------------------------------------------ low-rank adapters
+ * Adapters of many requests at once beside a shared projection (a dense
+ * linear of this library, or any other):
+ *   out[t] = base[t] + scale_a * B_a (A_a x[t]),  a = ids[t],
+ * with A_a [rank_a, K], B_a [N, rank_a] of the activation type, each
+ * adapter's own rank, and ids[t] = -1 for a row without an adapter. ids may
+ * come in any order and mix: one request's tokens, single tokens of many
+ * requests, or the rows of hmoe_dispatch with the expert as the adapter.
+ * A x is summed in fp32 and enters the second product as the sum of two
+ * values of the activation type (so with 16 or more significant bits); that
+ * product, the scale and the base are fp32, rounded once to the activation
+ * type. fp16: |A x| must fit fp16, like any activation.
+ * Each row's result depends on that row alone, not on the other rows.
+ *   These entry points have no counterpart on the pages.
+ * Conventions as for the layer. */
+typedef struct {
+  int K;         /* input width, a multiple of 8 up to 131072 */
+  int N;         /* output width, a multiple of 8 up to 131072 */
+  int slots;     /* adapters held at once, 1..512 */
+  int max_rank;  /* largest rank of an adapter, 1..128 */
+  int act_dtype; /* hmoe_act_dtype of x, base, out, A and B; 0 is bf16 */
+} hmoe_lora_desc;
+
+typedef struct hmoe_lora hmoe_lora; /* opaque host handle: no device memory */
+
+/* Bytes of the packed adapters' buffer (the packed argument of hmoe_lora_create).
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG,
+ *   HMOE_ERR_UNSUPPORTED_SHAPE (the limits above). */
+hmoe_status hmoe_lora_packed_size(const hmoe_lora_desc* desc, size_t* bytes);
+
+/* Workspace bytes for hmoe_lora_forward at up to max_tokens rows. Zero the
+ * workspace once before its first use (hmoe_workspace_init).
+ *   No page defines it. Errors as hmoe_lora_packed_size. */
+hmoe_status hmoe_lora_workspace_size(const hmoe_lora_desc* desc, int max_tokens, size_t* bytes);
+
+/* Create the handle over a device buffer of hmoe_lora_packed_size bytes,
+ * 256-byte aligned, alive while the handle is used; every slot starts empty.
+ *   No page defines it. Errors: as hmoe_lora_packed_size, HMOE_ERR_CUDA. */
+hmoe_status hmoe_lora_create(const hmoe_lora_desc* desc, void* packed, hmoe_stream_t stream, hmoe_lora** out);
+
+/* Put an adapter into a slot, on the stream: A device [rank][K], B device
+ * [N][rank], repacked into this library's tiles; they may be freed once the
+ * stream has passed this point. A later load replaces it; rank 0 empties the
+ * slot (A and B are then not read), and rows with an empty slot's id get
+ * base. Forwards on the same stream see the slots as of their place in it.
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (slot or rank out of
+ *   range, NULL, scale not finite), HMOE_ERR_CUDA. */
+hmoe_status hmoe_lora_load(const hmoe_lora* lora, int slot, const void* A, const void* B, int rank, float scale,
+                           hmoe_stream_t stream);
+
+/* The rows' adapters. x: device [T] rows of K, ldx elements apart; base:
+ * device [T] rows of N, ldbase apart, or NULL for zeros; out: device [T] rows
+ * of N, ldout apart, fully overwritten; all 16-byte aligned with strides a
+ * multiple of 8, so column ranges of wider tensors serve. base may be out
+ * itself (in place, the same stride) and may not overlap it otherwise. ids:
+ * device int32 [T] in -1..slots-1; an id outside is reported through
+ * hmoe_check_device_status (HMOE_ERR_BAD_ROUTE) and its row gets base. T = 0
+ * is valid.
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
+ *   pointer, T < 0, a bad stride), HMOE_ERR_WORKSPACE_TOO_SMALL,
+ *   HMOE_ERR_CUDA. */
+hmoe_status hmoe_lora_forward(const hmoe_lora* lora, const void* x, int ldx, int T, const int32_t* ids,
+                              const void* base, int ldbase, void* out, int ldout, void* ws, size_t ws_bytes,
+                              hmoe_stream_t stream);
+
+/* Free the handle (host memory only). NULL is ignored.
+ *   No page defines it. */
+void hmoe_lora_destroy(hmoe_lora* lora);
+
 /* Message for the last failing call on this thread ("" if none). Part of
  * the error convention at the top of this file; no page defines it. */
 const char* hmoe_last_error(void);

@@ -29,6 +29,11 @@ __all__ = [
     "LinearDesc", "hmoe_linear_packed_size", "hmoe_linear_workspace_size", "hmoe_linear_pack", "hmoe_linear_forward",
     "LinearW4A16", "ACT_BF16", "ACT_F16", "act_torch_dtype", "ACT_QUANT_NONE", "ACT_QUANT_NVFP4",
     "hmoe_quantize_act_nvfp4",
+    "DispatchDesc", "ROW_BF16", "ROW_F16", "ROW_F32", "row_torch_dtype", "hmoe_dispatch_rows",
+    "hmoe_dispatch_workspace_size", "hmoe_dispatch", "hmoe_dispatch_backward", "hmoe_combine", "hmoe_combine_backward",
+    "ExpertRows", "RowPlan",
+    "LoraDesc", "hmoe_lora_packed_size", "hmoe_lora_workspace_size", "hmoe_lora_create", "hmoe_lora_load",
+    "hmoe_lora_forward", "LoraAdapters",
 ]
 
 
@@ -406,3 +411,12 @@ def hmoe_quantize_act_nvfp4(x, global_scale, codes, scales, stream=None):
     _lib.check(_lib.lib().hmoe_quantize_act_nvfp4(_ptr(x), int(x.shape[0]), int(x.shape[1]), act,
                                                   ctypes.c_float(global_scale), _ptr(codes), _ptr(scales),
                                                   _stream(stream)))
+
+
+# ------------------------------------------------------------------ rows sorted by expert, low-rank adapters
+# These modules use the checks and helpers above.
+from ._lib import ROW_BF16, ROW_F16, ROW_F32, DispatchDesc, LoraDesc  # noqa: E402, F401
+from .rows import (ExpertRows, RowPlan, hmoe_combine, hmoe_combine_backward, hmoe_dispatch,  # noqa: E402, F401
+                   hmoe_dispatch_backward, hmoe_dispatch_rows, hmoe_dispatch_workspace_size, row_torch_dtype)
+from .lora import (Lora, LoraAdapters, hmoe_lora_create, hmoe_lora_forward, hmoe_lora_load,  # noqa: E402, F401
+                   hmoe_lora_packed_size, hmoe_lora_workspace_size)

@@ -19,6 +19,7 @@ STATUS_NAMES = {
 }
 FMT_NF3, FMT_NVFP4, FMT_MXFP4 = 3, 4, 5
 ACT_BF16, ACT_F16 = 0, 1
+ROW_BF16, ROW_F16, ROW_F32 = 0, 1, 2
 ACT_QUANT_NONE, ACT_QUANT_NVFP4 = 0, 1
 TIERS_ONE_LAUNCH, TIERS_KEPT_FIRST, TIERS_NF3_FIRST = 0, 1, 2
 PATH_AUTO, PATH_STREAM, PATH_GROUPED = 0, 1, 2
@@ -34,6 +35,10 @@ EXPORTS = (
     "hmoe_auto_path", "hmoe_debug_decode_operand", "hmoe_linear_packed_size", "hmoe_linear_workspace_size",
     "hmoe_linear_pack", "hmoe_linear_forward", "hmoe_linear_forward_ex", "hmoe_linear_destroy",
     "hmoe_quantize_act_nvfp4",
+    "hmoe_dispatch_rows", "hmoe_dispatch_workspace_size", "hmoe_dispatch", "hmoe_dispatch_backward", "hmoe_combine",
+    "hmoe_combine_backward",
+    "hmoe_lora_packed_size", "hmoe_lora_workspace_size", "hmoe_lora_create", "hmoe_lora_load", "hmoe_lora_forward",
+    "hmoe_lora_destroy",
 )
 
 
@@ -45,6 +50,16 @@ class LayerDesc(ctypes.Structure):
 
 class LinearDesc(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("fmt", ctypes.c_int), ("act_dtype", ctypes.c_int)]
+
+
+class DispatchDesc(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("E", ctypes.c_int), ("topk", ctypes.c_int), ("row_dtype", ctypes.c_int),
+                ("align", ctypes.c_int), ("capacity", ctypes.c_int)]
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int), ("N", ctypes.c_int), ("slots", ctypes.c_int), ("max_rank", ctypes.c_int),
+                ("act_dtype", ctypes.c_int)]
 
 
 class ExpertSrc(ctypes.Structure):
@@ -96,6 +111,18 @@ def load(path=LIB_PATH):
         "hmoe_linear_forward_ex": (i, [vp, vp, i, vp, vp, sz, P(ForwardOpts), vp]),
         "hmoe_linear_destroy": (None, [vp]),
         "hmoe_quantize_act_nvfp4": (i, [vp, i, i, i, ctypes.c_float, vp, vp, vp]),
+        "hmoe_dispatch_rows": (i, [P(DispatchDesc), i, P(i)]),
+        "hmoe_dispatch_workspace_size": (i, [P(DispatchDesc), i, P(sz)]),
+        "hmoe_dispatch": (i, [P(DispatchDesc), vp, i, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "hmoe_dispatch_backward": (i, [P(DispatchDesc), vp, i, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "hmoe_combine": (i, [P(DispatchDesc), vp, i, vp, vp, vp, vp, sz, vp]),
+        "hmoe_combine_backward": (i, [P(DispatchDesc), vp, i, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "hmoe_lora_packed_size": (i, [P(LoraDesc), P(sz)]),
+        "hmoe_lora_workspace_size": (i, [P(LoraDesc), i, P(sz)]),
+        "hmoe_lora_create": (i, [P(LoraDesc), vp, vp, P(vp)]),
+        "hmoe_lora_load": (i, [vp, i, vp, vp, i, ctypes.c_float, vp]),
+        "hmoe_lora_forward": (i, [vp, vp, i, i, vp, vp, i, vp, i, vp, sz, vp]),
+        "hmoe_lora_destroy": (None, [vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

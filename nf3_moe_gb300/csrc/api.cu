@@ -938,3 +938,356 @@ hmoe_status hmoe_quantize_act_nvfp4(const void* x, int rows, int K, int act_dtyp
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------ rows sorted by expert and back
+namespace {
+
+constexpr int MAX_ALIGN = 1024;
+constexpr int MAX_ROW_WIDTH = 1 << 20;
+
+hmoe_status check_dispatch_desc(const hmoe_dispatch_desc* d) {
+  if (!d) return fail(HMOE_ERR_INVALID_ARG, "desc is NULL");
+  if (d->row_dtype != HMOE_ROW_BF16 && d->row_dtype != HMOE_ROW_F16 && d->row_dtype != HMOE_ROW_F32)
+    return fail(HMOE_ERR_INVALID_ARG, "row_dtype must be HMOE_ROW_BF16 (0), HMOE_ROW_F16 (1) or HMOE_ROW_F32 (2), got %d",
+                d->row_dtype);
+  if (d->H <= 0 || d->E <= 0 || d->topk <= 0 || d->align <= 0 || d->capacity < 0)
+    return fail(HMOE_ERR_INVALID_ARG, "H, E, topk and align must be positive and capacity at least 0");
+  if (d->H > MAX_ROW_WIDTH) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "H=%d exceeds %d", d->H, MAX_ROW_WIDTH);
+  if (d->E > MAX_E) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "E=%d exceeds %d", d->E, MAX_E);
+  if (d->topk > MAX_TOPK || d->topk > d->E)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "topk=%d must be <= min(E, %d)", d->topk, MAX_TOPK);
+  if (d->align > MAX_ALIGN) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "align=%d exceeds %d", d->align, MAX_ALIGN);
+  return HMOE_OK;
+}
+
+// Rows of the sorted buffer for T tokens: every slot, and for each expert that
+// can have any up to align - 1 rows of padding; with a capacity no more than
+// every expert's padded capacity.
+hmoe_status dispatch_rows(const hmoe_dispatch_desc& d, int T, int* rows) {
+  if (T < 0) return fail(HMOE_ERR_INVALID_ARG, "T=%d < 0", T);
+  const long long S = (long long)T * d.topk;
+  long long R = S + std::min<long long>(d.E, S) * (d.align - 1);
+  if (d.capacity > 0) R = std::min(R, ((long long)d.capacity + d.align - 1) / d.align * d.align * d.E);
+  if (S > (long long)INT_MAX || R > (long long)INT_MAX)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T*topk = %lld slots or %lld rows exceed the 32-bit row index", S, R);
+  *rows = (int)R;
+  return HMOE_OK;
+}
+
+hmoe_status check_status_ws(void* ws, size_t ws_bytes) {
+  if (!ws) return fail(HMOE_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return fail(HMOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (ws_bytes < 256) return fail(HMOE_ERR_WORKSPACE_TOO_SMALL, "workspace holds %zu bytes, 256 are needed", ws_bytes);
+  return HMOE_OK;
+}
+
+bool aligned_rows(const void* p, int row_dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (row_dtype == HMOE_ROW_F32 ? 3u : 1u)) == 0;
+}
+
+hmoe_status device_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? HMOE_OK : cuda_fail(e, "device query");
+}
+
+// The checks the two gradients share: the gates' part needs gates and the dot
+// operand, the logits' part the ids too.
+hmoe_status check_gate_grads(const void* dot, const char* dot_name, const float* gates, const int32_t* ids,
+                             const float* dgates, const float* dlogits) {
+  if ((dgates || dlogits) && (!gates || !dot))
+    return fail(HMOE_ERR_INVALID_ARG, "dgates and dlogits need gates and %s", dot_name);
+  if (dlogits && !ids) return fail(HMOE_ERR_INVALID_ARG, "dlogits needs ids");
+  return HMOE_OK;
+}
+
+RowsParams rows_params(const hmoe_dispatch_desc& d, int T, int R, void* ws) {
+  RowsParams p{};
+  p.T = T;
+  p.H = d.H;
+  p.E = d.E;
+  p.topk = d.topk;
+  p.R = R;
+  p.row_dtype = d.row_dtype;
+  p.status = static_cast<int*>(ws);
+  p.has_pads = d.align > 1 || d.capacity > 0;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+hmoe_status hmoe_dispatch_rows(const hmoe_dispatch_desc* desc, int T, int* rows) {
+  hmoe_status s = check_dispatch_desc(desc);
+  if (s != HMOE_OK) return s;
+  if (!rows) return fail(HMOE_ERR_INVALID_ARG, "rows is NULL");
+  return dispatch_rows(*desc, T, rows);
+}
+
+hmoe_status hmoe_dispatch_workspace_size(const hmoe_dispatch_desc* desc, int max_tokens, size_t* bytes) {
+  hmoe_status s = check_dispatch_desc(desc);
+  if (s != HMOE_OK) return s;
+  int rows = 0;
+  if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  if ((s = dispatch_rows(*desc, max_tokens, &rows)) != HMOE_OK) return s;
+  *bytes = 256;
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_dispatch(const hmoe_dispatch_desc* desc, const void* x, int T, const float* gates, const int32_t* perm,
+                          const int32_t* offsets, void* rows, int32_t* row_slot, int32_t* slot_row,
+                          int32_t* row_offsets, void* ws, size_t ws_bytes, hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_dispatch");
+  hmoe_status s = check_dispatch_desc(desc);
+  if (s != HMOE_OK) return s;
+  int R = 0;
+  if ((s = dispatch_rows(*desc, T, &R)) != HMOE_OK) return s;
+  if (!offsets || !row_offsets || (T > 0 && (!x || !perm || !rows || !row_slot || !slot_row)))
+    return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
+  if (!aligned_rows(x, desc->row_dtype) || !aligned_rows(rows, desc->row_dtype))
+    return fail(HMOE_ERR_INVALID_ARG, "x and rows must be aligned to their elements");
+  if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HMOE_OK) return s;
+  cudaError_t e = launch_dispatch_plan(perm, offsets, T * desc->topk, desc->E, desc->align, desc->capacity, R, row_slot,
+                                       slot_row, row_offsets, static_cast<int*>(ws), sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "dispatch plan launch");
+  RowsParams p = rows_params(*desc, T, R, ws);
+  p.v = x;
+  p.rows_out = rows;
+  p.gates = gates;
+  p.row_slot = row_slot;
+  p.slot_row = slot_row;
+  if ((e = launch_spread(p, sms, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "dispatch launch");
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_dispatch_backward(const hmoe_dispatch_desc* desc, const void* drows, int T, const int32_t* slot_row,
+                                   const void* x, const float* gates, const int32_t* ids, void* dx, float* dgates,
+                                   float* dlogits, void* ws, size_t ws_bytes, hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_dispatch_backward");
+  hmoe_status s = check_dispatch_desc(desc);
+  if (s != HMOE_OK) return s;
+  int R = 0;
+  if ((s = dispatch_rows(*desc, T, &R)) != HMOE_OK) return s;
+  if (T > 0 && (!drows || !slot_row || !dx)) return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
+  if (!aligned_rows(drows, desc->row_dtype) || !aligned_rows(dx, desc->row_dtype) || !aligned_rows(x, desc->row_dtype))
+    return fail(HMOE_ERR_INVALID_ARG, "drows, dx and x must be aligned to their elements");
+  if ((s = check_gate_grads(x, "x", gates, ids, dgates, dlogits)) != HMOE_OK) return s;
+  if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
+  RowsParams p = rows_params(*desc, T, R, ws);
+  p.v = (dgates || dlogits) ? x : nullptr;
+  p.rows_in = drows;
+  p.out = dx;
+  p.gates = gates;
+  p.ids = ids;
+  p.slot_row = slot_row;
+  p.dgates = dgates;
+  p.dlogits = dlogits;
+  cudaError_t e = launch_collect(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "dispatch gradient launch");
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_combine(const hmoe_dispatch_desc* desc, const void* rows, int T, const int32_t* slot_row,
+                         const float* gates, void* out, void* ws, size_t ws_bytes, hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_combine");
+  hmoe_status s = check_dispatch_desc(desc);
+  if (s != HMOE_OK) return s;
+  int R = 0;
+  if ((s = dispatch_rows(*desc, T, &R)) != HMOE_OK) return s;
+  if (T > 0 && (!rows || !slot_row || !out)) return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
+  if (!aligned_rows(rows, desc->row_dtype) || !aligned_rows(out, desc->row_dtype))
+    return fail(HMOE_ERR_INVALID_ARG, "rows and out must be aligned to their elements");
+  if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
+  RowsParams p = rows_params(*desc, T, R, ws);
+  p.rows_in = rows;
+  p.out = out;
+  p.gates = gates;
+  p.slot_row = slot_row;
+  cudaError_t e = launch_collect(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "combine launch");
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_combine_backward(const hmoe_dispatch_desc* desc, const void* dout, int T, const int32_t* row_slot,
+                                  const int32_t* slot_row, const void* rows, const float* gates, const int32_t* ids,
+                                  void* drows, float* dgates, float* dlogits, void* ws, size_t ws_bytes,
+                                  hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_combine_backward");
+  hmoe_status s = check_dispatch_desc(desc);
+  if (s != HMOE_OK) return s;
+  int R = 0;
+  if ((s = dispatch_rows(*desc, T, &R)) != HMOE_OK) return s;
+  if (T > 0 && (!dout || !row_slot || !slot_row || !drows)) return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
+  if (!aligned_rows(dout, desc->row_dtype) || !aligned_rows(drows, desc->row_dtype) ||
+      !aligned_rows(rows, desc->row_dtype))
+    return fail(HMOE_ERR_INVALID_ARG, "dout, drows and rows must be aligned to their elements");
+  if ((s = check_gate_grads(rows, "rows", gates, ids, dgates, dlogits)) != HMOE_OK) return s;
+  if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HMOE_OK) return s;
+  RowsParams p = rows_params(*desc, T, R, ws);
+  p.v = dout;
+  p.other = (dgates || dlogits) ? rows : nullptr;
+  p.rows_out = drows;
+  p.gates = gates;
+  p.ids = ids;
+  p.row_slot = row_slot;
+  p.slot_row = slot_row;
+  p.dgates = dgates;
+  p.dlogits = dlogits;
+  cudaError_t e = launch_spread(p, sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "combine gradient launch");
+  return HMOE_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ low-rank adapters
+struct hmoe_lora {
+  hmoe_lora_desc d;
+  LoraGeom g;
+  uint8_t* packed;
+  int num_sms;
+};
+
+namespace {
+
+constexpr int LORA_MAX_WIDTH = 1 << 17;
+
+hmoe_status check_lora_desc(const hmoe_lora_desc* d) {
+  if (!d) return fail(HMOE_ERR_INVALID_ARG, "desc is NULL");
+  if (d->act_dtype != HMOE_ACT_BF16 && d->act_dtype != HMOE_ACT_F16)
+    return fail(HMOE_ERR_INVALID_ARG, "act_dtype must be HMOE_ACT_BF16 (0) or HMOE_ACT_F16 (1), got %d", d->act_dtype);
+  if (d->K <= 0 || d->N <= 0 || d->slots <= 0 || d->max_rank <= 0)
+    return fail(HMOE_ERR_INVALID_ARG, "K, N, slots and max_rank must be positive");
+  if (d->K % 8 != 0 || d->N % 8 != 0 || d->K > LORA_MAX_WIDTH || d->N > LORA_MAX_WIDTH)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "K and N must be multiples of 8 up to %d (K=%d N=%d)", LORA_MAX_WIDTH, d->K,
+                d->N);
+  if (d->slots > LORA_MAX_SLOTS) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "slots=%d exceeds %d", d->slots, LORA_MAX_SLOTS);
+  if (d->max_rank > LORA_MAX_RANK)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "max_rank=%d exceeds %d", d->max_rank, LORA_MAX_RANK);
+  return HMOE_OK;
+}
+
+struct LoraWsLayout {
+  size_t status, u, total;
+};
+LoraWsLayout lora_ws_layout(const LoraGeom& g, int T) {
+  LoraWsLayout w{};
+  size_t off = 0;
+  w.status = off;
+  off += 256;
+  w.u = off;
+  off += align256((size_t)T * g.max_r16 * 4);
+  w.total = off;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+hmoe_status hmoe_lora_packed_size(const hmoe_lora_desc* desc, size_t* bytes) {
+  hmoe_status s = check_lora_desc(desc);
+  if (s != HMOE_OK) return s;
+  if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  const LoraGeom g = lora_geom(desc->K, desc->N, desc->slots, desc->max_rank);
+  *bytes = g.block_off + (size_t)g.slots * g.block_bytes;
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_lora_workspace_size(const hmoe_lora_desc* desc, int max_tokens, size_t* bytes) {
+  hmoe_status s = check_lora_desc(desc);
+  if (s != HMOE_OK) return s;
+  if (!bytes || max_tokens < 0) return fail(HMOE_ERR_INVALID_ARG, "bytes NULL or max_tokens < 0");
+  *bytes = lora_ws_layout(lora_geom(desc->K, desc->N, desc->slots, desc->max_rank), max_tokens).total;
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_lora_create(const hmoe_lora_desc* desc, void* packed, hmoe_stream_t stream, hmoe_lora** out) {
+  const NvtxRange nvtx("hmoe_lora_create");
+  hmoe_status s = check_lora_desc(desc);
+  if (s != HMOE_OK) return s;
+  if (!packed || !out) return fail(HMOE_ERR_INVALID_ARG, "packed or out is NULL");
+  if (reinterpret_cast<uintptr_t>(packed) % 256 != 0)
+    return fail(HMOE_ERR_INVALID_ARG, "the packed buffer must be 256-byte aligned");
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HMOE_OK) return s;
+  hmoe_lora* L = new (std::nothrow) hmoe_lora();
+  if (!L) return fail(HMOE_ERR_INVALID_ARG, "out of host memory");
+  L->d = *desc;
+  L->g = lora_geom(desc->K, desc->N, desc->slots, desc->max_rank);
+  L->packed = static_cast<uint8_t*>(packed);
+  L->num_sms = sms;
+  cudaError_t e = launch_lora_clear(L->g, L->packed, (cudaStream_t)stream);
+  if (e != cudaSuccess) {
+    delete L;
+    return cuda_fail(e, "adapter table launch");
+  }
+  *out = L;
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_lora_load(const hmoe_lora* L, int slot, const void* A, const void* B, int rank, float scale,
+                           hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_lora_load");
+  if (!L) return fail(HMOE_ERR_INVALID_ARG, "lora is NULL");
+  if (slot < 0 || slot >= L->d.slots) return fail(HMOE_ERR_INVALID_ARG, "slot=%d is not in 0..%d", slot, L->d.slots - 1);
+  if (rank < 0 || rank > L->d.max_rank)
+    return fail(HMOE_ERR_INVALID_ARG, "rank=%d is not in 0..%d", rank, L->d.max_rank);
+  if (rank > 0 && (!A || !B)) return fail(HMOE_ERR_INVALID_ARG, "A or B is NULL");
+  if ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(B)) & 1)
+    return fail(HMOE_ERR_INVALID_ARG, "A and B must be aligned to their elements");
+  if (!(scale > -3.0e38f && scale < 3.0e38f)) return fail(HMOE_ERR_INVALID_ARG, "scale must be finite");
+  cudaError_t e = launch_lora_load(L->g, L->packed, slot, static_cast<const uint16_t*>(A),
+                                   static_cast<const uint16_t*>(B), rank, scale, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "adapter load launch");
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T, const int32_t* ids, const void* base,
+                              int ldbase, void* out, int ldout, void* ws, size_t ws_bytes, hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_lora_forward");
+  if (!L) return fail(HMOE_ERR_INVALID_ARG, "lora is NULL");
+  if (T < 0) return fail(HMOE_ERR_INVALID_ARG, "T=%d < 0", T);
+  if (T == 0) return HMOE_OK;
+  if (!x || !ids || !out) return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
+  if (!aligned16(x) || !aligned16(out) || (base && !aligned16(base)))
+    return fail(HMOE_ERR_INVALID_ARG, "x, base and out must be 16-byte aligned");
+  if (ldx < L->d.K || ldout < L->d.N || (base && ldbase < L->d.N) || ldx % 8 != 0 || ldout % 8 != 0 ||
+      (base && ldbase % 8 != 0))
+    return fail(HMOE_ERR_INVALID_ARG, "row strides must be multiples of 8 and hold a row (ldx=%d ldbase=%d ldout=%d)", ldx,
+                ldbase, ldout);
+  if (base == out && ldbase != ldout) return fail(HMOE_ERR_INVALID_ARG, "in place, ldbase and ldout must be equal");
+  hmoe_status s = check_status_ws(ws, ws_bytes);
+  if (s != HMOE_OK) return s;
+  const LoraWsLayout w = lora_ws_layout(L->g, T);
+  if (ws_bytes < w.total)
+    return fail(HMOE_ERR_WORKSPACE_TOO_SMALL, "workspace holds %zu bytes, T=%d needs %zu", ws_bytes, T, w.total);
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  LoraParams p{};
+  p.g = L->g;
+  p.packed = L->packed;
+  p.T = T;
+  p.act_type = L->d.act_dtype;
+  p.x = static_cast<const uint16_t*>(x);
+  p.base = static_cast<const uint16_t*>(base);
+  p.out = static_cast<uint16_t*>(out);
+  p.ldx = (size_t)ldx;
+  p.ldbase = (size_t)ldbase;
+  p.ldout = (size_t)ldout;
+  p.ids = ids;
+  p.status = reinterpret_cast<int*>(wsb + w.status);
+  p.u = reinterpret_cast<float*>(wsb + w.u);
+  cudaError_t e = launch_lora_forward(p, L->num_sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "adapter launch");
+  return HMOE_OK;
+}
+
+void hmoe_lora_destroy(hmoe_lora* lora) { delete lora; }
+
+}  // extern "C"

@@ -1,0 +1,407 @@
+// dispatch.cu -- token rows sorted by expert and back, with the gates applied, and their gradients.
+//
+// With s = t * topk + j a slot, slot_row[s] its row in the sorted buffer (or
+// none) and row_slot the inverse map:
+//   dispatch   rows[r] = (g[s]) x[s / topk], s = row_slot[r]; pad rows are zero
+//   combine    out[t] = sum_j (g[t,j]) rows[slot_row[t,j]]
+// The gradient of each is the other, plus the gates' part:
+//   combine:   drows[r] = (g[s]) dout[s / topk],     dg[s] = <rows[slot_row[s]], dout[t]>
+//   dispatch:  dx[t] = sum_j (g[t,j]) drows[slot_row[t,j]], dg[s] = <drows[slot_row[s]], x[t]>
+// and through the softmax over the chosen experts
+//   dlogits[t, ids[t,j]] = g_j (dg_j - sum_i g_i dg_i), zero elsewhere.
+// So two kernels do the data movement: spread (tokens to rows) and collect
+// (rows to tokens), each with the dot products of the gates' gradient as an
+// option. Every sum is fp32 in a fixed order; a slot without a row takes no
+// part (it is skipped, not multiplied by zero, so what pad rows hold never
+// reaches a result).
+#include "common.cuh"
+#include "internal.h"
+
+namespace hmoe {
+
+// ------------------------------------------------------------ element types
+constexpr int ROW_BF16 = 0, ROW_F16 = 1, ROW_F32 = 2;
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<ROW_BF16> {
+  using type = uint16_t;
+};
+template <>
+struct Elem<ROW_F16> {
+  using type = uint16_t;
+};
+template <>
+struct Elem<ROW_F32> {
+  using type = float;
+};
+template <int DT>
+__device__ __forceinline__ float to_f32(typename Elem<DT>::type v) {
+  if constexpr (DT == ROW_F32) return v;
+  else if constexpr (DT == ROW_F16) return __half2float(__ushort_as_half(v));
+  else return bf16_bits_to_float(v);
+}
+template <int DT>
+__device__ __forceinline__ typename Elem<DT>::type from_f32(float f) {
+  if constexpr (DT == ROW_F32) return f;
+  else if constexpr (DT == ROW_F16) return f32_to_act<ACT_F16>(f);
+  else return f32_to_act<ACT_BF16>(f);
+}
+
+// A piece of a row: 16 bytes where the width and the addresses allow it
+// (VEC), else one element.
+template <int DT, bool VEC>
+struct Piece {
+  using E = typename Elem<DT>::type;
+  static constexpr int N = VEC ? 16 / (int)sizeof(E) : 1;
+  E v[N];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (VEC) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+    else v[0] = *p;
+  }
+  __device__ __forceinline__ void store(E* p) const {
+    if constexpr (VEC) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+    else *p = v[0];
+  }
+  __device__ __forceinline__ float f(int i) const { return to_f32<DT>(v[i]); }
+  __device__ __forceinline__ void set(int i, float x) { v[i] = from_f32<DT>(x); }
+};
+
+// ------------------------------------------------------------ the row maps
+// Expert e keeps its first min(n_e, capacity) slots (capacity 0: all) in
+// ascending slot order; its rows start at row_offsets[e], a multiple of
+// align. Every CTA scans the E counts itself (E <= 512: one value a thread),
+// then takes its share of the rows and, with a capacity, of the slots.
+__global__ void __launch_bounds__(MAX_E) dispatch_plan_kernel(const int* __restrict__ perm,
+                                                              const int* __restrict__ offsets, int S, int E, int align,
+                                                              int capacity, int R, int* __restrict__ row_slot,
+                                                              int* __restrict__ slot_row,
+                                                              int* __restrict__ row_offsets, int* status) {
+  __shared__ int s_off[MAX_E], s_n[MAX_E], s_row[MAX_E + 1], s_warp[MAX_E / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int n = 0, o = 0;
+  bool bad = false;
+  if (tid < E) {
+    // The kernels below index perm with these, so they are clamped to it.
+    const int a = offsets[tid], b = offsets[tid + 1];
+    bad = a < 0 || b < a || b > S || (tid == 0 && a != 0) || (tid == E - 1 && b != S);
+    o = min(max(a, 0), S);
+    n = max(min(b, S) - o, 0);
+    if (capacity > 0) n = min(n, capacity);
+  }
+  if (bad) set_status(status, DEV_BAD_ROUTE);
+  const int padded = (int)(((long long)n + align - 1) / align) * align;
+  int incl = padded;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  const int start = before + incl - padded;
+  if (tid < E) {
+    s_off[tid] = o;
+    s_n[tid] = n;
+    s_row[tid] = start;
+    if (tid == E - 1) s_row[E] = start + padded;
+    if (blockIdx.x == 0) {
+      row_offsets[tid] = min(start, R);
+      if (tid == E - 1) row_offsets[E] = min(start + padded, R);
+    }
+  }
+  __syncthreads();
+  const int total = s_row[E];
+  for (int r = blockIdx.x * blockDim.x + tid; r < R; r += gridDim.x * blockDim.x) {
+    int slot = -1;
+    if (r < total) {
+      int lo = 0, hi = E - 1;  // the last expert that starts at or before r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_row[mid] <= r) lo = mid;
+        else hi = mid - 1;
+      }
+      const int rank = r - s_row[lo];
+      if (rank >= 0 && rank < s_n[lo]) {
+        slot = perm[s_off[lo] + rank];
+        if (slot < 0 || slot >= S) {
+          set_status(status, DEV_BAD_ROUTE);
+          slot = -1;
+        } else {
+          slot_row[slot] = r;
+        }
+      }
+    }
+    row_slot[r] = slot;
+  }
+  if (capacity > 0) {
+    for (int p = blockIdx.x * blockDim.x + tid; p < S; p += gridDim.x * blockDim.x) {
+      int lo = 0, hi = E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_off[mid] <= p) lo = mid;
+        else hi = mid - 1;
+      }
+      const int slot = perm[p];
+      if (p - s_off[lo] >= s_n[lo] && slot >= 0 && slot < S) slot_row[slot] = -1;
+    }
+  }
+}
+
+cudaError_t launch_dispatch_plan(const int* perm, const int* offsets, int S, int E, int align, int capacity, int R,
+                                 int* row_slot, int* slot_row, int* row_offsets, int* status, int num_sms,
+                                 cudaStream_t st) {
+  const int most = R > S ? R : S;
+  const int blocks = (most + MAX_E - 1) / MAX_E;
+  const int grid = blocks < 1 ? 1 : (blocks < num_sms ? blocks : num_sms);
+  cudaError_t e = launch_pdl(dispatch_plan_kernel, dim3(grid), dim3(MAX_E), 0, st, perm, offsets, S, E, align, capacity,
+                             R, row_slot, slot_row, row_offsets, status);
+  count_launches(1);
+  return e;
+}
+
+// ------------------------------------------------------------ the gates' gradient of one token
+// dg: the token's topk dot products, in shared memory. Called by all threads
+// of a group of nthreads; no barrier inside.
+__device__ __forceinline__ void write_gate_grads(const float* dg, const float* gates, const int* ids, int t, int k,
+                                                 int E, float* dgates, float* dlogits, int tid, int nthreads,
+                                                 int* status) {
+  if (dgates && tid < k) dgates[(size_t)t * k + tid] = dg[tid];
+  if (!dlogits) return;
+  float mean = 0.0f;  // sum_i g_i dg_i, ascending i
+  for (int j = 0; j < k; ++j) mean = fmaf(gates[(size_t)t * k + j], dg[j], mean);
+  for (int e = tid; e < E; e += nthreads) {
+    float v = 0.0f;
+    for (int j = 0; j < k; ++j)
+      if (ids[(size_t)t * k + j] == e) v = gates[(size_t)t * k + j] * (dg[j] - mean);
+    dlogits[(size_t)t * E + e] = v;
+  }
+  if (tid < k) {
+    const int e = ids[(size_t)t * k + tid];
+    if (e < 0 || e >= E) set_status(status, DEV_BAD_ROUTE);
+  }
+}
+
+// ------------------------------------------------------------ spread: tokens to rows
+// One warp per slot and column part: rows[slot_row[s]] = (g[s]) v[s / topk], and
+// with DOT dg[s] = <v[s / topk], other[slot_row[s]]>. The CTA holds whole
+// tokens (tokens_per_cta * topk warps), so the second to last warp of a token
+// find its row in L1, and the token's gate gradients are complete after one
+// barrier. The last pad_ctas CTAs write zeros to the rows without a slot.
+template <int DT, bool VEC, bool DOT>
+__global__ void __launch_bounds__(1024) spread_kernel(RowsParams p) {
+  using P = Piece<DT, VEC>;
+  using E = typename P::E;
+  __shared__ float s_dg[32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int k = p.topk;
+  const int cols = p.H / P::N;
+  E* rows = static_cast<E*>(p.rows_out);
+  if ((int)blockIdx.x >= p.token_ctas) {
+    const int nw = blockDim.x >> 5;
+    const int pads = gridDim.x - p.token_ctas;
+    P zero;
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) zero.set(i, 0.0f);
+    for (long long r = (long long)(blockIdx.x - p.token_ctas) * nw + warp; r < p.R; r += (long long)pads * nw) {
+      const int s = p.row_slot[r];
+      if (s >= 0 && s < p.T * k) continue;
+      if (blockIdx.y != 0) continue;
+      for (int c = lane; c < cols; c += 32) zero.store(rows + (size_t)r * p.H + (size_t)c * P::N);
+    }
+    return;
+  }
+  const int w_tok = warp / k, j = warp - w_tok * k;
+  const int t = blockIdx.x * p.tokens_per_cta + w_tok;
+  const bool live = w_tok < p.tokens_per_cta && t < p.T;
+  float dot = 0.0f;
+  if (live) {
+    const size_t s = (size_t)t * k + j;
+    const int r = p.slot_row[s];
+    if (r >= p.R) {
+      if (lane == 0) set_status(p.status, DEV_BAD_ROUTE);
+    } else if (r >= 0) {
+      const E* v = static_cast<const E*>(p.v) + (size_t)t * p.H;
+      E* dst = rows + (size_t)r * p.H;
+      const E* other = DOT ? static_cast<const E*>(p.other) + (size_t)r * p.H : nullptr;
+      const float g = p.gates ? p.gates[s] : 1.0f;
+      const int step = 32 * gridDim.y;
+#pragma unroll 4
+      for (int c = blockIdx.y * 32 + lane; c < cols; c += step) {
+        P a, b;
+        a.load(v + (size_t)c * P::N);
+        if constexpr (DOT) {
+          b.load(other + (size_t)c * P::N);
+#pragma unroll
+          for (int i = 0; i < P::N; ++i) dot = fmaf(a.f(i), b.f(i), dot);
+        }
+        if (p.gates) {
+#pragma unroll
+          for (int i = 0; i < P::N; ++i) a.set(i, g * a.f(i));
+        }
+        a.store(dst + (size_t)c * P::N);
+      }
+    }
+  }
+  if constexpr (DOT) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (lane == 0) s_dg[warp] = dot;
+    __syncthreads();
+    if (live)
+      write_gate_grads(s_dg + w_tok * k, p.gates, p.ids, t, k, p.E, p.dgates, p.dlogits, j * 32 + lane, k * 32,
+                       p.status);
+  }
+}
+
+// ------------------------------------------------------------ collect: rows to tokens
+// One CTA per token (and column part): out[t] = sum_j (g[t,j]) rows[slot_row[t,j]],
+// ascending j, and with KDOT > 0 (at least topk) dg[t,j] = <rows[slot_row[t,j]], v[t]>.
+constexpr int COLLECT_THREADS = 256;
+template <int DT, bool VEC, int KDOT>
+__global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(RowsParams p) {
+  using P = Piece<DT, VEC>;
+  using E = typename P::E;
+  constexpr int KD = KDOT > 0 ? KDOT : 1;
+  __shared__ int s_row[MAX_TOPK];
+  __shared__ float s_g[MAX_TOPK];
+  __shared__ float s_part[KD][COLLECT_THREADS / 32];
+  __shared__ float s_dg[KD];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int k = p.topk, t = blockIdx.x;
+  const int cols = p.H / P::N;
+  if (tid < k) {
+    int r = p.slot_row[(size_t)t * k + tid];
+    if (r >= p.R) {
+      set_status(p.status, DEV_BAD_ROUTE);
+      r = -1;
+    }
+    s_row[tid] = r;
+    s_g[tid] = p.gates ? p.gates[(size_t)t * k + tid] : 1.0f;
+  }
+  __syncthreads();
+  const E* rows = static_cast<const E*>(p.rows_in);
+  E* out = static_cast<E*>(p.out) + (size_t)t * p.H;
+  const E* v = KDOT ? static_cast<const E*>(p.v) + (size_t)t * p.H : nullptr;
+  float dot[KD];
+#pragma unroll
+  for (int j = 0; j < KD; ++j) dot[j] = 0.0f;
+  for (int c = blockIdx.y * COLLECT_THREADS + tid; c < cols; c += COLLECT_THREADS * gridDim.y) {
+    float acc[P::N], vv[P::N];
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) acc[i] = 0.0f;
+    if constexpr (KDOT > 0) {
+      P a;
+      a.load(v + (size_t)c * P::N);
+#pragma unroll
+      for (int i = 0; i < P::N; ++i) vv[i] = a.f(i);
+#pragma unroll
+      for (int j = 0; j < KDOT; ++j) {
+        if (j >= k || s_row[j] < 0) continue;
+        P b;
+        b.load(rows + (size_t)s_row[j] * p.H + (size_t)c * P::N);
+        const float g = s_g[j];
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) {
+          acc[i] = fmaf(g, b.f(i), acc[i]);
+          dot[j] = fmaf(vv[i], b.f(i), dot[j]);
+        }
+      }
+    } else {
+#pragma unroll 8
+      for (int j = 0; j < k; ++j) {
+        const int r = s_row[j];
+        if (r < 0) continue;
+        P b;
+        b.load(rows + (size_t)r * p.H + (size_t)c * P::N);
+        const float g = s_g[j];
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) acc[i] = fmaf(g, b.f(i), acc[i]);
+      }
+    }
+    P o;
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) o.set(i, acc[i]);
+    o.store(out + (size_t)c * P::N);
+  }
+  if constexpr (KDOT > 0) {
+#pragma unroll
+    for (int j = 0; j < KDOT; ++j) {
+      float d = dot[j];
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+      if (lane == 0) s_part[j][warp] = d;
+    }
+    __syncthreads();
+    if (tid < k) {
+      float d = 0.0f;
+      for (int w = 0; w < COLLECT_THREADS / 32; ++w) d += s_part[tid][w];
+      s_dg[tid] = d;
+    }
+    __syncthreads();
+    write_gate_grads(s_dg, p.gates, p.ids, t, k, p.E, p.dgates, p.dlogits, tid, COLLECT_THREADS, p.status);
+  }
+}
+
+// ------------------------------------------------------------ launchers
+static bool rows_vectorised(const RowsParams& p) {
+  const int es = p.row_dtype == ROW_F32 ? 4 : 2;
+  const uintptr_t all = (uintptr_t)p.v | (uintptr_t)p.other | (uintptr_t)p.rows_out | (uintptr_t)p.rows_in |
+                        (uintptr_t)p.out;
+  return ((size_t)p.H * es) % 16 == 0 && all % 16 == 0;
+}
+
+template <int DT, bool VEC>
+static cudaError_t spread_as(const RowsParams& p, dim3 grid, dim3 block, cudaStream_t st) {
+  return p.other ? launch_pdl(spread_kernel<DT, VEC, true>, grid, block, 0, st, p)
+                 : launch_pdl(spread_kernel<DT, VEC, false>, grid, block, 0, st, p);
+}
+cudaError_t launch_spread(RowsParams p, int num_sms, cudaStream_t st) {
+  // At most 8 warps of whole tokens a CTA, one token where it has more slots.
+  p.tokens_per_cta = p.topk >= 8 ? 1 : 8 / p.topk;
+  p.token_ctas = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+  const dim3 block(32 * p.topk * p.tokens_per_cta);
+  const int pads = p.has_pads ? (p.R < num_sms * 8 ? p.R : num_sms * 8) : 0;
+  const dim3 grid((unsigned)(p.token_ctas + pads), 1);
+  if (grid.x == 0) return cudaSuccess;
+  const bool vec = rows_vectorised(p);
+  cudaError_t e;
+  if (p.row_dtype == ROW_BF16)
+    e = vec ? spread_as<ROW_BF16, true>(p, grid, block, st) : spread_as<ROW_BF16, false>(p, grid, block, st);
+  else if (p.row_dtype == ROW_F16)
+    e = vec ? spread_as<ROW_F16, true>(p, grid, block, st) : spread_as<ROW_F16, false>(p, grid, block, st);
+  else
+    e = vec ? spread_as<ROW_F32, true>(p, grid, block, st) : spread_as<ROW_F32, false>(p, grid, block, st);
+  count_launches(1);
+  return e;
+}
+
+template <int DT, bool VEC>
+static cudaError_t collect_as(const RowsParams& p, dim3 grid, cudaStream_t st) {
+  const dim3 block(COLLECT_THREADS);
+  if (!p.v) return launch_pdl(collect_kernel<DT, VEC, 0>, grid, block, 0, st, p);
+  return p.topk <= 8 ? launch_pdl(collect_kernel<DT, VEC, 8>, grid, block, 0, st, p)
+                     : launch_pdl(collect_kernel<DT, VEC, MAX_TOPK>, grid, block, 0, st, p);
+}
+cudaError_t launch_collect(const RowsParams& p, cudaStream_t st) {
+  if (p.T == 0) return cudaSuccess;
+  const bool vec = rows_vectorised(p);
+  const dim3 grid((unsigned)p.T, 1);
+  cudaError_t e;
+  if (p.row_dtype == ROW_BF16) e = vec ? collect_as<ROW_BF16, true>(p, grid, st) : collect_as<ROW_BF16, false>(p, grid, st);
+  else if (p.row_dtype == ROW_F16) e = vec ? collect_as<ROW_F16, true>(p, grid, st) : collect_as<ROW_F16, false>(p, grid, st);
+  else e = vec ? collect_as<ROW_F32, true>(p, grid, st) : collect_as<ROW_F32, false>(p, grid, st);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace hmoe

@@ -132,6 +132,80 @@ cudaError_t launch_act_quant(const uint16_t* x, long long n_values, float g, int
 cudaError_t launch_finalize(const float* y, const float* gates, int T, int k, int H, uint16_t* out, int act_type,
                             cudaStream_t st);
 
+// ---------------------------------------------------------------- rows sorted by expert and back (dispatch.cu)
+// One pass of spread (tokens to rows) or collect (rows to tokens).
+struct RowsParams {
+  int T, H, E, topk, R;    // R: rows of the sorted buffer
+  int row_dtype;           // hmoe_row_dtype of v, other, rows and out
+  const void* v;           // [T][H]: spread's source; collect's dot operand, or NULL (no dot products)
+  const void* other;       // [R][H]: spread's dot operand, or NULL (no dot products)
+  const void* rows_in;     // [R][H]: collect's source
+  void* rows_out;          // [R][H]: spread's result
+  void* out;               // [T][H]: collect's result
+  const float* gates;      // [T][topk], or NULL (weights of one)
+  const int* ids;          // [T][topk], read with dlogits
+  const int* row_slot;     // [R], read by spread where has_pads
+  const int* slot_row;     // [T][topk]
+  float* dgates;           // [T][topk], or NULL
+  float* dlogits;          // [T][E], or NULL
+  int* status;
+  int has_pads;            // 1: the maps may hold rows without a slot, which spread fills with zeros
+  int tokens_per_cta, token_ctas;  // set by launch_spread
+};
+cudaError_t launch_dispatch_plan(const int* perm, const int* offsets, int S, int E, int align, int capacity, int R,
+                                 int* row_slot, int* slot_row, int* row_offsets, int* status, int num_sms,
+                                 cudaStream_t st);
+cudaError_t launch_spread(RowsParams p, int num_sms, cudaStream_t st);
+cudaError_t launch_collect(const RowsParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- low-rank adapters (lora.cu)
+// The packed buffer: ranks int32 [slots], scales fp32 [slots] (each padded to
+// 256 bytes), then one block per slot. With r16 the slot's rank rounded up to
+// 16, a block holds ceil(K / 64) tiles of A, each r16 rows of 64 values in the
+// tensor cores' K-major 128-byte-swizzled layout, then ceil(N / 64) tiles of
+// B, each 64 rows of r16 values in the K-major layout without swizzle (16-byte
+// core-matrix rows: [r16 / 8][64][8 values]). Either tile is r16 * 128 bytes.
+// Rows and columns past the rank, K and N hold zeros.
+constexpr int LORA_MAX_RANK = 128;
+constexpr int LORA_MAX_SLOTS = 512;
+struct LoraGeom {
+  int K, N, slots, max_r16;
+  int KB, NB;                  // 64-wide tiles of K and of N
+  size_t scale_off, block_off; // byte offsets of the scales and of slot 0's block
+  size_t b_off, block_bytes;   // B tiles in a block sized for max_r16, and that block's bytes
+};
+__host__ __device__ inline LoraGeom lora_geom(int K, int N, int slots, int max_rank) {
+  LoraGeom g;
+  g.K = K;
+  g.N = N;
+  g.slots = slots;
+  g.max_r16 = (max_rank + 15) / 16 * 16;
+  g.KB = (K + 63) / 64;
+  g.NB = (N + 63) / 64;
+  g.scale_off = ((size_t)slots * 4 + 255) / 256 * 256;
+  g.block_off = 2 * g.scale_off;
+  g.b_off = (size_t)g.KB * g.max_r16 * 128;
+  g.block_bytes = g.b_off + (size_t)g.NB * g.max_r16 * 128;
+  return g;
+}
+// Marks every slot empty (rank 0).
+cudaError_t launch_lora_clear(const LoraGeom& g, uint8_t* packed, cudaStream_t st);
+cudaError_t launch_lora_load(const LoraGeom& g, uint8_t* packed, int slot, const uint16_t* A, const uint16_t* B,
+                             int rank, float scale, cudaStream_t st);
+struct LoraParams {
+  LoraGeom g;
+  const uint8_t* packed;
+  int T, act_type;
+  const uint16_t* x;
+  const uint16_t* base;   // NULL: zeros
+  uint16_t* out;
+  size_t ldx, ldbase, ldout;  // row strides in elements
+  const int* ids;
+  int* status;
+  float* u;               // [T][max_r16] fp32 scratch
+};
+cudaError_t launch_lora_forward(const LoraParams& p, int num_sms, cudaStream_t st);
+
 // Raises a kernel's dynamic shared-memory limit once per device: the
 // attribute belongs to the current device, so a process that launches on
 // several GPUs sets it on each. done is the kernel's bit mask of devices

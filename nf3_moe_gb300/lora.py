@@ -1,0 +1,133 @@
+"""Low-rank adapters of many requests beside a shared projection (include/hmoe.h).
+
+    adapters = LoraAdapters(K, N, slots=32, max_rank=64, max_tokens=T)
+    adapters.load(3, A, B, scale=alpha / rank)       # A [rank, K], B [N, rank]
+    y = linear(x)                                    # the shared projection, [T, N]
+    adapters(x, ids, base=y, out=y)                  # y[t] += scale_a B_a (A_a x[t]), a = ids[t]; -1: none
+"""
+
+import ctypes
+
+import torch
+
+from . import _lib, _need, act_torch_dtype, hmoe_workspace_init
+from ._lib import ACT_BF16, LoraDesc
+from .rows import _is, _raw_stream
+
+
+def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
+    """A [T, width] tensor whose rows are contiguous and evenly spaced (a column range of a wider one serves).
+    Returns the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != width or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} must have shape [{'*' if T is None else T}, {width}], got {list(t.shape)}")
+    ld, one = t.stride()
+    if t.shape[0] <= 1:
+        ld = max(ld, width) if ld % 8 == 0 else width   # one row: its stride is never used
+    if one != 1 or ld < width:
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap, got strides {list(t.stride())}")
+    if cuda:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
+    return ld
+
+
+def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
+    """Returns T and the row strides of x, base and out."""
+    dt = act_torch_dtype(desc.act_dtype)
+    ldx = _need_rows("x", x, None, desc.K, dt, cuda=cuda)
+    T, dev = x.shape[0], x.device
+    _is("ids", ids, (T,), torch.int32, dev, cuda)
+    ldo = _need_rows("out", out, T, desc.N, dt, dev, cuda)
+    ldb = 0 if base is None else _need_rows("base", base, T, desc.N, dt, dev, cuda)
+    _need("ws", ws, device=dev, cuda=cuda)
+    return T, ldx, ldb, ldo
+
+
+def hmoe_lora_packed_size(desc):
+    b = ctypes.c_size_t()
+    _lib.check(_lib.lib().hmoe_lora_packed_size(ctypes.byref(desc), ctypes.byref(b)))
+    return b.value
+
+
+def hmoe_lora_workspace_size(desc, max_tokens):
+    b = ctypes.c_size_t()
+    _lib.check(_lib.lib().hmoe_lora_workspace_size(ctypes.byref(desc), int(max_tokens), ctypes.byref(b)))
+    return b.value
+
+
+class Lora:
+    """Owns the C handle of a set of adapters; keeps the packed buffer alive."""
+
+    def __init__(self, handle, desc, packed):
+        self.handle, self.desc, self.packed = handle, desc, packed
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib._LIB is not None:
+            _lib._LIB.hmoe_lora_destroy(h)
+
+
+def hmoe_lora_create(desc, packed, stream=None):
+    _need("packed", packed, min_bytes=hmoe_lora_packed_size(desc))
+    h = ctypes.c_void_p()
+    _lib.check(_lib.lib().hmoe_lora_create(ctypes.byref(desc), packed.data_ptr(), _raw_stream(stream), ctypes.byref(h)))
+    return Lora(h, desc, packed)
+
+
+def _check_lora_load(desc, slot, A, B, cuda=True):
+    dt = act_torch_dtype(desc.act_dtype)
+    _need("A", A, (None, desc.K), dt, cuda=cuda)
+    _need("B", B, (desc.N, A.shape[0]), dt, device=A.device, cuda=cuda)
+
+
+def hmoe_lora_load(lora, slot, A, B, scale=1.0, stream=None):
+    """Put the adapter A [rank, K], B [N, rank] into a slot; A and B None empty it."""
+    if A is None and B is None:
+        _lib.check(_lib.lib().hmoe_lora_load(lora.handle, int(slot), None, None, 0, 0.0, _raw_stream(stream)))
+        return
+    _check_lora_load(lora.desc, slot, A, B)
+    _lib.check(_lib.lib().hmoe_lora_load(lora.handle, int(slot), A.data_ptr(), B.data_ptr(), int(A.shape[0]),
+                                         float(scale), _raw_stream(stream)))
+
+
+def hmoe_lora_forward(lora, x, ids, out, ws, base=None, stream=None):
+    """out[t] = base[t] + scale_a B_a (A_a x[t]), a = ids[t]; base None: zeros; base may be out."""
+    T, ldx, ldb, ldo = _check_lora_forward(lora.desc, x, ids, base, out, ws)
+    _lib.check(_lib.lib().hmoe_lora_forward(lora.handle, x.data_ptr(), ldx, T, ids.data_ptr(),
+                                            None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
+                                            ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)))
+
+
+class LoraAdapters:
+    """Low-rank adapters with their packed buffer and workspace owned as torch tensors.
+
+    K, N: widths of the projection's input and output; slots: adapters held at once; max_rank:
+    the largest rank of any; max_tokens sizes the workspace.
+    """
+
+    def __init__(self, K, N, slots, max_rank, max_tokens=8, act_dtype=ACT_BF16, device="cuda"):
+        self.desc = LoraDesc(K, N, slots, max_rank, act_dtype)
+        self.dtype = act_torch_dtype(act_dtype)
+        self.packed = torch.empty(hmoe_lora_packed_size(self.desc), dtype=torch.uint8, device=device)
+        self.lora = hmoe_lora_create(self.desc, self.packed)
+        self.ws = torch.empty(hmoe_lora_workspace_size(self.desc, max_tokens), dtype=torch.uint8, device=device)
+        hmoe_workspace_init(self.ws)
+        self.N = N
+
+    def load(self, slot, A, B, scale=1.0):
+        hmoe_lora_load(self.lora, slot, A, B, scale)
+
+    def unload(self, slot):
+        hmoe_lora_load(self.lora, slot, None, None)
+
+    def __call__(self, x, ids, base=None, out=None):
+        if out is None:
+            out = torch.empty((x.shape[0], self.N), dtype=self.dtype, device=x.device)
+        hmoe_lora_forward(self.lora, x, ids, out, self.ws, base=base)
+        return out

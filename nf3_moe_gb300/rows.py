@@ -1,0 +1,232 @@
+"""Token rows sorted by expert and back, with the gates applied, and their gradients (include/hmoe.h).
+
+The functions keep the C names and take torch tensors the caller owns. ``ExpertRows`` owns the
+buffers instead and takes part in autograd:
+
+    rows_of = ExpertRows(H, E, topk, max_tokens=T)
+    ids, gates, perm, offsets = layer.plan(logits)
+    rows, plan = rows_of.dispatch(x, perm, offsets)      # [R, H], each expert's rows side by side
+    y = experts(rows, plan.row_offsets)                  # the caller's own work
+    out = rows_of.combine(y, plan, gates, ids=ids, logits=logits)
+    out.backward(...)                                    # x, y, gates and the router logits get gradients
+"""
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import _lib, _need
+from ._lib import ROW_BF16, ROW_F16, ROW_F32, DispatchDesc
+
+_TORCH = {ROW_BF16: torch.bfloat16, ROW_F16: torch.float16, ROW_F32: torch.float32}
+_ROW = {v: k for k, v in _TORCH.items()}
+
+
+def row_torch_dtype(row_dtype):
+    """The torch dtype of rows for a ROW_* value."""
+    return _TORCH[int(row_dtype)]
+
+
+def _is(name, t, shape, dtype, device, cuda=True):
+    """_need for a tensor that is nearly always right: one look, and the full check for its message."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.is_contiguous()
+            and (not cuda or (t.is_cuda and t.device == device))):
+        _need(name, t, shape, dtype, device=device, cuda=cuda)
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def hmoe_dispatch_rows(desc, T):
+    """Rows of the sorted buffer for T tokens."""
+    n = ctypes.c_int()
+    _lib.check(_lib.lib().hmoe_dispatch_rows(ctypes.byref(desc), int(T), ctypes.byref(n)))
+    return n.value
+
+
+def hmoe_dispatch_workspace_size(desc, max_tokens):
+    b = ctypes.c_size_t()
+    _lib.check(_lib.lib().hmoe_dispatch_workspace_size(ctypes.byref(desc), int(max_tokens), ctypes.byref(b)))
+    return b.value
+
+
+def _check_tokens(name, desc, t, cuda):
+    _need(name, t, (None, desc.H), row_torch_dtype(desc.row_dtype), cuda=cuda)
+    return t.shape[0], t.dtype, t.device
+
+
+def _check_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates, cuda=True):
+    T, dt, dev = _check_tokens("x", desc, x, cuda)
+    R, k, i32 = hmoe_dispatch_rows(desc, T), desc.topk, torch.int32
+    _is("perm", perm, (T * k,), i32, dev, cuda)
+    _is("offsets", offsets, (desc.E + 1,), i32, dev, cuda)
+    _is("rows", rows, (R, desc.H), dt, dev, cuda)
+    _is("row_slot", row_slot, (R,), i32, dev, cuda)
+    _is("slot_row", slot_row, (T, k), i32, dev, cuda)
+    _is("row_offsets", row_offsets, (desc.E + 1,), i32, dev, cuda)
+    if gates is not None:
+        _is("gates", gates, (T, k), torch.float32, dev, cuda)
+    _need("ws", ws, device=dev, cuda=cuda)
+    return T
+
+
+def _check_collect(desc, name, rows, slot_row, out_name, out, ws, gates, cuda=True):
+    T, dt, dev = _check_tokens(out_name, desc, out, cuda)
+    _is(name, rows, (hmoe_dispatch_rows(desc, T), desc.H), dt, dev, cuda)
+    _is("slot_row", slot_row, (T, desc.topk), torch.int32, dev, cuda)
+    if gates is not None:
+        _is("gates", gates, (T, desc.topk), torch.float32, dev, cuda)
+    _need("ws", ws, device=dev, cuda=cuda)
+    return T
+
+
+def _check_gate_grads(desc, T, dev, dot_name, dot, dot_shape, gates, ids, dgates, dlogits, cuda=True):
+    k = desc.topk
+    if (dgates is not None or dlogits is not None) and (gates is None or dot is None):
+        raise ValueError(f"dgates and dlogits need gates and {dot_name}")
+    if dlogits is not None and ids is None:
+        raise ValueError("dlogits needs ids")
+    for name, t, shape, dtype in ((dot_name, dot, dot_shape, row_torch_dtype(desc.row_dtype)), ("ids", ids, (T, k), torch.int32),
+                                  ("dgates", dgates, (T, k), torch.float32), ("dlogits", dlogits, (T, desc.E), torch.float32)):
+        if t is not None:
+            _is(name, t, shape, dtype, dev, cuda)
+
+
+def hmoe_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates=None, stream=None):
+    """rows[r] = (gates) x[row_slot[r] / topk], and the row maps; every output is fully written."""
+    T = _check_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates)
+    _lib.check(_lib.lib().hmoe_dispatch(ctypes.byref(desc), x.data_ptr(), T, _raw(gates), perm.data_ptr(),
+                                        offsets.data_ptr(), rows.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
+                                        row_offsets.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                        _raw_stream(stream)))
+
+
+def hmoe_dispatch_backward(desc, drows, slot_row, dx, ws, x=None, gates=None, ids=None, dgates=None, dlogits=None,
+                           stream=None):
+    """dx[t] = sum_j (gates) drows[slot_row[t, j]], and with gates and x the gates' and router logits' gradients."""
+    T = _check_collect(desc, "drows", drows, slot_row, "dx", dx, ws, gates)
+    _check_gate_grads(desc, T, dx.device, "x", x, dx.shape, gates, ids, dgates, dlogits)
+    _lib.check(_lib.lib().hmoe_dispatch_backward(ctypes.byref(desc), drows.data_ptr(), T, slot_row.data_ptr(), _raw(x),
+                                                 _raw(gates), _raw(ids), dx.data_ptr(), _raw(dgates), _raw(dlogits),
+                                                 ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)))
+
+
+def hmoe_combine(desc, rows, slot_row, out, ws, gates=None, stream=None):
+    """out[t] = sum_j (gates) rows[slot_row[t, j]]."""
+    T = _check_collect(desc, "rows", rows, slot_row, "out", out, ws, gates)
+    _lib.check(_lib.lib().hmoe_combine(ctypes.byref(desc), rows.data_ptr(), T, slot_row.data_ptr(), _raw(gates),
+                                       out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                       _raw_stream(stream)))
+
+
+def hmoe_combine_backward(desc, dout, row_slot, slot_row, drows, ws, rows=None, gates=None, ids=None, dgates=None,
+                          dlogits=None, stream=None):
+    """drows[r] = (gates) dout[row_slot[r] / topk], zero on padding, and with gates and rows the gates' and router
+    logits' gradients."""
+    T = _check_collect(desc, "drows", drows, slot_row, "dout", dout, ws, gates)
+    _is("row_slot", row_slot, (drows.shape[0],), torch.int32, dout.device)
+    _check_gate_grads(desc, T, dout.device, "rows", rows, drows.shape, gates, ids, dgates, dlogits)
+    _lib.check(_lib.lib().hmoe_combine_backward(ctypes.byref(desc), dout.data_ptr(), T, row_slot.data_ptr(),
+                                                slot_row.data_ptr(), _raw(rows), _raw(gates), _raw(ids),
+                                                drows.data_ptr(), _raw(dgates), _raw(dlogits), ws.data_ptr(),
+                                                ws.numel() * ws.element_size(), _raw_stream(stream)))
+
+
+# ------------------------------------------------------------------ owned buffers and autograd
+class RowPlan(NamedTuple):
+    """The row maps of one dispatch: row_slot [R], slot_row [T, topk], row_offsets [E + 1]."""
+    row_slot: torch.Tensor
+    slot_row: torch.Tensor
+    row_offsets: torch.Tensor
+
+
+def _gate_grad_bufs(ctx, T, E, gates, gates_at, logits_at):
+    dgates = torch.empty_like(gates) if ctx.needs_input_grad[gates_at] else None
+    dlogits = gates.new_empty((T, E)) if ctx.needs_input_grad[logits_at] else None
+    return dgates, dlogits
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gates, logits, ids, perm, offsets, desc, ws):
+        T, dev = x.shape[0], x.device
+        R = hmoe_dispatch_rows(desc, T)
+        rows = torch.empty((R, desc.H), dtype=x.dtype, device=dev)
+        row_slot = torch.empty((R,), dtype=torch.int32, device=dev)
+        slot_row = torch.empty((T, desc.topk), dtype=torch.int32, device=dev)
+        row_offsets = torch.empty((desc.E + 1,), dtype=torch.int32, device=dev)
+        hmoe_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates=gates)
+        ctx.save_for_backward(x if gates is not None else None, gates, ids, slot_row)
+        ctx.desc, ctx.ws, ctx.shape = desc, ws, x.shape
+        ctx.mark_non_differentiable(row_slot, slot_row, row_offsets)
+        return rows, row_slot, slot_row, row_offsets
+
+    @staticmethod
+    def backward(ctx, drows, *_):
+        x, gates, ids, slot_row = ctx.saved_tensors
+        drows = drows.contiguous()
+        dx = drows.new_empty(ctx.shape)
+        dgates = dlogits = None
+        if gates is not None:
+            dgates, dlogits = _gate_grad_bufs(ctx, ctx.shape[0], ctx.desc.E, gates, 1, 2)
+        hmoe_dispatch_backward(ctx.desc, drows, slot_row, dx, ctx.ws, x=x, gates=gates, ids=ids, dgates=dgates,
+                               dlogits=dlogits)
+        return dx, dgates, dlogits, None, None, None, None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, gates, logits, ids, row_slot, slot_row, desc, ws):
+        out = rows.new_empty((slot_row.shape[0], desc.H))
+        hmoe_combine(desc, rows, slot_row, out, ws, gates=gates)
+        ctx.save_for_backward(rows if gates is not None else None, gates, ids, row_slot, slot_row)
+        ctx.desc, ctx.ws, ctx.shape = desc, ws, rows.shape
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        rows, gates, ids, row_slot, slot_row = ctx.saved_tensors
+        dout = dout.contiguous()
+        drows = dout.new_empty(ctx.shape)
+        dgates = dlogits = None
+        if gates is not None:
+            dgates, dlogits = _gate_grad_bufs(ctx, dout.shape[0], ctx.desc.E, gates, 1, 2)
+        hmoe_combine_backward(ctx.desc, dout, row_slot, slot_row, drows, ctx.ws, rows=rows, gates=gates, ids=ids,
+                              dgates=dgates, dlogits=dlogits)
+        return drows, dgates, dlogits, None, None, None, None, None
+
+
+class ExpertRows:
+    """Sorting token rows by expert and bringing them back, differentiable.
+
+    H, E, topk, dtype (bf16, fp16 or fp32), align and capacity: as in DispatchDesc.
+
+    gates given to dispatch (or to combine) are applied there. Gradients flow to x, rows and
+    gates. The gates of hmoe_plan_routes are a softmax over the chosen router logits; give ids
+    and logits as well and the logits get their gradient through it (the logits' values are not
+    read). Then take the gates from plan as they are: a gates tensor that requires a gradient
+    itself gets one too.
+    """
+
+    def __init__(self, H, E, topk, max_tokens=8, dtype=torch.bfloat16, align=1, capacity=0, device="cuda"):
+        if dtype not in _ROW:
+            raise ValueError(f"dtype must be torch.bfloat16, torch.float16 or torch.float32, got {dtype}")
+        self.desc = DispatchDesc(H, E, topk, _ROW[dtype], align, capacity)
+        self.dtype = dtype
+        size = hmoe_dispatch_workspace_size(self.desc, max_tokens)
+        self.ws = torch.zeros(size, dtype=torch.uint8, device=device)
+
+    def dispatch(self, x, perm, offsets, gates=None, ids=None, logits=None):
+        """x [T, H] -> (rows [R, H], RowPlan)."""
+        rows, *plan = _Dispatch.apply(x, gates, logits, ids, perm, offsets, self.desc, self.ws)
+        return rows, RowPlan(*plan)
+
+    def combine(self, rows, plan, gates=None, ids=None, logits=None):
+        """rows [R, H] -> out [T, H]."""
+        return _Combine.apply(rows, gates, logits, ids, plan.row_slot, plan.slot_row, self.desc, self.ws)
