@@ -1173,19 +1173,8 @@ hmoe_status check_lora_desc(const hmoe_lora_desc* d) {
   return HMOE_OK;
 }
 
-struct LoraWsLayout {
-  size_t status, u, total;
-};
-LoraWsLayout lora_ws_layout(const LoraGeom& g, int T) {
-  LoraWsLayout w{};
-  size_t off = 0;
-  w.status = off;
-  off += 256;
-  w.u = off;
-  off += align256((size_t)T * g.max_r16 * 4);
-  w.total = off;
-  return w;
-}
+// The status word, then the scratch of batches above the one-launch limit.
+size_t lora_ws_total(const LoraGeom& g, int T) { return 256 + lora_scratch(g, T).total; }
 
 }  // namespace
 
@@ -1204,7 +1193,7 @@ hmoe_status hmoe_lora_workspace_size(const hmoe_lora_desc* desc, int max_tokens,
   hmoe_status s = check_lora_desc(desc);
   if (s != HMOE_OK) return s;
   if (!bytes || max_tokens < 0) return fail(HMOE_ERR_INVALID_ARG, "bytes NULL or max_tokens < 0");
-  *bytes = lora_ws_layout(lora_geom(desc->K, desc->N, desc->slots, desc->max_rank), max_tokens).total;
+  *bytes = lora_ws_total(lora_geom(desc->K, desc->N, desc->slots, desc->max_rank), max_tokens);
   return HMOE_OK;
 }
 
@@ -1265,10 +1254,11 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T,
   if (base == out && ldbase != ldout) return fail(HMOE_ERR_INVALID_ARG, "in place, ldbase and ldout must be equal");
   hmoe_status s = check_status_ws(ws, ws_bytes);
   if (s != HMOE_OK) return s;
-  const LoraWsLayout w = lora_ws_layout(L->g, T);
-  if (ws_bytes < w.total)
-    return fail(HMOE_ERR_WORKSPACE_TOO_SMALL, "workspace holds %zu bytes, T=%d needs %zu", ws_bytes, T, w.total);
-  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  const size_t need = lora_ws_total(L->g, T);
+  if (ws_bytes < need)
+    return fail(HMOE_ERR_WORKSPACE_TOO_SMALL, "workspace holds %zu bytes, T=%d needs %zu", ws_bytes, T, need);
+  const LoraScratch w = lora_scratch(L->g, T);
+  uint8_t* scratch = static_cast<uint8_t*>(ws) + 256;
   LoraParams p{};
   p.g = L->g;
   p.packed = L->packed;
@@ -1281,8 +1271,13 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T,
   p.ldbase = (size_t)ldbase;
   p.ldout = (size_t)ldout;
   p.ids = ids;
-  p.status = reinterpret_cast<int*>(wsb + w.status);
-  p.u = reinterpret_cast<float*>(wsb + w.u);
+  p.status = static_cast<int*>(ws);
+  p.wait_limit_ns = WAIT_LIMIT_NS;
+  p.meta = reinterpret_cast<int*>(scratch + w.meta);
+  p.tiles = reinterpret_cast<int4*>(scratch + w.tiles);
+  p.arrived = reinterpret_cast<int*>(scratch + w.arrived);
+  p.perm = reinterpret_cast<int*>(scratch + w.perm);
+  p.u = reinterpret_cast<float*>(scratch + w.u);
   cudaError_t e = launch_lora_forward(p, L->num_sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "adapter launch");
   return HMOE_OK;

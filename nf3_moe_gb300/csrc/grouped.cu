@@ -56,6 +56,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace hmoe {
 
@@ -124,58 +125,7 @@ static_assert(GT_SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(GT_OFF_P % 16 == 0 && GT_OFF_B % 1024 == 0, "alignment");
 static_assert(GT_TMEM_COLS <= 512, "TMEM columns");
 
-// ------------------------------------------------------------ tcgen05 / TMA wrappers
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// tcgen05.mma (kind::f16, A and B from shared memory, D in TMEM) and its
-// commit, issued from a converged warp: every lane executes
-// the instruction, and elect.sync predicates it to one lane (the lowest
-// active one, so MMAs and their commits come from the same thread). Measured
-// against issuing from inside an `if (lane == 0)` branch: a 128 x 128 x 16
-// MMA takes 65 instead of 120 cycles of the tensor core's issue slot, the
-// full rate of the tensor core, instead of half of it.
-__device__ __forceinline__ void umma_kf16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-
+// ------------------------------------------------------------ TMEM load, store and TMA wrappers
 // 16 lanes x 256 bits, four times along the columns: thread t gets rows
 // base + t/4 (regs 4j, 4j+1) and base + t/4 + 8 (regs 4j+2, 4j+3) at
 // columns 8j + 2(t % 4) and + 1 of repetition j.
@@ -265,33 +215,6 @@ __device__ __forceinline__ void bulk_g2s_stream_if(bool pred, void* dst, const v
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y)
                : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart (SBO), version 1, base offset 0 (atoms 1024-aligned).
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
-  uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1u << 16;                 // leading byte offset (unused for swizzled K-major)
-  d |= (uint64_t)(1024u >> 4) << 32;       // stride byte offset
-  d |= (uint64_t)1u << 46;                 // descriptor version
-  d |= (uint64_t)2u << 61;                 // SWIZZLE_128B
-  return d;
-}
-// The descriptor above as (low word, high word). The low word holds the start
-// address (>> 4) and the leading byte offset; the high word is constant.
-// Advancing 32 bytes along K adds 2 to the low word.
-constexpr uint32_t SW128_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t smem_desc_sw128_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
-__device__ __forceinline__ uint64_t desc_from_lo(uint32_t lo) {
-  return ((uint64_t)SW128_DESC_HI << 32) | (uint64_t)lo;
-}
-
-// Instruction descriptor, kind::f16: D fp32, A and B of the same type (bf16,
-// type code 1, or fp16, code 0), both K-major.
-template <int ACT = ACT_BF16>
-__device__ __forceinline__ uint32_t idesc_kf16(int M, int N) {
-  constexpr uint32_t ab = ACT == ACT_F16 ? 0u : 1u;
-  return (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // A work item: nt token tiles of 128 permuted slots from p0 (n slots in all)
