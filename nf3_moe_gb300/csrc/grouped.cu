@@ -194,14 +194,6 @@ __device__ __forceinline__ void tma_prefetch_2d_elect(const CUtensorMap* map, in
 // From a converged warp: an elected lane registers the bytes on the barrier,
 // then every lane whose predicate is set issues its own 1D bulk copy (L2
 // evict-first), all in one warp instruction.
-__device__ __forceinline__ void mbar_expect_tx_elect(uint64_t* bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(bytes)
-      : "memory");
-}
 __device__ __forceinline__ void bulk_g2s_stream_if(bool pred, void* dst, const void* src, uint32_t bytes, uint64_t* bar,
                                                    uint64_t policy) {
   asm volatile(

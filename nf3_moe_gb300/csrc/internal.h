@@ -209,32 +209,29 @@ struct LoraParams {
   int* arrived;
   int* perm;
   float* u;
+  float* part;
 };
-// Scratch of a larger batch of T rows: rows grouped by adapter (perm), cut
+// Scratch of a larger batch of T rows: the rows grouped by adapter (perm), cut
 // into tiles of up to LORA_TILE_ROWS rows (tiles: adapter or -1, first
-// position, rows), the number of finished K splits of each tile (arrived), and
-// A x of every position in up to LORA_MAX_SPLITS partial sums. meta: tiles
-// with an adapter, all tiles, K splits, rows with an adapter.
+// position, rows), the number of finished pieces of each tile (arrived), A x
+// of every position (u), and the pieces' sums, two for each CTA (part). meta:
+// tiles with an adapter, all tiles.
 constexpr int LORA_TILE_ROWS = 128;
-constexpr int LORA_MAX_SPLITS = 8;
-// The K splits of a batch make about this many work items, two for each SM.
-constexpr int LORA_SPLIT_ITEMS = 304;
+constexpr int LORA_MAX_CTAS = 160;
 struct LoraScratch {
-  size_t meta, tiles, arrived, perm, u, total;
+  size_t meta, tiles, arrived, perm, u, part, total;
 };
 inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
   auto pad = [](size_t b) { return (b + 255) / 256 * 256; };
   const size_t most = (size_t)T / LORA_TILE_ROWS + (size_t)(T < g.slots + 1 ? T : g.slots + 1);
-  // n rows with an adapter make at least n / 128 tiles, so splits * n is at most (SPLIT_ITEMS / tiles + 1) * n
-  // <= SPLIT_ITEMS * 128 + n, and at most MAX_SPLITS * n
-  const size_t by_items = (size_t)LORA_SPLIT_ITEMS * LORA_TILE_ROWS + (size_t)T, by_most = (size_t)LORA_MAX_SPLITS * T;
   LoraScratch s;
   s.meta = 0;
   s.tiles = s.meta + 256;
   s.arrived = s.tiles + pad(most * 16);
   s.perm = s.arrived + pad(most * 4);
   s.u = s.perm + pad((size_t)T * 4);
-  s.total = s.u + pad((by_items < by_most ? by_items : by_most) * g.max_r16 * 4);
+  s.part = s.u + pad((size_t)T * g.max_r16 * 4);
+  s.total = s.part + (size_t)LORA_MAX_CTAS * 2 * LORA_TILE_ROWS * g.max_r16 * 4;
   return s;
 }
 cudaError_t launch_lora_forward(const LoraParams& p, int num_sms, cudaStream_t st);

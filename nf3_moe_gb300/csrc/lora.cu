@@ -310,37 +310,64 @@ static cudaError_t small_of(const LoraParams& p, cudaStream_t st) {
 // and the adapter on its N side.
 
 // One CTA. Rows without an adapter (or with an empty slot) form the last group.
-// The order of the rows inside a group does not matter to any result.
+// The rows of a group keep their order, so that the tiles, and with them the
+// order of every sum, depend on the ids alone: each warp counts its own range
+// of rows (s_base[warp][group]), and the counts are summed over the warps.
 constexpr int LP_THREADS = 1024;
+constexpr int LP_WARPS = LP_THREADS / 32;
+constexpr int LP_IDS = 8;  // ids a thread holds at once: their loads are in flight together
 __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
-  __shared__ int s_cnt[LORA_MAX_SLOTS + 1], s_rank[LORA_MAX_SLOTS + 1], s_wsum[2][LP_THREADS / 32];
+  extern __shared__ int s_base[];  // [LP_WARPS][G]
+  __shared__ int s_rank[LORA_MAX_SLOTS + 1], s_wsum[2][LP_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.g.slots + 1;
-  for (int g = tid; g < G; g += LP_THREADS) s_cnt[g] = 0;
+  for (int i = tid; i < LP_WARPS * G; i += LP_THREADS) s_base[i] = 0;
   pdl_wait();
   pdl_trigger();
-  for (int g = tid; g < G; g += LP_THREADS) s_rank[g] = g < p.g.slots ? reinterpret_cast<const int*>(p.packed)[g] : 0;
-  __syncthreads();
-  auto group_of = [&](int t) {
-    const int a = lora_slot(p, t);
-    return a >= 0 && s_rank[a] > 0 ? a : G - 1;
-  };
-  // The place of a row in its group, one atomic per group and warp; kept in
-  // the u scratch, which nothing else uses yet.
+  if (tid < G) s_rank[tid] = tid < p.g.slots ? reinterpret_cast<const int*>(p.packed)[tid] : 0;
+  // The warp's rows, 32 a round; the place of a row in the warp's part of its
+  // group. Batches above LP_IDS rounds keep the places in the u scratch, unused
+  // as yet.
+  const int rounds = (p.T + LP_THREADS - 1) / LP_THREADS;
+  const int t0 = warp * rounds * 32 + lane;
+  int* mine = s_base + warp * G;
   int* place = reinterpret_cast<int*>(p.u);
-  for (int t0 = warp * 32; t0 < p.T; t0 += LP_THREADS) {
-    const int t = t0 + lane;
-    const int g = t < p.T ? group_of(t) : -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, g);
-    const int first = __ffs(peers) - 1;
-    int base = 0;
-    if (lane == first && g >= 0) base = atomicAdd(&s_cnt[g], __popc(peers));
-    base = __shfl_sync(0xffffffffu, base, first);
-    if (g >= 0) place[t] = base + __popc(peers & ((1u << lane) - 1u));
+  int g[LP_IDS], at[LP_IDS];
+  for (int r0 = 0; r0 < rounds; r0 += LP_IDS) {
+#pragma unroll
+    for (int i = 0; i < LP_IDS; ++i) {
+      const int t = t0 + (r0 + i) * 32;
+      g[i] = r0 + i < rounds && t < p.T ? lora_slot(p, t) : -2;
+    }
+    if (r0 == 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < LP_IDS; ++i) {
+      if (r0 + i < rounds) {
+        if (g[i] > -2 && (g[i] < 0 || s_rank[g[i]] == 0)) g[i] = G - 1;
+        const unsigned peers = __match_any_sync(0xffffffffu, g[i]);
+        if (g[i] >= 0) {
+          at[i] = mine[g[i]] + __popc(peers & ((1u << lane) - 1u));
+          if (rounds > LP_IDS) place[t0 + (r0 + i) * 32] = at[i];
+        }
+        __syncwarp();
+        if (g[i] >= 0 && lane == __ffs(peers) - 1) mine[g[i]] += __popc(peers);
+        __syncwarp();
+      }
+    }
   }
   __syncthreads();
-  // Exclusive scans of the groups' rows and tiles (G <= 513 <= LP_THREADS).
-  const int n = tid < G ? s_cnt[tid] : 0, nt = (n + LORA_TILE_ROWS - 1) / LORA_TILE_ROWS;
+  // Each group's counts become the warps' places in it; then exclusive scans
+  // of the groups' rows and tiles (G <= 513 <= LP_THREADS).
+  int n = 0;
+  if (tid < G) {
+#pragma unroll 8
+    for (int w = 0; w < LP_WARPS; ++w) {
+      const int c = s_base[w * G + tid];
+      s_base[w * G + tid] = n;
+      n += c;
+    }
+  }
+  const int nt = (n + LORA_TILE_ROWS - 1) / LORA_TILE_ROWS;
   int in = n, it = nt;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -355,66 +382,194 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
     s_wsum[1][warp] = it;
   }
   __syncthreads();
-  int bn = 0, bt = 0;
+  int row0 = in - n, tile0 = it - nt;
   for (int w = 0; w < warp; ++w) {
-    bn += s_wsum[0][w];
-    bt += s_wsum[1][w];
+    row0 += s_wsum[0][w];
+    tile0 += s_wsum[1][w];
   }
-  const int row0 = bn + in - n, tile0 = bt + it - nt;
-  __syncthreads();
   if (tid < G) {
-    s_cnt[tid] = row0;  // from here on: where the group starts
-    for (int j = 0; j < nt; ++j) {
-      p.tiles[tile0 + j] = make_int4(tid < G - 1 ? tid : -1, row0 + j * LORA_TILE_ROWS,
-                                     min(LORA_TILE_ROWS, n - j * LORA_TILE_ROWS), 0);
-      p.arrived[tile0 + j] = 0;
-    }
-    if (tid == G - 1) {
-      const int with = tile0;
-      p.meta[0] = with;
-      p.meta[1] = tile0 + nt;
-      p.meta[3] = row0;
-      const int s = with > 0 ? (LORA_SPLIT_ITEMS + with - 1) / with : 1;
-      p.meta[2] = max(1, min(min(s, LORA_MAX_SPLITS), p.g.KB));
+#pragma unroll 8
+    for (int w = 0; w < LP_WARPS; ++w) s_base[w * G + tid] += row0;
+  }
+  if (tid == G - 1) {
+    p.meta[0] = tile0;
+    p.meta[1] = tile0 + nt;
+  }
+  // The tiles of the warp's groups, group by group.
+  for (unsigned some = __ballot_sync(0xffffffffu, nt > 0); some; some &= some - 1) {
+    const int l = __ffs(some) - 1;
+    const int gn = __shfl_sync(0xffffffffu, n, l), gr = __shfl_sync(0xffffffffu, row0, l);
+    const int gt = __shfl_sync(0xffffffffu, tile0, l), who = warp * 32 + l;
+    for (int j = lane; j * LORA_TILE_ROWS < gn; j += 32) {
+      p.tiles[gt + j] = make_int4(who < G - 1 ? who : -1, gr + j * LORA_TILE_ROWS,
+                                  min(LORA_TILE_ROWS, gn - j * LORA_TILE_ROWS), s_rank[who]);
+      p.arrived[gt + j] = 0;
     }
   }
   __syncthreads();
-  for (int t = tid; t < p.T; t += LP_THREADS) p.perm[s_cnt[group_of(t)] + place[t]] = t;
+  if (rounds <= LP_IDS) {
+#pragma unroll
+    for (int i = 0; i < LP_IDS; ++i)
+      if (i < rounds && g[i] >= 0) p.perm[mine[g[i]] + at[i]] = t0 + i * 32;
+  } else {
+    for (int r = 0; r < rounds; ++r) {
+      const int t = t0 + r * 32;
+      if (t >= p.T) break;
+      const int a = lora_slot(p, t);
+      p.perm[mine[a >= 0 && s_rank[a] > 0 ? a : G - 1] + place[t]] = t;
+    }
+  }
 }
+constexpr int lp_smem(int slots) { return LP_WARPS * (slots + 1) * 4; }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-constexpr int LT_THREADS = 256;
-constexpr int LT_STAGES = 4;
+// ------------------------------------------------------------ the tile kernels
+// Both kernels run one persistent CTA per SM over a contiguous share of the
+// batch's units (64 of K, or 64 columns, of a tile), so that every SM has the
+// same number of units whatever the tiles are. Their warps have roles: one
+// brings tiles into a ring (rows by TMA gathers of four, the adapter's tiles by
+// bulk copies), one issues the MMAs, the others turn accumulators into results.
 constexpr int LT_X_BYTES = LORA_TILE_ROWS * 128;  // 128 rows x 64 values
+constexpr int LT_SMEM = 232448 - 1024 - 2048;     // a CTA's shared memory without alignment and barriers
+constexpr int LT_MAX_STAGES = 8;
 
-// Shared memory of the A x kernel: the stages' x tiles and A tiles.
-__host__ __device__ constexpr int lt_shrink_smem(int r16) { return 1024 + LT_STAGES * (LT_X_BYTES + r16 * 128); }
+// What a tile's unit range needs.
+struct LoraTile {
+  int adapter, pos, n, rank, r16;
+  const uint8_t* block;
+};
+__device__ __forceinline__ LoraTile lora_tile(const LoraParams& p, int tile) {
+  const int4 ti = p.tiles[tile];
+  LoraTile t;
+  t.adapter = ti.x;
+  t.pos = ti.y;
+  t.n = ti.z;
+  t.rank = ti.w;
+  t.r16 = (t.rank + 15) / 16 * 16;
+  t.block = p.packed + p.g.block_off + (size_t)(ti.x >= 0 ? ti.x : 0) * p.g.block_bytes;
+  return t;
+}
+// Ring position: slot and the parity of its current use.
+struct RingPos {
+  int slot = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++slot == stages) {
+      slot = 0;
+      ph ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void back(int stages) {
+    if (--slot < 0) {
+      slot = stages - 1;
+      ph ^= 1u;
+    }
+  }
+};
 
-// u[split][pos][r] = A x over one K split of one tile; the last split of a
-// tile to finish adds the others' sums to split 0, in order.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// This thread's arrival on the barrier, once all its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Four producer warps bring 128 rows x 128 bytes (64 values of each row) and
+// one adapter tile into each ring slot. The rows of a tile lie anywhere, so
+// they come by 16-byte cp.async, 8 a thread, into the 128-byte swizzled layout
+// that the tensor cores read. (TMA gathers of four rows took about 1.4 us for
+// the 128 rows, twice what HBM needs for them.) The copies themselves arrive on
+// the slot's barrier: announcing a slot from the producer some slots later
+// leaves the consumers as many slots less to hide the hand-over in (measured
+// with 6 slots announced 5 behind: 84 against 40 us for B u at 8192 rows).
+constexpr int LT_PROD_WARPS = 4;
+constexpr int LT_FULL_COUNT = LT_PROD_WARPS * 32 + 1;  // and the adapter tile's expected bytes
+struct LoraProducer {
+  uint8_t* ring;
+  uint64_t *full, *empty;
+  int stages, stage_bytes, tid;
+  volatile int* abort;
+  uint64_t lim;
+  RingPos at;
+  int issued = 0;
+  const uint16_t* src[8];
+
+  // Rows tid / 8 + 16 j of the tile, chunk tid % 8.
+  __device__ __forceinline__ void rows(const LoraParams& p, const LoraTile& t, const uint16_t* x, size_t ld) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = (tid >> 3) + 16 * j;
+      src[j] = x && r < t.n ? x + (size_t)p.perm[t.pos + r] * ld + (tid & 7) * 8 : nullptr;
+    }
+  }
+  // One unit: columns col .. col + 63 of width (zeros past it), and w_bytes of the adapter.
+  __device__ __forceinline__ bool fill(int col, int width, const uint8_t* w, uint32_t w_bytes) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[at.slot], at.ph ^ 1u, abort, lim))) return false;
+    uint8_t* st = ring + at.slot * stage_bytes;
+    if (tid < 32) {
+      mbar_expect_tx_elect(&full[at.slot], w_bytes);
+      bulk_g2s_if(tid == 0 && w_bytes > 0, st + LT_X_BYTES, w, w_bytes, &full[at.slot]);
+    }
+    const uint32_t bytes = col + (tid & 7) * 8 < width ? 16u : 0u;
+    const uint32_t dst = smem_u32(st) + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) * 16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (src[j]) cp_async16(dst + j * 2048, bytes ? src[j] + col : src[j] - (tid & 7) * 8, bytes);
+    cp_async_arrive(&full[at.slot]);
+    at.next(stages);
+    ++issued;
+    return true;
+  }
+  // After a wait gave up: the copies in flight are waited for (bounded).
+  __device__ __forceinline__ void drain() {
+    cp_async_wait_all();
+    volatile int never = 0;
+    for (int b = 0; b < stages && b < issued; ++b) {
+      at.back(stages);
+      mbar_wait(&full[at.slot], at.ph, &never, lim);
+    }
+  }
+};
+
+// Warp roles of the A x kernel: 0..3 producers, 4..7 epilogue, 8 MMA.
+constexpr int LA_THREADS = 288;
+__host__ __device__ constexpr int la_stages(int r16) {
+  return LT_SMEM / (LT_X_BYTES + r16 * 128) < LT_MAX_STAGES ? LT_SMEM / (LT_X_BYTES + r16 * 128) : LT_MAX_STAGES;
+}
+__host__ __device__ constexpr int la_smem(int r16) { return 1024 + la_stages(r16) * (LT_X_BYTES + r16 * 128); }
+// At least this many units a CTA, so that few pieces of a tile have to be joined.
+constexpr int LA_MIN_UNITS = 4;
+
+// u[pos][r] = A x. Where a tile's K extent is shared by several CTAs, each
+// leaves its sum in part, and the last of them to finish adds the sums up in
+// K order.
 template <int ACT>
-__global__ void __launch_bounds__(LT_THREADS) lora_shrink_kernel(LoraParams p) {
+__global__ void __launch_bounds__(LA_THREADS, 1)
+    lora_shrink_kernel(const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t lt_sm[];
-  __shared__ __align__(8) uint64_t s_free[LT_STAGES];
+  __shared__ __align__(8) uint64_t full[LT_MAX_STAGES], empty[LT_MAX_STAGES], acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_tok[LORA_TILE_ROWS], s_abort, s_last;
+  __shared__ int s_abort, s_last;
   uint8_t* smem = lt_sm + ((1024u - (smem_u32(lt_sm) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t cols = p.g.max_r16 <= 32 ? 32u : (p.g.max_r16 <= 64 ? 64u : 128u);
-  if (warp == 0) {
-    tmem_alloc(&s_tmem, cols);
+  const int stages = la_stages(p.g.max_r16);
+  const int stage_bytes = LT_X_BYTES + p.g.max_r16 * 128;
+  const uint32_t acc_cols = p.g.max_r16 <= 32 ? 32u : (p.g.max_r16 <= 64 ? 64u : 128u);
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, 2 * acc_cols);
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < LT_STAGES; ++i) mbar_init(&s_free[i], 1);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], LT_FULL_COUNT);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    mbar_init(&mma_done, 1);
     fence_mbar_init();
     s_abort = 0;
   }
@@ -424,158 +579,198 @@ __global__ void __launch_bounds__(LT_THREADS) lora_shrink_kernel(LoraParams p) {
   const uint32_t tmem = s_tmem;
   pdl_wait();
   pdl_trigger();  // after the TMEM allocation: the next kernel's may then wait for this one's end
-  const int splits = p.meta[2];
-  const int items = p.meta[0] * splits;
-  const size_t split_rows = (size_t)p.meta[3];
-  uint32_t phase = 0;  // bit i: parity of stage i's next completion
-  bool ok = true;
-  for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-    const int tile = item / splits, split = item - tile * splits;
-    const int4 ti = p.tiles[tile];
-    const int rank = reinterpret_cast<const int*>(p.packed)[ti.x];
-    const int r16 = (rank + 15) / 16 * 16;
-    const uint8_t* A = p.packed + p.g.block_off + (size_t)ti.x * p.g.block_bytes;
-    const int kb0 = (int)((long long)split * p.g.KB / splits), nk = (int)((long long)(split + 1) * p.g.KB / splits) - kb0;
-    if (tid < LORA_TILE_ROWS) s_tok[tid] = tid < ti.z ? p.perm[ti.y + tid] : -1;
-    __syncthreads();
-    // This thread's copies: chunk c of rows tid / 8 + 32 i.
-    const int c = tid & 7;
-    const uint16_t* src[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = s_tok[(tid >> 3) + 32 * i];
-      src[i] = t < 0 ? nullptr : p.x + (size_t)t * p.ldx;
+  volatile int* abort = &s_abort;
+  const uint64_t lim = p.wait_limit_ns;
+  const long long U = (long long)p.meta[0] * p.g.KB;
+  const long long G = min((long long)gridDim.x, max(1ll, U / LA_MIN_UNITS));
+  const long long v0 = blockIdx.x < G ? U * blockIdx.x / G : 0, v1 = blockIdx.x < G ? U * (blockIdx.x + 1) / G : 0;
+
+  if (warp < LT_PROD_WARPS) {
+    LoraProducer pr{smem, full, empty, stages, stage_bytes, tid, abort, lim};
+    bool ok = true;
+    for (long long v = v0; v < v1 && ok;) {
+      const int kb0 = (int)(v % p.g.KB), nk = (int)min(v1 - v, (long long)(p.g.KB - kb0));
+      const LoraTile t = lora_tile(p, (int)(v / p.g.KB));
+      v += nk;
+      pr.rows(p, t, p.x, p.ldx);
+      const uint32_t a_bytes = (uint32_t)t.r16 * 128;
+      for (int i = kb0; i < kb0 + nk && ok; ++i) ok = pr.fill(i * 64, p.g.K, t.block + (size_t)i * a_bytes, a_bytes);
     }
-    const int stage_bytes = LT_X_BYTES + r16 * 128;
-    auto load = [&](int i) {
-      uint8_t* st = smem + (i % LT_STAGES) * stage_bytes;
-      const int k = (kb0 + i) * 64 + c * 8;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = (tid >> 3) + 32 * j;
-        if (src[j]) cp_async16(st + r * 128 + ((c ^ (r & 7)) * 16), src[j] + (k < p.g.K ? k : 0), k < p.g.K ? 16u : 0u);
+    if (!ok) {
+      if (lane == 0) {
+        s_abort = 1;
+        set_status(p.status, DEV_TIMEOUT);
       }
-      const uint8_t* a = A + (size_t)(kb0 + i) * r16 * 128;
-      for (int j = tid; j < r16 * 8; j += LT_THREADS) cp_async16(st + LT_X_BYTES + j * 16, a + j * 16, 16u);
-    };
-#pragma unroll
-    for (int i = 0; i < LT_STAGES - 1; ++i) {
-      if (i < nk) load(i);
-      cp_async_commit();
+      pr.drain();
     }
-    const uint32_t idesc = idesc_kf16<ACT>(128, r16);
-    for (int i = 0; i < nk; ++i) {
-      cp_async_wait<LT_STAGES - 2>();
-      fence_async_smem();
-      if (__syncthreads_or(!ok)) {
-        ok = false;
-        break;
-      }
-      const int s = i % LT_STAGES;
-      if (warp == 0) {
-        const uint32_t x_lo = smem_desc_sw128_lo(smem_u32(smem + s * stage_bytes));
-        const uint32_t a_lo = smem_desc_sw128_lo(smem_u32(smem + s * stage_bytes + LT_X_BYTES));
+  } else if (warp == 8) {
+    RingPos rp;
+    bool ok = true;
+    int j = 0;
+    for (long long v = v0; v < v1 && ok; ++j) {
+      const int kb0 = (int)(v % p.g.KB), nk = (int)min(v1 - v, (long long)(p.g.KB - kb0));
+      const LoraTile t = lora_tile(p, (int)(v / p.g.KB));
+      v += nk;
+      const int buf = j & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort, lim));
+      tc_fence_after();
+      const uint32_t idesc = idesc_kf16<ACT>(128, t.r16), d = tmem + (uint32_t)buf * acc_cols;
+      for (int i = 0; i < nk && ok; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[rp.slot], rp.ph, abort, lim))) {
+          ok = false;
+          break;
+        }
+        fence_async_smem();  // the rows came through the generic proxy
+        const uint32_t x_lo = smem_desc_sw128_lo(smem_u32(smem + rp.slot * stage_bytes));
+        const uint32_t a_lo = x_lo + (LT_X_BYTES >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_kf16_warp(tmem, desc_from_lo(x_lo + 2 * ks), desc_from_lo(a_lo + 2 * ks), idesc, (i | ks) ? 1u : 0u);
-        umma_commit_warp(&s_free[s]);
+          umma_kf16_warp(d, desc_from_lo(x_lo + 2 * ks), desc_from_lo(a_lo + 2 * ks), idesc, (i | ks) ? 1u : 0u);
+        umma_commit_warp(&empty[rp.slot]);
+        rp.next(stages);
       }
-      // Refill the stage that the previous k-block's MMAs read.
-      if (i > 0) {
-        const int f = (i - 1) % LT_STAGES;
-        ok = mbar_wait(&s_free[f], (phase >> f) & 1u, &s_abort, p.wait_limit_ns) && ok;
-        phase ^= 1u << f;
+      if (ok) umma_commit_warp(&acc_full[buf]);
+    }
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_status(p.status, DEV_TIMEOUT);
+    }
+    umma_commit_warp(&mma_done);  // drain the MMAs before TMEM is released
+    volatile int never = 0;
+    mbar_wait(&mma_done, 0, &never, lim);
+  } else {
+    const int e = tid - 128, row = (warp & 3) * 32 + lane;
+    int j = 0;
+    for (long long v = v0; v < v1; ++j) {
+      const int tile = (int)(v / p.g.KB), kb0 = (int)(v % p.g.KB), nk = (int)min(v1 - v, (long long)(p.g.KB - kb0));
+      const LoraTile t = lora_tile(p, tile);
+      v += nk;
+      const int buf = j & 1;
+      const bool whole = nk == p.g.KB;
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(j >> 1) & 1u, abort, lim))) {
+        if (lane == 0) {
+          s_abort = 1;
+          set_status(p.status, DEV_TIMEOUT);
+        }
+        break;
       }
-      if (ok && i + LT_STAGES - 1 < nk) load(i + LT_STAGES - 1);
-      cp_async_commit();
-    }
-    if (ok) {
-      const int f = (nk - 1) % LT_STAGES;
-      ok = mbar_wait(&s_free[f], (phase >> f) & 1u, &s_abort, p.wait_limit_ns);
-      phase ^= 1u << f;
-    }
-    if (__syncthreads_or(!ok)) {
-      ok = false;
-      break;
-    }
-    tc_fence_after();
-    // Lane = row. The two warps of a quarter take alternate 16 columns.
-    const int row = (warp & 3) * 32 + lane;
-    float* u = p.u + (split * split_rows + ti.y + row) * p.g.max_r16;
-    for (int col = (warp >> 2) * 16; col < r16; col += 32) {
-      uint32_t v[16];
-      tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + col, v);
-      tmem_wait_ld();
-      if (row < ti.z) {
+      tc_fence_after();
+      // Lane = row. A CTA leaves at most two pieces: the end of a tile that
+      // another began (slot 2 b), and the beginning of one (slot 2 b + 1).
+      float* dst = whole ? p.u + (size_t)(t.pos + row) * p.g.max_r16
+                         : p.part + ((size_t)(2 * blockIdx.x + (kb0 == 0)) * LORA_TILE_ROWS + row) * p.g.max_r16;
+      for (int col = 0; col < t.r16; col += 16) {
+        uint32_t w[16];
+        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)buf * acc_cols + col, w);
+        tmem_wait_ld();
+        if (row < t.n) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(u + col + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      }
-    }
-    tc_fence_before();
-    if (splits > 1) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(&p.arrived[tile], 1) == splits - 1;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        const int per = r16 / 4;
-        for (int j = tid; j < ti.z * per; j += LT_THREADS) {
-          float* d = p.u + ((size_t)ti.y + j / per) * p.g.max_r16 + (j % per) * 4;
-          float4 sum = __ldcg(reinterpret_cast<const float4*>(d));
-          for (int q = 1; q < splits; ++q) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(d + q * split_rows * p.g.max_r16));
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
-          }
-          *reinterpret_cast<float4*>(d) = sum;
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(dst + col + 4 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (!whole) {
+        // CTA of unit w: the largest b with U b / G <= w
+        const long long w0 = (long long)tile * p.g.KB, w1 = w0 + p.g.KB - 1;
+        const int b0 = (int)(((w0 + 1) * G - 1) / U), b1 = (int)(((w1 + 1) * G - 1) / U);
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (e == 0) s_last = atomicAdd(&p.arrived[tile], 1) == b1 - b0;
+        named_bar_sync(1, 128);
+        if (s_last) {
+          __threadfence();
+          // 4 values a thread and 8 threads a row (so 32 columns a pass), two
+          // rows at once: up to 8 loads in flight.
+          const int c4 = (e & 7) * 4;
+          for (int c = c4; c < t.r16; c += 32) {
+            for (int r = e >> 3; r < t.n; r += 32) {
+              const size_t at0 = (size_t)r * p.g.max_r16 + c, at1 = at0 + (size_t)(r + 16 < t.n ? 16 : 0) * p.g.max_r16;
+              float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
+#pragma unroll 4
+              for (int b = b0; b <= b1; ++b) {
+                const float* from = p.part + (size_t)(2 * b + (b == b0)) * LORA_TILE_ROWS * p.g.max_r16;
+                const float4 f0 = __ldcg(reinterpret_cast<const float4*>(from + at0));
+                const float4 f1 = __ldcg(reinterpret_cast<const float4*>(from + at1));
+                s0 = make_float4(s0.x + f0.x, s0.y + f0.y, s0.z + f0.z, s0.w + f0.w);
+                s1 = make_float4(s1.x + f1.x, s1.y + f1.y, s1.z + f1.z, s1.w + f1.w);
+              }
+              float* u = p.u + (size_t)t.pos * p.g.max_r16;
+              *reinterpret_cast<float4*>(u + at0) = s0;
+              if (r + 16 < t.n) *reinterpret_cast<float4*>(u + at1) = s1;
+            }
+          }
+        }
+        named_bar_sync(1, 128);  // s_last is read
+      }
     }
-    __syncthreads();
-    tc_fence_after();
   }
-  if (!ok) {
-    if (tid == 0) set_status(p.status, DEV_TIMEOUT);
-    s_abort = 1;
-  }
-  cp_async_wait<0>();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 8) {
     tc_fence_after();
-    tmem_dealloc(tmem, cols);
+    tmem_dealloc(tmem, 2 * acc_cols);
   }
 }
 
-// Shared memory of the B u kernel: u's two parts and the stages' base tiles
-// and B tiles.
-constexpr int LX_STAGES = 3;
-constexpr int LX_TILE_BYTES = LORA_TILE_ROWS * 128;  // 128 rows x 64 columns
-__host__ __device__ constexpr int lx_smem(int r16) {
-  return 1024 + 2 * LORA_TILE_ROWS * r16 * 2 + LX_STAGES * (LX_TILE_BYTES + r16 * 128);
+// Warp roles of the B u kernel: 0..3 producers, 4..7 u operand, 8..15 epilogue
+// (two groups of 4, which take alternate units), 16 MMA.
+constexpr int LB_THREADS = 544;
+constexpr int LB_ACC = 4;  // accumulators of 64 columns
+// u's two parts are held twice, so that the next tile's are ready in time;
+// above rank 64 once, which leaves the room to the ring. The number of stages
+// is even: each epilogue group then has slots of its own, and meets every use
+// of them (a parity wait must not be two uses behind).
+__host__ __device__ constexpr int lb_u_bytes(int r16) { return 2 * LORA_TILE_ROWS * r16 * 2; }
+__host__ __device__ constexpr int lb_u_bufs(int r16) { return r16 <= 64 ? 2 : 1; }
+__host__ __device__ constexpr int lb_stages(int r16) {
+  return ((LT_SMEM - lb_u_bufs(r16) * lb_u_bytes(r16)) / (LT_X_BYTES + r16 * 128) < LT_MAX_STAGES
+              ? (LT_SMEM - lb_u_bufs(r16) * lb_u_bytes(r16)) / (LT_X_BYTES + r16 * 128)
+              : LT_MAX_STAGES) &
+         ~1;
 }
+__host__ __device__ constexpr int lb_smem(int r16) {
+  return 1024 + lb_u_bufs(r16) * lb_u_bytes(r16) + lb_stages(r16) * (LT_X_BYTES + r16 * 128);
+}
+static_assert(lb_stages(LORA_MAX_RANK) >= 4 && lb_stages(64) >= 4, "stages");
+static_assert(LB_ACC % 2 == 0, "each epilogue group has accumulators of its own");
 
-// out = base + scale B u. The (tile, 64 columns) units of the batch, tiles
-// slowest, are dealt to the CTAs in contiguous shares.
+// out = base + scale B u. u enters as its two parts (split_act), whose
+// products with B add up in the same accumulator.
 template <int ACT>
-__global__ void __launch_bounds__(LT_THREADS) lora_expand_kernel(LoraParams p) {
+__global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t lt_sm[];
-  __shared__ __align__(8) uint64_t s_full[2];
+  __shared__ __align__(8) uint64_t full[LT_MAX_STAGES], empty[LT_MAX_STAGES], acc_full[LB_ACC], acc_empty[LB_ACC],
+      u_full[2], u_empty[2], mma_done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_tok[LORA_TILE_ROWS], s_abort;
+  __shared__ int s_abort;
   uint8_t* smem = lt_sm + ((1024u - (smem_u32(lt_sm) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) {
-    tmem_alloc(&s_tmem, 128);
+  const int stages = lb_stages(p.g.max_r16);
+  const int stage_bytes = LT_X_BYTES + p.g.max_r16 * 128;
+  const int u_bytes = lb_u_bytes(p.g.max_r16), u_bufs = lb_u_bufs(p.g.max_r16);
+  uint8_t* ring = smem + u_bufs * u_bytes;
+  if (warp == 16) {
+    tmem_alloc(&s_tmem, LB_ACC * 64);
     tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], LT_FULL_COUNT);
+      mbar_init(&empty[i], 5);  // the MMAs that read B, and the 4 warps of the unit's epilogue
+    }
+    for (int i = 0; i < LB_ACC; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&u_full[i], 4);
+      mbar_init(&u_empty[i], 1);
+    }
+    mbar_init(&mma_done, 1);
     fence_mbar_init();
     s_abort = 0;
   }
@@ -585,160 +780,208 @@ __global__ void __launch_bounds__(LT_THREADS) lora_expand_kernel(LoraParams p) {
   const uint32_t tmem = s_tmem;
   pdl_wait();
   pdl_trigger();
+  volatile int* abort = &s_abort;
+  const uint64_t lim = p.wait_limit_ns;
   // In place, the rows without an adapter are as they should be.
-  const long long units = (long long)(p.base == p.out ? p.meta[0] : p.meta[1]) * p.g.NB;
-  long long v0 = units * blockIdx.x / gridDim.x;
-  const long long v1 = units * (blockIdx.x + 1) / gridDim.x;
-  uint32_t phase = 0;
+  const long long U = (long long)(p.base == p.out ? p.meta[0] : p.meta[1]) * p.g.NB;
+  const long long v0 = U * blockIdx.x / gridDim.x, v1 = U * (blockIdx.x + 1) / gridDim.x;
   bool ok = true;
-  while (v0 < v1 && ok) {
-    const int tile = (int)(v0 / p.g.NB), nt0 = (int)(v0 % p.g.NB);
-    const int nn = (int)min(v1 - v0, (long long)(p.g.NB - nt0));
-    v0 += nn;
-    const int4 ti = p.tiles[tile];
-    const bool with = ti.x >= 0;
-    const int rank = with ? reinterpret_cast<const int*>(p.packed)[ti.x] : 0;
-    const float scale = with ? reinterpret_cast<const float*>(p.packed + p.g.scale_off)[ti.x] : 0.0f;
-    const int r16 = (rank + 15) / 16 * 16;
-    const uint8_t* B = p.packed + p.g.block_off + (size_t)(with ? ti.x : 0) * p.g.block_bytes + p.g.b_off;
-    if (tid < LORA_TILE_ROWS) s_tok[tid] = tid < ti.z ? p.perm[ti.y + tid] : -1;
-    __syncthreads();
-    uint8_t* u_hi = smem;
-    uint8_t* u_lo = smem + LORA_TILE_ROWS * r16 * 2;
-    uint8_t* ring = u_lo + LORA_TILE_ROWS * r16 * 2;
-    const int stage_bytes = LX_TILE_BYTES + r16 * 128;
-    const int c = tid & 7;
-    int tok[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) tok[j] = s_tok[(tid >> 3) + 32 * j];
-    auto load = [&](int i) {
-      uint8_t* st = ring + (i % LX_STAGES) * stage_bytes;
-      const int n = (nt0 + i) * 64 + c * 8;
-      if (p.base && n < p.g.N) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = (tid >> 3) + 32 * j;
-          if (tok[j] >= 0) cp_async16(st + r * 128 + ((c ^ (r & 7)) * 16), p.base + (size_t)tok[j] * p.ldbase + n, 16u);
-        }
-      }
-      const uint8_t* b = B + (size_t)(nt0 + i) * r16 * 128;
-      for (int j = tid; j < r16 * 8; j += LT_THREADS) cp_async16(st + LX_TILE_BYTES + j * 16, b + j * 16, 16u);
-    };
-#pragma unroll
-    for (int i = 0; i < LX_STAGES - 1; ++i) {
-      if (i < nn) load(i);
-      cp_async_commit();
+
+  if (warp < LT_PROD_WARPS) {
+    LoraProducer pr{ring, full, empty, stages, stage_bytes, tid, abort, lim};
+    for (long long v = v0; v < v1 && ok;) {
+      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
+      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
+      v += nn;
+      pr.rows(p, t, p.base, p.ldbase);
+      const uint32_t b_bytes = (uint32_t)t.r16 * 128;
+      for (int i = nt0; i < nt0 + nn && ok; ++i)
+        ok = pr.fill(i * 64, p.g.N, t.block + p.g.b_off + (size_t)i * b_bytes, b_bytes);
     }
-    // u's two parts as the A operand: 16-byte core-matrix rows, [r16 / 8][128 rows].
-    {
-      const int row = tid & (LORA_TILE_ROWS - 1);
-      const float* u = p.u + ((size_t)ti.y + row) * p.g.max_r16;
-      for (int ch = tid >> 7; ch < r16 / 8; ch += LT_THREADS / LORA_TILE_ROWS) {
-        uint16_t hi[8], lo[8];
-        float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (row < ti.z) {
-          *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(u + ch * 8));
-          *reinterpret_cast<float4*>(f + 4) = __ldcg(reinterpret_cast<const float4*>(u + ch * 8 + 4));
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) split_act<ACT>(ch * 8 + j < rank ? f[j] : 0.0f, &hi[j], &lo[j]);
-        *reinterpret_cast<uint4*>(u_hi + (ch * LORA_TILE_ROWS + row) * 16) = *reinterpret_cast<const uint4*>(hi);
-        *reinterpret_cast<uint4*>(u_lo + (ch * LORA_TILE_ROWS + row) * 16) = *reinterpret_cast<const uint4*>(lo);
+    if (!ok) {
+      if (lane == 0) {
+        s_abort = 1;
+        set_status(p.status, DEV_TIMEOUT);
       }
+      pr.drain();
     }
+  } else if (warp == 16) {
+    RingPos rp;
+    int ju = 0, unit = 0;
     const uint32_t idesc = idesc_kf16<ACT>(128, 64);
-    auto issue = [&](int i) {  // the MMAs of unit i, by a converged warp
-      const uint32_t b = smem_u32(ring + (i % LX_STAGES) * stage_bytes + LX_TILE_BYTES);
-      const uint32_t d = tmem + (uint32_t)(i & 1) * 64;
-      for (int ks = 0; ks < r16 / 16; ++ks) {
-        const uint64_t bd = smem_desc_plain(b + ks * 2 * 1024, 1024);
-        const uint32_t off = (uint32_t)ks * 2 * LORA_TILE_ROWS * 16;
-        umma_kf16_warp(d, smem_desc_plain(smem_u32(u_hi) + off, LORA_TILE_ROWS * 16), bd, idesc, ks ? 1u : 0u);
-        umma_kf16_warp(d, smem_desc_plain(smem_u32(u_lo) + off, LORA_TILE_ROWS * 16), bd, idesc, 1u);
+    for (long long v = v0; v < v1 && ok;) {
+      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
+      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
+      v += nn;
+      if (t.adapter < 0) {
+        // No product, only the slots' turn (the tiles without an adapter are
+        // the last, so the accumulators' uses need no count of them).
+        for (int i = 0; i < nn && ok; ++i) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[rp.slot], rp.ph, abort, lim));
+          if (ok && lane == 0) mbar_arrive(&empty[rp.slot]);
+          rp.next(stages);
+        }
+        continue;
       }
-      umma_commit_warp(&s_full[i & 1]);
-    };
-    // Before unit i's epilogue the MMAs of unit i + 1 are issued.
-    for (int i = -1; i < nn; ++i) {
-      if (i + 1 < nn) cp_async_wait<LX_STAGES - 2>();
-      fence_async_smem();
-      tc_fence_before();
-      if (__syncthreads_or(!ok)) {
+      const int ub = ju % u_bufs;
+      ok = __all_sync(0xffffffffu, mbar_wait(&u_full[ub], (uint32_t)(ju / u_bufs) & 1u, abort, lim));
+      ++ju;
+      const uint32_t hi = smem_u32(smem + ub * u_bytes), lo = hi + (uint32_t)LORA_TILE_ROWS * t.r16 * 2;
+      for (int i = 0; i < nn && ok; ++i, ++unit) {
+        const int buf = unit % LB_ACC;
+        ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((uint32_t)(unit / LB_ACC) & 1u) ^ 1u, abort, lim)) &&
+             __all_sync(0xffffffffu, mbar_wait(&full[rp.slot], rp.ph, abort, lim));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t b = smem_u32(ring + rp.slot * stage_bytes + LT_X_BYTES), d = tmem + (uint32_t)buf * 64;
+        for (int ks = 0; ks < t.r16 / 16; ++ks) {
+          const uint64_t bd = smem_desc_plain(b + ks * 2 * 1024, 1024);
+          const uint32_t off = (uint32_t)ks * 2 * LORA_TILE_ROWS * 16;
+          umma_kf16_warp(d, smem_desc_plain(hi + off, LORA_TILE_ROWS * 16), bd, idesc, ks ? 1u : 0u);
+          umma_kf16_warp(d, smem_desc_plain(lo + off, LORA_TILE_ROWS * 16), bd, idesc, 1u);
+        }
+        umma_commit_warp(&acc_full[buf]);
+        umma_commit_warp(&empty[rp.slot]);
+        rp.next(stages);
+      }
+      if (ok) umma_commit_warp(&u_empty[ub]);
+    }
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_status(p.status, DEV_TIMEOUT);
+    }
+    umma_commit_warp(&mma_done);
+    volatile int never = 0;
+    mbar_wait(&mma_done, 0, &never, lim);
+  } else if (warp < 8) {
+    // u's two parts as the A operand: 16-byte core-matrix rows, [r16 / 8][128 rows]. Thread = row.
+    const int row = tid - 128;
+    int ju = 0;
+    for (long long v = v0; v < v1;) {
+      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
+      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
+      v += nn;
+      if (t.adapter < 0) continue;
+      const int ub = ju % u_bufs;
+      if (!__all_sync(0xffffffffu, mbar_wait(&u_empty[ub], ((uint32_t)(ju / u_bufs) & 1u) ^ 1u, abort, lim))) {
         ok = false;
         break;
       }
-      tc_fence_after();
-      if (with && i + 1 < nn && warp == 0) issue(i + 1);
-      if (i < 0) {
-        if (LX_STAGES - 1 < nn) load(LX_STAGES - 1);
-        cp_async_commit();
-        continue;
-      }
-      uint8_t* st = ring + (i % LX_STAGES) * stage_bytes;
-      if (with) {
-        ok = mbar_wait(&s_full[i & 1], (phase >> (i & 1)) & 1u, &s_abort, p.wait_limit_ns);
-        phase ^= 1u << (i & 1);
-        __syncwarp();
-        tc_fence_after();
-        const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-        uint32_t v[32];
-        tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(i & 1) * 64 + half * 32, v);
-        tmem_wait_ld();
+      ++ju;
+      uint8_t* hi = smem + ub * u_bytes + row * 16;
+      uint8_t* lo = hi + LORA_TILE_ROWS * t.r16 * 2;
+      const float* u = p.u + (size_t)(t.pos + min(row, t.n - 1)) * p.g.max_r16;
+#pragma unroll 4
+      for (int ch = 0; ch < t.r16 / 8; ++ch) {
+        uint16_t h[8], l[8];
+        float f[8];
+        *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(u + ch * 8));
+        *reinterpret_cast<float4*>(f + 4) = __ldcg(reinterpret_cast<const float4*>(u + ch * 8 + 4));
+        // past the rank A's zeros met whatever x held
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4* at = reinterpret_cast<uint4*>(st + row * 128 + (((half * 4 + j) ^ (row & 7)) * 16));
-          uint4 y = p.base ? *at : make_uint4(0, 0, 0, 0);
-          uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            yw[w] = f32x2_to_act<ACT>(
-                fmaf(scale, __uint_as_float(v[8 * j + 2 * w]), act_f32<ACT>((uint16_t)(yw[w] & 0xFFFFu))),
-                fmaf(scale, __uint_as_float(v[8 * j + 2 * w + 1]), act_f32<ACT>((uint16_t)(yw[w] >> 16))));
-          *at = y;
-        }
-        __syncthreads();
+        for (int j = 0; j < 8; ++j) split_act<ACT>(ch * 8 + j < t.rank ? f[j] : 0.0f, &h[j], &l[j]);
+        *reinterpret_cast<uint4*>(hi + ch * LORA_TILE_ROWS * 16) = *reinterpret_cast<const uint4*>(h);
+        *reinterpret_cast<uint4*>(lo + ch * LORA_TILE_ROWS * 16) = *reinterpret_cast<const uint4*>(l);
       }
-      const int n = (nt0 + i) * 64 + c * 8;
-      if (n < p.g.N) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = (tid >> 3) + 32 * j;
-          if (tok[j] >= 0)
-            *reinterpret_cast<uint4*>(p.out + (size_t)tok[j] * p.ldout + n) =
-                with || p.base ? *reinterpret_cast<const uint4*>(st + r * 128 + ((c ^ (r & 7)) * 16))
-                               : make_uint4(0, 0, 0, 0);
-        }
-      }
-      // A thread refills the chunks it has just stored; B's tile was read by MMAs that have completed.
-      if (i + LX_STAGES < nn) load(i + LX_STAGES);
-      cp_async_commit();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&u_full[ub]);
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_status(p.status, DEV_TIMEOUT);
+    }
+  } else {
+    // A warp owns 32 rows of every second unit. The results replace the base
+    // values in the slot, lane = row, and go out as 128-byte row segments.
+    const int group = (warp - 8) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int c = lane & 7;  // 16-byte chunk on the way out
+    RingPos rp;
+    int unit = 0;
+    for (long long v = v0; v < v1 && ok;) {
+      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
+      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
+      v += nn;
+      const float scale = t.adapter >= 0 ? reinterpret_cast<const float*>(p.packed + p.g.scale_off)[t.adapter] : 0.0f;
+      int tok[8];  // the rows this lane stores: quarter * 32 + lane / 8 + 4 i
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = quarter * 32 + (lane >> 3) + 4 * i;
+        tok[i] = r < t.n ? p.perm[t.pos + r] : -1;
+      }
+      for (int i = 0; i < nn; ++i, ++unit, rp.next(stages)) {
+        if ((unit & 1) != group) continue;
+        const int buf = unit % LB_ACC;
+        uint8_t* st = ring + rp.slot * stage_bytes;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[rp.slot], rp.ph, abort, lim));
+        if (ok && t.adapter >= 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(unit / LB_ACC) & 1u, abort, lim));
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t w[32];
+              tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)buf * 64 + half * 32, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint4* at = reinterpret_cast<uint4*>(st + row * 128 + (((half * 4 + j) ^ (row & 7)) * 16));
+                uint4 y = p.base ? *at : make_uint4(0, 0, 0, 0);
+                uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  yw[k] = f32x2_to_act<ACT>(
+                      fmaf(scale, __uint_as_float(w[8 * j + 2 * k]), act_f32<ACT>((uint16_t)(yw[k] & 0xFFFFu))),
+                      fmaf(scale, __uint_as_float(w[8 * j + 2 * k + 1]), act_f32<ACT>((uint16_t)(yw[k] >> 16))));
+                *at = y;
+              }
+            }
+            tc_fence_before();
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0 && t.adapter >= 0) mbar_arrive(&acc_empty[buf]);
+        const int n = (nt0 + i) * 64 + c * 8;
+        if (n < p.g.N) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = quarter * 32 + (lane >> 3) + 4 * j;
+            if (tok[j] >= 0)
+              *reinterpret_cast<uint4*>(p.out + (size_t)tok[j] * p.ldout + n) =
+                  t.adapter >= 0 || p.base ? *reinterpret_cast<const uint4*>(st + r * 128 + ((c ^ (r & 7)) * 16))
+                                           : make_uint4(0, 0, 0, 0);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[rp.slot]);
+      }
+    }
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_status(p.status, DEV_TIMEOUT);
+    }
   }
-  if (!ok) {
-    if (tid == 0) set_status(p.status, DEV_TIMEOUT);
-    s_abort = 1;
-  }
-  cp_async_wait<0>();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 16) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, LB_ACC * 64);
   }
 }
 
 template <int ACT>
-static cudaError_t tiled_as(const LoraParams& p, int num_sms, cudaStream_t st) {
-  static std::atomic<unsigned long long> done_a{0}, done_b{0};
-  const int sa = lt_shrink_smem(p.g.max_r16), sb = lx_smem(p.g.max_r16);
-  cudaError_t e = ensure_smem_attr(lora_shrink_kernel<ACT>, lt_shrink_smem(LORA_MAX_RANK), done_a);
-  if (e == cudaSuccess) e = ensure_smem_attr(lora_expand_kernel<ACT>, lx_smem(LORA_MAX_RANK), done_b);
-  if (e == cudaSuccess) e = launch_pdl(lora_plan_kernel, dim3(1), dim3(LP_THREADS), 0, st, p);
-  if (e == cudaSuccess) e = launch_pdl(lora_shrink_kernel<ACT>, dim3(2 * num_sms), dim3(LT_THREADS), (size_t)sa, st, p);
-  if (e == cudaSuccess) e = launch_pdl(lora_expand_kernel<ACT>, dim3(2 * num_sms), dim3(LT_THREADS), (size_t)sb, st, p);
+static cudaError_t tiled_of(const LoraParams& p, int num_sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> done_p{0}, done_a{0}, done_b{0};
+  const int sa = la_smem(p.g.max_r16), sb = lb_smem(p.g.max_r16);
+  const dim3 grid((unsigned)(num_sms < LORA_MAX_CTAS ? num_sms : LORA_MAX_CTAS));
+  cudaError_t e = ensure_smem_attr(lora_plan_kernel, lp_smem(LORA_MAX_SLOTS), done_p);
+  if (e == cudaSuccess) e = ensure_smem_attr(lora_shrink_kernel<ACT>, LT_SMEM + 1024, done_a);
+  if (e == cudaSuccess) e = ensure_smem_attr(lora_expand_kernel<ACT>, LT_SMEM + 1024, done_b);
+  if (e == cudaSuccess) e = launch_pdl(lora_plan_kernel, dim3(1), dim3(LP_THREADS), (size_t)lp_smem(p.g.slots), st, p);
+  if (e == cudaSuccess) e = launch_pdl(lora_shrink_kernel<ACT>, grid, dim3(LA_THREADS), (size_t)sa, st, p);
+  if (e == cudaSuccess) e = launch_pdl(lora_expand_kernel<ACT>, grid, dim3(LB_THREADS), (size_t)sb, st, p);
   count_launches(3);
   return e;
 }
@@ -746,7 +989,7 @@ static cudaError_t tiled_as(const LoraParams& p, int num_sms, cudaStream_t st) {
 cudaError_t launch_lora_forward(const LoraParams& p, int num_sms, cudaStream_t st) {
   if (p.T == 0) return cudaSuccess;
   if (p.T <= LS_MAX_T) return p.act_type == ACT_F16 ? small_of<ACT_F16>(p, st) : small_of<ACT_BF16>(p, st);
-  return p.act_type == ACT_F16 ? tiled_as<ACT_F16>(p, num_sms, st) : tiled_as<ACT_BF16>(p, num_sms, st);
+  return p.act_type == ACT_F16 ? tiled_of<ACT_F16>(p, num_sms, st) : tiled_of<ACT_BF16>(p, num_sms, st);
 }
 
 }  // namespace hmoe

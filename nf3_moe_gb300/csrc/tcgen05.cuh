@@ -104,4 +104,14 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t k_st
   return d;                              // layout type 0: no swizzle
 }
 
+// One elected lane registers the bytes on the barrier.
+__device__ __forceinline__ void mbar_expect_tx_elect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes)
+      : "memory");
+}
+
 }  // namespace hmoe

@@ -231,3 +231,16 @@ def test_workspace_serves_any_batch_up_to_its_size():
     for T in (900, 1, 64, 513, 8, 899):
         x, base, ids = s.randn(T, 256), s.randn(T, 256), ids_of("mixed", T, 6)
         s.check(s.hm(x, ids, base=base), x, ids, base)
+
+
+@pytest.mark.parametrize("shape", [(1500, 1032, 264, 3, 64, BF, "mixed"), (8200, 136, 72, 9, 16, HF, "mixed"), (20000, 72, 64, 4, 8, BF, "mixed")],
+                         ids=str)
+def test_the_same_inputs_give_the_same_bits(shape):
+    """Groups of many tiles whose rows lie scattered, K shared by several CTAs: every pass sums in the same order."""
+    T, K, N, slots, rank, dt, pattern = shape
+    s = Set(K, N, slots, rank, dt, T)
+    x, base, ids = s.randn(T, K), s.randn(T, N), ids_of(pattern, T, slots)
+    first = s.hm(x, ids, base=base)
+    s.check(first, x, ids, base)
+    for _ in range(10):
+        assert torch.equal(s.hm(x, ids, base=base), first)
