@@ -616,7 +616,7 @@ hmoe_status hmoe_lora_load(const hmoe_lora* lora, int slot, const void* A, const
  * device [T] rows of N, ldbase apart, or NULL for zeros; out: device [T] rows
  * of N, ldout apart, fully overwritten; all 16-byte aligned with strides a
  * multiple of 8, so column ranges of wider tensors serve. base may be out
- * itself (in place, the same stride) and may not overlap it otherwise. ids:
+ * itself (in place, the same stride); out overlaps nothing else. ids:
  * device int32 [T] in -1..slots-1; an id outside is reported through
  * hmoe_check_device_status (HMOE_ERR_BAD_ROUTE) and its row gets base. T = 0
  * is valid.

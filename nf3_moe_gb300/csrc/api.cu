@@ -1275,7 +1275,6 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T,
   p.wait_limit_ns = WAIT_LIMIT_NS;
   p.meta = reinterpret_cast<int*>(scratch + w.meta);
   p.tiles = reinterpret_cast<int4*>(scratch + w.tiles);
-  p.arrived = reinterpret_cast<int*>(scratch + w.arrived);
   p.perm = reinterpret_cast<int*>(scratch + w.perm);
   p.u = reinterpret_cast<float*>(scratch + w.u);
   p.part = reinterpret_cast<float*>(scratch + w.part);

@@ -206,20 +206,18 @@ struct LoraParams {
   // Scratch of the larger batches (lora.cu), see LoraScratch.
   int* meta;
   int4* tiles;
-  int* arrived;
   int* perm;
   float* u;
   float* part;
 };
 // Scratch of a larger batch of T rows: the rows grouped by adapter (perm), cut
 // into tiles of up to LORA_TILE_ROWS rows (tiles: adapter or -1, first
-// position, rows), the number of finished pieces of each tile (arrived), A x
-// of every position (u), and the pieces' sums, two for each CTA (part). meta:
-// tiles with an adapter, all tiles.
+// position, rows, rank), A x of every position (u), and the sums of the pieces
+// of tiles, two for each CTA (part). meta: tiles with an adapter, all tiles.
 constexpr int LORA_TILE_ROWS = 128;
 constexpr int LORA_MAX_CTAS = 160;
 struct LoraScratch {
-  size_t meta, tiles, arrived, perm, u, part, total;
+  size_t meta, tiles, perm, u, part, total;
 };
 inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
   auto pad = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -227,8 +225,7 @@ inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
   LoraScratch s;
   s.meta = 0;
   s.tiles = s.meta + 256;
-  s.arrived = s.tiles + pad(most * 16);
-  s.perm = s.arrived + pad(most * 4);
+  s.perm = s.tiles + pad(most * 16);
   s.u = s.perm + pad((size_t)T * 4);
   s.part = s.u + pad((size_t)T * g.max_r16 * 4);
   s.total = s.part + (size_t)LORA_MAX_CTAS * 2 * LORA_TILE_ROWS * g.max_r16 * 4;

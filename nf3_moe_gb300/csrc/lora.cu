@@ -313,61 +313,76 @@ static cudaError_t small_of(const LoraParams& p, cudaStream_t st) {
 // The rows of a group keep their order, so that the tiles, and with them the
 // order of every sum, depend on the ids alone: each warp counts its own range
 // of rows (s_base[warp][group]), and the counts are summed over the warps.
+// The loops are kept rolled: the kernel runs once through its code, and what
+// it costs is mostly latency, of instruction fetches too.
 constexpr int LP_THREADS = 1024;
 constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_IDS = 8;  // ids a thread holds at once: their loads are in flight together
+constexpr int LP_IDS = 8;
+constexpr int LP_ROWS = 8192;  // rows whose words fit shared memory; of a larger batch they are kept in the u scratch
+constexpr int lp_smem(int slots) { return (LP_ROWS + LP_WARPS * (slots + 1)) * 4; }
 __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
-  extern __shared__ int s_base[];  // [LP_WARPS][G]
+  extern __shared__ int s_word[];  // [LP_ROWS]: group, and place << 10 in the warp's part of it
   __shared__ int s_rank[LORA_MAX_SLOTS + 1], s_wsum[2][LP_WARPS];
+  static_assert(LORA_MAX_SLOTS + 1 <= 1 << 10 && LORA_MAX_SLOTS + 1 <= LP_THREADS, "group bits");
+  int* s_base = s_word + LP_ROWS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.g.slots + 1;
   for (int i = tid; i < LP_WARPS * G; i += LP_THREADS) s_base[i] = 0;
   pdl_wait();
   pdl_trigger();
-  if (tid < G) s_rank[tid] = tid < p.g.slots ? reinterpret_cast<const int*>(p.packed)[tid] : 0;
-  // The warp's rows, 32 a round; the place of a row in the warp's part of its
-  // group. Batches above LP_IDS rounds keep the places in the u scratch, unused
-  // as yet.
-  const int rounds = (p.T + LP_THREADS - 1) / LP_THREADS;
+  const int rounds = (p.T + LP_THREADS - 1) / LP_THREADS;  // 32 rows of the warp's range each
   const int t0 = warp * rounds * 32 + lane;
+  int* word = p.T <= LP_ROWS ? s_word : reinterpret_cast<int*>(p.u);
   int* mine = s_base + warp * G;
-  int* place = reinterpret_cast<int*>(p.u);
-  int g[LP_IDS], at[LP_IDS];
+  if (tid < G) s_rank[tid] = tid < p.g.slots ? __ldcg(reinterpret_cast<const int*>(p.packed) + tid) : 0;
+  int bits = 1;  // of a group's number
+  while (G > 1 << bits) ++bits;
   for (int r0 = 0; r0 < rounds; r0 += LP_IDS) {
+    int id[LP_IDS];  // loads in flight together
 #pragma unroll
-    for (int i = 0; i < LP_IDS; ++i) {
-      const int t = t0 + (r0 + i) * 32;
-      g[i] = r0 + i < rounds && t < p.T ? lora_slot(p, t) : -2;
-    }
+    for (int i = 0; i < LP_IDS; ++i) id[i] = t0 + (r0 + i) * 32 < p.T ? __ldcg(p.ids + t0 + (r0 + i) * 32) : -2;
     if (r0 == 0) __syncthreads();
 #pragma unroll
     for (int i = 0; i < LP_IDS; ++i) {
-      if (r0 + i < rounds) {
-        if (g[i] > -2 && (g[i] < 0 || s_rank[g[i]] == 0)) g[i] = G - 1;
-        const unsigned peers = __match_any_sync(0xffffffffu, g[i]);
-        if (g[i] >= 0) {
-          at[i] = mine[g[i]] + __popc(peers & ((1u << lane) - 1u));
-          if (rounds > LP_IDS) place[t0 + (r0 + i) * 32] = at[i];
-        }
-        __syncwarp();
-        if (g[i] >= 0 && lane == __ffs(peers) - 1) mine[g[i]] += __popc(peers);
-        __syncwarp();
+      if (r0 + i >= rounds) break;
+      int g = id[i];
+      const bool row = t0 + (r0 + i) * 32 < p.T;
+      if (row && (g < -1 || g >= p.g.slots)) set_status(p.status, DEV_BAD_ROUTE);
+      if (g < 0 || g >= p.g.slots || s_rank[g] == 0) g = G - 1;
+      // the lanes with this lane's group, bit by bit
+      unsigned peers = __ballot_sync(0xffffffffu, row);
+#pragma unroll 1
+      for (int b = 0; b < bits; ++b) {
+        const bool one = (g >> b) & 1;
+        const unsigned with = __ballot_sync(0xffffffffu, one);
+        peers &= one ? with : ~with;
       }
+      const int place = mine[g] + __popc(peers & ((1u << lane) - 1u));
+      __syncwarp();
+      if (row && lane == __ffs(peers) - 1) mine[g] += __popc(peers);
+      if (row) word[t0 + (r0 + i) * 32] = g | place << 10;
+      __syncwarp();
     }
   }
   __syncthreads();
-  // Each group's counts become the warps' places in it; then exclusive scans
-  // of the groups' rows and tiles (G <= 513 <= LP_THREADS).
-  int n = 0;
-  if (tid < G) {
-#pragma unroll 8
-    for (int w = 0; w < LP_WARPS; ++w) {
-      const int c = s_base[w * G + tid];
-      s_base[w * G + tid] = n;
-      n += c;
+  // Each group's counts become the warps' places in it: warp w takes the
+  // groups w, w + 32, .., lane = warp counted.
+  __shared__ int s_n[LORA_MAX_SLOTS + 1], s_tile[LORA_MAX_SLOTS + 2];
+#pragma unroll 1
+  for (int g = warp; g < G; g += LP_WARPS) {
+    const int c = s_base[lane * G + g];
+    int in = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, in, d);
+      if (lane >= d) in += a;
     }
+    s_base[lane * G + g] = in - c;
+    if (lane == 31) s_n[g] = in;
   }
-  const int nt = (n + LORA_TILE_ROWS - 1) / LORA_TILE_ROWS;
+  __syncthreads();
+  // Exclusive scans of the groups' rows and tiles.
+  const int n = tid < G ? s_n[tid] : 0, nt = (n + LORA_TILE_ROWS - 1) / LORA_TILE_ROWS;
   int in = n, it = nt;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -383,44 +398,41 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
   }
   __syncthreads();
   int row0 = in - n, tile0 = it - nt;
-  for (int w = 0; w < warp; ++w) {
+#pragma unroll 1
+  for (int w = 0; w < warp && warp * 32 < G; ++w) {
     row0 += s_wsum[0][w];
     tile0 += s_wsum[1][w];
   }
+  __syncthreads();
   if (tid < G) {
-#pragma unroll 8
-    for (int w = 0; w < LP_WARPS; ++w) s_base[w * G + tid] += row0;
+    s_n[tid] = row0;  // from here on: where the group starts
+    s_tile[tid] = tile0;
   }
   if (tid == G - 1) {
+    s_tile[G] = tile0 + nt;
     p.meta[0] = tile0;
     p.meta[1] = tile0 + nt;
   }
-  // The tiles of the warp's groups, group by group.
-  for (unsigned some = __ballot_sync(0xffffffffu, nt > 0); some; some &= some - 1) {
-    const int l = __ffs(some) - 1;
-    const int gn = __shfl_sync(0xffffffffu, n, l), gr = __shfl_sync(0xffffffffu, row0, l);
-    const int gt = __shfl_sync(0xffffffffu, tile0, l), who = warp * 32 + l;
-    for (int j = lane; j * LORA_TILE_ROWS < gn; j += 32) {
-      p.tiles[gt + j] = make_int4(who < G - 1 ? who : -1, gr + j * LORA_TILE_ROWS,
-                                  min(LORA_TILE_ROWS, gn - j * LORA_TILE_ROWS), s_rank[who]);
-      p.arrived[gt + j] = 0;
-    }
-  }
   __syncthreads();
-  if (rounds <= LP_IDS) {
-#pragma unroll
-    for (int i = 0; i < LP_IDS; ++i)
-      if (i < rounds && g[i] >= 0) p.perm[mine[g[i]] + at[i]] = t0 + i * 32;
-  } else {
-    for (int r = 0; r < rounds; ++r) {
-      const int t = t0 + r * 32;
-      if (t >= p.T) break;
-      const int a = lora_slot(p, t);
-      p.perm[mine[a >= 0 && s_rank[a] > 0 ? a : G - 1] + place[t]] = t;
+  for (int j = tid; j < s_tile[G]; j += LP_THREADS) {
+    int lo = 0, hi = G - 1;  // the last group that starts at or before tile j
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_tile[mid] <= j) lo = mid;
+      else hi = mid - 1;
+    }
+    const int first = s_n[lo] + (j - s_tile[lo]) * LORA_TILE_ROWS, end = lo < G - 1 ? s_n[lo + 1] : p.T;
+    p.tiles[j] = make_int4(lo < G - 1 ? lo : -1, first, min(LORA_TILE_ROWS, end - first), s_rank[lo]);
+  }
+#pragma unroll 2
+  for (int r = 0; r < rounds; ++r) {
+    const int t = t0 + r * 32;
+    if (t < p.T) {
+      const int w = word[t], g = w & 1023;
+      p.perm[s_n[g] + mine[g] + (w >> 10)] = t;
     }
   }
 }
-constexpr int lp_smem(int slots) { return LP_WARPS * (slots + 1) * 4; }
 
 // ------------------------------------------------------------ the tile kernels
 // Both kernels run one persistent CTA per SM over a contiguous share of the
@@ -438,7 +450,7 @@ struct LoraTile {
   const uint8_t* block;
 };
 __device__ __forceinline__ LoraTile lora_tile(const LoraParams& p, int tile) {
-  const int4 ti = p.tiles[tile];
+  const int4 ti = __ldcg(p.tiles + tile);
   LoraTile t;
   t.adapter = ti.x;
   t.pos = ti.y;
@@ -500,7 +512,7 @@ struct LoraProducer {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int r = (tid >> 3) + 16 * j;
-      src[j] = x && r < t.n ? x + (size_t)p.perm[t.pos + r] * ld + (tid & 7) * 8 : nullptr;
+      src[j] = x && r < t.n ? x + (size_t)__ldcg(p.perm + t.pos + r) * ld + (tid & 7) * 8 : nullptr;
     }
   }
   // One unit: columns col .. col + 63 of width (zeros past it), and w_bytes of the adapter.
@@ -540,17 +552,39 @@ __host__ __device__ constexpr int la_stages(int r16) {
 __host__ __device__ constexpr int la_smem(int r16) { return 1024 + la_stages(r16) * (LT_X_BYTES + r16 * 128); }
 // At least this many units a CTA, so that few pieces of a tile have to be joined.
 constexpr int LA_MIN_UNITS = 4;
+// The shares of A x: U units over G CTAs, in order. A tile whose K
+// extent lies in several shares is summed in pieces, at most two of a CTA's
+// own: the end of a tile that another began (piece slot 2 b), and the
+// beginning of one (2 b + 1).
+// All counts fit 32 bits: a unit stands for up to 128 x 64 values.
+struct LoraShares {
+  unsigned U, G, q, r;  // the first r CTAs have q + 1 units, the others q
+  __device__ __forceinline__ LoraShares(unsigned units, unsigned ctas) : U(units), G(ctas), q(units / ctas), r(units % ctas) {}
+  __device__ __forceinline__ unsigned begin(unsigned b) const { return b < G ? q * b + min(b, r) : U; }
+  __device__ __forceinline__ unsigned cta(unsigned v) const {
+    return v < r * (q + 1) ? v / (q + 1) : r + (v - r * (q + 1)) / q;
+  }
+};
+__device__ __forceinline__ LoraShares shrink_shares(const LoraParams& p) {
+  const unsigned U = (unsigned)__ldcg(p.meta) * (unsigned)p.g.KB;
+  return LoraShares(U, min(gridDim.x, max(1u, U / LA_MIN_UNITS)));
+}
+// The part of a share that lies in one tile: n units from `first` of `per`.
+struct LoraSpan {
+  int tile, first, n;
+  __device__ __forceinline__ LoraSpan(unsigned v, unsigned v1, unsigned per)
+      : tile((int)(v / per)), first((int)(v % per)), n((int)min(v1 - v, per - v % per)) {}
+};
 
-// u[pos][r] = A x. Where a tile's K extent is shared by several CTAs, each
-// leaves its sum in part, and the last of them to finish adds the sums up in
-// K order.
+// A x of a tile's rows: to u[pos][r] where a CTA has the tile's whole K extent,
+// else a sum for each piece to part[slot][row][r], which the reader adds up.
 template <int ACT>
 __global__ void __launch_bounds__(LA_THREADS, 1)
     lora_shrink_kernel(const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t lt_sm[];
   __shared__ __align__(8) uint64_t full[LT_MAX_STAGES], empty[LT_MAX_STAGES], acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_last;
+  __shared__ int s_abort;
   uint8_t* smem = lt_sm + ((1024u - (smem_u32(lt_sm) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int stages = la_stages(p.g.max_r16);
@@ -581,16 +615,16 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   pdl_trigger();  // after the TMEM allocation: the next kernel's may then wait for this one's end
   volatile int* abort = &s_abort;
   const uint64_t lim = p.wait_limit_ns;
-  const long long U = (long long)p.meta[0] * p.g.KB;
-  const long long G = min((long long)gridDim.x, max(1ll, U / LA_MIN_UNITS));
-  const long long v0 = blockIdx.x < G ? U * blockIdx.x / G : 0, v1 = blockIdx.x < G ? U * (blockIdx.x + 1) / G : 0;
+  const LoraShares shares = shrink_shares(p);
+  const unsigned v0 = shares.begin(blockIdx.x), v1 = shares.begin(blockIdx.x + 1);
 
   if (warp < LT_PROD_WARPS) {
     LoraProducer pr{smem, full, empty, stages, stage_bytes, tid, abort, lim};
     bool ok = true;
-    for (long long v = v0; v < v1 && ok;) {
-      const int kb0 = (int)(v % p.g.KB), nk = (int)min(v1 - v, (long long)(p.g.KB - kb0));
-      const LoraTile t = lora_tile(p, (int)(v / p.g.KB));
+    for (unsigned v = v0; v < v1 && ok;) {
+      const LoraSpan sp(v, v1, p.g.KB);
+      const int kb0 = sp.first, nk = sp.n;
+      const LoraTile t = lora_tile(p, sp.tile);
       v += nk;
       pr.rows(p, t, p.x, p.ldx);
       const uint32_t a_bytes = (uint32_t)t.r16 * 128;
@@ -607,9 +641,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     RingPos rp;
     bool ok = true;
     int j = 0;
-    for (long long v = v0; v < v1 && ok; ++j) {
-      const int kb0 = (int)(v % p.g.KB), nk = (int)min(v1 - v, (long long)(p.g.KB - kb0));
-      const LoraTile t = lora_tile(p, (int)(v / p.g.KB));
+    for (unsigned v = v0; v < v1 && ok; ++j) {
+      const LoraSpan sp(v, v1, p.g.KB);
+      const int kb0 = sp.first, nk = sp.n;
+      const LoraTile t = lora_tile(p, sp.tile);
       v += nk;
       const int buf = j & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort, lim));
@@ -639,14 +674,14 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     volatile int never = 0;
     mbar_wait(&mma_done, 0, &never, lim);
   } else {
-    const int e = tid - 128, row = (warp & 3) * 32 + lane;
+    const int row = (warp & 3) * 32 + lane;
     int j = 0;
-    for (long long v = v0; v < v1; ++j) {
-      const int tile = (int)(v / p.g.KB), kb0 = (int)(v % p.g.KB), nk = (int)min(v1 - v, (long long)(p.g.KB - kb0));
-      const LoraTile t = lora_tile(p, tile);
+    for (unsigned v = v0; v < v1; ++j) {
+      const LoraSpan sp(v, v1, p.g.KB);
+      const int kb0 = sp.first, nk = sp.n;
+      const LoraTile t = lora_tile(p, sp.tile);
       v += nk;
       const int buf = j & 1;
-      const bool whole = nk == p.g.KB;
       if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(j >> 1) & 1u, abort, lim))) {
         if (lane == 0) {
           s_abort = 1;
@@ -655,10 +690,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         break;
       }
       tc_fence_after();
-      // Lane = row. A CTA leaves at most two pieces: the end of a tile that
-      // another began (slot 2 b), and the beginning of one (slot 2 b + 1).
-      float* dst = whole ? p.u + (size_t)(t.pos + row) * p.g.max_r16
-                         : p.part + ((size_t)(2 * blockIdx.x + (kb0 == 0)) * LORA_TILE_ROWS + row) * p.g.max_r16;
+      // lane = row
+      float* dst = nk == p.g.KB ? p.u + (size_t)(t.pos + row) * p.g.max_r16
+                                : p.part + ((size_t)(2 * blockIdx.x + (kb0 == 0)) * LORA_TILE_ROWS + row) * p.g.max_r16;
       for (int col = 0; col < t.r16; col += 16) {
         uint32_t w[16];
         tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)buf * acc_cols + col, w);
@@ -672,39 +706,6 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
-      if (!whole) {
-        // CTA of unit w: the largest b with U b / G <= w
-        const long long w0 = (long long)tile * p.g.KB, w1 = w0 + p.g.KB - 1;
-        const int b0 = (int)(((w0 + 1) * G - 1) / U), b1 = (int)(((w1 + 1) * G - 1) / U);
-        __threadfence();
-        named_bar_sync(1, 128);
-        if (e == 0) s_last = atomicAdd(&p.arrived[tile], 1) == b1 - b0;
-        named_bar_sync(1, 128);
-        if (s_last) {
-          __threadfence();
-          // 4 values a thread and 8 threads a row (so 32 columns a pass), two
-          // rows at once: up to 8 loads in flight.
-          const int c4 = (e & 7) * 4;
-          for (int c = c4; c < t.r16; c += 32) {
-            for (int r = e >> 3; r < t.n; r += 32) {
-              const size_t at0 = (size_t)r * p.g.max_r16 + c, at1 = at0 + (size_t)(r + 16 < t.n ? 16 : 0) * p.g.max_r16;
-              float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
-#pragma unroll 4
-              for (int b = b0; b <= b1; ++b) {
-                const float* from = p.part + (size_t)(2 * b + (b == b0)) * LORA_TILE_ROWS * p.g.max_r16;
-                const float4 f0 = __ldcg(reinterpret_cast<const float4*>(from + at0));
-                const float4 f1 = __ldcg(reinterpret_cast<const float4*>(from + at1));
-                s0 = make_float4(s0.x + f0.x, s0.y + f0.y, s0.z + f0.z, s0.w + f0.w);
-                s1 = make_float4(s1.x + f1.x, s1.y + f1.y, s1.z + f1.z, s1.w + f1.w);
-              }
-              float* u = p.u + (size_t)t.pos * p.g.max_r16;
-              *reinterpret_cast<float4*>(u + at0) = s0;
-              if (r + 16 < t.n) *reinterpret_cast<float4*>(u + at1) = s1;
-            }
-          }
-        }
-        named_bar_sync(1, 128);  // s_last is read
-      }
     }
   }
   __syncwarp();
@@ -716,9 +717,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   }
 }
 
-// Warp roles of the B u kernel: 0..3 producers, 4..7 u operand, 8..15 epilogue
-// (two groups of 4, which take alternate units), 16 MMA.
-constexpr int LB_THREADS = 544;
+// Warp roles of the B u kernel: 0..3 producers, 4..11 u operand, 12..19 epilogue
+// (two groups of 4, which take alternate units), 20 MMA.
+constexpr int LB_THREADS = 672;
+constexpr int LB_WARP_U = 4, LB_U_WARPS = 8, LB_WARP_EPI = 12, LB_WARP_MMA = 20;
 constexpr int LB_ACC = 4;  // accumulators of 64 columns
 // u's two parts are held twice, so that the next tile's are ready in time;
 // above rank 64 once, which leaves the room to the ring. The number of stages
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
   const int stage_bytes = LT_X_BYTES + p.g.max_r16 * 128;
   const int u_bytes = lb_u_bytes(p.g.max_r16), u_bufs = lb_u_bufs(p.g.max_r16);
   uint8_t* ring = smem + u_bufs * u_bytes;
-  if (warp == 16) {
+  if (warp == LB_WARP_MMA) {
     tmem_alloc(&s_tmem, LB_ACC * 64);
     tmem_relinquish();
   }
@@ -767,7 +769,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
       mbar_init(&acc_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&u_full[i], 4);
+      mbar_init(&u_full[i], LB_U_WARPS);
       mbar_init(&u_empty[i], 1);
     }
     mbar_init(&mma_done, 1);
@@ -778,20 +780,28 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  pdl_wait();
-  pdl_trigger();
+  // Only the u operand's warps wait for the A x kernel. The others read what
+  // was complete before that kernel's own wait returned, which is before any
+  // CTA of this one may start: the plan, the base and the adapters (past L1,
+  // which may hold lines of an earlier batch's plan). Rows without an adapter
+  // may so be written while A x still runs, which reads x and the plan only.
+  if (warp >= LB_WARP_U && warp < LB_WARP_EPI) {
+    pdl_wait();
+    pdl_trigger();
+  }
   volatile int* abort = &s_abort;
   const uint64_t lim = p.wait_limit_ns;
   // In place, the rows without an adapter are as they should be.
-  const long long U = (long long)(p.base == p.out ? p.meta[0] : p.meta[1]) * p.g.NB;
-  const long long v0 = U * blockIdx.x / gridDim.x, v1 = U * (blockIdx.x + 1) / gridDim.x;
+  const LoraShares shares((unsigned)__ldcg(p.meta + (p.base == p.out ? 0 : 1)) * (unsigned)p.g.NB, gridDim.x);
+  const unsigned v0 = shares.begin(blockIdx.x), v1 = shares.begin(blockIdx.x + 1);
   bool ok = true;
 
   if (warp < LT_PROD_WARPS) {
     LoraProducer pr{ring, full, empty, stages, stage_bytes, tid, abort, lim};
-    for (long long v = v0; v < v1 && ok;) {
-      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
-      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
+    for (unsigned v = v0; v < v1 && ok;) {
+      const LoraSpan sp(v, v1, p.g.NB);
+      const int nt0 = sp.first, nn = sp.n;
+      const LoraTile t = lora_tile(p, sp.tile);
       v += nn;
       pr.rows(p, t, p.base, p.ldbase);
       const uint32_t b_bytes = (uint32_t)t.r16 * 128;
@@ -805,13 +815,14 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
       }
       pr.drain();
     }
-  } else if (warp == 16) {
+  } else if (warp == LB_WARP_MMA) {
     RingPos rp;
     int ju = 0, unit = 0;
     const uint32_t idesc = idesc_kf16<ACT>(128, 64);
-    for (long long v = v0; v < v1 && ok;) {
-      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
-      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
+    for (unsigned v = v0; v < v1 && ok;) {
+      const LoraSpan sp(v, v1, p.g.NB);
+      const int nt0 = sp.first, nn = sp.n;
+      const LoraTile t = lora_tile(p, sp.tile);
       v += nn;
       if (t.adapter < 0) {
         // No product, only the slots' turn (the tiles without an adapter are
@@ -853,14 +864,16 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
     umma_commit_warp(&mma_done);
     volatile int never = 0;
     mbar_wait(&mma_done, 0, &never, lim);
-  } else if (warp < 8) {
-    // u's two parts as the A operand: 16-byte core-matrix rows, [r16 / 8][128 rows]. Thread = row.
-    const int row = tid - 128;
+  } else if (warp < LB_WARP_EPI) {
+    // u's two parts as the A operand: 16-byte core-matrix rows, [r16 / 8][128
+    // rows]. A thread takes ranks 4 c .. 4 c + 3 of every 16, of two rows.
+    const int c = lane & 3, row = (warp - LB_WARP_U) * 8 + (lane >> 2);
+    const LoraShares ks = shrink_shares(p);
     int ju = 0;
-    for (long long v = v0; v < v1;) {
-      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
-      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
-      v += nn;
+    for (unsigned v = v0; v < v1;) {
+      const LoraSpan sp(v, v1, p.g.NB);
+      const LoraTile t = lora_tile(p, sp.tile);
+      v += sp.n;
       if (t.adapter < 0) continue;
       const int ub = ju % u_bufs;
       if (!__all_sync(0xffffffffu, mbar_wait(&u_empty[ub], ((uint32_t)(ju / u_bufs) & 1u) ^ 1u, abort, lim))) {
@@ -868,20 +881,42 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
         break;
       }
       ++ju;
-      uint8_t* hi = smem + ub * u_bytes + row * 16;
+      uint8_t* hi = smem + ub * u_bytes;
       uint8_t* lo = hi + LORA_TILE_ROWS * t.r16 * 2;
-      const float* u = p.u + (size_t)(t.pos + min(row, t.n - 1)) * p.g.max_r16;
-#pragma unroll 4
-      for (int ch = 0; ch < t.r16 / 8; ++ch) {
-        uint16_t h[8], l[8];
-        float f[8];
-        *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(u + ch * 8));
-        *reinterpret_cast<float4*>(f + 4) = __ldcg(reinterpret_cast<const float4*>(u + ch * 8 + 4));
-        // past the rank A's zeros met whatever x held
+      // the pieces' sums, in K order
+      const unsigned w0 = (unsigned)sp.tile * (unsigned)p.g.KB;
+      const int b0 = (int)ks.cta(w0), pieces = (int)ks.cta(w0 + p.g.KB - 1) - b0 + 1;
+      const float* from = pieces == 1 ? p.u + (size_t)t.pos * p.g.max_r16
+                                      : p.part + (size_t)(2 * b0 + 1) * LORA_TILE_ROWS * p.g.max_r16;
+      for (int r0 = 0; r0 < t.r16; r0 += 64) {
+        float4 f[8];  // [half of the rows][16 ranks]
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split_act<ACT>(ch * 8 + j < t.rank ? f[j] : 0.0f, &h[j], &l[j]);
-        *reinterpret_cast<uint4*>(hi + ch * LORA_TILE_ROWS * 16) = *reinterpret_cast<const uint4*>(h);
-        *reinterpret_cast<uint4*>(lo + ch * LORA_TILE_ROWS * 16) = *reinterpret_cast<const uint4*>(l);
+        for (int i = 0; i < 8; ++i) f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int b = 0; b < pieces; ++b) {
+          const float* u = b == 0 ? from : p.part + (size_t)2 * (b0 + b) * LORA_TILE_ROWS * p.g.max_r16;
+          float4 m[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = row + 64 * (i >> 2), k = r0 + 16 * (i & 3) + 4 * c;
+            m[i] = r < t.n && k < t.r16 ? __ldcg(reinterpret_cast<const float4*>(u + (size_t)r * p.g.max_r16 + k))
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = make_float4(f[i].x + m[i].x, f[i].y + m[i].y, f[i].z + m[i].z, f[i].w + m[i].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = row + 64 * (i >> 2), k = r0 + 16 * (i & 3) + 4 * c;
+          if (k >= t.r16) continue;
+          const float s[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+          uint16_t h[4], l[4];
+          // past the rank A's zeros met whatever x held
+#pragma unroll
+          for (int j = 0; j < 4; ++j) split_act<ACT>(k + j < t.rank ? s[j] : 0.0f, &h[j], &l[j]);
+          const int at = ((k >> 3) * LORA_TILE_ROWS + r) * 16 + (k & 4) * 2;
+          *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+          *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (uint32_t)l[1] << 16, l[2] | (uint32_t)l[3] << 16);
+        }
       }
       fence_async_smem();
       __syncwarp();
@@ -894,20 +929,21 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
   } else {
     // A warp owns 32 rows of every second unit. The results replace the base
     // values in the slot, lane = row, and go out as 128-byte row segments.
-    const int group = (warp - 8) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int group = (warp - LB_WARP_EPI) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const int c = lane & 7;  // 16-byte chunk on the way out
     RingPos rp;
     int unit = 0;
-    for (long long v = v0; v < v1 && ok;) {
-      const int nt0 = (int)(v % p.g.NB), nn = (int)min(v1 - v, (long long)(p.g.NB - nt0));
-      const LoraTile t = lora_tile(p, (int)(v / p.g.NB));
+    for (unsigned v = v0; v < v1 && ok;) {
+      const LoraSpan sp(v, v1, p.g.NB);
+      const int nt0 = sp.first, nn = sp.n;
+      const LoraTile t = lora_tile(p, sp.tile);
       v += nn;
-      const float scale = t.adapter >= 0 ? reinterpret_cast<const float*>(p.packed + p.g.scale_off)[t.adapter] : 0.0f;
+      const float scale = t.adapter >= 0 ? __ldcg(reinterpret_cast<const float*>(p.packed + p.g.scale_off) + t.adapter) : 0.0f;
       int tok[8];  // the rows this lane stores: quarter * 32 + lane / 8 + 4 i
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = quarter * 32 + (lane >> 3) + 4 * i;
-        tok[i] = r < t.n ? p.perm[t.pos + r] : -1;
+        tok[i] = r < t.n ? __ldcg(p.perm + t.pos + r) : -1;
       }
       for (int i = 0; i < nn; ++i, ++unit, rp.next(stages)) {
         if ((unit & 1) != group) continue;
@@ -965,7 +1001,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == LB_WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, LB_ACC * 64);
   }
