@@ -13,9 +13,14 @@ __host__ __device__ __forceinline__ size_t lora_a_byte(int r16, int r, int k) {
   const int chunk = ((k >> 3) & 7) ^ (r & 7);
   return ((size_t)(k >> 6) * r16 + r) * 128 + chunk * 16 + (k & 7) * 2;
 }
-// Byte of B[n][r] from the start of the block's B tiles.
+// Byte of B[n][r] from the start of the block's B tiles. The rows of a tile are
+// permuted inside each 32: row 8 q + 2 j + e lies at 8 j + 2 q + e. Where an
+// accumulator gives a lane the columns 8 j + 2 q + e of q fixed, as mma.sync and
+// the 16x256b loads from tensor memory do, these are 8 neighbouring columns of
+// the result: 16 bytes of a row, loaded and stored without shared memory.
 __host__ __device__ __forceinline__ size_t lora_b_byte(int r16, int n, int r) {
-  return (size_t)(n >> 6) * r16 * 128 + ((size_t)(r >> 3) * 64 + (n & 63)) * 16 + (r & 7) * 2;
+  const int at = (n & 32) + ((n >> 1) & 3) * 8 + ((n >> 3) & 3) * 2 + (n & 1);
+  return (size_t)(n >> 6) * r16 * 128 + ((size_t)(r >> 3) * 64 + at) * 16 + (r & 7) * 2;
 }
 
 __global__ void lora_clear_kernel(uint32_t* words, int n) {
@@ -107,7 +112,8 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 // weights, straight from global memory, on the N side. K inside a group of 32
 // (and the rank in the second product) is permuted alike for both operands, so
 // that a lane's operand words are 16 bytes of one row. The columns of the
-// second product are permuted so that a lane ends up with 8 neighbouring ones.
+// second product are permuted so that a lane ends up with 8 neighbouring ones
+// (lora_b_byte).
 constexpr int LS_C = 8;
 constexpr int LS_THREADS = 256;
 constexpr int LS_WARPS = LS_THREADS / 32;
@@ -247,8 +253,8 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[i][e] = 0.0f;
-    // column c of MMA i is n + 8 (c / 2) + 2 i + c % 2
-    const uint8_t* tile = btiles + (size_t)(n >> 6) * r16 * 128 + ((n & 63) + 8 * (g >> 1) + (g & 1)) * 16;
+    // MMA i takes the tile's packed rows 8 i .. 8 i + 7 of these 32 (lora_b_byte)
+    const uint8_t* tile = btiles + (size_t)(n >> 6) * r16 * 128 + ((n & 63) + g) * 16;
 #pragma unroll
     for (int r = 0; r < R; r += 16) {
       if (r < r16) {
@@ -260,7 +266,7 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
         const uint8_t* src = tile + (r / 8 + (q >> 1)) * 1024 + (q & 1) * 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + i * 32));
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + i * 128));
           mma_16816<ACT>(d[i], ha.x, hb.x, ha.y, hb.y, w.x, w.y);
           mma_16816<ACT>(d[i], la.x, lb.x, la.y, lb.y, w.x, w.y);
         }
@@ -276,9 +282,10 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
                          : make_uint4(0, 0, 0, 0);
         uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          yw[i] = f32x2_to_act<ACT>(fmaf(scale, d[i][2 * half], act_f32<ACT>((uint16_t)(yw[i] & 0xFFFFu))),
-                                    fmaf(scale, d[i][2 * half + 1], act_f32<ACT>((uint16_t)(yw[i] >> 16))));
+        for (int i = 0; i < 4; ++i) {
+          const float2 b = act_x2_to_f32<ACT>(yw[i]);
+          yw[i] = f32_to_act_x2<ACT>(fmaf(scale, d[i][2 * half], b.x), fmaf(scale, d[i][2 * half + 1], b.y));
+        }
         *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + c) = y;
       }
     }
@@ -351,8 +358,10 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
       if (g < 0 || g >= p.g.slots || s_rank[g] == 0) g = G - 1;
       // the lanes with this lane's group, bit by bit
       unsigned peers = __ballot_sync(0xffffffffu, row);
+      const int g0 = __shfl_sync(0xffffffffu, g, 0);
+      const int most = __all_sync(0xffffffffu, !row || g == g0) ? 0 : bits;  // often all the same
 #pragma unroll 1
-      for (int b = 0; b < bits; ++b) {
+      for (int b = 0; b < most; ++b) {
         const bool one = (g >> b) & 1;
         const unsigned with = __ballot_sync(0xffffffffu, one);
         peers &= one ? with : ~with;
@@ -523,11 +532,12 @@ struct LoraProducer {
       mbar_expect_tx_elect(&full[at.slot], w_bytes);
       bulk_g2s_if(tid == 0 && w_bytes > 0, st + LT_X_BYTES, w, w_bytes, &full[at.slot]);
     }
-    const uint32_t bytes = col + (tid & 7) * 8 < width ? 16u : 0u;
+    const bool in = col + (tid & 7) * 8 < width;
     const uint32_t dst = smem_u32(st) + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) * 16);
+    const int at_col = in ? col : -(tid & 7) * 8;  // past the width: zeros, and a source inside the row
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (src[j]) cp_async16(dst + j * 2048, bytes ? src[j] + col : src[j] - (tid & 7) * 8, bytes);
+      if (src[j]) cp_async16(dst + j * 2048, src[j] + at_col, in ? 16u : 0u);
     cp_async_arrive(&full[at.slot]);
     at.next(stages);
     ++issued;
@@ -717,56 +727,132 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   }
 }
 
-// Warp roles of the B u kernel: 0..3 producers, 4..11 u operand, 12..19 epilogue
-// (two groups of 4, which take alternate units), 20 MMA.
-constexpr int LB_THREADS = 672;
-constexpr int LB_WARP_U = 4, LB_U_WARPS = 8, LB_WARP_EPI = 12, LB_WARP_MMA = 20;
-constexpr int LB_ACC = 4;  // accumulators of 64 columns
-// u's two parts are held twice, so that the next tile's are ready in time;
-// above rank 64 once, which leaves the room to the ring. The number of stages
-// is even: each epilogue group then has slots of its own, and meets every use
-// of them (a parity wait must not be two uses behind).
+// Warp roles of the B u kernel: 0 producer, 1 MMA, 2..7 u operand, 8..23
+// epilogue (two groups of 8, which take alternate units).
+constexpr int LB_THREADS = 768;
+constexpr int LB_WARP_U = 2, LB_WARP_EPI = 8;
+constexpr int LB_U_WARPS = LB_WARP_EPI - LB_WARP_U, LB_EPI_WARPS = 8;  // epilogue warps of a group
+constexpr int LB_FIRST_WARPS = LB_U_WARPS + 2 * LB_EPI_WARPS;           // warps that form the first u
+constexpr int LB_ACC = 4;     // accumulators of 64 columns
+constexpr int LB_MAX_STAGES = 12;  // B tiles in the ring
 __host__ __device__ constexpr int lb_u_bytes(int r16) { return 2 * LORA_TILE_ROWS * r16 * 2; }
-__host__ __device__ constexpr int lb_u_bufs(int r16) { return r16 <= 64 ? 2 : 1; }
+// u's two parts are held twice, so that the next tile's are ready in time;
+// above rank 80 once, which leaves the room to the ring.
+__host__ __device__ constexpr int lb_u_bufs(int r16) { return r16 <= 80 ? 2 : 1; }
 __host__ __device__ constexpr int lb_stages(int r16) {
-  return ((LT_SMEM - lb_u_bufs(r16) * lb_u_bytes(r16)) / (LT_X_BYTES + r16 * 128) < LT_MAX_STAGES
-              ? (LT_SMEM - lb_u_bufs(r16) * lb_u_bytes(r16)) / (LT_X_BYTES + r16 * 128)
-              : LT_MAX_STAGES) &
-         ~1;
+  return (LT_SMEM - lb_u_bufs(r16) * lb_u_bytes(r16)) / (r16 * 128) < LB_MAX_STAGES
+             ? (LT_SMEM - lb_u_bufs(r16) * lb_u_bytes(r16)) / (r16 * 128)
+             : LB_MAX_STAGES;
 }
 __host__ __device__ constexpr int lb_smem(int r16) {
-  return 1024 + lb_u_bufs(r16) * lb_u_bytes(r16) + lb_stages(r16) * (LT_X_BYTES + r16 * 128);
+  return 1024 + lb_u_bufs(r16) * lb_u_bytes(r16) + lb_stages(r16) * r16 * 128;
 }
-static_assert(lb_stages(LORA_MAX_RANK) >= 4 && lb_stages(64) >= 4, "stages");
+static_assert(lb_stages(64) == LB_MAX_STAGES && lb_stages(96) >= 2 && lb_stages(LORA_MAX_RANK) >= 5, "stages");
 static_assert(LB_ACC % 2 == 0, "each epilogue group has accumulators of its own");
 
-// out = base + scale B u. u enters as its two parts (split_act), whose
-// products with B add up in the same accumulator.
+// u of one tile as the A operand, in its two parts: 16-byte core-matrix rows,
+// [r16 / 8][128 rows]. The sums of the pieces are added up in K order. Warp w of
+// nw; a lane takes 4 ranks of one row, a warp 8 rows of 16 ranks, Q such at once
+// (loads in flight together: the walk over the pieces is latency alone).
+struct LoraPieces {
+  const float* first;
+  const float* more;  // the second piece
+  int n;
+};
+template <int ACT, int Q>
+__device__ __forceinline__ void lora_u_operand(const LoraTile& t, const LoraPieces& pc, int max_r16, uint8_t* hi, int w,
+                                               int nw, int lane) {
+  uint8_t* lo = hi + LORA_TILE_ROWS * t.r16 * 2;
+  const size_t step = (size_t)2 * LORA_TILE_ROWS * max_r16;
+  const int items = (t.r16 / 16) * (LORA_TILE_ROWS / 8);
+  for (int i0 = w; i0 < items; i0 += Q * nw) {
+    float4 f[Q];
+    int row[Q], k[Q];
+    bool in[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = i0 + q * nw;
+      row[q] = (i & 15) * 8 + (lane >> 2);
+      k[q] = (i >> 4) * 16 + (lane & 3) * 4;
+      in[q] = i < items && row[q] < t.n;
+      f[q] = in[q] ? __ldcg(reinterpret_cast<const float4*>(pc.first + (size_t)row[q] * max_r16 + k[q]))
+                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (int b = 0; b < pc.n - 1; ++b) {
+      float4 m[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        m[q] = in[q] ? __ldcg(reinterpret_cast<const float4*>(pc.more + b * step + (size_t)row[q] * max_r16 + k[q]))
+                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        f[q] = make_float4(f[q].x + m[q].x, f[q].y + m[q].y, f[q].z + m[q].z, f[q].w + m[q].w);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if (i0 + q * nw >= items) break;
+      const float v[4] = {f[q].x, f[q].y, f[q].z, f[q].w};
+      uint16_t h[4], l[4];
+      // past the rank A's zeros met whatever x held
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split_act<ACT>(k[q] + j < t.rank ? v[j] : 0.0f, &h[j], &l[j]);
+      const int at = ((k[q] >> 3) * LORA_TILE_ROWS + row[q]) * 16 + (k[q] & 4) * 2;
+      *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+      *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (uint32_t)l[1] << 16, l[2] | (uint32_t)l[3] << 16);
+    }
+  }
+}
+__device__ __forceinline__ LoraPieces lora_pieces(const LoraParams& p, const LoraShares& ks, int tile, const LoraTile& t) {
+  const unsigned w0 = (unsigned)tile * (unsigned)p.g.KB;
+  const unsigned b0 = ks.cta(w0), b1 = ks.cta(w0 + p.g.KB - 1);
+  LoraPieces pc;
+  pc.n = (int)(b1 - b0) + 1;
+  pc.first = b0 == b1 ? p.u + (size_t)t.pos * p.g.max_r16
+                      : p.part + (size_t)(2 * b0 + 1) * LORA_TILE_ROWS * p.g.max_r16;
+  pc.more = p.part + (size_t)(2 * b0 + 2) * LORA_TILE_ROWS * p.g.max_r16;
+  return pc;
+}
+
+// (a, b) * s + (c, d), both halves in one instruction.
+__device__ __forceinline__ float2 fma_x2(float a, float b, float s, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(s), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// out = base + scale B u. u enters as its two parts (split_act), whose products
+// with B add up in the same accumulator. An epilogue warp owns 32 rows and 32
+// columns of every second unit; a lane holds 16 bytes of 4 rows, whose base
+// values it has loaded two units ahead.
 template <int ACT>
 __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t lt_sm[];
-  __shared__ __align__(8) uint64_t full[LT_MAX_STAGES], empty[LT_MAX_STAGES], acc_full[LB_ACC], acc_empty[LB_ACC],
-      u_full[2], u_empty[2], mma_done;
+  __shared__ __align__(8) uint64_t full[LB_MAX_STAGES], empty[LB_MAX_STAGES], acc_full[LB_ACC], acc_empty[LB_ACC], u_full[2],
+      u_empty[2], mma_done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* smem = lt_sm + ((1024u - (smem_u32(lt_sm) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int stages = lb_stages(p.g.max_r16);
-  const int stage_bytes = LT_X_BYTES + p.g.max_r16 * 128;
   const int u_bytes = lb_u_bytes(p.g.max_r16), u_bufs = lb_u_bufs(p.g.max_r16);
+  const int stage_bytes = p.g.max_r16 * 128, stages = lb_stages(p.g.max_r16);
   uint8_t* ring = smem + u_bufs * u_bytes;
-  if (warp == LB_WARP_MMA) {
+  if (warp == 1) {
     tmem_alloc(&s_tmem, LB_ACC * 64);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&full[i], LT_FULL_COUNT);
-      mbar_init(&empty[i], 5);  // the MMAs that read B, and the 4 warps of the unit's epilogue
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < LB_ACC; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], LB_EPI_WARPS);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&u_full[i], LB_U_WARPS);
@@ -780,71 +866,78 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // Only the u operand's warps wait for the A x kernel. The others read what
+  // Only the warps that read u wait for the A x kernel. The others read what
   // was complete before that kernel's own wait returned, which is before any
   // CTA of this one may start: the plan, the base and the adapters (past L1,
   // which may hold lines of an earlier batch's plan). Rows without an adapter
   // may so be written while A x still runs, which reads x and the plan only.
-  if (warp >= LB_WARP_U && warp < LB_WARP_EPI) {
-    pdl_wait();
-    pdl_trigger();
-  }
   volatile int* abort = &s_abort;
   const uint64_t lim = p.wait_limit_ns;
   // In place, the rows without an adapter are as they should be.
   const LoraShares shares((unsigned)__ldcg(p.meta + (p.base == p.out ? 0 : 1)) * (unsigned)p.g.NB, gridDim.x);
   const unsigned v0 = shares.begin(blockIdx.x), v1 = shares.begin(blockIdx.x + 1);
+  // The tiles without an adapter are the last: only the epilogue sees them.
+  const unsigned va = min(v1, (unsigned)__ldcg(p.meta) * (unsigned)p.g.NB);
   bool ok = true;
+  // The first tile's u, which everything waits for, by the u and the epilogue
+  // warps together, once the A x kernel has ended.
+  auto first_u = [&](const LoraTile& t, int tile) {
+    const LoraPieces pc = lora_pieces(p, shrink_shares(p), tile, t);
+    pdl_wait();
+    lora_u_operand<ACT, 2>(t, pc, p.g.max_r16, smem, warp - LB_WARP_U, LB_FIRST_WARPS, lane);
+    fence_async_smem();
+    named_bar_sync(1, LB_FIRST_WARPS * 32);
+  };
 
-  if (warp < LT_PROD_WARPS) {
-    LoraProducer pr{ring, full, empty, stages, stage_bytes, tid, abort, lim};
-    for (unsigned v = v0; v < v1 && ok;) {
-      const LoraSpan sp(v, v1, p.g.NB);
-      const int nt0 = sp.first, nn = sp.n;
+  if (warp == 0) {
+    RingPos rp;
+    int issued = 0;
+    for (unsigned v = v0; v < va && ok;) {
+      const LoraSpan sp(v, va, p.g.NB);
       const LoraTile t = lora_tile(p, sp.tile);
-      v += nn;
-      pr.rows(p, t, p.base, p.ldbase);
-      const uint32_t b_bytes = (uint32_t)t.r16 * 128;
-      for (int i = nt0; i < nt0 + nn && ok; ++i)
-        ok = pr.fill(i * 64, p.g.N, t.block + p.g.b_off + (size_t)i * b_bytes, b_bytes);
+      v += sp.n;
+      const uint32_t bytes = (uint32_t)t.r16 * 128;
+      const uint8_t* b = t.block + p.g.b_off + (size_t)sp.first * bytes;
+      for (int i = 0; i < sp.n; ++i, b += bytes) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[rp.slot], rp.ph ^ 1u, abort, lim))) {
+          ok = false;
+          break;
+        }
+        mbar_expect_tx_elect(&full[rp.slot], bytes);
+        bulk_g2s_if(lane == 0, ring + rp.slot * stage_bytes, b, bytes, &full[rp.slot]);
+        ++issued;
+        rp.next(stages);
+      }
     }
     if (!ok) {
       if (lane == 0) {
         s_abort = 1;
         set_status(p.status, DEV_TIMEOUT);
       }
-      pr.drain();
+      volatile int never = 0;
+      for (int i = 0; i < stages && i < issued; ++i) {
+        rp.back(stages);
+        mbar_wait(&full[rp.slot], rp.ph, &never, lim);
+      }
     }
-  } else if (warp == LB_WARP_MMA) {
+  } else if (warp == 1) {
     RingPos rp;
     int ju = 0, unit = 0;
     const uint32_t idesc = idesc_kf16<ACT>(128, 64);
-    for (unsigned v = v0; v < v1 && ok;) {
-      const LoraSpan sp(v, v1, p.g.NB);
-      const int nt0 = sp.first, nn = sp.n;
+    for (unsigned v = v0; v < va && ok; ++ju) {
+      const LoraSpan sp(v, va, p.g.NB);
       const LoraTile t = lora_tile(p, sp.tile);
-      v += nn;
-      if (t.adapter < 0) {
-        // No product, only the slots' turn (the tiles without an adapter are
-        // the last, so the accumulators' uses need no count of them).
-        for (int i = 0; i < nn && ok; ++i) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[rp.slot], rp.ph, abort, lim));
-          if (ok && lane == 0) mbar_arrive(&empty[rp.slot]);
-          rp.next(stages);
-        }
-        continue;
-      }
+      v += sp.n;
       const int ub = ju % u_bufs;
       ok = __all_sync(0xffffffffu, mbar_wait(&u_full[ub], (uint32_t)(ju / u_bufs) & 1u, abort, lim));
-      ++ju;
       const uint32_t hi = smem_u32(smem + ub * u_bytes), lo = hi + (uint32_t)LORA_TILE_ROWS * t.r16 * 2;
-      for (int i = 0; i < nn && ok; ++i, ++unit) {
+      for (int i = 0; i < sp.n && ok; ++i, ++unit) {
         const int buf = unit % LB_ACC;
         ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((uint32_t)(unit / LB_ACC) & 1u) ^ 1u, abort, lim)) &&
              __all_sync(0xffffffffu, mbar_wait(&full[rp.slot], rp.ph, abort, lim));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t b = smem_u32(ring + rp.slot * stage_bytes + LT_X_BYTES), d = tmem + (uint32_t)buf * 64;
+        const uint32_t b = smem_u32(ring + rp.slot * stage_bytes), d = tmem + (uint32_t)buf * 64;
         for (int ks = 0; ks < t.r16 / 16; ++ks) {
           const uint64_t bd = smem_desc_plain(b + ks * 2 * 1024, 1024);
           const uint32_t off = (uint32_t)ks * 2 * LORA_TILE_ROWS * 16;
@@ -865,133 +958,109 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
     volatile int never = 0;
     mbar_wait(&mma_done, 0, &never, lim);
   } else if (warp < LB_WARP_EPI) {
-    // u's two parts as the A operand: 16-byte core-matrix rows, [r16 / 8][128
-    // rows]. A thread takes ranks 4 c .. 4 c + 3 of every 16, of two rows.
-    const int c = lane & 3, row = (warp - LB_WARP_U) * 8 + (lane >> 2);
     const LoraShares ks = shrink_shares(p);
     int ju = 0;
-    for (unsigned v = v0; v < v1;) {
-      const LoraSpan sp(v, v1, p.g.NB);
+    for (unsigned v = v0; v < va; ++ju) {
+      const LoraSpan sp(v, va, p.g.NB);
       const LoraTile t = lora_tile(p, sp.tile);
       v += sp.n;
-      if (t.adapter < 0) continue;
       const int ub = ju % u_bufs;
-      if (!__all_sync(0xffffffffu, mbar_wait(&u_empty[ub], ((uint32_t)(ju / u_bufs) & 1u) ^ 1u, abort, lim))) {
-        ok = false;
-        break;
-      }
-      ++ju;
-      uint8_t* hi = smem + ub * u_bytes;
-      uint8_t* lo = hi + LORA_TILE_ROWS * t.r16 * 2;
-      // the pieces' sums, in K order
-      const unsigned w0 = (unsigned)sp.tile * (unsigned)p.g.KB;
-      const int b0 = (int)ks.cta(w0), pieces = (int)ks.cta(w0 + p.g.KB - 1) - b0 + 1;
-      const float* from = pieces == 1 ? p.u + (size_t)t.pos * p.g.max_r16
-                                      : p.part + (size_t)(2 * b0 + 1) * LORA_TILE_ROWS * p.g.max_r16;
-      for (int r0 = 0; r0 < t.r16; r0 += 64) {
-        float4 f[8];  // [half of the rows][16 ranks]
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int b = 0; b < pieces; ++b) {
-          const float* u = b == 0 ? from : p.part + (size_t)2 * (b0 + b) * LORA_TILE_ROWS * p.g.max_r16;
-          float4 m[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = row + 64 * (i >> 2), k = r0 + 16 * (i & 3) + 4 * c;
-            m[i] = r < t.n && k < t.r16 ? __ldcg(reinterpret_cast<const float4*>(u + (size_t)r * p.g.max_r16 + k))
-                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (ju == 0) {
+        first_u(t, sp.tile);
+        pdl_trigger();
+      } else {
+        if (!__all_sync(0xffffffffu, mbar_wait(&u_empty[ub], ((uint32_t)(ju / u_bufs) & 1u) ^ 1u, abort, lim))) {
+          if (lane == 0) {
+            s_abort = 1;
+            set_status(p.status, DEV_TIMEOUT);
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = make_float4(f[i].x + m[i].x, f[i].y + m[i].y, f[i].z + m[i].z, f[i].w + m[i].w);
+          break;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = row + 64 * (i >> 2), k = r0 + 16 * (i & 3) + 4 * c;
-          if (k >= t.r16) continue;
-          const float s[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
-          uint16_t h[4], l[4];
-          // past the rank A's zeros met whatever x held
-#pragma unroll
-          for (int j = 0; j < 4; ++j) split_act<ACT>(k + j < t.rank ? s[j] : 0.0f, &h[j], &l[j]);
-          const int at = ((k >> 3) * LORA_TILE_ROWS + r) * 16 + (k & 4) * 2;
-          *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-          *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (uint32_t)l[1] << 16, l[2] | (uint32_t)l[3] << 16);
-        }
+        lora_u_operand<ACT, 4>(t, lora_pieces(p, ks, sp.tile, t), p.g.max_r16, smem + ub * u_bytes, warp - LB_WARP_U,
+                            LB_U_WARPS, lane);
+        fence_async_smem();
+        __syncwarp();
       }
-      fence_async_smem();
-      __syncwarp();
       if (lane == 0) mbar_arrive(&u_full[ub]);
     }
-    if (!ok && lane == 0) {
-      s_abort = 1;
-      set_status(p.status, DEV_TIMEOUT);
+    if (ju == 0) {
+      pdl_wait();
+      pdl_trigger();
     }
   } else {
-    // A warp owns 32 rows of every second unit. The results replace the base
-    // values in the slot, lane = row, and go out as 128-byte row segments.
-    const int group = (warp - LB_WARP_EPI) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const int c = lane & 7;  // 16-byte chunk on the way out
-    RingPos rp;
+    const int e = warp - LB_WARP_EPI;
+    const int group = e / LB_EPI_WARPS, quarter = warp & 3, half = (e >> 2) & 1;
+    const int c = half * 32 + (lane & 3) * 8;  // the lane's 8 columns of a unit
     int unit = 0;
     for (unsigned v = v0; v < v1 && ok;) {
       const LoraSpan sp(v, v1, p.g.NB);
-      const int nt0 = sp.first, nn = sp.n;
       const LoraTile t = lora_tile(p, sp.tile);
-      v += nn;
-      const float scale = t.adapter >= 0 ? __ldcg(reinterpret_cast<const float*>(p.packed + p.g.scale_off) + t.adapter) : 0.0f;
-      int tok[8];  // the rows this lane stores: quarter * 32 + lane / 8 + 4 i
+      const bool with = t.adapter >= 0;
+      const float scale = with ? __ldcg(reinterpret_cast<const float*>(p.packed + p.g.scale_off) + t.adapter) : 0.0f;
+      // The lane's rows: quarter * 32 + lane / 4 + 8 k; -1 past the tile's.
+      int row[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = quarter * 32 + (lane >> 3) + 4 * i;
-        tok[i] = r < t.n ? __ldcg(p.perm + t.pos + r) : -1;
+      for (int k = 0; k < 4; ++k) {
+        const int r = quarter * 32 + (lane >> 2) + 8 * k;
+        row[k] = r < t.n ? __ldcg(p.perm + t.pos + r) : -1;
       }
-      for (int i = 0; i < nn; ++i, ++unit, rp.next(stages)) {
-        if ((unit & 1) != group) continue;
-        const int buf = unit % LB_ACC;
-        uint8_t* st = ring + rp.slot * stage_bytes;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[rp.slot], rp.ph, abort, lim));
-        if (ok && t.adapter >= 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(unit / LB_ACC) & 1u, abort, lim));
-          if (ok) {
-            tc_fence_after();
+      auto load = [&](int i, uint4* y) {  // the base values of unit i
+        const int n = (sp.first + i) * 64 + c;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t w[32];
-              tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)buf * 64 + half * 32, w);
-              tmem_wait_ld();
+        for (int k = 0; k < 4; ++k)
+          y[k] = p.base && row[k] >= 0 && i < sp.n && n < p.g.N
+                     ? __ldcg(reinterpret_cast<const uint4*>(p.base + (size_t)row[k] * p.ldbase + n))
+                     : make_uint4(0, 0, 0, 0);
+      };
+      // Unit i from its base values in y, which are then unit i + 4's.
+      auto unit_of = [&](int i, uint4* y) {
+        if (with) {
+          const int buf = (unit + i) % LB_ACC;
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)((unit + i) / LB_ACC) & 1u, abort, lim));
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)buf * 64 + half * 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 16 rows
+            uint32_t w[16];
+            tmem_ld16x256x4(at + ((uint32_t)(16 * h) << 16), w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t* yw = reinterpret_cast<uint32_t*>(&y[2 * h + k]);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                uint4* at = reinterpret_cast<uint4*>(st + row * 128 + (((half * 4 + j) ^ (row & 7)) * 16));
-                uint4 y = p.base ? *at : make_uint4(0, 0, 0, 0);
-                uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  yw[k] = f32x2_to_act<ACT>(
-                      fmaf(scale, __uint_as_float(w[8 * j + 2 * k]), act_f32<ACT>((uint16_t)(yw[k] & 0xFFFFu))),
-                      fmaf(scale, __uint_as_float(w[8 * j + 2 * k + 1]), act_f32<ACT>((uint16_t)(yw[k] >> 16))));
-                *at = y;
+                const float2 f = fma_x2(__uint_as_float(w[4 * j + 2 * k]), __uint_as_float(w[4 * j + 2 * k + 1]), scale,
+                                        act_x2_to_f32<ACT>(yw[j]));
+                yw[j] = f32_to_act_x2<ACT>(f.x, f.y);
               }
             }
-            tc_fence_before();
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0 && t.adapter >= 0) mbar_arrive(&acc_empty[buf]);
-        const int n = (nt0 + i) * 64 + c * 8;
+        const int n = (sp.first + i) * 64 + c;
         if (n < p.g.N) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = quarter * 32 + (lane >> 3) + 4 * j;
-            if (tok[j] >= 0)
-              *reinterpret_cast<uint4*>(p.out + (size_t)tok[j] * p.ldout + n) =
-                  t.adapter >= 0 || p.base ? *reinterpret_cast<const uint4*>(st + r * 128 + ((c ^ (r & 7)) * 16))
-                                           : make_uint4(0, 0, 0, 0);
-          }
+          for (int k = 0; k < 4; ++k)
+            if (row[k] >= 0) *reinterpret_cast<uint4*>(p.out + (size_t)row[k] * p.ldout + n) = y[k];
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[rp.slot]);
+        load(i + 4, y);
+      };
+      // Two sets of base values in flight, each in registers of its own (a copy
+      // from one to the other would wait for the load).
+      const int i0 = (unit & 1) != group;
+      uint4 y0[4], y1[4];
+      load(i0, y0);
+      load(i0 + 2, y1);
+      if (v == v0 && with) first_u(t, sp.tile);
+      for (int i = i0; i < sp.n && ok; i += 4) {
+        unit_of(i, y0);
+        if (i + 2 < sp.n && ok) unit_of(i + 2, y1);
       }
+      unit += sp.n;
+      v += sp.n;
     }
     if (!ok && lane == 0) {
       s_abort = 1;
@@ -1001,7 +1070,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == LB_WARP_MMA) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, LB_ACC * 64);
   }
