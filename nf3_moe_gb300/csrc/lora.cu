@@ -153,7 +153,7 @@ __host__ __device__ constexpr int ls_smem(int r16) {
 
 // R: the largest padded rank of the set, rounded up to 16, 32, 64 or 128.
 template <int ACT, int R>
-__global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_small_kernel(LoraParams p) {
+__global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS, R <= 64 ? 2 : 1) lora_small_kernel(LoraParams p) {
   extern __shared__ __align__(16) uint8_t ls_sm[];
   __shared__ int s_tok[LS_TOK], s_cnt[LS_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -171,6 +171,7 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
             p.base ? *reinterpret_cast<const uint4*>(p.base + (size_t)t0 * p.ldbase + n) : make_uint4(0, 0, 0, 0);
     return;
   }
+  const float scale = reinterpret_cast<const float*>(p.packed + p.g.scale_off)[a];
   // The group: T <= LS_THREADS, so thread j looks at row j.
   const bool same = tid < p.T && p.ids[tid] == a;
   if (__syncthreads_count(same && tid < t0) % LS_TOK != 0) return;
@@ -184,35 +185,89 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
     if (same && tid >= t0 && pos < LS_TOK) s_tok[pos] = tid;
   }
   __syncthreads();
-  const float scale = reinterpret_cast<const float*>(p.packed + p.g.scale_off)[a];
+  int n_tok = 0;
+#pragma unroll
+  for (int w = 0; w < LS_WARPS; ++w) n_tok += s_cnt[w];
+  n_tok = min(n_tok, LS_TOK);
   const int r16 = (rank + 15) / 16 * 16;
   const uint8_t* block = p.packed + p.g.block_off + (size_t)a * p.g.block_bytes;
   const uint8_t* btiles = block + p.g.b_off;
   const int g = lane >> 2, q = lane & 3;
   const int ta = s_tok[g], tb = s_tok[g + 8];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
 
-  // ---- A x over this CTA's k-blocks, half a block (32 of K) a step
+  // ---- A x over this CTA's k-blocks, half a block (32 of K) a step, the next
+  // step's operands on their way
   float acc[R / 8][4];
 #pragma unroll
   for (int j = 0; j < R / 8; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-  const int h0 = 2 * (cta * p.g.KB / LS_C), h1 = 2 * ((cta + 1) * p.g.KB / LS_C);
-  for (int h = h0 + warp; h < h1; h += LS_WARPS) {
+  struct Step {
+    uint4 xa, xb, w[R / 8];
+  };
+  const int h1 = 2 * ((cta + 1) * p.g.KB / LS_C);
+  auto load_a = [&](int h, Step& s) {
     const int k = h * 32 + q * 8;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 xa = (ta >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)ta * p.ldx + k) : zero;
-    const uint4 xb = (tb >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)tb * p.ldx + k) : zero;
+    s.xa = (h < h1 && ta >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)ta * p.ldx + k) : zero;
+    s.xb = (h < h1 && tb >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)tb * p.ldx + k) : zero;
     const uint8_t* tile = block + (size_t)(h >> 1) * r16 * 128 + g * 128 + ((((h & 1) * 4 + q) ^ g) * 16);
+#pragma unroll
+    for (int j = 0; j < R / 8; ++j) s.w[j] = (h < h1 && 8 * j < r16) ? ldg16(tile + j * 1024) : zero;
+  };
+  auto mma_a = [&](const Step& s) {
 #pragma unroll
     for (int j = 0; j < R / 8; ++j) {
       if (8 * j < r16) {
-        const uint4 w = ldg16(tile + j * 1024);
-        mma_16816<ACT>(acc[j], xa.x, xb.x, xa.y, xb.y, w.x, w.y);
-        mma_16816<ACT>(acc[j], xa.z, xb.z, xa.w, xb.w, w.z, w.w);
+        mma_16816<ACT>(acc[j], s.xa.x, s.xb.x, s.xa.y, s.xb.y, s.w[j].x, s.w[j].y);
+        mma_16816<ACT>(acc[j], s.xa.z, s.xb.z, s.xa.w, s.xb.w, s.w[j].z, s.w[j].w);
       }
     }
+  };
+  const int h0 = 2 * (cta * p.g.KB / LS_C) + warp;
+  if constexpr (R <= 64) {
+    Step s0, s1;
+    load_a(h0, s0);
+    for (int h = h0; h < h1; h += 2 * LS_WARPS) {
+      load_a(h + LS_WARPS, s1);
+      mma_a(s0);
+      load_a(h + 2 * LS_WARPS, s0);
+      mma_a(s1);
+    }
+  } else {
+    for (int h = h0; h < h1; h += LS_WARPS) {
+      Step s0;
+      load_a(h, s0);
+      mma_a(s0);
+    }
   }
+
+  // ---- B's operands for the first 32 columns: they do not wait for u
+  // MMA i takes the tile's packed rows 8 i .. 8 i + 7 of these 32 (lora_b_byte)
+  struct Cols {
+    uint2 w[R / 16][4];
+  };
+  auto load_b = [&](int n, Cols& s) {
+    const uint8_t* tile = btiles + (size_t)(n >> 6) * r16 * 128 + ((n & 63) + g) * 16 + (q >> 1) * 1024 + (q & 1) * 8;
+#pragma unroll
+    for (int r = 0; r < R / 16; ++r)  // ranks 16 r + 4 q .. + 3 of this lane
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s.w[r][i] = (n < n1 && 16 * r < r16) ? __ldg(reinterpret_cast<const uint2*>(tile + r * 2048 + i * 128)) : make_uint2(0, 0);
+  };
+  auto load_base = [&](int n, uint4* y) {
+    const int c = n + 8 * q;
+    const bool in = p.base && n < n1 && c < p.g.N;
+    y[0] = in && ta >= 0 ? *reinterpret_cast<const uint4*>(p.base + (size_t)ta * p.ldbase + c) : zero;
+    y[1] = in && tb >= 0 ? *reinterpret_cast<const uint4*>(p.base + (size_t)tb * p.ldbase + c) : zero;
+  };
+  const int nw = n0 + warp * 32;
+  Cols b0;
+  uint4 y0[2];
+  load_b(nw, b0);
+  load_base(nw, y0);
+
+  // ---- the group's u: sums over the CTA's warps, then over the cluster
   float* part = reinterpret_cast<float*>(ls_sm);
   float* sum = part + LS_WARPS * LS_TOK * r16;
   uint16_t* u_hi = reinterpret_cast<uint16_t*>(sum + LS_TOK * r16);
@@ -222,12 +277,12 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
   for (int j = 0; j < R / 8; ++j) {
     if (8 * j < r16) {
       float* d = part + (warp * LS_TOK + g) * r16 + 8 * j + 2 * q;
-      *reinterpret_cast<float2*>(d) = make_float2(acc[j][0], acc[j][1]);
-      *reinterpret_cast<float2*>(d + 8 * r16) = make_float2(acc[j][2], acc[j][3]);
+      if (g < n_tok) *reinterpret_cast<float2*>(d) = make_float2(acc[j][0], acc[j][1]);
+      if (g + 8 < n_tok) *reinterpret_cast<float2*>(d + 8 * r16) = make_float2(acc[j][2], acc[j][3]);
     }
   }
   __syncthreads();
-  for (int i = tid; i < LS_TOK * r16; i += LS_THREADS) {
+  for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < LS_WARPS; ++w) v += part[w * LS_TOK * r16 + i];
@@ -235,7 +290,7 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
   }
   cluster_arrive();
   cluster_wait();
-  for (int i = tid; i < LS_TOK * r16; i += LS_THREADS) {
+  for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
     float v = 0.0f;
 #pragma unroll
     for (int c = 0; c < LS_C; ++c) v += ld_cluster_f32(sum + i, c);  // the same order in every CTA
@@ -246,29 +301,26 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
   __syncthreads();
   cluster_arrive();  // this CTA has read the others' sums
 
-  // ---- B u over this CTA's columns, 32 a step
-  for (int n = n0 + warp * 32; n < n1; n += LS_WARPS * 32) {
+  // ---- B u over this CTA's columns, 32 a step (rows of u past n_tok are not
+  // set; they meet no other row, and their results are not stored)
+  auto mma_b = [&](int n, const Cols& s, uint4* y) {
     float d[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[i][e] = 0.0f;
-    // MMA i takes the tile's packed rows 8 i .. 8 i + 7 of these 32 (lora_b_byte)
-    const uint8_t* tile = btiles + (size_t)(n >> 6) * r16 * 128 + ((n & 63) + g) * 16;
 #pragma unroll
-    for (int r = 0; r < R; r += 16) {
-      if (r < r16) {
-        // ranks r + 4 q .. r + 4 q + 3 of this lane
-        const uint2 ha = *reinterpret_cast<const uint2*>(u_hi + g * ur + r + 4 * q);
-        const uint2 hb = *reinterpret_cast<const uint2*>(u_hi + (g + 8) * ur + r + 4 * q);
-        const uint2 la = *reinterpret_cast<const uint2*>(u_lo + g * ur + r + 4 * q);
-        const uint2 lb = *reinterpret_cast<const uint2*>(u_lo + (g + 8) * ur + r + 4 * q);
-        const uint8_t* src = tile + (r / 8 + (q >> 1)) * 1024 + (q & 1) * 8;
+    for (int r = 0; r < R / 16; ++r) {
+      if (16 * r < r16) {
+        const int o = 16 * r + 4 * q;
+        const uint2 ha = *reinterpret_cast<const uint2*>(u_hi + g * ur + o);
+        const uint2 hb = *reinterpret_cast<const uint2*>(u_hi + (g + 8) * ur + o);
+        const uint2 la = *reinterpret_cast<const uint2*>(u_lo + g * ur + o);
+        const uint2 lb = *reinterpret_cast<const uint2*>(u_lo + (g + 8) * ur + o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + i * 128));
-          mma_16816<ACT>(d[i], ha.x, hb.x, ha.y, hb.y, w.x, w.y);
-          mma_16816<ACT>(d[i], la.x, lb.x, la.y, lb.y, w.x, w.y);
+          mma_16816<ACT>(d[i], ha.x, hb.x, ha.y, hb.y, s.w[r][i].x, s.w[r][i].y);
+          mma_16816<ACT>(d[i], la.x, lb.x, la.y, lb.y, s.w[r][i].x, s.w[r][i].y);
         }
       }
     }
@@ -278,16 +330,33 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS) lora_
       for (int half = 0; half < 2; ++half) {
         const int t = half ? tb : ta;
         if (t < 0) continue;
-        uint4 y = p.base ? *reinterpret_cast<const uint4*>(p.base + (size_t)t * p.ldbase + c)
-                         : make_uint4(0, 0, 0, 0);
-        uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+        uint32_t* yw = reinterpret_cast<uint32_t*>(&y[half]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 b = act_x2_to_f32<ACT>(yw[i]);
           yw[i] = f32_to_act_x2<ACT>(fmaf(scale, d[i][2 * half], b.x), fmaf(scale, d[i][2 * half + 1], b.y));
         }
-        *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + c) = y;
+        *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + c) = y[half];
       }
+    }
+  };
+  if constexpr (R <= 64) {
+    Cols b1;
+    uint4 y1[2];
+    for (int n = nw; n < n1; n += 2 * LS_WARPS * 32) {
+      load_b(n + LS_WARPS * 32, b1);
+      load_base(n + LS_WARPS * 32, y1);
+      mma_b(n, b0, y0);
+      if (n + LS_WARPS * 32 >= n1) break;
+      load_b(n + 2 * LS_WARPS * 32, b0);
+      load_base(n + 2 * LS_WARPS * 32, y0);
+      mma_b(n + LS_WARPS * 32, b1, y1);
+    }
+  } else {
+    for (int n = nw; n < n1; n += LS_WARPS * 32) {
+      mma_b(n, b0, y0);
+      load_b(n + LS_WARPS * 32, b0);
+      load_base(n + LS_WARPS * 32, y0);
     }
   }
   cluster_wait();  // the others have read this CTA's sums
