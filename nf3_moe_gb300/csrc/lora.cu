@@ -101,8 +101,8 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 }
 
 // ------------------------------------------------------------ small batches: one launch
-// A cluster of LS_C CTAs serves up to LS_TOK rows of one adapter: CTA c sums
-// A x over its share of K, the CTAs exchange their partial sums through
+// A cluster of C CTAs serves up to LS_TOK rows of one adapter: CTA c sums A x
+// over its share of K, the CTAs exchange their partial sums through
 // distributed shared memory, and each adds B u for its share of N. The batch
 // is grouped without a pass of its own: cluster t belongs to row t, and goes
 // on only if row t is the first of a group, that is if the number of earlier
@@ -114,11 +114,20 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 // that a lane's operand words are 16 bytes of one row. The columns of the
 // second product are permuted so that a lane ends up with 8 neighbouring ones
 // (lora_b_byte).
-constexpr int LS_C = 8;
 constexpr int LS_THREADS = 256;
 constexpr int LS_WARPS = LS_THREADS / 32;
 constexpr int LS_TOK = 16;
 constexpr int LS_MAX_T = LS_THREADS;  // the grouping looks at one row a thread
+// CTAs of a cluster: 8, so that a single row's adapter is read by many SMs,
+// while 8 T CTAs fit the GPU (two on each of 152 SMs), and up to 64 rows where
+// the adapters are large; else 4, whose clusters start and join sooner.
+// Measured, 8 against 4: 1 row of rank 64, 6144x6144: 5.9, 8.3 us; 64 rows of 64
+// such adapters: 16.8, 18.4; 64 rows of rank 16, 2048x2048: 7.1, 5.1; 128 rows of
+// 128 adapters of rank 32, 6144x6144: 22.9, 19.9; 256 rows of rank 64: 27.5, 22.7.
+inline int ls_cluster(const LoraGeom& g, int T) {
+  const long long bytes = (long long)(g.KB + g.NB) * g.max_r16 * 128;
+  return T <= 38 || (T <= 64 && bytes >= 512 << 10) ? 8 : 4;
+}
 
 __device__ __forceinline__ uint32_t ls_cluster_rank() {
   uint32_t r;
@@ -153,17 +162,17 @@ __host__ __device__ constexpr int ls_smem(int r16) {
 
 // R: the largest padded rank of the set, rounded up to 16, 32, 64 or 128.
 template <int ACT, int R>
-__global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS, R <= 64 ? 2 : 1) lora_small_kernel(LoraParams p) {
+__global__ void __launch_bounds__(LS_THREADS, R <= 64 ? 2 : 1) lora_small_kernel(LoraParams p) {
   extern __shared__ __align__(16) uint8_t ls_sm[];
   __shared__ int s_tok[LS_TOK], s_cnt[LS_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cta = (int)ls_cluster_rank();
+  const int cta = (int)ls_cluster_rank(), ctas = gridDim.x;  // one cluster a grid row
   const int t0 = blockIdx.y;
   pdl_wait();
   pdl_trigger();
   const int a = lora_slot(p, t0);
   const int rank = a >= 0 ? reinterpret_cast<const int*>(p.packed)[a] : 0;
-  const int n0 = cta * p.g.NB / LS_C * 64, n1 = min(p.g.N, (cta + 1) * p.g.NB / LS_C * 64);
+  const int n0 = cta * p.g.NB / ctas * 64, n1 = min(p.g.N, (cta + 1) * p.g.NB / ctas * 64);
   if (rank == 0) {  // base alone
     if (p.base != p.out)
       for (int n = n0 + tid * 8; n < n1; n += LS_THREADS * 8)
@@ -206,7 +215,7 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS, R <= 
   struct Step {
     uint4 xa, xb, w[R / 8];
   };
-  const int h1 = 2 * ((cta + 1) * p.g.KB / LS_C);
+  const int h1 = 2 * ((cta + 1) * p.g.KB / ctas);
   auto load_a = [&](int h, Step& s) {
     const int k = h * 32 + q * 8;
     s.xa = (h < h1 && ta >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)ta * p.ldx + k) : zero;
@@ -224,7 +233,7 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS, R <= 
       }
     }
   };
-  const int h0 = 2 * (cta * p.g.KB / LS_C) + warp;
+  const int h0 = 2 * (cta * p.g.KB / ctas) + warp;
   if constexpr (R <= 64) {
     Step s0, s1;
     load_a(h0, s0);
@@ -291,9 +300,11 @@ __global__ void __cluster_dims__(LS_C, 1, 1) __launch_bounds__(LS_THREADS, R <= 
   cluster_arrive();
   cluster_wait();
   for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
-    float v = 0.0f;
+    float f[8], v = 0.0f;
 #pragma unroll
-    for (int c = 0; c < LS_C; ++c) v += ld_cluster_f32(sum + i, c);  // the same order in every CTA
+    for (int c = 0; c < 8; ++c) f[c] = c < ctas ? ld_cluster_f32(sum + i, c) : 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v += f[c];  // the same order in every CTA
     const int row = i / r16, r = i - row * r16;
     // past the rank A's zeros met whatever x held
     split_act<ACT>(r < rank ? v : 0.0f, u_hi + row * ur + r, u_lo + row * ur + r);
@@ -367,8 +378,22 @@ static cudaError_t small_as(const LoraParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   const int smem = ls_smem(p.g.max_r16);
   cudaError_t e = ensure_smem_attr(lora_small_kernel<ACT, R>, ls_smem(R), done);
-  if (e == cudaSuccess)
-    e = launch_pdl(lora_small_kernel<ACT, R>, dim3(LS_C, (unsigned)p.T), dim3(LS_THREADS), (size_t)smem, st, p);
+  if (e == cudaSuccess) {
+    const unsigned ctas = (unsigned)ls_cluster(p.g, p.T);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (unsigned)p.T);
+    cfg.blockDim = dim3(LS_THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {ctas, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, lora_small_kernel<ACT, R>, p);
+  }
   count_launches(1);
   return e;
 }
