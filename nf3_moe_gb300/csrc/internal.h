@@ -203,6 +203,7 @@ struct LoraParams {
   const int* ids;
   int* status;
   unsigned long long wait_limit_ns;
+  int tile_rows;          // rows of a tile of the plan
   // Scratch of the larger batches (lora.cu), see LoraScratch.
   int* meta;
   int4* tiles;
@@ -215,13 +216,14 @@ struct LoraParams {
 // position, rows, rank), A x of every position (u), and the sums of the pieces
 // of tiles, two for each CTA (part). meta: tiles with an adapter, all tiles.
 constexpr int LORA_TILE_ROWS = 128;
+constexpr int LORA_MIN_TILE_ROWS = 16;  // of the plan for the small kernel
 constexpr int LORA_MAX_CTAS = 160;
 struct LoraScratch {
   size_t meta, tiles, perm, u, part, total;
 };
 inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
   auto pad = [](size_t b) { return (b + 255) / 256 * 256; };
-  const size_t most = (size_t)T / LORA_TILE_ROWS + (size_t)(T < g.slots + 1 ? T : g.slots + 1);
+  const size_t most = (size_t)T / LORA_MIN_TILE_ROWS + (size_t)(T < g.slots + 1 ? T : g.slots + 1);
   LoraScratch s;
   s.meta = 0;
   s.tiles = s.meta + 256;

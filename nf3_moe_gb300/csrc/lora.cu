@@ -118,6 +118,12 @@ constexpr int LS_THREADS = 256;
 constexpr int LS_WARPS = LS_THREADS / 32;
 constexpr int LS_TOK = 16;
 constexpr int LS_MAX_T = LS_THREADS;  // the grouping looks at one row a thread
+// Up to this many rows the small kernel serves the plan's groups of 16 rows:
+// it reads an adapter again for each group, but has fewer steps than the tile
+// kernels. Measured against them, 6144x6144, rank 64: 260 rows of 64 adapters
+// 23.9, 51.3 us; 1024 of 64: 39.3, 53.7; 1024 of 8: 24.5, 38.8; 2048 of 64: 59.7,
+// 55.6; 2048 of 8: 40.7, 35.2.
+constexpr int LS_PLANNED_MAX_T = 1536;
 // CTAs of a cluster: 8, so that a single row's adapter is read by many SMs,
 // while 8 T CTAs fit the GPU (two on each of 152 SMs), and up to 64 rows where
 // the adapters are large; else 4, whose clusters start and join sooner.
@@ -161,248 +167,269 @@ __host__ __device__ constexpr int ls_smem(int r16) {
 }
 
 // R: the largest padded rank of the set, rounded up to 16, 32, 64 or 128.
-template <int ACT, int R>
+// PLANNED: the groups come from the plan kernel's tiles of LS_TOK rows, which a
+// fixed number of clusters takes in turn.
+template <int ACT, int R, bool PLANNED>
 __global__ void __launch_bounds__(LS_THREADS, R <= 64 ? 2 : 1) lora_small_kernel(LoraParams p) {
   extern __shared__ __align__(16) uint8_t ls_sm[];
   __shared__ int s_tok[LS_TOK], s_cnt[LS_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = (int)ls_cluster_rank(), ctas = gridDim.x;  // one cluster a grid row
-  const int t0 = blockIdx.y;
   pdl_wait();
   pdl_trigger();
-  const int a = lora_slot(p, t0);
-  const int rank = a >= 0 ? reinterpret_cast<const int*>(p.packed)[a] : 0;
   const int n0 = cta * p.g.NB / ctas * 64, n1 = min(p.g.N, (cta + 1) * p.g.NB / ctas * 64);
-  if (rank == 0) {  // base alone
-    if (p.base != p.out)
-      for (int n = n0 + tid * 8; n < n1; n += LS_THREADS * 8)
-        *reinterpret_cast<uint4*>(p.out + (size_t)t0 * p.ldout + n) =
-            p.base ? *reinterpret_cast<const uint4*>(p.base + (size_t)t0 * p.ldbase + n) : make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const float scale = reinterpret_cast<const float*>(p.packed + p.g.scale_off)[a];
-  // The group: T <= LS_THREADS, so thread j looks at row j.
-  const bool same = tid < p.T && p.ids[tid] == a;
-  if (__syncthreads_count(same && tid < t0) % LS_TOK != 0) return;
-  const unsigned later = __ballot_sync(0xffffffffu, same && tid >= t0);
-  if (lane == 0) s_cnt[warp] = __popc(later);
-  if (tid < LS_TOK) s_tok[tid] = -1;
-  __syncthreads();
-  {
-    int pos = __popc(later & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) pos += s_cnt[w];
-    if (same && tid >= t0 && pos < LS_TOK) s_tok[pos] = tid;
-  }
-  __syncthreads();
-  int n_tok = 0;
+  // base alone, for row t
+  auto copy_row = [&](int t) {
+    if (p.base == p.out) return;
+    for (int n = n0 + tid * 8; n < n1; n += LS_THREADS * 8)
+      *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + n) =
+          p.base ? *reinterpret_cast<const uint4*>(p.base + (size_t)t * p.ldbase + n) : make_uint4(0, 0, 0, 0);
+  };
+  const int groups = PLANNED ? p.meta[1] : (int)blockIdx.y + 1;
+  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
+    int a, rank, n_tok;
+    if constexpr (PLANNED) {
+      const int4 ti = p.tiles[gi];
+      a = ti.x;
+      rank = ti.w;
+      n_tok = ti.z;
+      if (tid < LS_TOK) s_tok[tid] = tid < n_tok ? p.perm[ti.y + tid] : -1;
+      __syncthreads();
+      if (a < 0) {
+        for (int i = 0; i < n_tok; ++i) copy_row(s_tok[i]);
+        __syncthreads();
+        continue;
+      }
+    } else {
+      a = lora_slot(p, gi);
+      rank = a >= 0 ? reinterpret_cast<const int*>(p.packed)[a] : 0;
+      if (rank == 0) {
+        copy_row(gi);
+        return;
+      }
+      // The group: T <= LS_THREADS, so thread j looks at row j.
+      const bool same = tid < p.T && p.ids[tid] == a;
+      if (__syncthreads_count(same && tid < gi) % LS_TOK != 0) return;
+      const unsigned later = __ballot_sync(0xffffffffu, same && tid >= gi);
+      if (lane == 0) s_cnt[warp] = __popc(later);
+      if (tid < LS_TOK) s_tok[tid] = -1;
+      __syncthreads();
+      {
+        int pos = __popc(later & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) pos += s_cnt[w];
+        if (same && tid >= gi && pos < LS_TOK) s_tok[pos] = tid;
+      }
+      __syncthreads();
+      n_tok = 0;
 #pragma unroll
-  for (int w = 0; w < LS_WARPS; ++w) n_tok += s_cnt[w];
-  n_tok = min(n_tok, LS_TOK);
-  const int r16 = (rank + 15) / 16 * 16;
-  const uint8_t* block = p.packed + p.g.block_off + (size_t)a * p.g.block_bytes;
-  const uint8_t* btiles = block + p.g.b_off;
-  const int g = lane >> 2, q = lane & 3;
-  const int ta = s_tok[g], tb = s_tok[g + 8];
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+      for (int w = 0; w < LS_WARPS; ++w) n_tok += s_cnt[w];
+      n_tok = min(n_tok, LS_TOK);
+    }
+    const float scale = reinterpret_cast<const float*>(p.packed + p.g.scale_off)[a];
+    const int r16 = (rank + 15) / 16 * 16;
+    const uint8_t* block = p.packed + p.g.block_off + (size_t)a * p.g.block_bytes;
+    const uint8_t* btiles = block + p.g.b_off;
+    const int g = lane >> 2, q = lane & 3;
+    const int ta = s_tok[g], tb = s_tok[g + 8];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
 
-  // ---- A x over this CTA's k-blocks, half a block (32 of K) a step, the next
-  // step's operands on their way
-  float acc[R / 8][4];
+    // ---- A x over this CTA's k-blocks, half a block (32 of K) a step, the next
+    // step's operands on their way
+    float acc[R / 8][4];
 #pragma unroll
-  for (int j = 0; j < R / 8; ++j)
+    for (int j = 0; j < R / 8; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-  struct Step {
-    uint4 xa, xb, w[R / 8];
-  };
-  const int h1 = 2 * ((cta + 1) * p.g.KB / ctas);
-  auto load_a = [&](int h, Step& s) {
-    const int k = h * 32 + q * 8;
-    s.xa = (h < h1 && ta >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)ta * p.ldx + k) : zero;
-    s.xb = (h < h1 && tb >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)tb * p.ldx + k) : zero;
-    const uint8_t* tile = block + (size_t)(h >> 1) * r16 * 128 + g * 128 + ((((h & 1) * 4 + q) ^ g) * 16);
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    struct Step {
+      uint4 xa, xb, w[R / 8];
+    };
+    const int h1 = 2 * ((cta + 1) * p.g.KB / ctas);
+    auto load_a = [&](int h, Step& s) {
+      const int k = h * 32 + q * 8;
+      s.xa = (h < h1 && ta >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)ta * p.ldx + k) : zero;
+      s.xb = (h < h1 && tb >= 0 && k < p.g.K) ? ldg16(p.x + (size_t)tb * p.ldx + k) : zero;
+      const uint8_t* tile = block + (size_t)(h >> 1) * r16 * 128 + g * 128 + ((((h & 1) * 4 + q) ^ g) * 16);
 #pragma unroll
-    for (int j = 0; j < R / 8; ++j) s.w[j] = (h < h1 && 8 * j < r16) ? ldg16(tile + j * 1024) : zero;
-  };
-  auto mma_a = [&](const Step& s) {
+      for (int j = 0; j < R / 8; ++j) s.w[j] = (h < h1 && 8 * j < r16) ? ldg16(tile + j * 1024) : zero;
+    };
+    auto mma_a = [&](const Step& s) {
+#pragma unroll
+      for (int j = 0; j < R / 8; ++j) {
+        if (8 * j < r16) {
+          mma_16816<ACT>(acc[j], s.xa.x, s.xb.x, s.xa.y, s.xb.y, s.w[j].x, s.w[j].y);
+          mma_16816<ACT>(acc[j], s.xa.z, s.xb.z, s.xa.w, s.xb.w, s.w[j].z, s.w[j].w);
+        }
+      }
+    };
+    const int h0 = 2 * (cta * p.g.KB / ctas) + warp;
+    if constexpr (R <= 64) {
+      Step s0, s1;
+      load_a(h0, s0);
+      for (int h = h0; h < h1; h += 2 * LS_WARPS) {
+        load_a(h + LS_WARPS, s1);
+        mma_a(s0);
+        load_a(h + 2 * LS_WARPS, s0);
+        mma_a(s1);
+      }
+    } else {
+      for (int h = h0; h < h1; h += LS_WARPS) {
+        Step s0;
+        load_a(h, s0);
+        mma_a(s0);
+      }
+    }
+
+    // ---- B's operands for the first 32 columns: they do not wait for u
+    // MMA i takes the tile's packed rows 8 i .. 8 i + 7 of these 32 (lora_b_byte)
+    struct Cols {
+      uint2 w[R / 16][4];
+    };
+    auto load_b = [&](int n, Cols& s) {
+      const uint8_t* tile = btiles + (size_t)(n >> 6) * r16 * 128 + ((n & 63) + g) * 16 + (q >> 1) * 1024 + (q & 1) * 8;
+#pragma unroll
+      for (int r = 0; r < R / 16; ++r)  // ranks 16 r + 4 q .. + 3 of this lane
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s.w[r][i] = (n < n1 && 16 * r < r16) ? __ldg(reinterpret_cast<const uint2*>(tile + r * 2048 + i * 128)) : make_uint2(0, 0);
+    };
+    auto load_base = [&](int n, uint4* y) {
+      const int c = n + 8 * q;
+      const bool in = p.base && n < n1 && c < p.g.N;
+      y[0] = in && ta >= 0 ? *reinterpret_cast<const uint4*>(p.base + (size_t)ta * p.ldbase + c) : zero;
+      y[1] = in && tb >= 0 ? *reinterpret_cast<const uint4*>(p.base + (size_t)tb * p.ldbase + c) : zero;
+    };
+    const int nw = n0 + warp * 32;
+    Cols b0;
+    uint4 y0[2];
+    load_b(nw, b0);
+    load_base(nw, y0);
+
+    // ---- the group's u: sums over the CTA's warps, then over the cluster
+    float* part = reinterpret_cast<float*>(ls_sm);
+    float* sum = part + LS_WARPS * LS_TOK * r16;
+    uint16_t* u_hi = reinterpret_cast<uint16_t*>(sum + LS_TOK * r16);
+    const int ur = r16 + 8;  // row stride of u: 16-byte rows in different banks
+    uint16_t* u_lo = u_hi + LS_TOK * ur;
 #pragma unroll
     for (int j = 0; j < R / 8; ++j) {
       if (8 * j < r16) {
-        mma_16816<ACT>(acc[j], s.xa.x, s.xb.x, s.xa.y, s.xb.y, s.w[j].x, s.w[j].y);
-        mma_16816<ACT>(acc[j], s.xa.z, s.xb.z, s.xa.w, s.xb.w, s.w[j].z, s.w[j].w);
+        float* d = part + (warp * LS_TOK + g) * r16 + 8 * j + 2 * q;
+        if (g < n_tok) *reinterpret_cast<float2*>(d) = make_float2(acc[j][0], acc[j][1]);
+        if (g + 8 < n_tok) *reinterpret_cast<float2*>(d + 8 * r16) = make_float2(acc[j][2], acc[j][3]);
       }
     }
-  };
-  const int h0 = 2 * (cta * p.g.KB / ctas) + warp;
-  if constexpr (R <= 64) {
-    Step s0, s1;
-    load_a(h0, s0);
-    for (int h = h0; h < h1; h += 2 * LS_WARPS) {
-      load_a(h + LS_WARPS, s1);
-      mma_a(s0);
-      load_a(h + 2 * LS_WARPS, s0);
-      mma_a(s1);
-    }
-  } else {
-    for (int h = h0; h < h1; h += LS_WARPS) {
-      Step s0;
-      load_a(h, s0);
-      mma_a(s0);
-    }
-  }
-
-  // ---- B's operands for the first 32 columns: they do not wait for u
-  // MMA i takes the tile's packed rows 8 i .. 8 i + 7 of these 32 (lora_b_byte)
-  struct Cols {
-    uint2 w[R / 16][4];
-  };
-  auto load_b = [&](int n, Cols& s) {
-    const uint8_t* tile = btiles + (size_t)(n >> 6) * r16 * 128 + ((n & 63) + g) * 16 + (q >> 1) * 1024 + (q & 1) * 8;
+    __syncthreads();
+    for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
+      float v = 0.0f;
 #pragma unroll
-    for (int r = 0; r < R / 16; ++r)  // ranks 16 r + 4 q .. + 3 of this lane
+      for (int w = 0; w < LS_WARPS; ++w) v += part[w * LS_TOK * r16 + i];
+      sum[i] = v;
+    }
+    cluster_arrive();
+    cluster_wait();
+    for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
+      float f[8], v = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[c] = c < ctas ? ld_cluster_f32(sum + i, c) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v += f[c];  // the same order in every CTA
+      const int row = i / r16, r = i - row * r16;
+      // past the rank A's zeros met whatever x held
+      split_act<ACT>(r < rank ? v : 0.0f, u_hi + row * ur + r, u_lo + row * ur + r);
+    }
+    __syncthreads();
+    cluster_arrive();  // this CTA has read the others' sums
+
+    // ---- B u over this CTA's columns, 32 a step (rows of u past n_tok are not
+    // set; they meet no other row, and their results are not stored)
+    auto mma_b = [&](int n, const Cols& s, uint4* y) {
+      float d[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        s.w[r][i] = (n < n1 && 16 * r < r16) ? __ldg(reinterpret_cast<const uint2*>(tile + r * 2048 + i * 128)) : make_uint2(0, 0);
-  };
-  auto load_base = [&](int n, uint4* y) {
-    const int c = n + 8 * q;
-    const bool in = p.base && n < n1 && c < p.g.N;
-    y[0] = in && ta >= 0 ? *reinterpret_cast<const uint4*>(p.base + (size_t)ta * p.ldbase + c) : zero;
-    y[1] = in && tb >= 0 ? *reinterpret_cast<const uint4*>(p.base + (size_t)tb * p.ldbase + c) : zero;
-  };
-  const int nw = n0 + warp * 32;
-  Cols b0;
-  uint4 y0[2];
-  load_b(nw, b0);
-  load_base(nw, y0);
-
-  // ---- the group's u: sums over the CTA's warps, then over the cluster
-  float* part = reinterpret_cast<float*>(ls_sm);
-  float* sum = part + LS_WARPS * LS_TOK * r16;
-  uint16_t* u_hi = reinterpret_cast<uint16_t*>(sum + LS_TOK * r16);
-  const int ur = r16 + 8;  // row stride of u: 16-byte rows in different banks
-  uint16_t* u_lo = u_hi + LS_TOK * ur;
 #pragma unroll
-  for (int j = 0; j < R / 8; ++j) {
-    if (8 * j < r16) {
-      float* d = part + (warp * LS_TOK + g) * r16 + 8 * j + 2 * q;
-      if (g < n_tok) *reinterpret_cast<float2*>(d) = make_float2(acc[j][0], acc[j][1]);
-      if (g + 8 < n_tok) *reinterpret_cast<float2*>(d + 8 * r16) = make_float2(acc[j][2], acc[j][3]);
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
-    float v = 0.0f;
+        for (int e = 0; e < 4; ++e) d[i][e] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < LS_WARPS; ++w) v += part[w * LS_TOK * r16 + i];
-    sum[i] = v;
-  }
-  cluster_arrive();
-  cluster_wait();
-  for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
-    float f[8], v = 0.0f;
+      for (int r = 0; r < R / 16; ++r) {
+        if (16 * r < r16) {
+          const int o = 16 * r + 4 * q;
+          const uint2 ha = *reinterpret_cast<const uint2*>(u_hi + g * ur + o);
+          const uint2 hb = *reinterpret_cast<const uint2*>(u_hi + (g + 8) * ur + o);
+          const uint2 la = *reinterpret_cast<const uint2*>(u_lo + g * ur + o);
+          const uint2 lb = *reinterpret_cast<const uint2*>(u_lo + (g + 8) * ur + o);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) f[c] = c < ctas ? ld_cluster_f32(sum + i, c) : 0.0f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) v += f[c];  // the same order in every CTA
-    const int row = i / r16, r = i - row * r16;
-    // past the rank A's zeros met whatever x held
-    split_act<ACT>(r < rank ? v : 0.0f, u_hi + row * ur + r, u_lo + row * ur + r);
-  }
-  __syncthreads();
-  cluster_arrive();  // this CTA has read the others' sums
-
-  // ---- B u over this CTA's columns, 32 a step (rows of u past n_tok are not
-  // set; they meet no other row, and their results are not stored)
-  auto mma_b = [&](int n, const Cols& s, uint4* y) {
-    float d[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[i][e] = 0.0f;
-#pragma unroll
-    for (int r = 0; r < R / 16; ++r) {
-      if (16 * r < r16) {
-        const int o = 16 * r + 4 * q;
-        const uint2 ha = *reinterpret_cast<const uint2*>(u_hi + g * ur + o);
-        const uint2 hb = *reinterpret_cast<const uint2*>(u_hi + (g + 8) * ur + o);
-        const uint2 la = *reinterpret_cast<const uint2*>(u_lo + g * ur + o);
-        const uint2 lb = *reinterpret_cast<const uint2*>(u_lo + (g + 8) * ur + o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mma_16816<ACT>(d[i], ha.x, hb.x, ha.y, hb.y, s.w[r][i].x, s.w[r][i].y);
-          mma_16816<ACT>(d[i], la.x, lb.x, la.y, lb.y, s.w[r][i].x, s.w[r][i].y);
+          for (int i = 0; i < 4; ++i) {
+            mma_16816<ACT>(d[i], ha.x, hb.x, ha.y, hb.y, s.w[r][i].x, s.w[r][i].y);
+            mma_16816<ACT>(d[i], la.x, lb.x, la.y, lb.y, s.w[r][i].x, s.w[r][i].y);
+          }
         }
       }
-    }
-    const int c = n + 8 * q;
-    if (c < p.g.N) {
+      const int c = n + 8 * q;
+      if (c < p.g.N) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int t = half ? tb : ta;
-        if (t < 0) continue;
-        uint32_t* yw = reinterpret_cast<uint32_t*>(&y[half]);
+        for (int half = 0; half < 2; ++half) {
+          const int t = half ? tb : ta;
+          if (t < 0) continue;
+          uint32_t* yw = reinterpret_cast<uint32_t*>(&y[half]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 b = act_x2_to_f32<ACT>(yw[i]);
-          yw[i] = f32_to_act_x2<ACT>(fmaf(scale, d[i][2 * half], b.x), fmaf(scale, d[i][2 * half + 1], b.y));
+          for (int i = 0; i < 4; ++i) {
+            const float2 b = act_x2_to_f32<ACT>(yw[i]);
+            yw[i] = f32_to_act_x2<ACT>(fmaf(scale, d[i][2 * half], b.x), fmaf(scale, d[i][2 * half + 1], b.y));
+          }
+          *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + c) = y[half];
         }
-        *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + c) = y[half];
+      }
+    };
+    if constexpr (R <= 64) {
+      Cols b1;
+      uint4 y1[2];
+      for (int n = nw; n < n1; n += 2 * LS_WARPS * 32) {
+        load_b(n + LS_WARPS * 32, b1);
+        load_base(n + LS_WARPS * 32, y1);
+        mma_b(n, b0, y0);
+        if (n + LS_WARPS * 32 >= n1) break;
+        load_b(n + 2 * LS_WARPS * 32, b0);
+        load_base(n + 2 * LS_WARPS * 32, y0);
+        mma_b(n + LS_WARPS * 32, b1, y1);
+      }
+    } else {
+      for (int n = nw; n < n1; n += LS_WARPS * 32) {
+        mma_b(n, b0, y0);
+        load_b(n + LS_WARPS * 32, b0);
+        load_base(n + LS_WARPS * 32, y0);
       }
     }
-  };
-  if constexpr (R <= 64) {
-    Cols b1;
-    uint4 y1[2];
-    for (int n = nw; n < n1; n += 2 * LS_WARPS * 32) {
-      load_b(n + LS_WARPS * 32, b1);
-      load_base(n + LS_WARPS * 32, y1);
-      mma_b(n, b0, y0);
-      if (n + LS_WARPS * 32 >= n1) break;
-      load_b(n + 2 * LS_WARPS * 32, b0);
-      load_base(n + 2 * LS_WARPS * 32, y0);
-      mma_b(n + LS_WARPS * 32, b1, y1);
-    }
-  } else {
-    for (int n = nw; n < n1; n += LS_WARPS * 32) {
-      mma_b(n, b0, y0);
-      load_b(n + LS_WARPS * 32, b0);
-      load_base(n + LS_WARPS * 32, y0);
-    }
+    cluster_wait();  // the others have read this CTA's sums
   }
-  cluster_wait();  // the others have read this CTA's sums
 }
 
-template <int ACT, int R>
-static cudaError_t small_as(const LoraParams& p, cudaStream_t st) {
+// rows: grid rows, each a cluster; PLANNED: the groups are in the plan.
+template <int ACT, int R, bool PLANNED>
+static cudaError_t small_as(const LoraParams& p, unsigned rows, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const int smem = ls_smem(p.g.max_r16);
-  cudaError_t e = ensure_smem_attr(lora_small_kernel<ACT, R>, ls_smem(R), done);
-  if (e == cudaSuccess) {
-    const unsigned ctas = (unsigned)ls_cluster(p.g, p.T);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, (unsigned)p.T);
-    cfg.blockDim = dim3(LS_THREADS);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {ctas, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, lora_small_kernel<ACT, R>, p);
-  }
+  cudaError_t e = ensure_smem_attr(lora_small_kernel<ACT, R, PLANNED>, ls_smem(R), done);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = (unsigned)ls_cluster(p.g, p.T);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, rows);
+  cfg.blockDim = dim3(LS_THREADS);
+  cfg.dynamicSmemBytes = (size_t)ls_smem(p.g.max_r16);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {ctas, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   count_launches(1);
-  return e;
+  return cudaLaunchKernelEx(&cfg, lora_small_kernel<ACT, R, PLANNED>, p);
 }
-template <int ACT>
-static cudaError_t small_of(const LoraParams& p, cudaStream_t st) {
-  if (p.g.max_r16 <= 16) return small_as<ACT, 16>(p, st);
-  if (p.g.max_r16 <= 32) return small_as<ACT, 32>(p, st);
-  if (p.g.max_r16 <= 64) return small_as<ACT, 64>(p, st);
-  return small_as<ACT, 128>(p, st);
+template <int ACT, bool PLANNED>
+static cudaError_t small_of(const LoraParams& p, unsigned rows, cudaStream_t st) {
+  if (p.g.max_r16 <= 16) return small_as<ACT, 16, PLANNED>(p, rows, st);
+  if (p.g.max_r16 <= 32) return small_as<ACT, 32, PLANNED>(p, rows, st);
+  if (p.g.max_r16 <= 64) return small_as<ACT, 64, PLANNED>(p, rows, st);
+  return small_as<ACT, 128, PLANNED>(p, rows, st);
 }
 
 // ------------------------------------------------------------ larger batches: plan, A x, B u
@@ -485,7 +512,7 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
   }
   __syncthreads();
   // Exclusive scans of the groups' rows and tiles.
-  const int n = tid < G ? s_n[tid] : 0, nt = (n + LORA_TILE_ROWS - 1) / LORA_TILE_ROWS;
+  const int n = tid < G ? s_n[tid] : 0, nt = (n + p.tile_rows - 1) / p.tile_rows;
   int in = n, it = nt;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -524,8 +551,8 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
       if (s_tile[mid] <= j) lo = mid;
       else hi = mid - 1;
     }
-    const int first = s_n[lo] + (j - s_tile[lo]) * LORA_TILE_ROWS, end = lo < G - 1 ? s_n[lo + 1] : p.T;
-    p.tiles[j] = make_int4(lo < G - 1 ? lo : -1, first, min(LORA_TILE_ROWS, end - first), s_rank[lo]);
+    const int first = s_n[lo] + (j - s_tile[lo]) * p.tile_rows, end = lo < G - 1 ? s_n[lo + 1] : p.T;
+    p.tiles[j] = make_int4(lo < G - 1 ? lo : -1, first, min(p.tile_rows, end - first), s_rank[lo]);
   }
 #pragma unroll 2
   for (int r = 0; r < rounds; ++r) {
@@ -1170,25 +1197,44 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
   }
 }
 
+static cudaError_t launch_plan(LoraParams& p, int tile_rows, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  p.tile_rows = tile_rows;
+  cudaError_t e = ensure_smem_attr(lora_plan_kernel, lp_smem(LORA_MAX_SLOTS), done);
+  if (e == cudaSuccess)
+    e = launch_pdl(lora_plan_kernel, dim3(1), dim3(LP_THREADS), (size_t)lp_smem(p.g.slots), st, p);
+  count_launches(1);
+  return e;
+}
+
 template <int ACT>
-static cudaError_t tiled_of(const LoraParams& p, int num_sms, cudaStream_t st) {
-  static std::atomic<unsigned long long> done_p{0}, done_a{0}, done_b{0};
+static cudaError_t tiled_of(LoraParams p, int num_sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> done_a{0}, done_b{0};
   const int sa = la_smem(p.g.max_r16), sb = lb_smem(p.g.max_r16);
   const dim3 grid((unsigned)(num_sms < LORA_MAX_CTAS ? num_sms : LORA_MAX_CTAS));
-  cudaError_t e = ensure_smem_attr(lora_plan_kernel, lp_smem(LORA_MAX_SLOTS), done_p);
-  if (e == cudaSuccess) e = ensure_smem_attr(lora_shrink_kernel<ACT>, LT_SMEM + 1024, done_a);
+  cudaError_t e = ensure_smem_attr(lora_shrink_kernel<ACT>, LT_SMEM + 1024, done_a);
   if (e == cudaSuccess) e = ensure_smem_attr(lora_expand_kernel<ACT>, LT_SMEM + 1024, done_b);
-  if (e == cudaSuccess) e = launch_pdl(lora_plan_kernel, dim3(1), dim3(LP_THREADS), (size_t)lp_smem(p.g.slots), st, p);
+  if (e == cudaSuccess) e = launch_plan(p, LORA_TILE_ROWS, st);
   if (e == cudaSuccess) e = launch_pdl(lora_shrink_kernel<ACT>, grid, dim3(LA_THREADS), (size_t)sa, st, p);
   if (e == cudaSuccess) e = launch_pdl(lora_expand_kernel<ACT>, grid, dim3(LB_THREADS), (size_t)sb, st, p);
-  count_launches(3);
+  count_launches(2);
   return e;
+}
+
+template <int ACT>
+static cudaError_t forward_of(LoraParams p, int num_sms, cudaStream_t st) {
+  if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, (unsigned)p.T, st);
+  if (p.T <= LS_PLANNED_MAX_T) {
+    const cudaError_t e = launch_plan(p, LS_TOK, st);
+    // two CTAs an SM, in clusters of 4
+    return e == cudaSuccess ? small_of<ACT, true>(p, (unsigned)(2 * num_sms / ls_cluster(p.g, p.T)), st) : e;
+  }
+  return tiled_of<ACT>(p, num_sms, st);
 }
 
 cudaError_t launch_lora_forward(const LoraParams& p, int num_sms, cudaStream_t st) {
   if (p.T == 0) return cudaSuccess;
-  if (p.T <= LS_MAX_T) return p.act_type == ACT_F16 ? small_of<ACT_F16>(p, st) : small_of<ACT_BF16>(p, st);
-  return p.act_type == ACT_F16 ? tiled_of<ACT_F16>(p, num_sms, st) : tiled_of<ACT_BF16>(p, num_sms, st);
+  return p.act_type == ACT_F16 ? forward_of<ACT_F16>(p, num_sms, st) : forward_of<ACT_BF16>(p, num_sms, st);
 }
 
 }  // namespace hmoe
