@@ -1086,7 +1086,9 @@ hmoe_status hmoe_dispatch_backward(const hmoe_dispatch_desc* desc, const void* d
   p.slot_row = slot_row;
   p.dgates = dgates;
   p.dlogits = dlogits;
-  cudaError_t e = launch_collect(p, (cudaStream_t)stream);
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HMOE_OK) return s;
+  cudaError_t e = launch_collect(p, sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "dispatch gradient launch");
   return HMOE_OK;
 }
@@ -1107,7 +1109,9 @@ hmoe_status hmoe_combine(const hmoe_dispatch_desc* desc, const void* rows, int T
   p.out = out;
   p.gates = gates;
   p.slot_row = slot_row;
-  cudaError_t e = launch_collect(p, (cudaStream_t)stream);
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HMOE_OK) return s;
+  cudaError_t e = launch_collect(p, sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   return HMOE_OK;
 }

@@ -64,6 +64,15 @@ struct Piece {
     if constexpr (VEC) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
     else *p = v[0];
   }
+  // For rows that pass through once: they leave L2 before what is kept.
+  __device__ __forceinline__ void load_once(const E* p) {
+    if constexpr (VEC) *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(p));
+    else v[0] = __ldcs(p);
+  }
+  __device__ __forceinline__ void store_once(E* p) const {
+    if constexpr (VEC) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(v));
+    else __stcs(p, v[0]);
+  }
   __device__ __forceinline__ float f(int i) const { return to_f32<DT>(v[i]); }
   __device__ __forceinline__ void set(int i, float x) { v[i] = from_f32<DT>(x); }
 };
@@ -166,8 +175,8 @@ cudaError_t launch_dispatch_plan(const int* perm, const int* offsets, int S, int
 }
 
 // ------------------------------------------------------------ the gates' gradient of one token
-// dg: the token's topk dot products, in shared memory. Called by all threads
-// of a group of nthreads; no barrier inside.
+// dg: the token's topk dot products, in shared memory. Called by nthreads
+// threads; no barrier inside.
 __device__ __forceinline__ void write_gate_grads(const float* dg, const float* gates, const int* ids, int t, int k,
                                                  int E, float* dgates, float* dlogits, int tid, int nthreads,
                                                  int* status) {
@@ -187,107 +196,144 @@ __device__ __forceinline__ void write_gate_grads(const float* dg, const float* g
   }
 }
 
-// ------------------------------------------------------------ spread: tokens to rows
-// One warp per slot and column part: rows[slot_row[s]] = (g[s]) v[s / topk], and
-// with DOT dg[s] = <v[s / topk], other[slot_row[s]]>. The CTA holds whole
-// tokens (tokens_per_cta * topk warps), so the second to last warp of a token
-// find its row in L1, and the token's gate gradients are complete after one
-// barrier. The last pad_ctas CTAs write zeros to the rows without a slot.
-template <int DT, bool VEC, bool DOT>
-__global__ void __launch_bounds__(1024) spread_kernel(RowsParams p) {
-  using P = Piece<DT, VEC>;
-  using E = typename P::E;
-  __shared__ float s_dg[32];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int k = p.topk;
-  const int cols = p.H / P::N;
-  E* rows = static_cast<E*>(p.rows_out);
-  if ((int)blockIdx.x >= p.token_ctas) {
-    const int nw = blockDim.x >> 5;
-    const int pads = gridDim.x - p.token_ctas;
-    P zero;
-#pragma unroll
-    for (int i = 0; i < P::N; ++i) zero.set(i, 0.0f);
-    for (long long r = (long long)(blockIdx.x - p.token_ctas) * nw + warp; r < p.R; r += (long long)pads * nw) {
-      const int s = p.row_slot[r];
-      if (s >= 0 && s < p.T * k) continue;
-      if (blockIdx.y != 0) continue;
-      for (int c = lane; c < cols; c += 32) zero.store(rows + (size_t)r * p.H + (size_t)c * P::N);
-    }
-    return;
-  }
-  const int w_tok = warp / k, j = warp - w_tok * k;
-  const int t = blockIdx.x * p.tokens_per_cta + w_tok;
-  const bool live = w_tok < p.tokens_per_cta && t < p.T;
-  float dot = 0.0f;
-  if (live) {
-    const size_t s = (size_t)t * k + j;
-    const int r = p.slot_row[s];
+// ------------------------------------------------------------ one token a CTA
+// The columns of a token are dealt to the threads (and to the grid's y where no
+// dot products need them together), 16 bytes each. A thread meets the token's
+// topk rows at its columns, so each value of the token is read or written once
+// and the rows' accesses are in flight together.
+constexpr int ROWS_THREADS = 256;
+
+// The rows and weights of token t's slots, in shared memory (a barrier follows).
+__device__ __forceinline__ void token_slots(const RowsParams& p, int t, int* s_row, float* s_g) {
+  const int j = threadIdx.x;
+  if (j < p.topk) {
+    int r = p.slot_row[(size_t)t * p.topk + j];
     if (r >= p.R) {
-      if (lane == 0) set_status(p.status, DEV_BAD_ROUTE);
-    } else if (r >= 0) {
-      const E* v = static_cast<const E*>(p.v) + (size_t)t * p.H;
-      E* dst = rows + (size_t)r * p.H;
-      const E* other = DOT ? static_cast<const E*>(p.other) + (size_t)r * p.H : nullptr;
-      const float g = p.gates ? p.gates[s] : 1.0f;
-      const int step = 32 * gridDim.y;
-#pragma unroll 4
-      for (int c = blockIdx.y * 32 + lane; c < cols; c += step) {
-        P a, b;
-        a.load(v + (size_t)c * P::N);
-        if constexpr (DOT) {
-          b.load(other + (size_t)c * P::N);
-#pragma unroll
-          for (int i = 0; i < P::N; ++i) dot = fmaf(a.f(i), b.f(i), dot);
-        }
-        if (p.gates) {
-#pragma unroll
-          for (int i = 0; i < P::N; ++i) a.set(i, g * a.f(i));
-        }
-        a.store(dst + (size_t)c * P::N);
-      }
+      set_status(p.status, DEV_BAD_ROUTE);
+      r = -1;
     }
-  }
-  if constexpr (DOT) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if (lane == 0) s_dg[warp] = dot;
-    __syncthreads();
-    if (live)
-      write_gate_grads(s_dg + w_tok * k, p.gates, p.ids, t, k, p.E, p.dgates, p.dlogits, j * 32 + lane, k * 32,
-                       p.status);
+    s_row[j] = r;
+    s_g[j] = p.gates ? p.gates[(size_t)t * p.topk + j] : 1.0f;
   }
 }
 
-// ------------------------------------------------------------ collect: rows to tokens
-// One CTA per token (and column part): out[t] = sum_j (g[t,j]) rows[slot_row[t,j]],
-// ascending j, and with KDOT > 0 (at least topk) dg[t,j] = <rows[slot_row[t,j]], v[t]>.
-constexpr int COLLECT_THREADS = 256;
+// The token's dot products from the threads' parts, then its gate gradients.
+template <int KD>
+__device__ __forceinline__ void token_dots(const RowsParams& p, int t, const float* dot, float (*s_part)[ROWS_THREADS / 32],
+                                           float* s_dg) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int j = 0; j < KD; ++j) {
+    float d = dot[j];
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+    if (lane == 0) s_part[j][warp] = d;
+  }
+  __syncthreads();
+  if (tid < p.topk) {
+    float d = 0.0f;
+    for (int w = 0; w < ROWS_THREADS / 32; ++w) d += s_part[tid][w];
+    s_dg[tid] = d;
+  }
+  __syncthreads();
+  write_gate_grads(s_dg, p.gates, p.ids, t, p.topk, p.E, p.dgates, p.dlogits, tid, ROWS_THREADS, p.status);
+}
+
+// spread: rows[slot_row[t,j]] = (g[t,j]) v[t], and with KDOT > 0 (at least topk)
+// dg[t,j] = <v[t], other[slot_row[t,j]]>. The CTAs past the tokens write zeros
+// to the rows without a slot.
 template <int DT, bool VEC, int KDOT>
-__global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(RowsParams p) {
+__global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
   using P = Piece<DT, VEC>;
   using E = typename P::E;
   constexpr int KD = KDOT > 0 ? KDOT : 1;
   __shared__ int s_row[MAX_TOPK];
   __shared__ float s_g[MAX_TOPK];
-  __shared__ float s_part[KD][COLLECT_THREADS / 32];
+  __shared__ float s_part[KD][ROWS_THREADS / 32];
   __shared__ float s_dg[KD];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int k = p.topk, t = blockIdx.x;
-  const int cols = p.H / P::N;
-  if (tid < k) {
-    int r = p.slot_row[(size_t)t * k + tid];
-    if (r >= p.R) {
-      set_status(p.status, DEV_BAD_ROUTE);
-      r = -1;
+  const int cols = p.H / P::N, step = ROWS_THREADS * gridDim.y;
+  E* rows = static_cast<E*>(p.rows_out);
+  if (t >= p.T) {
+    P zero;
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) zero.set(i, 0.0f);
+    const long long nw = (long long)(gridDim.x - p.T) * gridDim.y * (ROWS_THREADS / 32);
+    for (long long r = ((long long)(t - p.T) * gridDim.y + blockIdx.y) * (ROWS_THREADS / 32) + warp; r < p.R; r += nw) {
+      const int s = p.row_slot[r];
+      if (s >= 0 && s < p.T * k) continue;
+      for (int c = lane; c < cols; c += 32) zero.store_once(rows + (size_t)r * p.H + (size_t)c * P::N);
     }
-    s_row[tid] = r;
-    s_g[tid] = p.gates ? p.gates[(size_t)t * k + tid] : 1.0f;
+    return;
   }
+  token_slots(p, t, s_row, s_g);
+  __syncthreads();
+  const E* v = static_cast<const E*>(p.v) + (size_t)t * p.H;
+  const E* other = static_cast<const E*>(p.other);
+  float dot[KD];
+#pragma unroll
+  for (int j = 0; j < KD; ++j) dot[j] = 0.0f;
+  for (int c = blockIdx.y * ROWS_THREADS + tid; c < cols; c += step) {
+    P a;
+    a.load(v + (size_t)c * P::N);
+    if constexpr (KDOT > 0) {
+      P b[KDOT <= 8 ? KDOT : 1];
+      if constexpr (KDOT <= 8) {
+#pragma unroll
+        for (int j = 0; j < KDOT; ++j)
+          if (j < k && s_row[j] >= 0) b[j].load_once(other + (size_t)s_row[j] * p.H + (size_t)c * P::N);
+      }
+#pragma unroll
+      for (int j = 0; j < KDOT; ++j) {
+        if (j >= k || s_row[j] < 0) continue;
+        const size_t at = (size_t)s_row[j] * p.H + (size_t)c * P::N;
+        if constexpr (KDOT > 8) b[0].load_once(other + at);
+        const float g = s_g[j];
+        P o;
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) {
+          dot[j] = fmaf(a.f(i), b[KDOT <= 8 ? j : 0].f(i), dot[j]);
+          o.set(i, g * a.f(i));
+        }
+        o.store_once(rows + at);
+      }
+    } else {
+#pragma unroll 8
+      for (int j = 0; j < k; ++j) {
+        const int r = s_row[j];
+        if (r < 0) continue;
+        P o = a;
+        if (p.gates) {
+#pragma unroll
+          for (int i = 0; i < P::N; ++i) o.set(i, s_g[j] * a.f(i));
+        }
+        o.store_once(rows + (size_t)r * p.H + (size_t)c * P::N);
+      }
+    }
+  }
+  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg);
+}
+
+// collect: out[t] = sum_j (g[t,j]) rows[slot_row[t,j]], ascending j, and with
+// KDOT > 0 (at least topk) dg[t,j] = <rows[slot_row[t,j]], v[t]>.
+template <int DT, bool VEC, int KDOT>
+__global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
+  using P = Piece<DT, VEC>;
+  using E = typename P::E;
+  constexpr int KD = KDOT > 0 ? KDOT : 1;
+  __shared__ int s_row[MAX_TOPK];
+  __shared__ float s_g[MAX_TOPK];
+  __shared__ float s_part[KD][ROWS_THREADS / 32];
+  __shared__ float s_dg[KD];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int k = p.topk, t = blockIdx.x;
+  const int cols = p.H / P::N;
+  token_slots(p, t, s_row, s_g);
   __syncthreads();
   const E* rows = static_cast<const E*>(p.rows_in);
   E* out = static_cast<E*>(p.out) + (size_t)t * p.H;
@@ -295,25 +341,23 @@ __global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(RowsParams p) 
   float dot[KD];
 #pragma unroll
   for (int j = 0; j < KD; ++j) dot[j] = 0.0f;
-  for (int c = blockIdx.y * COLLECT_THREADS + tid; c < cols; c += COLLECT_THREADS * gridDim.y) {
-    float acc[P::N], vv[P::N];
+  for (int c = blockIdx.y * ROWS_THREADS + tid; c < cols; c += ROWS_THREADS * gridDim.y) {
+    float acc[P::N];
 #pragma unroll
     for (int i = 0; i < P::N; ++i) acc[i] = 0.0f;
     if constexpr (KDOT > 0) {
       P a;
       a.load(v + (size_t)c * P::N);
 #pragma unroll
-      for (int i = 0; i < P::N; ++i) vv[i] = a.f(i);
-#pragma unroll
       for (int j = 0; j < KDOT; ++j) {
         if (j >= k || s_row[j] < 0) continue;
         P b;
-        b.load(rows + (size_t)s_row[j] * p.H + (size_t)c * P::N);
+        b.load_once(rows + (size_t)s_row[j] * p.H + (size_t)c * P::N);
         const float g = s_g[j];
 #pragma unroll
         for (int i = 0; i < P::N; ++i) {
           acc[i] = fmaf(g, b.f(i), acc[i]);
-          dot[j] = fmaf(vv[i], b.f(i), dot[j]);
+          dot[j] = fmaf(a.f(i), b.f(i), dot[j]);
         }
       }
     } else {
@@ -322,7 +366,7 @@ __global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(RowsParams p) 
         const int r = s_row[j];
         if (r < 0) continue;
         P b;
-        b.load(rows + (size_t)r * p.H + (size_t)c * P::N);
+        b.load_once(rows + (size_t)r * p.H + (size_t)c * P::N);
         const float g = s_g[j];
 #pragma unroll
         for (int i = 0; i < P::N; ++i) acc[i] = fmaf(g, b.f(i), acc[i]);
@@ -333,23 +377,7 @@ __global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(RowsParams p) 
     for (int i = 0; i < P::N; ++i) o.set(i, acc[i]);
     o.store(out + (size_t)c * P::N);
   }
-  if constexpr (KDOT > 0) {
-#pragma unroll
-    for (int j = 0; j < KDOT; ++j) {
-      float d = dot[j];
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-      if (lane == 0) s_part[j][warp] = d;
-    }
-    __syncthreads();
-    if (tid < k) {
-      float d = 0.0f;
-      for (int w = 0; w < COLLECT_THREADS / 32; ++w) d += s_part[tid][w];
-      s_dg[tid] = d;
-    }
-    __syncthreads();
-    write_gate_grads(s_dg, p.gates, p.ids, t, k, p.E, p.dgates, p.dlogits, tid, COLLECT_THREADS, p.status);
-  }
+  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg);
 }
 
 // ------------------------------------------------------------ launchers
@@ -360,42 +388,47 @@ static bool rows_vectorised(const RowsParams& p) {
   return ((size_t)p.H * es) % 16 == 0 && all % 16 == 0;
 }
 
-template <int DT, bool VEC>
-static cudaError_t spread_as(const RowsParams& p, dim3 grid, dim3 block, cudaStream_t st) {
-  return p.other ? launch_pdl(spread_kernel<DT, VEC, true>, grid, block, 0, st, p)
-                 : launch_pdl(spread_kernel<DT, VEC, false>, grid, block, 0, st, p);
+// Column parts of a token: enough CTAs for every SM where the batch is small
+// (8 tokens of 6144 columns of 16 bits: 3 parts), one where dot products need
+// the whole token or the tokens are many.
+static unsigned column_parts(const RowsParams& p, bool vec, bool dots, int num_sms) {
+  const int n = vec ? 16 / (p.row_dtype == ROW_F32 ? 4 : 2) : 1;
+  const int parts = (p.H / n + ROWS_THREADS - 1) / ROWS_THREADS;
+  if (dots || p.T >= 4 * num_sms) return 1;
+  return (unsigned)(parts < 1 ? 1 : (parts < 65535 ? parts : 65535));
 }
-cudaError_t launch_spread(RowsParams p, int num_sms, cudaStream_t st) {
-  // At most 8 warps of whole tokens a CTA, one token where it has more slots.
-  p.tokens_per_cta = p.topk >= 8 ? 1 : 8 / p.topk;
-  p.token_ctas = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
-  const dim3 block(32 * p.topk * p.tokens_per_cta);
-  const int pads = p.has_pads ? (p.R < num_sms * 8 ? p.R : num_sms * 8) : 0;
-  const dim3 grid((unsigned)(p.token_ctas + pads), 1);
-  if (grid.x == 0) return cudaSuccess;
+
+template <int DT, bool VEC>
+static cudaError_t spread_as(const RowsParams& p, dim3 grid, cudaStream_t st) {
+  const dim3 block(ROWS_THREADS);
+  if (!p.other) return launch_pdl(spread_kernel<DT, VEC, 0>, grid, block, 0, st, p);
+  return p.topk <= 8 ? launch_pdl(spread_kernel<DT, VEC, 8>, grid, block, 0, st, p)
+                     : launch_pdl(spread_kernel<DT, VEC, MAX_TOPK>, grid, block, 0, st, p);
+}
+cudaError_t launch_spread(const RowsParams& p, int num_sms, cudaStream_t st) {
   const bool vec = rows_vectorised(p);
+  const int pads = p.has_pads ? (p.R / 8 + 1 < num_sms * 4 ? p.R / 8 + 1 : num_sms * 4) : 0;
+  const dim3 grid((unsigned)p.T + (unsigned)pads, column_parts(p, vec, p.other != nullptr, num_sms));
+  if (p.T == 0) return cudaSuccess;
   cudaError_t e;
-  if (p.row_dtype == ROW_BF16)
-    e = vec ? spread_as<ROW_BF16, true>(p, grid, block, st) : spread_as<ROW_BF16, false>(p, grid, block, st);
-  else if (p.row_dtype == ROW_F16)
-    e = vec ? spread_as<ROW_F16, true>(p, grid, block, st) : spread_as<ROW_F16, false>(p, grid, block, st);
-  else
-    e = vec ? spread_as<ROW_F32, true>(p, grid, block, st) : spread_as<ROW_F32, false>(p, grid, block, st);
+  if (p.row_dtype == ROW_BF16) e = vec ? spread_as<ROW_BF16, true>(p, grid, st) : spread_as<ROW_BF16, false>(p, grid, st);
+  else if (p.row_dtype == ROW_F16) e = vec ? spread_as<ROW_F16, true>(p, grid, st) : spread_as<ROW_F16, false>(p, grid, st);
+  else e = vec ? spread_as<ROW_F32, true>(p, grid, st) : spread_as<ROW_F32, false>(p, grid, st);
   count_launches(1);
   return e;
 }
 
 template <int DT, bool VEC>
 static cudaError_t collect_as(const RowsParams& p, dim3 grid, cudaStream_t st) {
-  const dim3 block(COLLECT_THREADS);
+  const dim3 block(ROWS_THREADS);
   if (!p.v) return launch_pdl(collect_kernel<DT, VEC, 0>, grid, block, 0, st, p);
   return p.topk <= 8 ? launch_pdl(collect_kernel<DT, VEC, 8>, grid, block, 0, st, p)
                      : launch_pdl(collect_kernel<DT, VEC, MAX_TOPK>, grid, block, 0, st, p);
 }
-cudaError_t launch_collect(const RowsParams& p, cudaStream_t st) {
+cudaError_t launch_collect(const RowsParams& p, int num_sms, cudaStream_t st) {
   if (p.T == 0) return cudaSuccess;
   const bool vec = rows_vectorised(p);
-  const dim3 grid((unsigned)p.T, 1);
+  const dim3 grid((unsigned)p.T, column_parts(p, vec, p.v != nullptr, num_sms));
   cudaError_t e;
   if (p.row_dtype == ROW_BF16) e = vec ? collect_as<ROW_BF16, true>(p, grid, st) : collect_as<ROW_BF16, false>(p, grid, st);
   else if (p.row_dtype == ROW_F16) e = vec ? collect_as<ROW_F16, true>(p, grid, st) : collect_as<ROW_F16, false>(p, grid, st);

@@ -150,13 +150,12 @@ struct RowsParams {
   float* dlogits;          // [T][E], or NULL
   int* status;
   int has_pads;            // 1: the maps may hold rows without a slot, which spread fills with zeros
-  int tokens_per_cta, token_ctas;  // set by launch_spread
 };
 cudaError_t launch_dispatch_plan(const int* perm, const int* offsets, int S, int E, int align, int capacity, int R,
                                  int* row_slot, int* slot_row, int* row_offsets, int* status, int num_sms,
                                  cudaStream_t st);
-cudaError_t launch_spread(RowsParams p, int num_sms, cudaStream_t st);
-cudaError_t launch_collect(const RowsParams& p, cudaStream_t st);
+cudaError_t launch_spread(const RowsParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_collect(const RowsParams& p, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- low-rank adapters (lora.cu)
 // The packed buffer: ranks int32 [slots], scales fp32 [slots] (each padded to
