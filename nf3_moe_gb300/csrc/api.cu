@@ -985,11 +985,18 @@ bool aligned_rows(const void* p, int row_dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (row_dtype == HMOE_ROW_F32 ? 3u : 1u)) == 0;
 }
 
+// The current device's SM count, looked up once for each device.
 hmoe_status device_sms(int* sms) {
+  static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  const bool cached = e == cudaSuccess && dev >= 0 && dev < 64;
+  *sms = cached ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms > 0) return HMOE_OK;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? HMOE_OK : cuda_fail(e, "device query");
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  if (cached) known[dev].store(*sms, std::memory_order_relaxed);
+  return HMOE_OK;
 }
 
 // The checks the two gradients share: the gates' part needs gates and the dot
@@ -1051,16 +1058,15 @@ hmoe_status hmoe_dispatch(const hmoe_dispatch_desc* desc, const void* x, int T, 
   if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
   int sms = 0;
   if ((s = device_sms(&sms)) != HMOE_OK) return s;
-  cudaError_t e = launch_dispatch_plan(perm, offsets, T * desc->topk, desc->E, desc->align, desc->capacity, R, row_slot,
-                                       slot_row, row_offsets, static_cast<int*>(ws), sms, (cudaStream_t)stream);
-  if (e != cudaSuccess) return cuda_fail(e, "dispatch plan launch");
   RowsParams p = rows_params(*desc, T, R, ws);
   p.v = x;
   p.rows_out = rows;
   p.gates = gates;
   p.row_slot = row_slot;
   p.slot_row = slot_row;
-  if ((e = launch_spread(p, sms, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "dispatch launch");
+  cudaError_t e = launch_dispatch(p, perm, offsets, desc->align, desc->capacity, row_slot, slot_row, row_offsets, sms,
+                                  (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "dispatch launch");
   return HMOE_OK;
 }
 

@@ -151,9 +151,9 @@ struct RowsParams {
   int* status;
   int has_pads;            // 1: the maps may hold rows without a slot, which spread fills with zeros
 };
-cudaError_t launch_dispatch_plan(const int* perm, const int* offsets, int S, int E, int align, int capacity, int R,
-                                 int* row_slot, int* slot_row, int* row_offsets, int* status, int num_sms,
-                                 cudaStream_t st);
+// The row maps and the rows of one dispatch (p: spread's parameters).
+cudaError_t launch_dispatch(const RowsParams& p, const int* perm, const int* offsets, int align, int capacity,
+                            int* row_slot, int* slot_row, int* row_offsets, int num_sms, cudaStream_t st);
 cudaError_t launch_spread(const RowsParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_collect(const RowsParams& p, int num_sms, cudaStream_t st);
 

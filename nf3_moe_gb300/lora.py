@@ -12,7 +12,7 @@ import torch
 
 from . import _lib, _need, act_torch_dtype, hmoe_workspace_init
 from ._lib import ACT_BF16, LoraDesc
-from .rows import _is, _raw_stream
+from .rows import _bytes, _is, _is_ws, _raw_stream
 
 
 def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
@@ -24,16 +24,16 @@ def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2 or t.shape[1] != width or (T is not None and t.shape[0] != T):
         raise ValueError(f"{name} must have shape [{'*' if T is None else T}, {width}], got {list(t.shape)}")
-    ld, one = t.stride()
-    if t.shape[0] <= 1:
-        ld = max(ld, width) if ld % 8 == 0 else width   # one row: its stride is never used
-    if one != 1 or ld < width:
-        raise ValueError(f"the rows of {name} must be contiguous and must not overlap, got strides {list(t.stride())}")
-    if cuda:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
+    if t.is_contiguous():
+        ld = width
+    else:
+        ld, one = t.stride()
+        if one != 1 or (ld < width and t.shape[0] > 1):
+            raise ValueError(f"the rows of {name} must be contiguous and must not overlap, got strides {list(t.stride())}")
+        if t.shape[0] <= 1:                              # one row: its stride is never used
+            ld = width
+    if cuda and not (t.is_cuda and (device is None or t.device == device)):
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on {device}" if device is not None else "") + f", got one on {t.device}")
     return ld
 
 
@@ -45,7 +45,7 @@ def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
     _is("ids", ids, (T,), torch.int32, dev, cuda)
     ldo = _need_rows("out", out, T, desc.N, dt, dev, cuda)
     ldb = 0 if base is None else _need_rows("base", base, T, desc.N, dt, dev, cuda)
-    _need("ws", ws, device=dev, cuda=cuda)
+    _is_ws(ws, dev, cuda)
     return T, ldx, ldb, ldo
 
 
@@ -76,7 +76,7 @@ class Lora:
 def hmoe_lora_create(desc, packed, stream=None):
     _need("packed", packed, min_bytes=hmoe_lora_packed_size(desc))
     h = ctypes.c_void_p()
-    _lib.check(_lib.lib().hmoe_lora_create(ctypes.byref(desc), packed.data_ptr(), _raw_stream(stream), ctypes.byref(h)))
+    _lib.check(_lib.lib().hmoe_lora_create(ctypes.byref(desc), packed.data_ptr(), _raw_stream(stream, packed.device), ctypes.byref(h)))
     return Lora(h, desc, packed)
 
 
@@ -89,11 +89,12 @@ def _check_lora_load(desc, slot, A, B, cuda=True):
 def hmoe_lora_load(lora, slot, A, B, scale=1.0, stream=None):
     """Put the adapter A [rank, K], B [N, rank] into a slot; A and B None empty it."""
     if A is None and B is None:
-        _lib.check(_lib.lib().hmoe_lora_load(lora.handle, int(slot), None, None, 0, 0.0, _raw_stream(stream)))
+        _lib.check(_lib.lib().hmoe_lora_load(lora.handle, int(slot), None, None, 0, 0.0,
+                                             _raw_stream(stream, lora.packed.device)))
         return
     _check_lora_load(lora.desc, slot, A, B)
     _lib.check(_lib.lib().hmoe_lora_load(lora.handle, int(slot), A.data_ptr(), B.data_ptr(), int(A.shape[0]),
-                                         float(scale), _raw_stream(stream)))
+                                         float(scale), _raw_stream(stream, A.device)))
 
 
 def hmoe_lora_forward(lora, x, ids, out, ws, base=None, stream=None):
@@ -101,7 +102,7 @@ def hmoe_lora_forward(lora, x, ids, out, ws, base=None, stream=None):
     T, ldx, ldb, ldo = _check_lora_forward(lora.desc, x, ids, base, out, ws)
     _lib.check(_lib.lib().hmoe_lora_forward(lora.handle, x.data_ptr(), ldx, T, ids.data_ptr(),
                                             None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
-                                            ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)))
+                                            ws.data_ptr(), _bytes(ws), _raw_stream(stream, x.device)))
 
 
 class LoraAdapters:
