@@ -11,6 +11,10 @@ Typical use (see ``HybridMoELayer`` for the same thing with owned buffers):
     hmoe_workspace_init(ws)
     hmoe_plan_routes(layer, logits, ids, gates, perm, offsets, ws)
     hmoe_forward(layer, x, ids, gates, perm, offsets, out, ws)
+
+Beside the layer: rows sorted by expert and back with their gradients (rows.py,
+``ExpertRows``) and low-rank adapters of many requests (lora.py, ``LoraAdapters``);
+examples/adapters.py runs them together.
 """
 
 import ctypes
@@ -390,10 +394,14 @@ class LinearW4A16:
         hmoe_workspace_init(self.ws)
         self.N = N
 
-    def __call__(self, x, out=None, path=PATH_AUTO):
+    def __call__(self, x, out=None, path=PATH_AUTO, adapters=None, ids=None):
+        """adapters, ids: a LoraAdapters of the same widths and each row's adapter (int32 [T], -1: none),
+        added to the result in place."""
         if out is None:
             out = torch.empty((x.shape[0], self.N), dtype=self.dtype, device=x.device)
         hmoe_linear_forward(self.linear, x, out, self.ws, path=path)
+        if adapters is not None:
+            adapters(x, ids, base=out, out=out)
         return out
 
 
