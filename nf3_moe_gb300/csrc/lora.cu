@@ -1,5 +1,7 @@
 // lora.cu -- low-rank adapters of many requests beside a shared projection:
 //   out[t] = base[t] + scale_a * B_a (A_a x[t]),  a = ids[t] (-1: none).
+#include <math.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -124,15 +126,25 @@ constexpr int LS_MAX_T = LS_THREADS;  // the grouping looks at one row a thread
 // 23.9, 51.3 us; 1024 of 64: 39.3, 53.7; 1024 of 8: 24.5, 38.8; 2048 of 64: 59.7,
 // 55.6; 2048 of 8: 40.7, 35.2.
 constexpr int LS_PLANNED_MAX_T = 1536;
-// CTAs of a cluster: 8, so that a single row's adapter is read by many SMs,
-// while 8 T CTAs fit the GPU (two on each of 152 SMs), and up to 64 rows where
-// the adapters are large; else 4, whose clusters start and join sooner.
-// Measured, 8 against 4: 1 row of rank 64, 6144x6144: 5.9, 8.3 us; 64 rows of 64
-// such adapters: 16.8, 18.4; 64 rows of rank 16, 2048x2048: 7.1, 5.1; 128 rows of
-// 128 adapters of rank 32, 6144x6144: 22.9, 19.9; 256 rows of rank 64: 27.5, 22.7.
-inline int ls_cluster(const LoraGeom& g, int T) {
-  const long long bytes = (long long)(g.KB + g.NB) * g.max_r16 * 128;
-  return T <= 38 || (T <= 64 && bytes >= 512 << 10) ? 8 : 4;
+// CTAs of an SM, by the registers of the kernel for this rank.
+constexpr int ls_per_sm(int r16) { return r16 <= 64 ? 2 : 1; }
+// CTAs of a cluster, 2 to 8: as many as let the groups run in one wave (a
+// twelfth of the places is left over, clusters do not pack exactly). The groups
+// are not known here; rows that draw their adapters at random from the slots
+// make max(a, T / 16 + a / 2) of them, a = slots (1 - exp(-T / slots)) adapters.
+// A group of more CTAs is a shorter wait, a second wave is another: 64 rows
+// of 64 adapters of rank 64, 6144x6144 took 17.9, 14.6 and 17.3 us with 4, 6 and
+// 8, 128 of 128, rank 32: 16.9, 20.0 and 23.1 with 3, 4 and 8, 1024 of 64: 38.1,
+// 31.8 and 39.1 with 2, 3 and 4, one row 8.3, 6.7 and 6.1 with 4, 6 and 8.
+// Where the adapters are small and each row has a cluster of its own, starting
+// the clusters is what counts: 256 CTAs in all (64 rows of rank 16, 2048x2048:
+// 4.9, 5.8 and 7.4 us with 4, 6 and 8; 256 rows: 7.4 and 9.2 with 2 and 4).
+inline int ls_cluster(const LoraGeom& g, int T, int num_sms) {
+  const double a = g.slots * (1.0 - exp(-(double)T / g.slots));
+  const double groups = fmax(a, T / (double)LS_TOK + a / 2);
+  double c = 0.92 * ls_per_sm(g.max_r16) * num_sms / groups;
+  if (T <= LS_MAX_T && (long long)(g.KB + g.NB) * g.max_r16 * 128 < 512 << 10) c = fmin(c, 256.0 / T);
+  return c < 2 ? 2 : (c > 8 ? 8 : (int)c);
 }
 
 __device__ __forceinline__ uint32_t ls_cluster_rank() {
@@ -170,7 +182,7 @@ __host__ __device__ constexpr int ls_smem(int r16) {
 // PLANNED: the groups come from the plan kernel's tiles of LS_TOK rows, which a
 // fixed number of clusters takes in turn.
 template <int ACT, int R, bool PLANNED>
-__global__ void __launch_bounds__(LS_THREADS, R <= 64 ? 2 : 1) lora_small_kernel(LoraParams p) {
+__global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(LoraParams p) {
   extern __shared__ __align__(16) uint8_t ls_sm[];
   __shared__ int s_tok[LS_TOK], s_cnt[LS_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -402,15 +414,16 @@ __global__ void __launch_bounds__(LS_THREADS, R <= 64 ? 2 : 1) lora_small_kernel
   }
 }
 
-// rows: grid rows, each a cluster; PLANNED: the groups are in the plan.
+// One cluster a grid row; PLANNED: the groups are in the plan, and as many
+// clusters as run at once take them.
 template <int ACT, int R, bool PLANNED>
-static cudaError_t small_as(const LoraParams& p, unsigned rows, cudaStream_t st) {
+static cudaError_t small_as(const LoraParams& p, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = ensure_smem_attr(lora_small_kernel<ACT, R, PLANNED>, ls_smem(R), done);
   if (e != cudaSuccess) return e;
-  const unsigned ctas = (unsigned)ls_cluster(p.g, p.T);
+  const unsigned ctas = (unsigned)ls_cluster(p.g, p.T, num_sms);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, rows);
+  cfg.gridDim = dim3(ctas, PLANNED ? (unsigned)(ls_per_sm(R) * num_sms) / ctas : (unsigned)p.T);
   cfg.blockDim = dim3(LS_THREADS);
   cfg.dynamicSmemBytes = (size_t)ls_smem(p.g.max_r16);
   cfg.stream = st;
@@ -425,11 +438,11 @@ static cudaError_t small_as(const LoraParams& p, unsigned rows, cudaStream_t st)
   return cudaLaunchKernelEx(&cfg, lora_small_kernel<ACT, R, PLANNED>, p);
 }
 template <int ACT, bool PLANNED>
-static cudaError_t small_of(const LoraParams& p, unsigned rows, cudaStream_t st) {
-  if (p.g.max_r16 <= 16) return small_as<ACT, 16, PLANNED>(p, rows, st);
-  if (p.g.max_r16 <= 32) return small_as<ACT, 32, PLANNED>(p, rows, st);
-  if (p.g.max_r16 <= 64) return small_as<ACT, 64, PLANNED>(p, rows, st);
-  return small_as<ACT, 128, PLANNED>(p, rows, st);
+static cudaError_t small_of(const LoraParams& p, int num_sms, cudaStream_t st) {
+  if (p.g.max_r16 <= 16) return small_as<ACT, 16, PLANNED>(p, num_sms, st);
+  if (p.g.max_r16 <= 32) return small_as<ACT, 32, PLANNED>(p, num_sms, st);
+  if (p.g.max_r16 <= 64) return small_as<ACT, 64, PLANNED>(p, num_sms, st);
+  return small_as<ACT, 128, PLANNED>(p, num_sms, st);
 }
 
 // ------------------------------------------------------------ larger batches: plan, A x, B u
@@ -1223,11 +1236,10 @@ static cudaError_t tiled_of(LoraParams p, int num_sms, cudaStream_t st) {
 
 template <int ACT>
 static cudaError_t forward_of(LoraParams p, int num_sms, cudaStream_t st) {
-  if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, (unsigned)p.T, st);
+  if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, num_sms, st);
   if (p.T <= LS_PLANNED_MAX_T) {
     const cudaError_t e = launch_plan(p, LS_TOK, st);
-    // two CTAs an SM, in clusters of 4
-    return e == cudaSuccess ? small_of<ACT, true>(p, (unsigned)(2 * num_sms / ls_cluster(p.g, p.T)), st) : e;
+    return e == cudaSuccess ? small_of<ACT, true>(p, num_sms, st) : e;
   }
   return tiled_of<ACT>(p, num_sms, st);
 }
