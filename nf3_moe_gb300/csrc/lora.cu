@@ -130,8 +130,9 @@ constexpr int LS_PLANNED_MAX_T = 1536;
 constexpr int ls_per_sm(int r16) { return r16 <= 64 ? 2 : 1; }
 // CTAs of a cluster, 2 to 8: as many as let the groups run in one wave (a
 // twelfth of the places is left over, clusters do not pack exactly). The groups
-// are not known here; rows that draw their adapters at random from the slots
-// make max(a, T / 16 + a / 2) of them, a = slots (1 - exp(-T / slots)) adapters.
+// are not known here: rows that draw their adapters at random from the slots
+// have a = slots (1 - exp(-T / slots)) of them, and make about
+// max(a, T / 16 + 0.4 a) groups.
 // A group of more CTAs is a shorter wait, a second wave is another: 64 rows
 // of 64 adapters of rank 64, 6144x6144 took 17.9, 14.6 and 17.3 us with 4, 6 and
 // 8, 128 of 128, rank 32: 16.9, 20.0 and 23.1 with 3, 4 and 8, 1024 of 64: 38.1,
@@ -141,7 +142,7 @@ constexpr int ls_per_sm(int r16) { return r16 <= 64 ? 2 : 1; }
 // 4.9, 5.8 and 7.4 us with 4, 6 and 8; 256 rows: 7.4 and 9.2 with 2 and 4).
 inline int ls_cluster(const LoraGeom& g, int T, int num_sms) {
   const double a = g.slots * (1.0 - exp(-(double)T / g.slots));
-  const double groups = fmax(a, T / (double)LS_TOK + a / 2);
+  const double groups = fmax(a, T / (double)LS_TOK + 0.4 * a);
   double c = 0.92 * ls_per_sm(g.max_r16) * num_sms / groups;
   if (T <= LS_MAX_T && (long long)(g.KB + g.NB) * g.max_r16 * 128 < 512 << 10) c = fmin(c, 256.0 / T);
   return c < 2 ? 2 : (c > 8 ? 8 : (int)c);
