@@ -120,32 +120,47 @@ constexpr int LS_THREADS = 256;
 constexpr int LS_WARPS = LS_THREADS / 32;
 constexpr int LS_TOK = 16;
 constexpr int LS_MAX_T = LS_THREADS;  // the grouping looks at one row a thread
-// Up to this many rows the small kernel serves the plan's groups of 16 rows:
-// it reads an adapter again for each group, but has fewer steps than the tile
-// kernels. Measured against them, 6144x6144, rank 64: 260 rows of 64 adapters
-// 23.9, 51.3 us; 1024 of 64: 39.3, 53.7; 1024 of 8: 24.5, 38.8; 2048 of 64: 59.7,
-// 55.6; 2048 of 8: 40.7, 35.2.
-constexpr int LS_PLANNED_MAX_T = 1536;
 // CTAs of an SM, by the registers of the kernel for this rank.
 constexpr int ls_per_sm(int r16) { return r16 <= 64 ? 2 : 1; }
+// What a batch is likely to look like, from what the host knows of it: rows
+// that draw their adapters at random from the slots have slots (1 - exp(-T /
+// slots)) of them, and each makes about max(1, rows / 16 + 0.4) groups.
+struct LoraBatch {
+  double adapters, rows, groups;  // rows: of one adapter
+};
+inline LoraBatch lora_batch(const LoraGeom& g, int T) {
+  LoraBatch b;
+  b.adapters = g.slots * (1.0 - exp(-(double)T / g.slots));
+  b.rows = T / b.adapters;
+  b.groups = b.adapters * fmax(1.0, b.rows / LS_TOK + 0.4);
+  return b;
+}
 // CTAs of a cluster, 2 to 8: as many as let the groups run in one wave (a
-// twelfth of the places is left over, clusters do not pack exactly). The groups
-// are not known here: rows that draw their adapters at random from the slots
-// have a = slots (1 - exp(-T / slots)) of them, and make about
-// max(a, T / 16 + 0.4 a) groups.
-// A group of more CTAs is a shorter wait, a second wave is another: 64 rows
-// of 64 adapters of rank 64, 6144x6144 took 17.9, 14.6 and 17.3 us with 4, 6 and
-// 8, 128 of 128, rank 32: 16.9, 20.0 and 23.1 with 3, 4 and 8, 1024 of 64: 38.1,
-// 31.8 and 39.1 with 2, 3 and 4, one row 8.3, 6.7 and 6.1 with 4, 6 and 8.
+// twelfth of the places is left over, clusters do not pack exactly). A group of
+// more CTAs is a shorter wait, a second wave is another: 64 rows of 64 adapters
+// of rank 64, 6144x6144 took 17.9, 14.6 and 17.3 us with 4, 6 and 8; 128 of 128,
+// rank 32, 16.9, 20.0 and 23.1 with 3, 4 and 8; 1024 of 64 38.1, 31.8 and 39.1
+// with 2, 3 and 4; one row 8.3, 6.7 and 6.1 with 4, 6 and 8.
 // Where the adapters are small and each row has a cluster of its own, starting
 // the clusters is what counts: 256 CTAs in all (64 rows of rank 16, 2048x2048:
 // 4.9, 5.8 and 7.4 us with 4, 6 and 8; 256 rows: 7.4 and 9.2 with 2 and 4).
 inline int ls_cluster(const LoraGeom& g, int T, int num_sms) {
-  const double a = g.slots * (1.0 - exp(-(double)T / g.slots));
-  const double groups = fmax(a, T / (double)LS_TOK + 0.4 * a);
-  double c = 0.92 * ls_per_sm(g.max_r16) * num_sms / groups;
+  double c = 0.92 * ls_per_sm(g.max_r16) * num_sms / lora_batch(g, T).groups;
   if (T <= LS_MAX_T && (long long)(g.KB + g.NB) * g.max_r16 * 128 < 512 << 10) c = fmin(c, 256.0 / T);
   return c < 2 ? 2 : (c > 8 ? 8 : (int)c);
+}
+// Whether the small kernel serves a batch above LS_MAX_T rows over planned groups
+// of 16 rows, or the tile kernels do. It reads an adapter again for each group,
+// but has fewer steps than they, whose cost goes by tiles of 128 rows, however
+// few there are in one. So it takes a batch whose groups run in one wave of
+// small clusters, and one whose adapters have few rows, the fewer the larger
+// the rank. Measured at 6144x6144, small against tiles: 260 rows of 64 adapters,
+// rank 64: 23.9, 51.3 us; 1536 of 8, rank 64: 38.5, 41.6; 3000 of 8, rank 16: 41.2,
+// 35.9; 2048 of 64, rank 64: 59.7, 55.5; 2048 of 64, rank 32: 47.1, 52.5; 4096 of
+// 256, rank 64: 106, 171; rank 128, 1024 of 8: 45.8, 62.1; 1024 of 64: 80.6, 67.7.
+inline bool lora_planned_small(const LoraGeom& g, int T, int num_sms) {
+  const LoraBatch b = lora_batch(g, T);
+  return b.groups <= 0.45 * ls_per_sm(g.max_r16) * num_sms || b.rows * g.max_r16 <= 1024.0;
 }
 
 __device__ __forceinline__ uint32_t ls_cluster_rank() {
@@ -1238,7 +1253,7 @@ static cudaError_t tiled_of(LoraParams p, int num_sms, cudaStream_t st) {
 template <int ACT>
 static cudaError_t forward_of(LoraParams p, int num_sms, cudaStream_t st) {
   if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, num_sms, st);
-  if (p.T <= LS_PLANNED_MAX_T) {
+  if (lora_planned_small(p.g, p.T, num_sms)) {
     const cudaError_t e = launch_plan(p, LS_TOK, st);
     return e == cudaSuccess ? small_of<ACT, true>(p, num_sms, st) : e;
   }

@@ -90,7 +90,10 @@ SHAPES = [  # T, K, N, slots, max_rank, dtype, pattern
     (2050, 72, 64, 7, 80, BF, "requests"), (65, 128, 128, 4, 8, BF, "none"), (600, 128, 128, 4, 8, HF, "none"),
     (1536, 264, 136, 20, 24, BF, "mixed"), (1537, 264, 136, 20, 24, HF, "mixed"), (1700, 8, 8, 2, 1, BF, "requests"),
     (1600, 1032, 264, 3, 128, HF, "requests"), (3000, 136, 1000, 512, 112, BF, "mixed"), (4100, 72, 72, 30, 70, HF, "requests"),
-    (2000, 64, 64, 1, 16, BF, "one"), (1800, 128, 128, 4, 8, HF, "none"), (2500, 2056, 520, 5, 96, BF, "requests")]
+    (2000, 64, 64, 1, 16, BF, "one"), (1800, 128, 128, 4, 8, HF, "none"), (2500, 2056, 520, 5, 96, BF, "requests"),
+    (2600, 264, 72, 3, 16, HF, "mixed"), (2300, 1032, 328, 6, 128, BF, "requests"), (5000, 72, 1032, 2, 33, HF, "requests"),
+    (2200, 520, 136, 40, 80, BF, "requests"), (8200, 64, 64, 5, 48, BF, "requests"), (9001, 8, 16, 3, 5, HF, "mixed"),
+    (2400, 128, 128, 4, 8, BF, "none")]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
@@ -106,7 +109,7 @@ def test_forward(shape, based):
     hm.hmoe_check_device_status(s.hm.ws)
 
 
-@pytest.mark.parametrize("T", [1, 5, 40, 300, 700, 1900])
+@pytest.mark.parametrize("T", [1, 5, 40, 300, 700, 2900])
 @pytest.mark.parametrize("dt", [BF, HF])
 def test_column_ranges_and_in_place(T, dt):
     """x, base and out as column ranges of wider tensors, and in place; what lies beside them stays."""
@@ -125,7 +128,7 @@ def test_column_ranges_and_in_place(T, dt):
     assert torch.equal(wide, before)
 
 
-@pytest.mark.parametrize("T", [6, 90, 640, 1900])
+@pytest.mark.parametrize("T", [6, 90, 640, 2900])
 def test_rows_do_not_touch_each_other(T):
     """A row of NaN or infinity marks itself alone; a row without an adapter is base whatever its x holds."""
     s = Set(136, 200, 4, 20, BF, T)
@@ -142,7 +145,7 @@ def test_rows_do_not_touch_each_other(T):
     assert torch.equal(got[2:T - 1], want[2:T - 1])
 
 
-@pytest.mark.parametrize("T", [4, 400, 1900])
+@pytest.mark.parametrize("T", [4, 400, 2900])
 def test_slots_are_replaced_emptied_and_checked(T):
     s = Set(128, 192, 3, 40, BF, T)
     x, base = s.randn(T, 128), s.randn(T, 192)
@@ -190,7 +193,7 @@ def test_refusals_on_the_host():
     hm.hmoe_lora_forward(h, x, ids, wide[:, :64], ws)
 
 
-@pytest.mark.parametrize("T", [3, 64, 500, 2100])
+@pytest.mark.parametrize("T", [3, 64, 500, 2900])
 def test_other_streams_graphs_and_repeats(T):
     s = Set(512, 640, 9, 32, BF, T)
     x, base, ids = s.randn(T, 512), s.randn(T, 640), ids_of("mixed", T, 9)
@@ -218,7 +221,7 @@ def test_other_streams_graphs_and_repeats(T):
     assert torch.equal(out, s.hm(x, ids, base=base))
 
 
-@pytest.mark.parametrize("T", [4, 70, 500, 2100])
+@pytest.mark.parametrize("T", [4, 70, 500, 2900])
 def test_no_write_outside_out(T):
     s = Set(136, 72, 3, 9, HF, T)
     whole = torch.full((T * 72 + 512,), 3.0, dtype=HF, device="cuda")
@@ -230,8 +233,8 @@ def test_no_write_outside_out(T):
 
 
 def test_workspace_serves_any_batch_up_to_its_size():
-    s = Set(256, 256, 6, 32, BF, 2300)
-    for T in (2300, 900, 1, 64, 513, 8, 1999, 899):
+    s = Set(256, 256, 6, 32, BF, 2900)
+    for T in (2900, 900, 1, 64, 513, 8, 2500, 899):
         x, base, ids = s.randn(T, 256), s.randn(T, 256), ids_of("mixed", T, 6)
         s.check(s.hm(x, ids, base=base), x, ids, base)
 
