@@ -1159,7 +1159,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           y[k] = p.base && row[k] >= 0 && i < sp.n && n < p.g.N
-                     ? __ldcg(reinterpret_cast<const uint4*>(p.base + (size_t)row[k] * p.ldbase + n))
+                     ? __ldcs(reinterpret_cast<const uint4*>(p.base + (size_t)row[k] * p.ldbase + n))
                      : make_uint4(0, 0, 0, 0);
       };
       // Unit i from its base values in y, which are then unit i + 4's.
@@ -1194,7 +1194,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
         if (n < p.g.N) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (row[k] >= 0) *reinterpret_cast<uint4*>(p.out + (size_t)row[k] * p.ldout + n) = y[k];
+            if (row[k] >= 0) __stcs(reinterpret_cast<uint4*>(p.out + (size_t)row[k] * p.ldout + n), y[k]);
         }
         load(i + 4, y);
       };
