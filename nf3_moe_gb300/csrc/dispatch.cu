@@ -14,6 +14,14 @@
 // option. Every sum is fp32 in a fixed order; a slot without a row takes no
 // part (it is skipped, not multiplied by zero, so what pad rows hold never
 // reaches a result).
+//
+// HBM bounds them all from some hundred rows on. At 4096 tokens of 6144 16-bit
+// columns, 256 experts, top-8 (of the copy bandwidth 6.70 TB/s):
+//   dispatch, with its plan      453 MB   74 us   91%
+//   combine                      453 MB   69 us   98%
+//   combine's gradient, with the gates' and logits', 860 MB, 133 us, 97%
+// Small batches are a launch or two: 8 tokens dispatched in 3.2 us, one token
+// combined in 2.2 us.
 #include "common.cuh"
 #include "internal.h"
 

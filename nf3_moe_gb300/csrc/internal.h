@@ -162,8 +162,9 @@ cudaError_t launch_collect(const RowsParams& p, int num_sms, cudaStream_t st);
 // 256 bytes), then one block per slot. With r16 the slot's rank rounded up to
 // 16, a block holds ceil(K / 64) tiles of A, each r16 rows of 64 values in the
 // tensor cores' K-major 128-byte-swizzled layout, then ceil(N / 64) tiles of
-// B, each 64 rows of r16 values in the K-major layout without swizzle (16-byte
-// core-matrix rows: [r16 / 8][64][8 values]). Either tile is r16 * 128 bytes.
+// B, each 64 rows (in the order of lora_b_byte) of r16 values in the K-major
+// layout without swizzle (16-byte core-matrix rows: [r16 / 8][64][8 values]).
+// Either tile is r16 * 128 bytes.
 // Rows and columns past the rank, K and N hold zeros.
 constexpr int LORA_MAX_RANK = 128;
 constexpr int LORA_MAX_SLOTS = 512;

@@ -1,5 +1,20 @@
 // lora.cu -- low-rank adapters of many requests beside a shared projection:
 //   out[t] = base[t] + scale_a * B_a (A_a x[t]),  a = ids[t] (-1: none).
+//
+// What a batch cannot do without: x, base and each used adapter read once, out
+// written once. That bounds every size: at rank 128 the products are 128
+// operations for a byte of x, base or out (B u's two parts counted), of which
+// the tensor cores do about 290 in a byte's time at HBM.
+//
+// u = A x is summed in fp32 and enters the second product as the sum of two
+// values of the activation type (split_act): u then keeps at least 16 bits, and
+// out has one rounding, its own. One 16-bit u would add an error as large as
+// that. No sum's order depends on the schedule.
+//
+// Two ways, by what the host knows of the batch (lora_planned_small): a kernel
+// that serves 16 rows of one adapter with a small cluster, whose time is
+// latency (one launch up to 256 rows, two above), and a pair of persistent
+// tensor-core kernels over tiles of 128 rows of one adapter (three launches).
 #include <math.h>
 
 #include "common.cuh"
@@ -110,8 +125,18 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 // on only if row t is the first of a group, that is if the number of earlier
 // rows with the same id is a multiple of LS_TOK.
 //
-// Both products run on mma.sync m16n8k16 with the rows on the M side and the
-// weights, straight from global memory, on the N side. K inside a group of 32
+// The adapters' bytes bound it where the batch is large (64 rows of 64 adapters
+// of ranks 1 to 64, 6144x6144: 33 MB in 14.4 us); below, a chain of waits does:
+// ids, A and x, the cluster's exchange, B (one row of rank 16, 2048x2048: 3.6 us,
+// of rank 64, 6144x6144: 6.1 us). So a CTA has the next step's operands on their
+// way, B's first ones and the base's before the exchange, and only the group's
+// own rows are exchanged. (Asking L2 for B at the start made 64 rows 2 us slower:
+// it delays A.)
+//
+// Both products run on mma.sync m16n8k16, whose 16 rows suit a group (tcgen05's
+// smallest M is 64, and would want the weights staged in shared memory first),
+// with the rows on the M side and the weights, straight from global memory, on
+// the N side. K inside a group of 32
 // (and the rank in the second product) is permuted alike for both operands, so
 // that a lane's operand words are 16 bytes of one row. The columns of the
 // second product are permuted so that a lane ends up with 8 neighbouring ones
@@ -464,7 +489,9 @@ static cudaError_t small_of(const LoraParams& p, int num_sms, cudaStream_t st) {
 // ------------------------------------------------------------ larger batches: plan, A x, B u
 // Three launches. The plan groups the rows by adapter and cuts the groups into
 // tiles of up to 128 rows; the rows of a tile sit on the M side of tcgen05.mma
-// and the adapter on its N side.
+// and the adapter on its N side. 8192 rows of 12 requests, ranks up to 64,
+// 6144x6144 take 71.8 us, about 5 for the plan, 22 for A x (104 MB, at 6.9 TB/s
+// once its rings run) and 45 for B u (200 MB, 5.7 TB/s); the floor is 46.
 
 // One CTA. Rows without an adapter (or with an empty slot) form the last group.
 // The rows of a group keep their order, so that the tiles, and with them the
@@ -596,9 +623,9 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
 // ------------------------------------------------------------ the tile kernels
 // Both kernels run one persistent CTA per SM over a contiguous share of the
 // batch's units (64 of K, or 64 columns, of a tile), so that every SM has the
-// same number of units whatever the tiles are. Their warps have roles: one
-// brings tiles into a ring (rows by TMA gathers of four, the adapter's tiles by
-// bulk copies), one issues the MMAs, the others turn accumulators into results.
+// same number of units whatever the tiles are. Their warps have roles: some
+// bring tiles into a ring, one issues the MMAs, the others turn accumulators
+// into results.
 constexpr int LT_X_BYTES = LORA_TILE_ROWS * 128;  // 128 rows x 64 values
 constexpr int LT_SMEM = 232448 - 1024 - 2048;     // a CTA's shared memory without alignment and barriers
 constexpr int LT_MAX_STAGES = 8;
@@ -737,7 +764,9 @@ struct LoraSpan {
 };
 
 // A x of a tile's rows: to u[pos][r] where a CTA has the tile's whole K extent,
-// else a sum for each piece to part[slot][row][r], which the reader adds up.
+// else a sum for each piece to part[slot][row][r], which the reader adds up
+// (letting the last CTA of a tile add them up here cost 10 us of this kernel's
+// tail at 8192 rows). HBM bounds it: 16 KB of x a unit, four MMAs of 128 x r x 16.
 template <int ACT>
 __global__ void __launch_bounds__(LA_THREADS, 1)
     lora_shrink_kernel(const __grid_constant__ LoraParams p) {
@@ -978,7 +1007,9 @@ __device__ __forceinline__ float2 fma_x2(float a, float b, float s, float2 c) {
 // out = base + scale B u. u enters as its two parts (split_act), whose products
 // with B add up in the same accumulator. An epilogue warp owns 32 rows and 32
 // columns of every second unit; a lane holds 16 bytes of 4 rows, whose base
-// values it has loaded two units ahead.
+// values it has loaded two units ahead. HBM bounds it, 16 KB of base in and of
+// out a unit. Without B's permuted rows the results had to cross shared memory
+// to reach 64 bytes of a row together: 54 against 44 us at 8192 rows.
 template <int ACT>
 __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t lt_sm[];
