@@ -16,37 +16,34 @@ from .rows import _bytes, _is, _is_ws, _raw_stream
 
 
 def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
-    """A [T, width] tensor whose rows are contiguous and evenly spaced (a column range of a wider one serves).
-    Returns the row stride."""
+    """A [T, width] tensor whose rows are contiguous and evenly spaced (a column range of a wider one serves), on the
+    device of this index. Returns the row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2 or t.shape[1] != width or (T is not None and t.shape[0] != T):
         raise ValueError(f"{name} must have shape [{'*' if T is None else T}, {width}], got {list(t.shape)}")
+    if cuda and (t.get_device() < 0 or (device is not None and t.get_device() != device)):
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{device}" if device is not None else "") + f", got one on {t.device}")
     if t.is_contiguous():
-        ld = width
-    else:
-        ld, one = t.stride()
-        if one != 1 or (ld < width and t.shape[0] > 1):
-            raise ValueError(f"the rows of {name} must be contiguous and must not overlap, got strides {list(t.stride())}")
-        if t.shape[0] <= 1:                              # one row: its stride is never used
-            ld = width
-    if cuda and not (t.is_cuda and (device is None or t.device == device)):
-        raise ValueError(f"{name} must be a CUDA tensor" + (f" on {device}" if device is not None else "") + f", got one on {t.device}")
-    return ld
+        return width
+    ld, one = t.stride()
+    if one != 1 or (ld < width and t.shape[0] > 1):
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap, got strides {list(t.stride())}")
+    return ld if t.shape[0] > 1 else width               # one row: its stride is never used
 
 
 def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
-    """Returns T and the row strides of x, base and out."""
-    dt = act_torch_dtype(desc.act_dtype)
+    """Returns T, the row strides of x, base and out, and the device index."""
+    dt, N = act_torch_dtype(desc.act_dtype), desc.N
     ldx = _need_rows("x", x, None, desc.K, dt, cuda=cuda)
-    T, dev = x.shape[0], x.device
+    T, dev = x.shape[0], x.get_device()
     _is("ids", ids, (T,), torch.int32, dev, cuda)
-    ldo = _need_rows("out", out, T, desc.N, dt, dev, cuda)
-    ldb = 0 if base is None else _need_rows("base", base, T, desc.N, dt, dev, cuda)
+    ldo = _need_rows("out", out, T, N, dt, dev, cuda)
+    ldb = 0 if base is None else ldo if base is out else _need_rows("base", base, T, N, dt, dev, cuda)
     _is_ws(ws, dev, cuda)
-    return T, ldx, ldb, ldo
+    return T, ldx, ldb, ldo, dev
 
 
 def hmoe_lora_packed_size(desc):
@@ -76,7 +73,7 @@ class Lora:
 def hmoe_lora_create(desc, packed, stream=None):
     _need("packed", packed, min_bytes=hmoe_lora_packed_size(desc))
     h = ctypes.c_void_p()
-    _lib.check(_lib.lib().hmoe_lora_create(ctypes.byref(desc), packed.data_ptr(), _raw_stream(stream, packed.device), ctypes.byref(h)))
+    _lib.check(_lib.lib().hmoe_lora_create(ctypes.byref(desc), packed.data_ptr(), _raw_stream(stream, packed.get_device()), ctypes.byref(h)))
     return Lora(h, desc, packed)
 
 
@@ -90,19 +87,19 @@ def hmoe_lora_load(lora, slot, A, B, scale=1.0, stream=None):
     """Put the adapter A [rank, K], B [N, rank] into a slot; A and B None empty it."""
     if A is None and B is None:
         _lib.check(_lib.lib().hmoe_lora_load(lora.handle, int(slot), None, None, 0, 0.0,
-                                             _raw_stream(stream, lora.packed.device)))
+                                             _raw_stream(stream, lora.packed.get_device())))
         return
     _check_lora_load(lora.desc, slot, A, B)
     _lib.check(_lib.lib().hmoe_lora_load(lora.handle, int(slot), A.data_ptr(), B.data_ptr(), int(A.shape[0]),
-                                         float(scale), _raw_stream(stream, A.device)))
+                                         float(scale), _raw_stream(stream, A.get_device())))
 
 
 def hmoe_lora_forward(lora, x, ids, out, ws, base=None, stream=None):
     """out[t] = base[t] + scale_a B_a (A_a x[t]), a = ids[t]; base None: zeros; base may be out."""
-    T, ldx, ldb, ldo = _check_lora_forward(lora.desc, x, ids, base, out, ws)
+    T, ldx, ldb, ldo, dev = _check_lora_forward(lora.desc, x, ids, base, out, ws)
     _lib.check(_lib.lib().hmoe_lora_forward(lora.handle, x.data_ptr(), ldx, T, ids.data_ptr(),
                                             None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
-                                            ws.data_ptr(), _bytes(ws), _raw_stream(stream, x.device)))
+                                            ws.data_ptr(), _bytes(ws), _raw_stream(stream, dev)))
 
 
 class LoraAdapters:

@@ -29,15 +29,23 @@ def row_torch_dtype(row_dtype):
 
 
 def _is(name, t, shape, dtype, device, cuda=True):
-    """_need for a tensor that is nearly always right: one look, and the full check for its message."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.is_contiguous()
-            and (not cuda or (t.is_cuda and t.device == device))):
-        _need(name, t, shape, dtype, device=device, cuda=cuda)
+    """_need for a tensor that is nearly always right: one look, and the full check for its message. device: its
+    index, as get_device gives it (-1 on the host)."""
+    try:
+        if t.shape == shape and t.dtype == dtype and t.is_contiguous() and (t.get_device() == device >= 0 or not cuda):
+            return
+    except AttributeError:
+        pass
+    _need(name, t, shape, dtype, device=torch.device("cuda", device) if device >= 0 else None, cuda=cuda)
 
 
 def _is_ws(ws, device, cuda=True):
-    if not (isinstance(ws, torch.Tensor) and ws.is_contiguous() and (not cuda or (ws.is_cuda and ws.device == device))):
-        _need("ws", ws, device=device, cuda=cuda)
+    try:
+        if ws.is_contiguous() and (ws.get_device() == device >= 0 or not cuda):
+            return
+    except AttributeError:
+        pass
+    _need("ws", ws, device=torch.device("cuda", device) if device >= 0 else None, cuda=cuda)
 
 
 def _raw(t):
@@ -46,7 +54,7 @@ def _raw(t):
 
 def _raw_stream(stream, device):
     """The stream's handle; None: the device's current stream (this look-up takes 0.1 us, the Stream object 2.9)."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _bytes(ws):
@@ -67,11 +75,17 @@ def hmoe_dispatch_workspace_size(desc, max_tokens):
 
 
 def _check_tokens(name, desc, t, cuda):
+    """T, H, the rows' dtype and the device index of a [T, H] tensor."""
     dt, H = _TORCH[desc.row_dtype], desc.H
-    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.shape[1] == H and t.dtype == dt and t.is_contiguous()
-            and (not cuda or t.is_cuda)):
-        _need(name, t, (None, H), dt, cuda=cuda)
-    return t.shape[0], dt, t.device
+    try:
+        T, width = t.shape
+        device = t.get_device()
+        if width == H and t.dtype == dt and t.is_contiguous() and (device >= 0 or not cuda):
+            return T, H, dt, device
+    except (AttributeError, ValueError):
+        pass
+    _need(name, t, (None, H), dt, cuda=cuda)
+    return t.shape[0], H, dt, t.get_device()
 
 
 def _rows_of(desc, T):
@@ -82,80 +96,87 @@ def _rows_of(desc, T):
 
 
 def _check_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates, cuda=True):
-    T, dt, dev = _check_tokens("x", desc, x, cuda)
-    R, k, i32 = _rows_of(desc, T), desc.topk, torch.int32
+    T, H, dt, dev = _check_tokens("x", desc, x, cuda)
+    R, k, E, i32 = _rows_of(desc, T), desc.topk, desc.E, torch.int32
     _is("perm", perm, (T * k,), i32, dev, cuda)
-    _is("offsets", offsets, (desc.E + 1,), i32, dev, cuda)
-    _is("rows", rows, (R, desc.H), dt, dev, cuda)
+    _is("offsets", offsets, (E + 1,), i32, dev, cuda)
+    _is("rows", rows, (R, H), dt, dev, cuda)
     _is("row_slot", row_slot, (R,), i32, dev, cuda)
     _is("slot_row", slot_row, (T, k), i32, dev, cuda)
-    _is("row_offsets", row_offsets, (desc.E + 1,), i32, dev, cuda)
+    _is("row_offsets", row_offsets, (E + 1,), i32, dev, cuda)
     if gates is not None:
         _is("gates", gates, (T, k), torch.float32, dev, cuda)
     _is_ws(ws, dev, cuda)
-    return T
+    return T, dev
 
 
 def _check_collect(desc, name, rows, slot_row, out_name, out, ws, gates, cuda=True):
-    T, dt, dev = _check_tokens(out_name, desc, out, cuda)
-    _is(name, rows, (_rows_of(desc, T), desc.H), dt, dev, cuda)
-    _is("slot_row", slot_row, (T, desc.topk), torch.int32, dev, cuda)
+    T, H, dt, dev = _check_tokens(out_name, desc, out, cuda)
+    k = desc.topk
+    _is(name, rows, (_rows_of(desc, T), H), dt, dev, cuda)
+    _is("slot_row", slot_row, (T, k), torch.int32, dev, cuda)
     if gates is not None:
-        _is("gates", gates, (T, desc.topk), torch.float32, dev, cuda)
+        _is("gates", gates, (T, k), torch.float32, dev, cuda)
     _is_ws(ws, dev, cuda)
-    return T
+    return T, dev
 
 
 def _check_gate_grads(desc, T, dev, dot_name, dot, dot_shape, gates, ids, dgates, dlogits, cuda=True):
+    if dgates is None and dlogits is None and dot is None and ids is None:
+        return
     k = desc.topk
     if (dgates is not None or dlogits is not None) and (gates is None or dot is None):
         raise ValueError(f"dgates and dlogits need gates and {dot_name}")
-    if dlogits is not None and ids is None:
-        raise ValueError("dlogits needs ids")
-    for name, t, shape, dtype in ((dot_name, dot, dot_shape, row_torch_dtype(desc.row_dtype)), ("ids", ids, (T, k), torch.int32),
-                                  ("dgates", dgates, (T, k), torch.float32), ("dlogits", dlogits, (T, desc.E), torch.float32)):
-        if t is not None:
-            _is(name, t, shape, dtype, dev, cuda)
+    if dlogits is not None:
+        if ids is None:
+            raise ValueError("dlogits needs ids")
+        _is("dlogits", dlogits, (T, desc.E), torch.float32, dev, cuda)
+    if dot is not None:
+        _is(dot_name, dot, dot_shape, _TORCH[desc.row_dtype], dev, cuda)
+    if ids is not None:
+        _is("ids", ids, (T, k), torch.int32, dev, cuda)
+    if dgates is not None:
+        _is("dgates", dgates, (T, k), torch.float32, dev, cuda)
 
 
 def hmoe_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates=None, stream=None):
     """rows[r] = (gates) x[row_slot[r] / topk], and the row maps; every output is fully written."""
-    T = _check_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates)
+    T, dev = _check_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates)
     _lib.check(_lib.lib().hmoe_dispatch(ctypes.byref(desc), x.data_ptr(), T, _raw(gates), perm.data_ptr(),
                                         offsets.data_ptr(), rows.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
                                         row_offsets.data_ptr(), ws.data_ptr(), _bytes(ws),
-                                        _raw_stream(stream, x.device)))
+                                        _raw_stream(stream, dev)))
 
 
 def hmoe_dispatch_backward(desc, drows, slot_row, dx, ws, x=None, gates=None, ids=None, dgates=None, dlogits=None,
                            stream=None):
     """dx[t] = sum_j (gates) drows[slot_row[t, j]], and with gates and x the gates' and router logits' gradients."""
-    T = _check_collect(desc, "drows", drows, slot_row, "dx", dx, ws, gates)
-    _check_gate_grads(desc, T, dx.device, "x", x, dx.shape, gates, ids, dgates, dlogits)
+    T, dev = _check_collect(desc, "drows", drows, slot_row, "dx", dx, ws, gates)
+    _check_gate_grads(desc, T, dev, "x", x, dx.shape, gates, ids, dgates, dlogits)
     _lib.check(_lib.lib().hmoe_dispatch_backward(ctypes.byref(desc), drows.data_ptr(), T, slot_row.data_ptr(), _raw(x),
                                                  _raw(gates), _raw(ids), dx.data_ptr(), _raw(dgates), _raw(dlogits),
-                                                 ws.data_ptr(), _bytes(ws), _raw_stream(stream, dx.device)))
+                                                 ws.data_ptr(), _bytes(ws), _raw_stream(stream, dev)))
 
 
 def hmoe_combine(desc, rows, slot_row, out, ws, gates=None, stream=None):
     """out[t] = sum_j (gates) rows[slot_row[t, j]]."""
-    T = _check_collect(desc, "rows", rows, slot_row, "out", out, ws, gates)
+    T, dev = _check_collect(desc, "rows", rows, slot_row, "out", out, ws, gates)
     _lib.check(_lib.lib().hmoe_combine(ctypes.byref(desc), rows.data_ptr(), T, slot_row.data_ptr(), _raw(gates),
                                        out.data_ptr(), ws.data_ptr(), _bytes(ws),
-                                       _raw_stream(stream, out.device)))
+                                       _raw_stream(stream, dev)))
 
 
 def hmoe_combine_backward(desc, dout, row_slot, slot_row, drows, ws, rows=None, gates=None, ids=None, dgates=None,
                           dlogits=None, stream=None):
     """drows[r] = (gates) dout[row_slot[r] / topk], zero on padding, and with gates and rows the gates' and router
     logits' gradients."""
-    T = _check_collect(desc, "drows", drows, slot_row, "dout", dout, ws, gates)
-    _is("row_slot", row_slot, (drows.shape[0],), torch.int32, dout.device)
-    _check_gate_grads(desc, T, dout.device, "rows", rows, drows.shape, gates, ids, dgates, dlogits)
+    T, dev = _check_collect(desc, "drows", drows, slot_row, "dout", dout, ws, gates)
+    _is("row_slot", row_slot, (drows.shape[0],), torch.int32, dev)
+    _check_gate_grads(desc, T, dev, "rows", rows, drows.shape, gates, ids, dgates, dlogits)
     _lib.check(_lib.lib().hmoe_combine_backward(ctypes.byref(desc), dout.data_ptr(), T, row_slot.data_ptr(),
                                                 slot_row.data_ptr(), _raw(rows), _raw(gates), _raw(ids),
                                                 drows.data_ptr(), _raw(dgates), _raw(dlogits), ws.data_ptr(),
-                                                _bytes(ws), _raw_stream(stream, dout.device)))
+                                                _bytes(ws), _raw_stream(stream, dev)))
 
 
 # ------------------------------------------------------------------ owned buffers and autograd

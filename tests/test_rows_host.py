@@ -97,7 +97,7 @@ def _bufs(T=4, k=2, E=8, H=64, dt=torch.bfloat16):
 
 def test_binding_checks_of_dispatch(lib):
     d = hm.DispatchDesc(64, 8, 2, hm.ROW_BF16, 1, 0)
-    assert rows_mod._check_dispatch(d, **_bufs(), cuda=False) == 4
+    assert rows_mod._check_dispatch(d, **_bufs(), cuda=False)[0] == 4
     for name, bad in (("x", torch.zeros(4, 63, dtype=torch.bfloat16)), ("x", torch.zeros(4, 64, dtype=torch.float16)),
                       ("x", torch.zeros(64, 4, dtype=torch.bfloat16).t()), ("perm", torch.zeros(8, dtype=torch.int64)),
                       ("perm", torch.zeros(7, dtype=torch.int32)), ("offsets", torch.zeros(8, dtype=torch.int32)),
@@ -116,7 +116,7 @@ def test_binding_checks_of_the_gradients(lib):
     d = hm.DispatchDesc(64, 8, 2, hm.ROW_BF16, 1, 0)
     b = _bufs()
     ids, dg, dl = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), torch.zeros(4, 8)
-    dev = b["x"].device
+    dev = b["x"].get_device()
     check = lambda **kw: rows_mod._check_gate_grads(d, 4, dev, "x", **({"dot": b["x"], "dot_shape": b["x"].shape, "gates": b["gates"],  # noqa: E731
                                                     "ids": ids, "dgates": dg, "dlogits": dl} | kw), cuda=False)
     check()
