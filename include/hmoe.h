@@ -574,7 +574,9 @@ hmoe_status hmoe_combine_backward(const hmoe_dispatch_desc* desc, const void* do
  * values of the activation type (so with 16 or more significant bits); that
  * product, the scale and the base are fp32, rounded once to the activation
  * type. fp16: |A x| must fit fp16, like any activation.
- * Each row's result depends on that row alone, not on the other rows.
+ * No value of another row enters a row's result, a NaN or an infinity
+ * included. The same call gives the same bits; how a batch is composed can
+ * change the order of the fp32 sums.
  *   These entry points have no counterpart on the pages.
  * Conventions as for the layer. */
 typedef struct {

@@ -17,6 +17,7 @@
 // tensor-core kernels over tiles of 128 rows of one adapter (three launches).
 #include <math.h>
 
+#include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
