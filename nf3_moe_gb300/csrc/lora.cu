@@ -145,7 +145,7 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 constexpr int LS_THREADS = 256;
 constexpr int LS_WARPS = LS_THREADS / 32;
 constexpr int LS_TOK = 16;
-constexpr int LS_MAX_T = LS_THREADS;  // the grouping looks at one row a thread
+constexpr int LS_MAX_T = 128;  // at most LS_THREADS: the grouping looks at one row a thread
 // CTAs of an SM, by the registers of the kernel for this rank.
 constexpr int ls_per_sm(int r16) { return r16 <= 64 ? 2 : 1; }
 // What a batch is likely to look like, from what the host knows of it: rows
@@ -194,12 +194,18 @@ __device__ __forceinline__ uint32_t ls_cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ float ld_cluster_f32(const void* p, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster_f32x4(const void* p, uint32_t rank) {
   uint32_t a;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -220,15 +226,126 @@ __host__ __device__ constexpr int ls_smem(int r16) {
   return (LS_WARPS + 1) * LS_TOK * r16 * 4 + 2 * LS_TOK * (r16 + 8) * 2;
 }
 
+// The groups of a batch of up to LS_COUNT_T rows, found in every CTA: the rows
+// of each adapter counted (counts do not depend on the order of the atomics),
+// the counts scanned to the adapters' first groups, and a group's rows picked
+// out by their places among its adapter's rows. The plan kernel finds the same
+// groups, in the same order, and is a launch to wait for.
+constexpr int LS_COUNT_T = 2048;
+template <bool PLANNED>
+struct LsGroups {
+  int n[LORA_MAX_SLOTS + 1], first[LORA_MAX_SLOTS + 2], rank[LORA_MAX_SLOTS + 1];  // the last: rows without an adapter
+  int found;
+  uint16_t of[LS_COUNT_T];  // the rows' adapters
+
+  __device__ __forceinline__ void clear(const LoraParams& p, int tid) {
+    for (int g = tid; g <= p.g.slots; g += LS_THREADS) n[g] = 0;
+  }
+  // A warp's range of rows.
+  __device__ __forceinline__ int rounds(const LoraParams& p) const { return (p.T + LS_THREADS - 1) / LS_THREADS; }
+
+  // Returns the number of groups. wsum: scratch of LS_WARPS words.
+  __device__ __forceinline__ int count(const LoraParams& p, int tid, int* wsum) {
+    constexpr int IDS = 8;  // loads in flight together
+    const int lane = tid & 31, warp = tid >> 5, G = p.g.slots + 1;
+    const int many = rounds(p), t0 = warp * many * 32 + lane;
+    for (int r0 = 0; r0 < many; r0 += IDS) {
+      int id[IDS];
+#pragma unroll
+      for (int i = 0; i < IDS; ++i) id[i] = r0 + i < many && t0 + (r0 + i) * 32 < p.T ? __ldg(p.ids + t0 + (r0 + i) * 32) : -1;
+      if (r0 == 0) {
+        for (int g = tid; g < G; g += LS_THREADS) rank[g] = g < G - 1 ? __ldg(reinterpret_cast<const int*>(p.packed) + g) : 0;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < IDS; ++i) {
+        if (r0 + i >= many) break;
+        const int t = t0 + (r0 + i) * 32;
+        const bool row = t < p.T;
+        int g = id[i];
+        if (g < -1 || g >= G - 1) set_status(p.status, DEV_BAD_ROUTE);
+        if (g < 0 || g >= G - 1 || rank[g] == 0) g = G - 1;
+        of[t] = row ? (uint16_t)g : (uint16_t)0xFFFF;
+        const int g0 = __shfl_sync(0xffffffffu, g, 0);
+        if (__all_sync(0xffffffffu, row && g == g0)) {  // a prompt's rows
+          if (lane == 0) atomicAdd(&n[g], 32);
+        } else if (row) {
+          atomicAdd(&n[g], 1);
+        }
+      }
+    }
+    __syncthreads();
+    // exclusive scan of the adapters' groups, a run of them a thread
+    const int per = (G + LS_THREADS - 1) / LS_THREADS;
+    int sum = 0;
+    for (int g = tid * per; g < min(G, (tid + 1) * per); ++g) sum += (n[g] + LS_TOK - 1) / LS_TOK;
+    int in = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, in, d);
+      if (lane >= d) in += a;
+    }
+    if (lane == 31) wsum[warp] = in;
+    __syncthreads();
+    int at = in - sum;
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    for (int g = tid * per; g < min(G, (tid + 1) * per); ++g) {
+      first[g] = at;
+      at += (n[g] + LS_TOK - 1) / LS_TOK;
+    }
+    if (tid == LS_THREADS - 1) first[G] = at;
+    __syncthreads();
+    return first[G];
+  }
+
+  // Group gi: its adapter (or -1), that one's rank, and its rows in tok. cnt:
+  // scratch of LS_WARPS words.
+  __device__ __forceinline__ void rows_of(const LoraParams& p, int gi, int tid, int* cnt, int* tok, int* a, int* r, int* n_tok) {
+    const int lane = tid & 31, warp = tid >> 5, G = p.g.slots + 1;
+    for (int g = tid; g < G; g += LS_THREADS)
+      if (first[g] <= gi && gi < first[g + 1]) found = g;
+    if (tid < LS_TOK) tok[tid] = -1;
+    __syncthreads();
+    const int g = found, skip = (gi - first[g]) * LS_TOK;
+    const int many = rounds(p), t0 = warp * many * 32 + lane;
+    int mine = 0;
+    for (int i = 0; i < many; ++i) mine += __popc(__ballot_sync(0xffffffffu, of[t0 + i * 32] == g));
+    if (lane == 0) cnt[warp] = mine;
+    __syncthreads();
+    int at = -skip;
+    for (int w = 0; w < warp; ++w) at += cnt[w];
+    if (mine && at < LS_TOK && at + mine > 0) {
+      for (int i = 0; i < many; ++i) {
+        const bool same = of[t0 + i * 32] == g;
+        const unsigned with = __ballot_sync(0xffffffffu, same);
+        const int pos = at + __popc(with & ((1u << lane) - 1u));
+        if (same && pos >= 0 && pos < LS_TOK) tok[pos] = t0 + i * 32;
+        at += __popc(with);
+      }
+    }
+    __syncthreads();
+    *a = g < G - 1 ? g : -1;
+    *r = rank[g];
+    *n_tok = min(LS_TOK, n[g] - skip);
+  }
+};
+template <>
+struct LsGroups<false> {
+  __device__ __forceinline__ void clear(const LoraParams&, int) {}
+};
+
 // R: the largest padded rank of the set, rounded up to 16, 32, 64 or 128.
-// PLANNED: the groups come from the plan kernel's tiles of LS_TOK rows, which a
-// fixed number of clusters takes in turn.
+// PLANNED: the batch's groups of LS_TOK rows, counted in each CTA or from the
+// plan kernel's tiles, are taken in turn by as many clusters as run at once.
 template <int ACT, int R, bool PLANNED>
 __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(LoraParams p) {
   extern __shared__ __align__(16) uint8_t ls_sm[];
   __shared__ int s_tok[LS_TOK], s_cnt[LS_WARPS];
+  __shared__ LsGroups<PLANNED> s_groups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = (int)ls_cluster_rank(), ctas = gridDim.x;  // one cluster a grid row
+  const bool counts = PLANNED && p.T <= LS_COUNT_T;
+  if (counts) s_groups.clear(p, tid);
   pdl_wait();
   pdl_trigger();
   const int n0 = cta * p.g.NB / ctas * 64, n1 = min(p.g.N, (cta + 1) * p.g.NB / ctas * 64);
@@ -239,16 +356,21 @@ __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(Lo
       *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + n) =
           p.base ? *reinterpret_cast<const uint4*>(p.base + (size_t)t * p.ldbase + n) : make_uint4(0, 0, 0, 0);
   };
-  const int groups = PLANNED ? p.meta[1] : (int)blockIdx.y + 1;
+  int groups = blockIdx.y + 1;
+  if constexpr (PLANNED) groups = counts ? s_groups.count(p, tid, s_cnt) : p.meta[1];
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
     int a, rank, n_tok;
     if constexpr (PLANNED) {
-      const int4 ti = p.tiles[gi];
-      a = ti.x;
-      rank = ti.w;
-      n_tok = ti.z;
-      if (tid < LS_TOK) s_tok[tid] = tid < n_tok ? p.perm[ti.y + tid] : -1;
-      __syncthreads();
+      if (counts) {
+        s_groups.rows_of(p, gi, tid, s_cnt, s_tok, &a, &rank, &n_tok);
+      } else {
+        const int4 ti = p.tiles[gi];
+        a = ti.x;
+        rank = ti.w;
+        n_tok = ti.z;
+        if (tid < LS_TOK) s_tok[tid] = tid < n_tok ? p.perm[ti.y + tid] : -1;
+        __syncthreads();
+      }
       if (a < 0) {
         for (int i = 0; i < n_tok; ++i) copy_row(s_tok[i]);
         __syncthreads();
@@ -261,7 +383,7 @@ __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(Lo
         copy_row(gi);
         return;
       }
-      // The group: T <= LS_THREADS, so thread j looks at row j.
+      // The group: T <= LS_MAX_T, so thread j looks at row j.
       const bool same = tid < p.T && p.ids[tid] == a;
       if (__syncthreads_count(same && tid < gi) % LS_TOK != 0) return;
       const unsigned later = __ballot_sync(0xffffffffu, same && tid >= gi);
@@ -373,23 +495,28 @@ __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(Lo
       }
     }
     __syncthreads();
-    for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
-      float v = 0.0f;
+    for (int i = 4 * tid; i < n_tok * r16; i += 4 * LS_THREADS) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < LS_WARPS; ++w) v += part[w * LS_TOK * r16 + i];
-      sum[i] = v;
+      for (int w = 0; w < LS_WARPS; ++w) add4(v, *reinterpret_cast<const float4*>(part + w * LS_TOK * r16 + i));
+      *reinterpret_cast<float4*>(sum + i) = v;
     }
     cluster_arrive();
     cluster_wait();
-    for (int i = tid; i < n_tok * r16; i += LS_THREADS) {
-      float f[8], v = 0.0f;
+    for (int i = 4 * tid; i < n_tok * r16; i += 4 * LS_THREADS) {
+      float4 f[8], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) f[c] = c < ctas ? ld_cluster_f32(sum + i, c) : 0.0f;
+      for (int c = 0; c < 8; ++c) f[c] = c < ctas ? ld_cluster_f32x4(sum + i, c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v += f[c];  // the same order in every CTA
+      for (int c = 0; c < 8; ++c) add4(v, f[c]);  // the same order in every CTA
       const int row = i / r16, r = i - row * r16;
       // past the rank A's zeros met whatever x held
-      split_act<ACT>(r < rank ? v : 0.0f, u_hi + row * ur + r, u_lo + row * ur + r);
+      const float u[4] = {r < rank ? v.x : 0.0f, r + 1 < rank ? v.y : 0.0f, r + 2 < rank ? v.z : 0.0f, r + 3 < rank ? v.w : 0.0f};
+      uint16_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_act<ACT>(u[e], hi + e, lo + e);
+      *reinterpret_cast<uint2*>(u_hi + row * ur + r) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+      *reinterpret_cast<uint2*>(u_lo + row * ur + r) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
     }
     __syncthreads();
     cluster_arrive();  // this CTA has read the others' sums
@@ -1286,7 +1413,7 @@ template <int ACT>
 static cudaError_t forward_of(LoraParams p, int num_sms, cudaStream_t st) {
   if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, num_sms, st);
   if (lora_planned_small(p.g, p.T, num_sms)) {
-    const cudaError_t e = launch_plan(p, LS_TOK, st);
+    const cudaError_t e = p.T <= LS_COUNT_T ? cudaSuccess : launch_plan(p, LS_TOK, st);
     return e == cudaSuccess ? small_of<ACT, true>(p, num_sms, st) : e;
   }
   return tiled_of<ACT>(p, num_sms, st);
