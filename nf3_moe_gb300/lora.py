@@ -11,13 +11,23 @@ import ctypes
 import torch
 
 from . import _lib, _need, act_torch_dtype, hmoe_workspace_init
-from ._lib import ACT_BF16, LoraDesc
+from ._lib import ACT_BF16, ACT_F16, LoraDesc
 from .rows import _bytes, _is, _is_ws, _raw_stream
+
+_TORCH = {ACT_BF16: torch.bfloat16, ACT_F16: torch.float16}
 
 
 def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
     """A [T, width] tensor whose rows are contiguous and evenly spaced (a column range of a wider one serves), on the
     device of this index. Returns the row stride."""
+    try:  # nearly always right: one look, and the checks below for their messages
+        rows, wide = t.shape
+        at = t.get_device()
+        if t.dtype is dtype and wide == width and (rows == T or T is None) and t.is_contiguous() and (
+                not cuda or at >= 0 and (at == device or device is None)):
+            return width
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -26,8 +36,6 @@ def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
         raise ValueError(f"{name} must have shape [{'*' if T is None else T}, {width}], got {list(t.shape)}")
     if cuda and (t.get_device() < 0 or (device is not None and t.get_device() != device)):
         raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{device}" if device is not None else "") + f", got one on {t.device}")
-    if t.is_contiguous():
-        return width
     ld, one = t.stride()
     if one != 1 or (ld < width and t.shape[0] > 1):
         raise ValueError(f"the rows of {name} must be contiguous and must not overlap, got strides {list(t.stride())}")
@@ -36,7 +44,7 @@ def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
 
 def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
     """Returns T, the row strides of x, base and out, and the device index."""
-    dt, N = act_torch_dtype(desc.act_dtype), desc.N
+    dt, N = _TORCH[desc.act_dtype], desc.N
     ldx = _need_rows("x", x, None, desc.K, dt, cuda=cuda)
     T, dev = x.shape[0], x.get_device()
     _is("ids", ids, (T,), torch.int32, dev, cuda)

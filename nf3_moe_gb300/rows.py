@@ -32,7 +32,7 @@ def _is(name, t, shape, dtype, device, cuda=True):
     """_need for a tensor that is nearly always right: one look, and the full check for its message. device: its
     index, as get_device gives it (-1 on the host)."""
     try:
-        if t.shape == shape and t.dtype == dtype and t.is_contiguous() and (t.get_device() == device >= 0 or not cuda):
+        if t.shape == shape and t.dtype is dtype and t.is_contiguous() and (t.get_device() == device >= 0 or not cuda):
             return
     except AttributeError:
         pass
@@ -58,7 +58,7 @@ def _raw_stream(stream, device):
 
 
 def _bytes(ws):
-    return ws.numel() * ws.element_size()
+    return ws.nbytes
 
 
 def hmoe_dispatch_rows(desc, T):
@@ -80,7 +80,7 @@ def _check_tokens(name, desc, t, cuda):
     try:
         T, width = t.shape
         device = t.get_device()
-        if width == H and t.dtype == dt and t.is_contiguous() and (device >= 0 or not cuda):
+        if width == H and t.dtype is dt and t.is_contiguous() and (device >= 0 or not cuda):
             return T, H, dt, device
     except (AttributeError, ValueError):
         pass
