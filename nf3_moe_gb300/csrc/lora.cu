@@ -150,7 +150,7 @@ constexpr int LS_MAX_T = 128;  // at most LS_THREADS: the grouping looks at one 
 constexpr int ls_per_sm(int r16) { return r16 <= 64 ? 2 : 1; }
 // What a batch is likely to look like, from what the host knows of it: rows
 // that draw their adapters at random from the slots have slots (1 - exp(-T /
-// slots)) of them, and each makes about max(1, rows / 16 + 0.4) groups.
+// slots)) of them, and each makes about max(1, rows / 16 + 0.47) groups.
 struct LoraBatch {
   double adapters, rows, groups;  // rows: of one adapter
 };
@@ -158,35 +158,42 @@ inline LoraBatch lora_batch(const LoraGeom& g, int T) {
   LoraBatch b;
   b.adapters = g.slots * (1.0 - exp(-(double)T / g.slots));
   b.rows = T / b.adapters;
-  b.groups = b.adapters * fmax(1.0, b.rows / LS_TOK + 0.4);
+  b.groups = b.adapters * fmax(1.0, b.rows / LS_TOK + 0.47);
   return b;
 }
-// CTAs of a cluster, 2 to 8: as many as let the groups run in one wave (a
-// twelfth of the places is left over, clusters do not pack exactly). A group of
-// more CTAs is a shorter wait, a second wave is another: 64 rows of 64 adapters
-// of rank 64, 6144x6144 took 17.9, 14.6 and 17.3 us with 4, 6 and 8; 128 of 128,
-// rank 32, 16.9, 20.0 and 23.1 with 3, 4 and 8; 1024 of 64 38.1, 31.8 and 39.1
-// with 2, 3 and 4; one row 8.3, 6.7 and 6.1 with 4, 6 and 8.
+// CTAs of a cluster, 2 to 8: as many as let the groups run in one wave, by how
+// many clusters of a size run at once (fits[c]; a cluster stays in one part of
+// the chip, so 43 of 7 do not run at once on 152 SMs with two CTAs each). A
+// group of more CTAs is a shorter wait, a second wave is another: 64 rows of 64
+// adapters of rank 64, 6144x6144 took 17.9, 14.6 and 17.3 us with 4, 6 and 8; 128
+// of 128, rank 32, 16.9, 20.0 and 23.1 with 3, 4 and 8; 1024 of 64 38.1, 30.6 and
+// 39.1 with 2, 3 and 4; 581 of 7, rank 13, 176x768, 7.9 and 12.7 with 6 and 7;
+// one row 8.3, 6.7 and 6.1 with 4, 6 and 8.
 // Where the adapters are small and each row has a cluster of its own, starting
 // the clusters is what counts: 256 CTAs in all (64 rows of rank 16, 2048x2048:
-// 4.9, 5.8 and 7.4 us with 4, 6 and 8; 256 rows: 7.4 and 9.2 with 2 and 4).
-inline int ls_cluster(const LoraGeom& g, int T, int num_sms) {
-  double c = 0.92 * ls_per_sm(g.max_r16) * num_sms / lora_batch(g, T).groups;
-  if (T <= LS_MAX_T && (long long)(g.KB + g.NB) * g.max_r16 * 128 < 512 << 10) c = fmin(c, 256.0 / T);
-  return c < 2 ? 2 : (c > 8 ? 8 : (int)c);
+// 4.9, 5.8 and 7.4 us with 4, 6 and 8).
+constexpr int LS_MAX_CLUSTER = 8;
+inline int ls_cluster(const LoraGeom& g, int T, const int* fits) {
+  const double groups = lora_batch(g, T).groups;
+  int c = LS_MAX_CLUSTER;
+  while (c > 2 && fits[c] < 1.02 * groups) --c;
+  if (T <= LS_MAX_T && (long long)(g.KB + g.NB) * g.max_r16 * 128 < 512 << 10)
+    while (c > 2 && c * T > 256) --c;
+  return c;
 }
 // Whether the small kernel serves a batch above LS_MAX_T rows over planned groups
 // of 16 rows, or the tile kernels do. It reads an adapter again for each group,
 // but has fewer steps than they, whose cost goes by tiles of 128 rows, however
 // few there are in one. So it takes a batch whose groups run in one wave of
 // small clusters, and one whose adapters have few rows, the fewer the larger
-// the rank. Measured at 6144x6144, small against tiles: 260 rows of 64 adapters,
-// rank 64: 23.9, 51.3 us; 1536 of 8, rank 64: 38.5, 41.6; 3000 of 8, rank 16: 41.2,
-// 35.9; 2048 of 64, rank 64: 59.7, 55.5; 2048 of 64, rank 32: 47.1, 52.5; 4096 of
-// 256, rank 64: 106, 171; rank 128, 1024 of 8: 45.8, 62.1; 1024 of 64: 80.6, 67.7.
+// the rank (above 64 it has one CTA an SM). Measured at 6144x6144, small against
+// tiles: 260 rows of 64 adapters, rank 64: 22.5, 51.5 us; 1536 of 8, rank 64: 39.3,
+// 40.0; 3000 of 8, rank 16: 42.2, 35.3; 2048 of 64, rank 64: 57.6, 55.8 (704x704:
+// 12.1, 21.3); 2048 of 64, rank 32: 46.2, 52.3; 4096 of 256, rank 64: 108, 170;
+// rank 128, 1024 of 8: 46.9, 57.9; 1024 of 64: 87.7, 67.5.
 inline bool lora_planned_small(const LoraGeom& g, int T, int num_sms) {
   const LoraBatch b = lora_batch(g, T);
-  return b.groups <= 0.45 * ls_per_sm(g.max_r16) * num_sms || b.rows * g.max_r16 <= 1024.0;
+  return b.groups <= 0.45 * ls_per_sm(g.max_r16) * num_sms || b.rows * g.max_r16 <= (g.max_r16 <= 64 ? 2200.0 : 1100.0);
 }
 
 __device__ __forceinline__ uint32_t ls_cluster_rank() {
@@ -586,32 +593,45 @@ __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(Lo
 // One cluster a grid row; PLANNED: the groups are in the plan, and as many
 // clusters as run at once take them.
 template <int ACT, int R, bool PLANNED>
-static cudaError_t small_as(const LoraParams& p, int num_sms, cudaStream_t st) {
+static cudaError_t small_as(const LoraParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = ensure_smem_attr(lora_small_kernel<ACT, R, PLANNED>, ls_smem(R), done);
   if (e != cudaSuccess) return e;
-  const unsigned ctas = (unsigned)ls_cluster(p.g, p.T, num_sms);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, PLANNED ? (unsigned)(ls_per_sm(R) * num_sms) / ctas : (unsigned)p.T);
   cfg.blockDim = dim3(LS_THREADS);
-  cfg.dynamicSmemBytes = (size_t)ls_smem(p.g.max_r16);
+  cfg.dynamicSmemBytes = (size_t)ls_smem(R);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {ctas, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  // How many clusters of each size run at once, asked once.
+  static std::atomic<int> known[LS_MAX_CLUSTER + 1];
+  int fits[LS_MAX_CLUSTER + 1] = {};
+  for (unsigned c = 2; c <= LS_MAX_CLUSTER; ++c) {
+    fits[c] = known[c].load(std::memory_order_relaxed);
+    if (fits[c] > 0) continue;
+    attr[1].val.clusterDim = {c, 1, 1};
+    cfg.gridDim = dim3(c);
+    e = cudaOccupancyMaxActiveClusters(&fits[c], lora_small_kernel<ACT, R, PLANNED>, &cfg);
+    if (e != cudaSuccess) return e;
+    fits[c] = fits[c] < 1 ? 1 : fits[c];
+    known[c].store(fits[c], std::memory_order_relaxed);
+  }
+  const unsigned ctas = (unsigned)ls_cluster(p.g, p.T, fits);
+  attr[1].val.clusterDim = {ctas, 1, 1};
+  cfg.gridDim = dim3(ctas, PLANNED ? (unsigned)fits[ctas] : (unsigned)p.T);
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, lora_small_kernel<ACT, R, PLANNED>, p);
 }
 template <int ACT, bool PLANNED>
-static cudaError_t small_of(const LoraParams& p, int num_sms, cudaStream_t st) {
-  if (p.g.max_r16 <= 16) return small_as<ACT, 16, PLANNED>(p, num_sms, st);
-  if (p.g.max_r16 <= 32) return small_as<ACT, 32, PLANNED>(p, num_sms, st);
-  if (p.g.max_r16 <= 64) return small_as<ACT, 64, PLANNED>(p, num_sms, st);
-  return small_as<ACT, 128, PLANNED>(p, num_sms, st);
+static cudaError_t small_of(const LoraParams& p, cudaStream_t st) {
+  if (p.g.max_r16 <= 16) return small_as<ACT, 16, PLANNED>(p, st);
+  if (p.g.max_r16 <= 32) return small_as<ACT, 32, PLANNED>(p, st);
+  if (p.g.max_r16 <= 64) return small_as<ACT, 64, PLANNED>(p, st);
+  return small_as<ACT, 128, PLANNED>(p, st);
 }
 
 // ------------------------------------------------------------ larger batches: plan, A x, B u
@@ -1411,10 +1431,10 @@ static cudaError_t tiled_of(LoraParams p, int num_sms, cudaStream_t st) {
 
 template <int ACT>
 static cudaError_t forward_of(LoraParams p, int num_sms, cudaStream_t st) {
-  if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, num_sms, st);
+  if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, st);
   if (lora_planned_small(p.g, p.T, num_sms)) {
     const cudaError_t e = p.T <= LS_COUNT_T ? cudaSuccess : launch_plan(p, LS_TOK, st);
-    return e == cudaSuccess ? small_of<ACT, true>(p, num_sms, st) : e;
+    return e == cudaSuccess ? small_of<ACT, true>(p, st) : e;
   }
   return tiled_of<ACT>(p, num_sms, st);
 }
