@@ -122,12 +122,16 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 // A cluster of C CTAs serves up to LS_TOK rows of one adapter: CTA c sums A x
 // over its share of K, the CTAs exchange their partial sums through
 // distributed shared memory, and each adds B u for its share of N. The batch
-// is grouped without a pass of its own: cluster t belongs to row t, and goes
-// on only if row t is the first of a group, that is if the number of earlier
-// rows with the same id is a multiple of LS_TOK.
+// is grouped without a pass of its own: up to LS_MAX_T rows, cluster t belongs to
+// row t, and goes on only if row t is the first of a group, that is if the number
+// of earlier rows with the same id is a multiple of LS_TOK (256 rows of 8 adapters
+// of rank 64, 6144x6144: 17.5 us, counted as below 15.8; 64 rows 14.6, counted
+// 16.0).
 //
-// The adapters' bytes bound it where the batch is large (64 rows of 64 adapters
-// of ranks 1 to 64, 6144x6144: 33 MB in 14.4 us); below, a chain of waits does:
+// What the busiest SM fetches bounds it where the batch is large (64 rows of 64
+// adapters of ranks 1 to 64, 6144x6144: 33 MB in 14.0 us, but two CTAs of rank 64
+// on one SM fetch 512 KB, at 30 to 36 KB a us however many loads are in flight:
+// rings of bulk copies took 16.7 us); below, a chain of waits does:
 // ids, A and x, the cluster's exchange, B (one row of rank 16, 2048x2048: 3.6 us,
 // of rank 64, 6144x6144: 6.1 us). So a CTA has the next step's operands on their
 // way, B's first ones and the base's before the exchange, and only the group's
@@ -237,7 +241,9 @@ __host__ __device__ constexpr int ls_smem(int r16) {
 // of each adapter counted (counts do not depend on the order of the atomics),
 // the counts scanned to the adapters' first groups, and a group's rows picked
 // out by their places among its adapter's rows. The plan kernel finds the same
-// groups, in the same order, and is a launch to wait for.
+// groups, in the same order, and is a launch to wait for (1111 rows of 32
+// adapters of ranks to 48, 6144x2056: 21.2 us with it, 19.6 without; 512 rows of
+// 64, rank 16, 2048x2048: 9.7, 7.9; 3000 of 512, rank 16, 6144x6144: 82.7, 85.8).
 constexpr int LS_COUNT_T = 2048;
 template <bool PLANNED>
 struct LsGroups {
