@@ -231,25 +231,21 @@ __global__ void __launch_bounds__(MAX_E) dispatch_small_kernel(DispatchPlan p, R
 }
 
 // ------------------------------------------------------------ the gates' gradient of one token
-// dg: the token's topk dot products, in shared memory. Called by nthreads
-// threads; no barrier inside.
-__device__ __forceinline__ void write_gate_grads(const float* dg, const float* gates, const int* ids, int t, int k,
-                                                 int E, float* dgates, float* dlogits, int tid, int nthreads,
-                                                 int* status) {
+// dg, g, ids: the token's topk dot products, gates and experts, in shared
+// memory. Called by nthreads threads; no barrier inside.
+__device__ __forceinline__ void write_gate_grads(const float* dg, const float* g, const int* ids, int t, int k, int E,
+                                                 float* dgates, float* dlogits, int tid, int nthreads, int* status) {
   if (dgates && tid < k) dgates[(size_t)t * k + tid] = dg[tid];
   if (!dlogits) return;
   float mean = 0.0f;  // sum_i g_i dg_i, ascending i
-  for (int j = 0; j < k; ++j) mean = fmaf(gates[(size_t)t * k + j], dg[j], mean);
+  for (int j = 0; j < k; ++j) mean = fmaf(g[j], dg[j], mean);
   for (int e = tid; e < E; e += nthreads) {
     float v = 0.0f;
     for (int j = 0; j < k; ++j)
-      if (ids[(size_t)t * k + j] == e) v = gates[(size_t)t * k + j] * (dg[j] - mean);
+      if (ids[j] == e) v = g[j] * (dg[j] - mean);
     dlogits[(size_t)t * E + e] = v;
   }
-  if (tid < k) {
-    const int e = ids[(size_t)t * k + tid];
-    if (e < 0 || e >= E) set_status(status, DEV_BAD_ROUTE);
-  }
+  if (tid < k && (ids[tid] < 0 || ids[tid] >= E)) set_status(status, DEV_BAD_ROUTE);
 }
 
 // ------------------------------------------------------------ one token a CTA
@@ -259,24 +255,33 @@ __device__ __forceinline__ void write_gate_grads(const float* dg, const float* g
 // and the rows' accesses are in flight together.
 constexpr int ROWS_THREADS = 256;
 
-// The rows and weights of token t's slots, in shared memory (a barrier follows).
-__device__ __forceinline__ void token_slots(const RowsParams& p, int t, int* s_row, float* s_g) {
+// The rows and weights of token t's slots (and, for the router's gradient, their
+// experts: at the end they would be waited for), in shared memory (a barrier
+// follows).
+struct TokenSlots {
+  int row[MAX_TOPK], id[MAX_TOPK];
+  float g[MAX_TOPK];
+};
+template <bool IDS>
+__device__ __forceinline__ void token_slots(const RowsParams& p, int t, TokenSlots& s) {
   const int j = threadIdx.x;
   if (j < p.topk) {
-    int r = p.slot_row[(size_t)t * p.topk + j];
+    const size_t at = (size_t)t * p.topk + j;
+    int r = p.slot_row[at];
+    if constexpr (IDS) s.id[j] = p.dlogits ? p.ids[at] : 0;
+    s.g[j] = p.gates ? p.gates[at] : 1.0f;
     if (r >= p.R) {
       set_status(p.status, DEV_BAD_ROUTE);
       r = -1;
     }
-    s_row[j] = r;
-    s_g[j] = p.gates ? p.gates[(size_t)t * p.topk + j] : 1.0f;
+    s.row[j] = r;
   }
 }
 
 // The token's dot products from the threads' parts, then its gate gradients.
 template <int KD>
 __device__ __forceinline__ void token_dots(const RowsParams& p, int t, const float* dot, float (*s_part)[ROWS_THREADS / 32],
-                                           float* s_dg) {
+                                           float* s_dg, const TokenSlots& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 #pragma unroll
   for (int j = 0; j < KD; ++j) {
@@ -292,7 +297,7 @@ __device__ __forceinline__ void token_dots(const RowsParams& p, int t, const flo
     s_dg[tid] = d;
   }
   __syncthreads();
-  write_gate_grads(s_dg, p.gates, p.ids, t, p.topk, p.E, p.dgates, p.dlogits, tid, ROWS_THREADS, p.status);
+  write_gate_grads(s_dg, s.g, s.id, t, p.topk, p.E, p.dgates, p.dlogits, tid, ROWS_THREADS, p.status);
 }
 
 // spread: rows[slot_row[t,j]] = (g[t,j]) v[t], and with KDOT > 0 (at least topk)
@@ -303,8 +308,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
   using P = Piece<DT, VEC>;
   using E = typename P::E;
   constexpr int KD = KDOT > 0 ? KDOT : 1;
-  __shared__ int s_row[MAX_TOPK];
-  __shared__ float s_g[MAX_TOPK];
+  __shared__ TokenSlots s;
   __shared__ float s_part[KD][ROWS_THREADS / 32];
   __shared__ float s_dg[KD];
   pdl_wait();
@@ -319,13 +323,13 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
     for (int i = 0; i < P::N; ++i) zero.set(i, 0.0f);
     const long long nw = (long long)(gridDim.x - p.T) * gridDim.y * (ROWS_THREADS / 32);
     for (long long r = ((long long)(t - p.T) * gridDim.y + blockIdx.y) * (ROWS_THREADS / 32) + warp; r < p.R; r += nw) {
-      const int s = p.row_slot[r];
-      if (s >= 0 && s < p.T * k) continue;
+      const int slot = p.row_slot[r];
+      if (slot >= 0 && slot < p.T * k) continue;
       for (int c = lane; c < cols; c += 32) zero.store_once(rows + (size_t)r * p.H + (size_t)c * P::N);
     }
     return;
   }
-  token_slots(p, t, s_row, s_g);
+  token_slots<(KDOT > 0)>(p, t, s);
   __syncthreads();
   const E* v = static_cast<const E*>(p.v) + (size_t)t * p.H;
   const E* other = static_cast<const E*>(p.other);
@@ -342,35 +346,35 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
         P b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j0 + j < k && s_row[j0 + j] >= 0) b[j].load_once(other + (size_t)s_row[j0 + j] * p.H + (size_t)c * P::N);
+          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load_once(other + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (j0 + j >= k || s_row[j0 + j] < 0) continue;
-          const float g = s_g[j0 + j];
+          if (j0 + j >= k || s.row[j0 + j] < 0) continue;
+          const float g = s.g[j0 + j];
           P o;
 #pragma unroll
           for (int i = 0; i < P::N; ++i) {
             dot[j0 + j] = fmaf(a.f(i), b[j].f(i), dot[j0 + j]);
             o.set(i, g * a.f(i));
           }
-          o.store_once(rows + (size_t)s_row[j0 + j] * p.H + (size_t)c * P::N);
+          o.store_once(rows + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
         }
       }
     } else {
 #pragma unroll 8
       for (int j = 0; j < k; ++j) {
-        const int r = s_row[j];
+        const int r = s.row[j];
         if (r < 0) continue;
         P o = a;
         if (p.gates) {
 #pragma unroll
-          for (int i = 0; i < P::N; ++i) o.set(i, s_g[j] * a.f(i));
+          for (int i = 0; i < P::N; ++i) o.set(i, s.g[j] * a.f(i));
         }
         o.store_once(rows + (size_t)r * p.H + (size_t)c * P::N);
       }
     }
   }
-  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg);
+  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg, s);
 }
 
 // collect: out[t] = sum_j (g[t,j]) rows[slot_row[t,j]], ascending j, and with
@@ -380,8 +384,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
   using P = Piece<DT, VEC>;
   using E = typename P::E;
   constexpr int KD = KDOT > 0 ? KDOT : 1;
-  __shared__ int s_row[MAX_TOPK];
-  __shared__ float s_g[MAX_TOPK];
+  __shared__ TokenSlots s;
   __shared__ float s_part[KD][ROWS_THREADS / 32];
   __shared__ float s_dg[KD];
   pdl_wait();
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
   const int tid = threadIdx.x;
   const int k = p.topk, t = blockIdx.x;
   const int cols = p.H / P::N;
-  token_slots(p, t, s_row, s_g);
+  token_slots<(KDOT > 0)>(p, t, s);
   __syncthreads();
   const E* rows = static_cast<const E*>(p.rows_in);
   E* out = static_cast<E*>(p.out) + (size_t)t * p.H;
@@ -413,11 +416,11 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
         P b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j0 + j < k && s_row[j0 + j] >= 0) b[j].load_once(rows + (size_t)s_row[j0 + j] * p.H + (size_t)c * P::N);
+          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load_once(rows + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (j0 + j >= k || s_row[j0 + j] < 0) continue;
-          const float g = s_g[j0 + j];
+          if (j0 + j >= k || s.row[j0 + j] < 0) continue;
+          const float g = s.g[j0 + j];
 #pragma unroll
           for (int i = 0; i < P::N; ++i) {
             acc[i] = fmaf(g, b[j].f(i), acc[i]);
@@ -434,11 +437,11 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
         P b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j0 + j < k && s_row[j0 + j] >= 0) b[j].load(rows + (size_t)s_row[j0 + j] * p.H + (size_t)c * P::N);
+          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load(rows + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (j0 + j >= k || s_row[j0 + j] < 0) continue;
-          const float g = s_g[j0 + j];
+          if (j0 + j >= k || s.row[j0 + j] < 0) continue;
+          const float g = s.g[j0 + j];
 #pragma unroll
           for (int i = 0; i < P::N; ++i) acc[i] = fmaf(g, b[j].f(i), acc[i]);
         }
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
     for (int i = 0; i < P::N; ++i) o.set(i, acc[i]);
     o.store(out + (size_t)c * P::N);
   }
-  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg);
+  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg, s);
 }
 
 // ------------------------------------------------------------ launchers
