@@ -17,11 +17,11 @@
 //
 // HBM bounds them all from some hundred rows on. At 4096 tokens of 6144 16-bit
 // columns, 256 experts, top-8 (of the copy bandwidth 6.70 TB/s):
-//   dispatch, with its plan      453 MB   74 us   91%
-//   combine                      453 MB   69 us   98%
-//   combine's gradient, with the gates' and logits', 860 MB, 133 us, 97%
+//   dispatch, with its plan      453 MB   73.4 us   92%
+//   combine                      453 MB   67.3 us   100%
+//   combine's gradient, with the gates' and logits', 860 MB, 131 us, 98%
 // Small batches are a launch or two: 8 tokens dispatched in 3.2 us, one token
-// combined in 2.2 us.
+// combined in 2.1 us.
 #include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -253,7 +253,17 @@ __device__ __forceinline__ void write_gate_grads(const float* dg, const float* g
 // dot products need them together), 16 bytes each. A thread meets the token's
 // topk rows at its columns, so each value of the token is read or written once
 // and the rows' accesses are in flight together.
+// Narrow rows share a CTA, each with 32, 64 or 128 of its threads.
 constexpr int ROWS_THREADS = 256;
+constexpr int ROWS_TOKENS = 8;  // of a CTA, at most
+template <bool MANY>
+struct TokenCta {
+  static constexpr int TOKENS = MANY ? ROWS_TOKENS : 1;
+  static __device__ __forceinline__ int threads() { return MANY ? blockDim.x : ROWS_THREADS; }  // of a token
+  static __device__ __forceinline__ int tokens() { return MANY ? blockDim.y : 1; }
+  static __device__ __forceinline__ int at() { return MANY ? threadIdx.y : 0; }
+  static __device__ __forceinline__ int token() { return blockIdx.x * tokens() + at(); }
+};
 
 // The rows and weights of token t's slots (and, for the router's gradient, their
 // experts: at the end they would be waited for), in shared memory (a barrier
@@ -265,7 +275,7 @@ struct TokenSlots {
 template <bool IDS>
 __device__ __forceinline__ void token_slots(const RowsParams& p, int t, TokenSlots& s) {
   const int j = threadIdx.x;
-  if (j < p.topk) {
+  if (j < p.topk && t < p.T) {
     const size_t at = (size_t)t * p.topk + j;
     int r = p.slot_row[at];
     if constexpr (IDS) s.id[j] = p.dlogits ? p.ids[at] : 0;
@@ -278,51 +288,61 @@ __device__ __forceinline__ void token_slots(const RowsParams& p, int t, TokenSlo
   }
 }
 
-// The token's dot products from the threads' parts, then its gate gradients.
-template <int KD>
-__device__ __forceinline__ void token_dots(const RowsParams& p, int t, const float* dot, float (*s_part)[ROWS_THREADS / 32],
-                                           float* s_dg, const TokenSlots& s) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The tokens' dot products from the threads' parts, then their gate gradients.
+template <int KD, bool MANY>
+struct TokenDots {
+  float part[KD][ROWS_THREADS / 32], dg[TokenCta<MANY>::TOKENS][KD];
+};
+template <int KD, bool MANY>
+__device__ __forceinline__ void token_dots(const RowsParams& p, int t, const float* dot, TokenDots<KD, MANY>& d, const TokenSlots& s) {
+  using C = TokenCta<MANY>;
+  const int tid = threadIdx.x, y = C::at(), lane = tid & 31, warps = C::threads() / 32, w0 = y * warps;
 #pragma unroll
   for (int j = 0; j < KD; ++j) {
-    float d = dot[j];
+    float v = dot[j];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-    if (lane == 0) s_part[j][warp] = d;
+    for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+    if (lane == 0) d.part[j][w0 + (tid >> 5)] = v;
   }
   __syncthreads();
   if (tid < p.topk) {
-    float d = 0.0f;
-    for (int w = 0; w < ROWS_THREADS / 32; ++w) d += s_part[tid][w];
-    s_dg[tid] = d;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < ROWS_THREADS / 32; ++w)
+      if (w < warps) v += d.part[tid][w0 + w];
+    d.dg[y][tid] = v;
   }
   __syncthreads();
-  write_gate_grads(s_dg, s.g, s.id, t, p.topk, p.E, p.dgates, p.dlogits, tid, ROWS_THREADS, p.status);
+  if (t < p.T) write_gate_grads(d.dg[y], s.g, s.id, t, p.topk, p.E, p.dgates, p.dlogits, tid, C::threads(), p.status);
 }
 
 // spread: rows[slot_row[t,j]] = (g[t,j]) v[t], and with KDOT > 0 (at least topk)
 // dg[t,j] = <v[t], other[slot_row[t,j]]>. The CTAs past the tokens write zeros
 // to the rows without a slot.
-template <int DT, bool VEC, int KDOT>
+template <int DT, bool VEC, int KDOT, bool MANY>
 __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
   using P = Piece<DT, VEC>;
   using E = typename P::E;
   constexpr int KD = KDOT > 0 ? KDOT : 1;
-  __shared__ TokenSlots s;
-  __shared__ float s_part[KD][ROWS_THREADS / 32];
-  __shared__ float s_dg[KD];
+  using C = TokenCta<MANY>;
+  __shared__ TokenSlots s_slots[C::TOKENS];
+  __shared__ TokenDots<KD, MANY> s_dots;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int k = p.topk, t = blockIdx.x;
-  const int cols = p.H / P::N, step = ROWS_THREADS * gridDim.y;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int k = p.topk, t = C::token();
+  const int cols = p.H / P::N, step = C::threads() * gridDim.y;
+  const int blocks = (p.T + C::tokens() - 1) / C::tokens();  // with tokens
+  TokenSlots& s = s_slots[C::at()];
   E* rows = static_cast<E*>(p.rows_out);
-  if (t >= p.T) {
+  if ((int)blockIdx.x >= blocks) {
     P zero;
 #pragma unroll
     for (int i = 0; i < P::N; ++i) zero.set(i, 0.0f);
-    const long long nw = (long long)(gridDim.x - p.T) * gridDim.y * (ROWS_THREADS / 32);
-    for (long long r = ((long long)(t - p.T) * gridDim.y + blockIdx.y) * (ROWS_THREADS / 32) + warp; r < p.R; r += nw) {
+    constexpr int warps = ROWS_THREADS / 32;
+    const int warp = (C::at() * C::threads() + tid) / 32;
+    const long long nw = (long long)(gridDim.x - blocks) * gridDim.y * warps;
+    for (long long r = ((long long)(blockIdx.x - blocks) * gridDim.y + blockIdx.y) * warps + warp; r < p.R; r += nw) {
       const int slot = p.row_slot[r];
       if (slot >= 0 && slot < p.T * k) continue;
       for (int c = lane; c < cols; c += 32) zero.store_once(rows + (size_t)r * p.H + (size_t)c * P::N);
@@ -336,7 +356,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
   float dot[KD];
 #pragma unroll
   for (int j = 0; j < KD; ++j) dot[j] = 0.0f;
-  for (int c = blockIdx.y * ROWS_THREADS + tid; c < cols; c += step) {
+  for (int c = blockIdx.y * C::threads() + tid; c < cols && (!MANY || t < p.T); c += step) {
     P a;
     a.load(v + (size_t)c * P::N);
     if constexpr (KDOT > 0) {
@@ -374,24 +394,25 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
       }
     }
   }
-  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg, s);
+  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_dots, s);
 }
 
 // collect: out[t] = sum_j (g[t,j]) rows[slot_row[t,j]], ascending j, and with
 // KDOT > 0 (at least topk) dg[t,j] = <rows[slot_row[t,j]], v[t]>.
-template <int DT, bool VEC, int KDOT>
+template <int DT, bool VEC, int KDOT, bool MANY>
 __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
   using P = Piece<DT, VEC>;
   using E = typename P::E;
   constexpr int KD = KDOT > 0 ? KDOT : 1;
-  __shared__ TokenSlots s;
-  __shared__ float s_part[KD][ROWS_THREADS / 32];
-  __shared__ float s_dg[KD];
+  using C = TokenCta<MANY>;
+  __shared__ TokenSlots s_slots[C::TOKENS];
+  __shared__ TokenDots<KD, MANY> s_dots;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  const int k = p.topk, t = blockIdx.x;
+  const int k = p.topk, t = C::token();
   const int cols = p.H / P::N;
+  TokenSlots& s = s_slots[C::at()];
   token_slots<(KDOT > 0)>(p, t, s);
   __syncthreads();
   const E* rows = static_cast<const E*>(p.rows_in);
@@ -400,7 +421,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
   float dot[KD];
 #pragma unroll
   for (int j = 0; j < KD; ++j) dot[j] = 0.0f;
-  for (int c = blockIdx.y * ROWS_THREADS + tid; c < cols; c += ROWS_THREADS * gridDim.y) {
+  for (int c = blockIdx.y * C::threads() + tid; c < cols && (!MANY || t < p.T); c += C::threads() * gridDim.y) {
     float acc[P::N];
 #pragma unroll
     for (int i = 0; i < P::N; ++i) acc[i] = 0.0f;
@@ -452,7 +473,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
     for (int i = 0; i < P::N; ++i) o.set(i, acc[i]);
     o.store(out + (size_t)c * P::N);
   }
-  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_part, s_dg, s);
+  if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_dots, s);
 }
 
 // ------------------------------------------------------------ launchers
@@ -472,22 +493,44 @@ static unsigned column_parts(const RowsParams& p, bool vec) {
   return (unsigned)(parts < 1 ? 1 : (parts < 65535 ? parts : 65535));
 }
 
+// Threads of a token and tokens of a CTA. Where tokens are many and rows narrow,
+// a CTA of 256 threads for each costs more than its rows: its start, the slots'
+// look-up and the dot products' barriers. So below 256 pieces a token gets as few
+// threads as leave each up to 4 pieces, and one piece where rows are only written
+// (8192 tokens of 256 16-bit columns, top-8, with 32 threads and with 256:
+// dispatch 9.3 and 12.8 us, combine 9.2 and 28.2, their gradients 13.2 and 39.7,
+// 16.4 and 47.2; 4096 of 1536, top-4, with 64 and 256: the gradients 15.9 and
+// 22.0, 23.8 and 30.7). With 256 pieces and more a token has all threads (2051 of
+// 2048, top-8: dispatch's gradient 15.5 us, 17.8 with 128), and so it has where
+// tokens are few (300 of 1000: combine 2.1 us, 4.1 with 32).
+static dim3 token_block(const RowsParams& p, bool vec, bool reads, int num_sms) {
+  const int n = vec ? 16 / (p.row_dtype == ROW_F32 ? 4 : 2) : 1, cols = p.H / n;
+  unsigned threads = ROWS_THREADS;
+  if (p.T >= 4 * num_sms && cols < ROWS_THREADS)
+    while (threads > 32 && cols <= (int)threads / 2 * (reads ? 4 : 1)) threads /= 2;
+  return dim3(threads, ROWS_THREADS / threads);
+}
+
+template <int DT, bool VEC, bool MANY>
+static cudaError_t spread_with(const RowsParams& p, dim3 grid, dim3 block, cudaStream_t st) {
+  if (!p.other) return launch_pdl(spread_kernel<DT, VEC, 0, MANY>, grid, block, 0, st, p);
+  return p.topk <= 8 ? launch_pdl(spread_kernel<DT, VEC, 8, MANY>, grid, block, 0, st, p)
+                     : launch_pdl(spread_kernel<DT, VEC, MAX_TOPK, MANY>, grid, block, 0, st, p);
+}
 template <int DT, bool VEC>
-static cudaError_t spread_as(const RowsParams& p, dim3 grid, cudaStream_t st) {
-  const dim3 block(ROWS_THREADS);
-  if (!p.other) return launch_pdl(spread_kernel<DT, VEC, 0>, grid, block, 0, st, p);
-  return p.topk <= 8 ? launch_pdl(spread_kernel<DT, VEC, 8>, grid, block, 0, st, p)
-                     : launch_pdl(spread_kernel<DT, VEC, MAX_TOPK>, grid, block, 0, st, p);
+static cudaError_t spread_as(const RowsParams& p, dim3 grid, dim3 block, cudaStream_t st) {
+  return block.y > 1 ? spread_with<DT, VEC, true>(p, grid, block, st) : spread_with<DT, VEC, false>(p, grid, block, st);
 }
 cudaError_t launch_spread(const RowsParams& p, int num_sms, cudaStream_t st) {
   const bool vec = rows_vectorised(p);
   const int pads = p.has_pads ? (p.R / 8 + 1 < num_sms * 4 ? p.R / 8 + 1 : num_sms * 4) : 0;
-  const dim3 grid((unsigned)p.T + (unsigned)pads, p.other ? 1 : column_parts(p, vec));
   if (p.T == 0) return cudaSuccess;
+  const dim3 block = token_block(p, vec, p.other != nullptr, num_sms);
+  const dim3 grid(((unsigned)p.T + block.y - 1) / block.y + (unsigned)pads, p.other || block.y > 1 ? 1 : column_parts(p, vec));
   cudaError_t e;
-  if (p.row_dtype == ROW_BF16) e = vec ? spread_as<ROW_BF16, true>(p, grid, st) : spread_as<ROW_BF16, false>(p, grid, st);
-  else if (p.row_dtype == ROW_F16) e = vec ? spread_as<ROW_F16, true>(p, grid, st) : spread_as<ROW_F16, false>(p, grid, st);
-  else e = vec ? spread_as<ROW_F32, true>(p, grid, st) : spread_as<ROW_F32, false>(p, grid, st);
+  if (p.row_dtype == ROW_BF16) e = vec ? spread_as<ROW_BF16, true>(p, grid, block, st) : spread_as<ROW_BF16, false>(p, grid, block, st);
+  else if (p.row_dtype == ROW_F16) e = vec ? spread_as<ROW_F16, true>(p, grid, block, st) : spread_as<ROW_F16, false>(p, grid, block, st);
+  else e = vec ? spread_as<ROW_F32, true>(p, grid, block, st) : spread_as<ROW_F32, false>(p, grid, block, st);
   count_launches(1);
   return e;
 }
@@ -519,23 +562,27 @@ cudaError_t launch_dispatch(const RowsParams& p, const int* perm, const int* off
   return e == cudaSuccess ? launch_spread(p, num_sms, st) : e;
 }
 
+template <int DT, bool VEC, bool MANY>
+static cudaError_t collect_with(const RowsParams& p, dim3 grid, dim3 block, cudaStream_t st) {
+  if (!p.v) return launch_pdl(collect_kernel<DT, VEC, 0, MANY>, grid, block, 0, st, p);
+  return p.topk <= 8 ? launch_pdl(collect_kernel<DT, VEC, 8, MANY>, grid, block, 0, st, p)
+                     : launch_pdl(collect_kernel<DT, VEC, MAX_TOPK, MANY>, grid, block, 0, st, p);
+}
 template <int DT, bool VEC>
-static cudaError_t collect_as(const RowsParams& p, dim3 grid, cudaStream_t st) {
-  const dim3 block(ROWS_THREADS);
-  if (!p.v) return launch_pdl(collect_kernel<DT, VEC, 0>, grid, block, 0, st, p);
-  return p.topk <= 8 ? launch_pdl(collect_kernel<DT, VEC, 8>, grid, block, 0, st, p)
-                     : launch_pdl(collect_kernel<DT, VEC, MAX_TOPK>, grid, block, 0, st, p);
+static cudaError_t collect_as(const RowsParams& p, dim3 grid, dim3 block, cudaStream_t st) {
+  return block.y > 1 ? collect_with<DT, VEC, true>(p, grid, block, st) : collect_with<DT, VEC, false>(p, grid, block, st);
 }
 cudaError_t launch_collect(const RowsParams& p, int num_sms, cudaStream_t st) {
   if (p.T == 0) return cudaSuccess;
   const bool vec = rows_vectorised(p);
   // Large batches have CTAs enough, and the slots' look-up is paid once a token
   // (4096 tokens of 6144 columns, top-8: 69.3 against 73.3 us).
-  const dim3 grid((unsigned)p.T, p.v || p.T >= 4 * num_sms ? 1 : column_parts(p, vec));
+  const dim3 block = token_block(p, vec, true, num_sms);
+  const dim3 grid(((unsigned)p.T + block.y - 1) / block.y, p.v || p.T >= 4 * num_sms ? 1 : column_parts(p, vec));
   cudaError_t e;
-  if (p.row_dtype == ROW_BF16) e = vec ? collect_as<ROW_BF16, true>(p, grid, st) : collect_as<ROW_BF16, false>(p, grid, st);
-  else if (p.row_dtype == ROW_F16) e = vec ? collect_as<ROW_F16, true>(p, grid, st) : collect_as<ROW_F16, false>(p, grid, st);
-  else e = vec ? collect_as<ROW_F32, true>(p, grid, st) : collect_as<ROW_F32, false>(p, grid, st);
+  if (p.row_dtype == ROW_BF16) e = vec ? collect_as<ROW_BF16, true>(p, grid, block, st) : collect_as<ROW_BF16, false>(p, grid, block, st);
+  else if (p.row_dtype == ROW_F16) e = vec ? collect_as<ROW_F16, true>(p, grid, block, st) : collect_as<ROW_F16, false>(p, grid, block, st);
+  else e = vec ? collect_as<ROW_F32, true>(p, grid, block, st) : collect_as<ROW_F32, false>(p, grid, block, st);
   count_launches(1);
   return e;
 }

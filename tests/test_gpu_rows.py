@@ -104,7 +104,11 @@ SHAPES = [  # T, E, k, H, dtype, align, capacity
     (1, 1, 1, 1, FF, 1, 0), (1, 8, 2, 64, BF, 1, 0), (3, 4, 4, 7, HF, 1, 0), (8, 256, 8, 256, BF, 1, 0), (37, 8, 2, 256, BF, 1, 0),
     (37, 8, 2, 256, HF, 16, 0), (64, 16, 3, 1001, FF, 1, 0), (65, 16, 5, 1000, BF, 128, 9), (29, 512, 32, 72, HF, 1, 0),
     (130, 128, 9, 136, FF, 8, 4), (257, 5, 1, 2048, BF, 1, 0), (200, 3, 2, 520, HF, 1, 1), (19, 8, 2, 6144, BF, 1024, 0),
-    (33, 7, 7, 33, BF, 3, 20), (513, 32, 4, 24, FF, 1, 0), (2, 300, 16, 2056, HF, 64, 0)]
+    (33, 7, 7, 33, BF, 3, 20), (513, 32, 4, 24, FF, 1, 0), (2, 300, 16, 2056, HF, 64, 0),
+    # many tokens of narrow rows: 32 to 128 threads a token, and a last CTA that is not full
+    (701, 16, 4, 256, BF, 1, 0), (613, 8, 2, 64, HF, 1, 0), (650, 12, 3, 200, FF, 16, 0), (903, 32, 9, 1000, BF, 8, 0),
+    (643, 6, 2, 1536, HF, 1, 0), (700, 64, 32, 33, BF, 1, 0), (777, 5, 2, 130, FF, 1, 0), (1001, 20, 3, 712, FF, 1, 0),
+    (811, 8, 2, 328, HF, 32, 150), (621, 4, 1, 24, BF, 1, 100), (2051, 8, 8, 8, HF, 4, 2000), (610, 3, 3, 1, BF, 1, 0)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
