@@ -58,29 +58,49 @@ __device__ __forceinline__ typename Elem<DT>::type from_f32(float f) {
   else return f32_to_act<ACT_BF16>(f);
 }
 
-// A piece of a row: 16 bytes where the width and the addresses allow it
-// (VEC), else one element.
+// A piece of a row: 16 bytes where the width and the addresses allow it (VEC),
+// else 4 elements, as far apart as the row has threads, so that a warp's accesses
+// stay side by side and each thread has 4 on their way (3000 tokens of 999 16-bit
+// columns, top-2, and one element at a time: dispatch 7.5 and 15.7 us, combine
+// 8.8 and 10.3, their gradients 12.6 and 18.4, 14.6 and 21.6).
 template <int DT, bool VEC>
 struct Piece {
   using E = typename Elem<DT>::type;
-  static constexpr int N = VEC ? 16 / (int)sizeof(E) : 1;
-  E v[N];
-  __device__ __forceinline__ void load(const E* p) {
-    if constexpr (VEC) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
-    else v[0] = *p;
+  static constexpr int N = VEC ? 16 / (int)sizeof(E) : 4;
+  // Where a thread's piece begins among `threads` that share a row, and how far
+  // they get together.
+  static __device__ __forceinline__ int first(int part, int threads, int tid) {
+    return VEC ? (part * threads + tid) * N : part * threads * N + tid;
   }
-  __device__ __forceinline__ void store(E* p) const {
+  E v[N];
+  // p: the first element; threads: of the row; left: elements from the first to
+  // the row's end. Elements past it read as zero.
+  __device__ __forceinline__ void load(const E* p, int threads, int left) {
+    if constexpr (VEC) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+    else
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = i * threads < left ? p[i * threads] : E(0);
+  }
+  __device__ __forceinline__ void store(E* p, int threads, int left) const {
     if constexpr (VEC) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
-    else *p = v[0];
+    else
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * threads < left) p[i * threads] = v[i];
   }
   // For rows that pass through once: they leave L2 before what is kept.
-  __device__ __forceinline__ void load_once(const E* p) {
+  __device__ __forceinline__ void load_once(const E* p, int threads, int left) {
     if constexpr (VEC) *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(p));
-    else v[0] = __ldcs(p);
+    else
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = i * threads < left ? __ldcs(p + i * threads) : E(0);
   }
-  __device__ __forceinline__ void store_once(E* p) const {
+  __device__ __forceinline__ void store_once(E* p, int threads, int left) const {
     if constexpr (VEC) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(v));
-    else __stcs(p, v[0]);
+    else
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * threads < left) __stcs(p + i * threads, v[i]);
   }
   __device__ __forceinline__ float f(int i) const { return to_f32<DT>(v[i]); }
   __device__ __forceinline__ void set(int i, float x) { v[i] = from_f32<DT>(x); }
@@ -198,7 +218,7 @@ __global__ void __launch_bounds__(MAX_E) dispatch_small_kernel(DispatchPlan p, R
   pdl_wait();
   pdl_trigger();
   plan_scan(p, s);
-  const int tid = threadIdx.x, cols = q.H / P::N;
+  const int tid = threadIdx.x;
   for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
     if (tid == 0) {
       const int slot = plan_row(p, s, r);
@@ -211,10 +231,10 @@ __global__ void __launch_bounds__(MAX_E) dispatch_small_kernel(DispatchPlan p, R
     const E* v = static_cast<const E*>(q.v) + (size_t)(max(slot, 0) / q.topk) * q.H;
     E* dst = static_cast<E*>(q.rows_out) + (size_t)r * q.H;
     const float g = q.gates && slot >= 0 ? q.gates[slot] : 1.0f;
-    for (int c = tid; c < cols; c += MAX_E) {
+    for (int c = P::first(0, MAX_E, tid); c < q.H; c += MAX_E * P::N) {
       P a;
       if (slot >= 0) {
-        a.load(v + (size_t)c * P::N);
+        a.load(v + c, MAX_E, q.H - c);
         if (q.gates) {
 #pragma unroll
           for (int i = 0; i < P::N; ++i) a.set(i, g * a.f(i));
@@ -223,7 +243,7 @@ __global__ void __launch_bounds__(MAX_E) dispatch_small_kernel(DispatchPlan p, R
 #pragma unroll
         for (int i = 0; i < P::N; ++i) a.set(i, 0.0f);
       }
-      a.store(dst + (size_t)c * P::N);
+      a.store(dst + c, MAX_E, q.H - c);
     }
     __syncthreads();
   }
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
   const int k = p.topk, t = C::token();
-  const int cols = p.H / P::N, step = C::threads() * gridDim.y;
+  const int H = p.H, threads = C::threads(), step = threads * gridDim.y * P::N;
   const int blocks = (p.T + C::tokens() - 1) / C::tokens();  // with tokens
   TokenSlots& s = s_slots[C::at()];
   E* rows = static_cast<E*>(p.rows_out);
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
     for (long long r = ((long long)(blockIdx.x - blocks) * gridDim.y + blockIdx.y) * warps + warp; r < p.R; r += nw) {
       const int slot = p.row_slot[r];
       if (slot >= 0 && slot < p.T * k) continue;
-      for (int c = lane; c < cols; c += 32) zero.store_once(rows + (size_t)r * p.H + (size_t)c * P::N);
+      for (int c = P::first(0, 32, lane); c < H; c += 32 * P::N) zero.store_once(rows + (size_t)r * H + c, 32, H - c);
     }
     return;
   }
@@ -356,9 +376,9 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
   float dot[KD];
 #pragma unroll
   for (int j = 0; j < KD; ++j) dot[j] = 0.0f;
-  for (int c = blockIdx.y * C::threads() + tid; c < cols && (!MANY || t < p.T); c += step) {
+  for (int c = P::first(blockIdx.y, threads, tid); c < H && (!MANY || t < p.T); c += step) {
     P a;
-    a.load(v + (size_t)c * P::N);
+    a.load(v + c, threads, H - c);
     if constexpr (KDOT > 0) {
 #pragma unroll
       for (int j0 = 0; j0 < KDOT; j0 += 8) {
@@ -366,7 +386,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
         P b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load_once(other + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
+          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load_once(other + (size_t)s.row[j0 + j] * H + c, threads, H - c);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (j0 + j >= k || s.row[j0 + j] < 0) continue;
@@ -377,7 +397,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
             dot[j0 + j] = fmaf(a.f(i), b[j].f(i), dot[j0 + j]);
             o.set(i, g * a.f(i));
           }
-          o.store_once(rows + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
+          o.store_once(rows + (size_t)s.row[j0 + j] * H + c, threads, H - c);
         }
       }
     } else {
@@ -390,7 +410,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
 #pragma unroll
           for (int i = 0; i < P::N; ++i) o.set(i, s.g[j] * a.f(i));
         }
-        o.store_once(rows + (size_t)r * p.H + (size_t)c * P::N);
+        o.store_once(rows + (size_t)r * H + c, threads, H - c);
       }
     }
   }
@@ -411,7 +431,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
   pdl_trigger();
   const int tid = threadIdx.x;
   const int k = p.topk, t = C::token();
-  const int cols = p.H / P::N;
+  const int H = p.H, threads = C::threads();
   TokenSlots& s = s_slots[C::at()];
   token_slots<(KDOT > 0)>(p, t, s);
   __syncthreads();
@@ -421,13 +441,13 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
   float dot[KD];
 #pragma unroll
   for (int j = 0; j < KD; ++j) dot[j] = 0.0f;
-  for (int c = blockIdx.y * C::threads() + tid; c < cols && (!MANY || t < p.T); c += C::threads() * gridDim.y) {
+  for (int c = P::first(blockIdx.y, threads, tid); c < H && (!MANY || t < p.T); c += threads * gridDim.y * P::N) {
     float acc[P::N];
 #pragma unroll
     for (int i = 0; i < P::N; ++i) acc[i] = 0.0f;
     if constexpr (KDOT > 0) {
       P a;
-      a.load(v + (size_t)c * P::N);
+      a.load(v + c, threads, H - c);
       // 4 rows at once, past L2 so that x and dx keep their place in it
       // (fp16, 2051 tokens of 2048, top-8: 16.5 us; 8 at once 17.7, loads kept
       // in L2 29.7).
@@ -437,7 +457,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
         P b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load_once(rows + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
+          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load_once(rows + (size_t)s.row[j0 + j] * H + c, threads, H - c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j0 + j >= k || s.row[j0 + j] < 0) continue;
@@ -458,7 +478,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
         P b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load(rows + (size_t)s.row[j0 + j] * p.H + (size_t)c * P::N);
+          if (j0 + j < k && s.row[j0 + j] >= 0) b[j].load(rows + (size_t)s.row[j0 + j] * H + c, threads, H - c);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (j0 + j >= k || s.row[j0 + j] < 0) continue;
@@ -471,7 +491,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) collect_kernel(RowsParams p) {
     P o;
 #pragma unroll
     for (int i = 0; i < P::N; ++i) o.set(i, acc[i]);
-    o.store(out + (size_t)c * P::N);
+    o.store(out + c, threads, H - c);
   }
   if constexpr (KDOT > 0) token_dots<KDOT>(p, t, dot, s_dots, s);
 }
@@ -484,12 +504,17 @@ static bool rows_vectorised(const RowsParams& p) {
   return ((size_t)p.H * es) % 16 == 0 && all % 16 == 0;
 }
 
+// Pieces of a row.
+static int pieces(const RowsParams& p, bool vec) {
+  const int n = vec && p.row_dtype != ROW_F32 ? 8 : 4;
+  return (p.H + n - 1) / n;
+}
+
 // Column parts of a token, one load a thread: none of a CTA's time is a second
 // round of latency, and small batches reach more SMs (8 tokens of 6144 16-bit
 // columns: 24 CTAs). One part where dot products need the whole token.
 static unsigned column_parts(const RowsParams& p, bool vec) {
-  const int n = vec ? 16 / (p.row_dtype == ROW_F32 ? 4 : 2) : 1;
-  const int parts = (p.H / n + ROWS_THREADS - 1) / ROWS_THREADS;
+  const int parts = (pieces(p, vec) + ROWS_THREADS - 1) / ROWS_THREADS;
   return (unsigned)(parts < 1 ? 1 : (parts < 65535 ? parts : 65535));
 }
 
@@ -504,7 +529,7 @@ static unsigned column_parts(const RowsParams& p, bool vec) {
 // 2048, top-8: dispatch's gradient 15.5 us, 17.8 with 128), and so it has where
 // tokens are few (300 of 1000: combine 2.1 us, 4.1 with 32).
 static dim3 token_block(const RowsParams& p, bool vec, bool reads, int num_sms) {
-  const int n = vec ? 16 / (p.row_dtype == ROW_F32 ? 4 : 2) : 1, cols = p.H / n;
+  const int cols = pieces(p, vec);
   unsigned threads = ROWS_THREADS;
   if (p.T >= 4 * num_sms && cols < ROWS_THREADS)
     while (threads > 32 && cols <= (int)threads / 2 * (reads ? 4 : 1)) threads /= 2;

@@ -108,7 +108,9 @@ SHAPES = [  # T, E, k, H, dtype, align, capacity
     # many tokens of narrow rows: 32 to 128 threads a token, and a last CTA that is not full
     (701, 16, 4, 256, BF, 1, 0), (613, 8, 2, 64, HF, 1, 0), (650, 12, 3, 200, FF, 16, 0), (903, 32, 9, 1000, BF, 8, 0),
     (643, 6, 2, 1536, HF, 1, 0), (700, 64, 32, 33, BF, 1, 0), (777, 5, 2, 130, FF, 1, 0), (1001, 20, 3, 712, FF, 1, 0),
-    (811, 8, 2, 328, HF, 32, 150), (621, 4, 1, 24, BF, 1, 100), (2051, 8, 8, 8, HF, 4, 2000), (610, 3, 3, 1, BF, 1, 0)]
+    (811, 8, 2, 328, HF, 32, 150), (621, 4, 1, 24, BF, 1, 100), (2051, 8, 8, 8, HF, 4, 2000), (610, 3, 3, 1, BF, 1, 0),
+    # odd widths below, at and past what a CTA's threads take together
+    (9, 64, 8, 6001, BF, 1, 0), (3, 4, 2, 4099, FF, 1, 0), (700, 5, 2, 1025, HF, 16, 0), (6, 9, 3, 1023, BF, 1, 1)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
