@@ -594,9 +594,10 @@ typedef struct hmoe_lora hmoe_lora; /* opaque host handle: no device memory */
  *   HMOE_ERR_UNSUPPORTED_SHAPE (the limits above). */
 hmoe_status hmoe_lora_packed_size(const hmoe_lora_desc* desc, size_t* bytes);
 
-/* Workspace bytes for hmoe_lora_forward at up to max_tokens rows. Zero the
- * workspace once before its first use (hmoe_workspace_init).
- *   No page defines it. Errors as hmoe_lora_packed_size. */
+/* Workspace bytes for hmoe_lora_forward at up to max_tokens rows, 0..2^26.
+ * Zero the workspace once before its first use (hmoe_workspace_init).
+ *   No page defines it. Errors as hmoe_lora_packed_size (more rows are
+ *   HMOE_ERR_UNSUPPORTED_SHAPE). */
 hmoe_status hmoe_lora_workspace_size(const hmoe_lora_desc* desc, int max_tokens, size_t* bytes);
 
 /* Create the handle over a device buffer of hmoe_lora_packed_size bytes,
@@ -620,11 +621,11 @@ hmoe_status hmoe_lora_load(const hmoe_lora* lora, int slot, const void* A, const
  * multiple of 8, so column ranges of wider tensors serve. base may be out
  * itself (in place, the same stride); out overlaps nothing else. ids:
  * device int32 [T] in -1..slots-1; an id outside is reported through
- * hmoe_check_device_status (HMOE_ERR_BAD_ROUTE) and its row gets base. T = 0
- * is valid.
+ * hmoe_check_device_status (HMOE_ERR_BAD_ROUTE) and its row gets base. T: up
+ * to 2^26; 0 is valid.
  *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
- *   pointer, T < 0, a bad stride), HMOE_ERR_WORKSPACE_TOO_SMALL,
- *   HMOE_ERR_CUDA. */
+ *   pointer, T < 0, a bad stride), HMOE_ERR_UNSUPPORTED_SHAPE (T above 2^26),
+ *   HMOE_ERR_WORKSPACE_TOO_SMALL, HMOE_ERR_CUDA. */
 hmoe_status hmoe_lora_forward(const hmoe_lora* lora, const void* x, int ldx, int T, const int32_t* ids,
                               const void* base, int ldbase, void* out, int ldout, void* ws, size_t ws_bytes,
                               hmoe_stream_t stream);

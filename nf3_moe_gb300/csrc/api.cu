@@ -1183,6 +1183,12 @@ hmoe_status check_lora_desc(const hmoe_lora_desc* d) {
   return HMOE_OK;
 }
 
+hmoe_status check_lora_rows(int T) {
+  if (T < 0) return fail(HMOE_ERR_INVALID_ARG, "T=%d < 0", T);
+  if (T > LORA_MAX_ROWS) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d exceeds %d rows", T, LORA_MAX_ROWS);
+  return HMOE_OK;
+}
+
 // The status word, then the scratch of batches above the one-launch limit.
 size_t lora_ws_total(const LoraGeom& g, int T) { return 256 + lora_scratch(g, T).total; }
 
@@ -1202,7 +1208,8 @@ hmoe_status hmoe_lora_packed_size(const hmoe_lora_desc* desc, size_t* bytes) {
 hmoe_status hmoe_lora_workspace_size(const hmoe_lora_desc* desc, int max_tokens, size_t* bytes) {
   hmoe_status s = check_lora_desc(desc);
   if (s != HMOE_OK) return s;
-  if (!bytes || max_tokens < 0) return fail(HMOE_ERR_INVALID_ARG, "bytes NULL or max_tokens < 0");
+  if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  if ((s = check_lora_rows(max_tokens)) != HMOE_OK) return s;
   *bytes = lora_ws_total(lora_geom(desc->K, desc->N, desc->slots, desc->max_rank), max_tokens);
   return HMOE_OK;
 }
@@ -1252,7 +1259,8 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T,
                               int ldbase, void* out, int ldout, void* ws, size_t ws_bytes, hmoe_stream_t stream) {
   const NvtxRange nvtx("hmoe_lora_forward");
   if (!L) return fail(HMOE_ERR_INVALID_ARG, "lora is NULL");
-  if (T < 0) return fail(HMOE_ERR_INVALID_ARG, "T=%d < 0", T);
+  hmoe_status s = check_lora_rows(T);
+  if (s != HMOE_OK) return s;
   if (T == 0) return HMOE_OK;
   if (!x || !ids || !out) return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
   if (!aligned16(x) || !aligned16(out) || (base && !aligned16(base)))
@@ -1262,8 +1270,7 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T,
     return fail(HMOE_ERR_INVALID_ARG, "row strides must be multiples of 8 and hold a row (ldx=%d ldbase=%d ldout=%d)", ldx,
                 ldbase, ldout);
   if (base == out && ldbase != ldout) return fail(HMOE_ERR_INVALID_ARG, "in place, ldbase and ldout must be equal");
-  hmoe_status s = check_status_ws(ws, ws_bytes);
-  if (s != HMOE_OK) return s;
+  if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
   const size_t need = lora_ws_total(L->g, T);
   if (ws_bytes < need)
     return fail(HMOE_ERR_WORKSPACE_TOO_SMALL, "workspace holds %zu bytes, T=%d needs %zu", ws_bytes, T, need);

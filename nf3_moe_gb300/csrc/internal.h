@@ -168,6 +168,7 @@ cudaError_t launch_collect(const RowsParams& p, int num_sms, cudaStream_t st);
 // Rows and columns past the rank, K and N hold zeros.
 constexpr int LORA_MAX_RANK = 128;
 constexpr int LORA_MAX_SLOTS = 512;
+constexpr int LORA_MAX_ROWS = 1 << 26;  // of a batch: what a row's word in the plan holds
 struct LoraGeom {
   int K, N, slots, max_r16;
   int KB, NB;                  // 64-wide tiles of K and of N

@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
   extern __shared__ int s_word[];  // [LP_ROWS]: group, and place << 10 in the warp's part of it
   __shared__ int s_rank[LORA_MAX_SLOTS + 1], s_wsum[2][LP_WARPS];
   static_assert(LORA_MAX_SLOTS + 1 <= 1 << 10 && LORA_MAX_SLOTS + 1 <= LP_THREADS, "group bits");
+  static_assert(LORA_MAX_ROWS / LP_WARPS <= 1 << 21 && LORA_MAX_ROWS % LP_THREADS == 0, "place bits, the sign left out");
   int* s_base = s_word + LP_ROWS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.g.slots + 1;
