@@ -180,9 +180,12 @@ __device__ __forceinline__ int plan_row(const DispatchPlan& p, const PlanScan& s
   return slot;
 }
 // With a capacity: -1 for the slots that it drops. All threads of the grid.
+// Rows and slots go up to INT_MAX, so the counters that step by a grid past
+// them are unsigned.
 __device__ __forceinline__ void plan_dropped(const DispatchPlan& p, const PlanScan& s) {
   if (p.capacity <= 0) return;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.S; i += gridDim.x * blockDim.x) {
+  for (unsigned at = blockIdx.x * blockDim.x + threadIdx.x; at < (unsigned)p.S; at += gridDim.x * blockDim.x) {
+    const int i = (int)at;
     int lo = 0, hi = p.E - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -199,10 +202,10 @@ __global__ void __launch_bounds__(MAX_E) dispatch_plan_kernel(DispatchPlan p) {
   pdl_wait();
   pdl_trigger();
   plan_scan(p, s);
-  for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < p.R; r += gridDim.x * blockDim.x) {
-    const int slot = plan_row(p, s, r);
+  for (unsigned r = blockIdx.x * blockDim.x + threadIdx.x; r < (unsigned)p.R; r += gridDim.x * blockDim.x) {
+    const int slot = plan_row(p, s, (int)r);
     p.row_slot[r] = slot;
-    if (slot >= 0) p.slot_row[slot] = r;
+    if (slot >= 0) p.slot_row[slot] = (int)r;
   }
   plan_dropped(p, s);
 }
@@ -352,10 +355,10 @@ __global__ void __launch_bounds__(ROWS_THREADS) spread_kernel(RowsParams p) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int k = p.topk, t = C::token();
   const int H = p.H, threads = C::threads(), step = threads * gridDim.y * P::N;
-  const int blocks = (p.T + C::tokens() - 1) / C::tokens();  // with tokens
+  const unsigned blocks = ((unsigned)p.T + C::tokens() - 1) / C::tokens();  // with tokens
   TokenSlots& s = s_slots[C::at()];
   E* rows = static_cast<E*>(p.rows_out);
-  if ((int)blockIdx.x >= blocks) {
+  if (blockIdx.x >= blocks) {
     P zero;
 #pragma unroll
     for (int i = 0; i < P::N; ++i) zero.set(i, 0.0f);
@@ -581,8 +584,8 @@ cudaError_t launch_dispatch(const RowsParams& p, const int* perm, const int* off
     count_launches(1);
     return e;
   }
-  const int blocks = (most + MAX_E - 1) / MAX_E;
-  e = launch_pdl(dispatch_plan_kernel, dim3((unsigned)(blocks < num_sms ? blocks : num_sms)), dim3(MAX_E), 0, st, d);
+  const unsigned blocks = ((unsigned)most + MAX_E - 1) / MAX_E, sms = (unsigned)num_sms;
+  e = launch_pdl(dispatch_plan_kernel, dim3(blocks < sms ? blocks : sms), dim3(MAX_E), 0, st, d);
   count_launches(1);
   return e == cudaSuccess ? launch_spread(p, num_sms, st) : e;
 }
