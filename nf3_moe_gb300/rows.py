@@ -193,6 +193,34 @@ def _gate_grad_bufs(ctx, T, E, gates, gates_at, logits_at):
     return dgates, dlogits
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """The first n tensors, as if they came of the others: to differentiate them is an error."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.detach() for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the gradients of ExpertRows have no second derivative (they were used in a loss or in another "
+                           "gradient, with create_graph=True)")
+
+
+def _first_order(grads, given, gates, logits, dot):
+    """What backward returns for its gradients (of the moved rows, the gates and the logits). Where a graph of them is
+    asked for (create_graph=True), they must not pass for constants if they depend on a tensor that requires a gradient:
+    the given one and the gates (through which the logits), for the gates' part also the dot products' operand."""
+    if not torch.is_grad_enabled():
+        return grads
+    of = [given, gates, logits if gates is not None else None, dot if grads[1] is not None or grads[2] is not None else None]
+    of = [t for t in of if t is not None and t.requires_grad]
+    if not of:
+        return grads
+    live = [t for t in grads if t is not None]
+    marked = iter(_NoSecondDerivative.apply(len(live), *live, *of))
+    return tuple(None if t is None else next(marked) for t in grads)
+
+
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gates, logits, ids, perm, offsets, desc, ws):
@@ -204,21 +232,22 @@ class _Dispatch(torch.autograd.Function):
         row_offsets = torch.empty((desc.E + 1,), dtype=torch.int32, device=dev)
         hmoe_dispatch(desc, x, perm, offsets, rows, row_slot, slot_row, row_offsets, ws, gates=gates)
         ctx.save_for_backward(x if gates is not None else None, gates, ids, slot_row)
-        ctx.desc, ctx.ws, ctx.shape = desc, ws, x.shape
+        ctx.desc, ctx.ws, ctx.shape, ctx.logits = desc, ws, x.shape, logits
         ctx.mark_non_differentiable(row_slot, slot_row, row_offsets)
         return rows, row_slot, slot_row, row_offsets
 
     @staticmethod
     def backward(ctx, drows, *_):
         x, gates, ids, slot_row = ctx.saved_tensors
-        drows = drows.contiguous()
-        dx = drows.new_empty(ctx.shape)
-        dgates = dlogits = None
-        if gates is not None:
-            dgates, dlogits = _gate_grad_bufs(ctx, ctx.shape[0], ctx.desc.E, gates, 1, 2)
-        hmoe_dispatch_backward(ctx.desc, drows, slot_row, dx, ctx.ws, x=x, gates=gates, ids=ids, dgates=dgates,
-                               dlogits=dlogits)
-        return dx, dgates, dlogits, None, None, None, None, None
+        with torch.no_grad():
+            d = drows.contiguous()
+            dx = d.new_empty(ctx.shape)
+            dgates = dlogits = None
+            if gates is not None:
+                dgates, dlogits = _gate_grad_bufs(ctx, ctx.shape[0], ctx.desc.E, gates, 1, 2)
+            hmoe_dispatch_backward(ctx.desc, d, slot_row, dx, ctx.ws, x=x, gates=gates, ids=ids, dgates=dgates,
+                                   dlogits=dlogits)
+        return *_first_order((dx, dgates, dlogits), drows, gates, ctx.logits, x), None, None, None, None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -227,20 +256,21 @@ class _Combine(torch.autograd.Function):
         out = rows.new_empty((slot_row.shape[0], desc.H))
         hmoe_combine(desc, rows, slot_row, out, ws, gates=gates)
         ctx.save_for_backward(rows if gates is not None else None, gates, ids, row_slot, slot_row)
-        ctx.desc, ctx.ws, ctx.shape = desc, ws, rows.shape
+        ctx.desc, ctx.ws, ctx.shape, ctx.logits = desc, ws, rows.shape, logits
         return out
 
     @staticmethod
     def backward(ctx, dout):
         rows, gates, ids, row_slot, slot_row = ctx.saved_tensors
-        dout = dout.contiguous()
-        drows = dout.new_empty(ctx.shape)
-        dgates = dlogits = None
-        if gates is not None:
-            dgates, dlogits = _gate_grad_bufs(ctx, dout.shape[0], ctx.desc.E, gates, 1, 2)
-        hmoe_combine_backward(ctx.desc, dout, row_slot, slot_row, drows, ctx.ws, rows=rows, gates=gates, ids=ids,
-                              dgates=dgates, dlogits=dlogits)
-        return drows, dgates, dlogits, None, None, None, None, None
+        with torch.no_grad():
+            d = dout.contiguous()
+            drows = d.new_empty(ctx.shape)
+            dgates = dlogits = None
+            if gates is not None:
+                dgates, dlogits = _gate_grad_bufs(ctx, d.shape[0], ctx.desc.E, gates, 1, 2)
+            hmoe_combine_backward(ctx.desc, d, row_slot, slot_row, drows, ctx.ws, rows=rows, gates=gates, ids=ids,
+                                  dgates=dgates, dlogits=dlogits)
+        return *_first_order((drows, dgates, dlogits), dout, gates, ctx.logits, rows), None, None, None, None, None
 
 
 class ExpertRows:
@@ -252,7 +282,7 @@ class ExpertRows:
     gates. The gates of hmoe_plan_routes are a softmax over the chosen router logits; give ids
     and logits as well and the logits get their gradient through it (the logits' values are not
     read). Then take the gates from plan as they are: a gates tensor that requires a gradient
-    itself gets one too.
+    itself gets one too. These are first derivatives: differentiating them again is an error.
     """
 
     def __init__(self, H, E, topk, max_tokens=8, dtype=torch.bfloat16, align=1, capacity=0, device="cuda"):
