@@ -273,6 +273,12 @@ class _Combine(torch.autograd.Function):
         return *_first_order((drows, dgates, dlogits), dout, gates, ctx.logits, rows), None, None, None, None, None
 
 
+def _check_logits(gates, ids, logits):
+    """Before anything runs: logits whose gradient could not be formed, or would be left out."""
+    if logits is not None and (gates is None or ids is None) and logits.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"the gradient of logits needs {'gates' if gates is None else 'ids'}")
+
+
 class ExpertRows:
     """Sorting token rows by expert and bringing them back, differentiable.
 
@@ -295,9 +301,11 @@ class ExpertRows:
 
     def dispatch(self, x, perm, offsets, gates=None, ids=None, logits=None):
         """x [T, H] -> (rows [R, H], RowPlan)."""
+        _check_logits(gates, ids, logits)
         rows, *plan = _Dispatch.apply(x, gates, logits, ids, perm, offsets, self.desc, self.ws)
         return rows, RowPlan(*plan)
 
     def combine(self, rows, plan, gates=None, ids=None, logits=None):
         """rows [R, H] -> out [T, H]."""
+        _check_logits(gates, ids, logits)
         return _Combine.apply(rows, gates, logits, ids, plan.row_slot, plan.slot_row, self.desc, self.ws)

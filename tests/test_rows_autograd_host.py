@@ -138,3 +138,23 @@ def test_create_graph_alone_changes_nothing(plain):
     loss, xs, src = _loss(plain, "combine", "logits", False)
     again = torch.autograd.grad(loss, (xs, src), create_graph=True)
     assert all(torch.equal(a, b) for a, b in zip(once, again))
+
+
+@pytest.mark.parametrize("at", ["dispatch", "combine"])
+def test_logits_that_would_get_no_gradient_are_refused_at_once(plain, at):
+    """Logits get theirs through the gates and the ids; where one is missing the call says so, not the backward (or
+    nobody). Logits that want no gradient are no error."""
+    er, x, logits, ids, gates, perm, offsets = plain
+    rows, plan = er.dispatch(x, perm, offsets)
+
+    def call(**kw):
+        return er.dispatch(x, perm, offsets, **kw) if at == "dispatch" else er.combine(rows, plan, **kw)
+
+    want = logits.clone().requires_grad_()
+    for kw, missing in ((dict(gates=gates, logits=want), "ids"), (dict(ids=ids, logits=want), "gates"), (dict(logits=want), "gates")):
+        with pytest.raises(ValueError, match=missing):
+            call(**kw)
+        with torch.no_grad():
+            call(**kw)
+        call(**(kw | {"logits": logits}))
+    call(gates=gates, ids=ids, logits=want)
