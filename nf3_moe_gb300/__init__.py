@@ -397,6 +397,8 @@ class LinearW4A16:
     def __call__(self, x, out=None, path=PATH_AUTO, adapters=None, ids=None):
         """adapters, ids: a LoraAdapters of the same widths and each row's adapter (int32 [T], -1: none),
         added to the result in place."""
+        if adapters is not None:
+            _no_gradient(x, None, out)
         if out is None:
             out = torch.empty((x.shape[0], self.N), dtype=self.dtype, device=x.device)
         hmoe_linear_forward(self.linear, x, out, self.ws, path=path)
@@ -426,5 +428,5 @@ def hmoe_quantize_act_nvfp4(x, global_scale, codes, scales, stream=None):
 from ._lib import ROW_BF16, ROW_F16, ROW_F32, DispatchDesc, LoraDesc  # noqa: E402, F401
 from .rows import (ExpertRows, RowPlan, hmoe_combine, hmoe_combine_backward, hmoe_dispatch,  # noqa: E402, F401
                    hmoe_dispatch_backward, hmoe_dispatch_rows, hmoe_dispatch_workspace_size, row_torch_dtype)
-from .lora import (Lora, LoraAdapters, hmoe_lora_create, hmoe_lora_forward, hmoe_lora_load,  # noqa: E402, F401
+from .lora import (Lora, LoraAdapters, _no_gradient, hmoe_lora_create, hmoe_lora_forward, hmoe_lora_load,  # noqa: E402, F401
                    hmoe_lora_packed_size, hmoe_lora_workspace_size)

@@ -9,10 +9,11 @@
 import ctypes
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib, _need, act_torch_dtype, hmoe_workspace_init
 from ._lib import ACT_BF16, ACT_F16, LoraDesc
-from .rows import _bytes, _is, _is_ws, _raw_stream
+from .rows import _is, _is_ws, _raw_stream
 
 _TORCH = {ACT_BF16: torch.bfloat16, ACT_F16: torch.float16}
 
@@ -20,14 +21,6 @@ _TORCH = {ACT_BF16: torch.bfloat16, ACT_F16: torch.float16}
 def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
     """A [T, width] tensor whose rows are contiguous and evenly spaced (a column range of a wider one serves), on the
     device of this index. Returns the row stride."""
-    try:  # nearly always right: one look, and the checks below for their messages
-        rows, wide = t.shape
-        at = t.get_device()
-        if t.dtype is dtype and wide == width and (rows == T or T is None) and t.is_contiguous() and (
-                not cuda or at >= 0 and (at == device or device is None)):
-            return width
-    except (AttributeError, ValueError):
-        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -44,14 +37,42 @@ def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
 
 def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
     """Returns T, the row strides of x, base and out, and the device index."""
-    dt, N = _TORCH[desc.act_dtype], desc.N
-    ldx = _need_rows("x", x, None, desc.K, dt, cuda=cuda)
+    dt, K, N = _TORCH[desc.act_dtype], desc.K, desc.N
+    try:  # nearly always right: one look at all of them, and the checks below for their messages
+        T, wide = x.shape
+        dev, row = x.get_device(), (T, N)
+        (ldx, one), (ldo, one_o) = x.stride(), out.stride()
+        if T == 1:                                       # its stride is never used
+            ldx, ldo = K, N
+        ldb, one_b = 0, 1
+        if base is out:
+            ldb = ldo
+        elif base is not None:
+            ldb, one_b = base.stride()
+            if T == 1:
+                ldb = N
+        if (wide == K and out.shape == row and x.dtype is dt is out.dtype and one == one_o == one_b == 1 and ldx >= K and ldo >= N
+                and ids.shape == (T,) and ids.dtype is torch.int32 and ids.is_contiguous() and ws.is_contiguous()
+                and (not cuda or dev >= 0 and out.get_device() == ids.get_device() == ws.get_device() == dev)
+                and (base is None or base is out or ldb >= N and base.dtype is dt and base.shape == row
+                     and (not cuda or base.get_device() == dev))):
+            return T, ldx, ldb, ldo, dev
+    except (AttributeError, ValueError):
+        pass
+    ldx = _need_rows("x", x, None, K, dt, cuda=cuda)
     T, dev = x.shape[0], x.get_device()
     _is("ids", ids, (T,), torch.int32, dev, cuda)
     ldo = _need_rows("out", out, T, N, dt, dev, cuda)
     ldb = 0 if base is None else ldo if base is out else _need_rows("base", base, T, N, dt, dev, cuda)
     _is_ws(ws, dev, cuda)
     return T, ldx, ldb, ldo, dev
+
+
+def _no_gradient(x, base, out):
+    """The adapters have no gradient: a call that would lose one in silence is refused."""
+    for name, t in (("x", x), ("base", base), ("out", out)):
+        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
+            raise RuntimeError(f"{name} requires a gradient, and the adapters have none: detach it, or call under torch.no_grad()")
 
 
 def hmoe_lora_packed_size(desc):
@@ -103,18 +124,25 @@ def hmoe_lora_load(lora, slot, A, B, scale=1.0, stream=None):
 
 
 def hmoe_lora_forward(lora, x, ids, out, ws, base=None, stream=None):
-    """out[t] = base[t] + scale_a B_a (A_a x[t]), a = ids[t]; base None: zeros; base may be out."""
+    """out[t] = base[t] + scale_a B_a (A_a x[t]), a = ids[t]; base None: zeros; base may be out. No gradient: x, base
+    and out may not require one (outside torch.no_grad())."""
     T, ldx, ldb, ldo, dev = _check_lora_forward(lora.desc, x, ids, base, out, ws)
-    _lib.check(_lib.lib().hmoe_lora_forward(lora.handle, x.data_ptr(), ldx, T, ids.data_ptr(),
-                                            None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
-                                            ws.data_ptr(), _bytes(ws), _raw_stream(stream, dev)))
+    if x.requires_grad or out.requires_grad or base is not None and base.requires_grad:
+        _no_gradient(x, base, out)
+    increment_version(out)                               # autograd does not see the library's writes
+    status = _lib.lib().hmoe_lora_forward(lora.handle, x.data_ptr(), ldx, T, ids.data_ptr(),
+                                          None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
+                                          ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev))
+    if status:
+        _lib.check(status)
 
 
 class LoraAdapters:
     """Low-rank adapters with their packed buffer and workspace owned as torch tensors.
 
     K, N: widths of the projection's input and output; slots: adapters held at once; max_rank:
-    the largest rank of any; max_tokens sizes the workspace.
+    the largest rank of any; max_tokens sizes the workspace. For serving, and beside trained parts as
+    constants: no gradient goes through them, and a call that would need one is an error.
     """
 
     def __init__(self, K, N, slots, max_rank, max_tokens=8, act_dtype=ACT_BF16, device="cuda"):
