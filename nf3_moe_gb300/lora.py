@@ -13,7 +13,7 @@ from torch.autograd.graph import increment_version
 
 from . import _lib, _need, act_torch_dtype, hmoe_workspace_init
 from ._lib import ACT_BF16, ACT_F16, LoraDesc
-from .rows import _is, _is_ws, _raw_stream
+from .rows import _INT_MAX, _int32, _is, _is_ws, _raw_stream
 
 _TORCH = {ACT_BF16: torch.bfloat16, ACT_F16: torch.float16}
 
@@ -32,7 +32,8 @@ def _need_rows(name, t, T, width, dtype, device=None, cuda=True):
     ld, one = t.stride()
     if one != 1 or (ld < width and t.shape[0] > 1):
         raise ValueError(f"the rows of {name} must be contiguous and must not overlap, got strides {list(t.stride())}")
-    return ld if t.shape[0] > 1 else width               # one row: its stride is never used
+    _int32(f"the rows of {name}", t.shape[0])
+    return _int32(f"the row stride of {name}", ld) if t.shape[0] > 1 else width   # one row: its stride is never used
 
 
 def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
@@ -51,7 +52,8 @@ def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
             ldb, one_b = base.stride()
             if T == 1:
                 ldb = N
-        if (wide == K and out.shape == row and x.dtype is dt is out.dtype and one == one_o == one_b == 1 and ldx >= K and ldo >= N
+        if (wide == K and out.shape == row and x.dtype is dt is out.dtype and one == one_o == one_b == 1
+                and ldx >= K and ldo >= N and T | ldx | ldo | ldb <= _INT_MAX
                 and ids.shape == (T,) and ids.dtype is torch.int32 and ids.is_contiguous() and ws.is_contiguous()
                 and (not cuda or dev >= 0 and out.get_device() == ids.get_device() == ws.get_device() == dev)
                 and (base is None or base is out or ldb >= N and base.dtype is dt and base.shape == row
@@ -83,7 +85,7 @@ def hmoe_lora_packed_size(desc):
 
 def hmoe_lora_workspace_size(desc, max_tokens):
     b = ctypes.c_size_t()
-    _lib.check(_lib.lib().hmoe_lora_workspace_size(ctypes.byref(desc), int(max_tokens), ctypes.byref(b)))
+    _lib.check(_lib.lib().hmoe_lora_workspace_size(ctypes.byref(desc), _int32("max_tokens", max_tokens), ctypes.byref(b)))
     return b.value
 
 

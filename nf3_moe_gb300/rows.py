@@ -21,6 +21,14 @@ from ._lib import ROW_BF16, ROW_F16, ROW_F32, DispatchDesc
 
 _TORCH = {ROW_BF16: torch.bfloat16, ROW_F16: torch.float16, ROW_F32: torch.float32}
 _ROW = {v: k for k, v in _TORCH.items()}
+_INT_MAX = 2 ** 31 - 1  # of the library's int arguments; ctypes would pass the low 32 bits of more
+
+
+def _int32(name, n):
+    n = int(n)
+    if not -_INT_MAX <= n <= _INT_MAX:
+        raise ValueError(f"{name}={n} exceeds the library's 32-bit index")
+    return n
 
 
 def row_torch_dtype(row_dtype):
@@ -64,13 +72,13 @@ def _bytes(ws):
 def hmoe_dispatch_rows(desc, T):
     """Rows of the sorted buffer for T tokens."""
     n = ctypes.c_int()
-    _lib.check(_lib.lib().hmoe_dispatch_rows(ctypes.byref(desc), int(T), ctypes.byref(n)))
+    _lib.check(_lib.lib().hmoe_dispatch_rows(ctypes.byref(desc), _int32("T", T), ctypes.byref(n)))
     return n.value
 
 
 def hmoe_dispatch_workspace_size(desc, max_tokens):
     b = ctypes.c_size_t()
-    _lib.check(_lib.lib().hmoe_dispatch_workspace_size(ctypes.byref(desc), int(max_tokens), ctypes.byref(b)))
+    _lib.check(_lib.lib().hmoe_dispatch_workspace_size(ctypes.byref(desc), _int32("max_tokens", max_tokens), ctypes.byref(b)))
     return b.value
 
 
@@ -80,12 +88,12 @@ def _check_tokens(name, desc, t, cuda):
     try:
         T, width = t.shape
         device = t.get_device()
-        if width == H and t.dtype is dt and t.is_contiguous() and (device >= 0 or not cuda):
+        if width == H and t.dtype is dt and t.is_contiguous() and T <= _INT_MAX and (device >= 0 or not cuda):
             return T, H, dt, device
     except (AttributeError, ValueError):
         pass
     _need(name, t, (None, H), dt, cuda=cuda)
-    return t.shape[0], H, dt, t.get_device()
+    return _int32(f"the rows of {name}", t.shape[0]), H, dt, t.get_device()
 
 
 def _rows_of(desc, T):
