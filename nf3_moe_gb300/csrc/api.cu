@@ -1189,7 +1189,7 @@ hmoe_status check_lora_rows(int T) {
   return HMOE_OK;
 }
 
-// The status word, then the scratch of batches above the one-launch limit.
+// The status word, then the scratch (lora_scratch).
 size_t lora_ws_total(const LoraGeom& g, int T) { return 256 + lora_scratch(g, T).total; }
 
 }  // namespace

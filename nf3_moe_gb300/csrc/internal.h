@@ -212,6 +212,9 @@ struct LoraParams {
   float* u;
   float* part;
 };
+// Up to this many rows a batch is one launch that finds its groups itself and
+// keeps nothing outside it: no scratch but the (then unused) meta words.
+constexpr int LORA_ONE_LAUNCH_ROWS = 128;
 // Scratch of a larger batch of T rows: the rows grouped by adapter (perm), cut
 // into tiles of up to LORA_TILE_ROWS rows (tiles: adapter or -1, first
 // position, rows, rank), A x of every position (u), and the sums of the pieces
@@ -231,7 +234,7 @@ inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
   s.perm = s.tiles + pad(most * 16);
   s.u = s.perm + pad((size_t)T * 4);
   s.part = s.u + pad((size_t)T * g.max_r16 * 4);
-  s.total = s.part + (size_t)LORA_MAX_CTAS * 2 * LORA_TILE_ROWS * g.max_r16 * 4;
+  s.total = T <= LORA_ONE_LAUNCH_ROWS ? s.tiles : s.part + (size_t)LORA_MAX_CTAS * 2 * LORA_TILE_ROWS * g.max_r16 * 4;
   return s;
 }
 cudaError_t launch_lora_forward(const LoraParams& p, int num_sms, cudaStream_t st);

@@ -149,7 +149,8 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 constexpr int LS_THREADS = 256;
 constexpr int LS_WARPS = LS_THREADS / 32;
 constexpr int LS_TOK = 16;
-constexpr int LS_MAX_T = 128;  // at most LS_THREADS: the grouping looks at one row a thread
+constexpr int LS_MAX_T = LORA_ONE_LAUNCH_ROWS;
+static_assert(LS_MAX_T <= LS_THREADS, "the grouping looks at one row a thread");
 // CTAs of an SM, by the registers of the kernel for this rank.
 constexpr int ls_per_sm(int r16) { return r16 <= 64 ? 2 : 1; }
 // What a batch is likely to look like, from what the host knows of it: rows

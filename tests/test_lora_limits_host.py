@@ -32,3 +32,13 @@ def test_larger_batches_are_refused(T):
     with pytest.raises(hm.HmoeError) as ei:
         hm.hmoe_lora_workspace_size(d, T)
     assert ei.value.status == -2
+
+
+@pytest.mark.parametrize("rank", [16, 64, 128])
+def test_batches_of_one_launch_need_no_scratch(rank):
+    """Up to 128 rows a batch keeps nothing outside its one kernel: a server's workspace for a decode step is small."""
+    d = hm.LoraDesc(2048, 2048, 16, rank)
+    sizes = [hm.hmoe_lora_workspace_size(d, T) for T in (0, 1, 8, 128, 129, 4096)]
+    assert sizes == sorted(sizes)
+    assert sizes[0] >= 256 and sizes[3] <= 4096
+    assert sizes[4] >= 2 * 129 * 4
