@@ -9,6 +9,7 @@
 // validated).
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -1248,7 +1249,7 @@ hmoe_status hmoe_lora_load(const hmoe_lora* L, int slot, const void* A, const vo
   if (rank > 0 && (!A || !B)) return fail(HMOE_ERR_INVALID_ARG, "A or B is NULL");
   if ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(B)) & 1)
     return fail(HMOE_ERR_INVALID_ARG, "A and B must be aligned to their elements");
-  if (!(scale > -3.0e38f && scale < 3.0e38f)) return fail(HMOE_ERR_INVALID_ARG, "scale must be finite");
+  if (!std::isfinite(scale)) return fail(HMOE_ERR_INVALID_ARG, "scale must be finite");
   cudaError_t e = launch_lora_load(L->g, L->packed, slot, static_cast<const uint16_t*>(A),
                                    static_cast<const uint16_t*>(B), rank, scale, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "adapter load launch");
