@@ -571,9 +571,11 @@ hmoe_status hmoe_combine_backward(const hmoe_dispatch_desc* desc, const void* do
  * come in any order and mix: one request's tokens, single tokens of many
  * requests, or the rows of hmoe_dispatch with the expert as the adapter.
  * A x is summed in fp32 and enters the second product as the sum of two
- * values of the activation type (so with 16 or more significant bits); that
- * product, the scale and the base are fp32, rounded once to the activation
- * type. fp16: |A x| must fit fp16, like any activation.
+ * values of the activation type: with 16 significant bits in bf16; in fp16,
+ * where each row is brought into the type's range by a power of two first (so
+ * |A x| may be of any size), with 22, or to 2^-39 of a bound on the row's
+ * largest |A x| where that is more. That product, the scale and the base are
+ * fp32, rounded once to the activation type.
  * No value of another row enters a row's result, a NaN or an infinity
  * included. The same call gives the same bits; how a batch is composed can
  * change the order of the fp32 sums.

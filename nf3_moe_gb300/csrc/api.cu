@@ -1296,6 +1296,7 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T,
   p.perm = reinterpret_cast<int*>(scratch + w.perm);
   p.u = reinterpret_cast<float*>(scratch + w.u);
   p.part = reinterpret_cast<float*>(scratch + w.part);
+  p.bound = L->d.act_dtype == HMOE_ACT_F16 ? reinterpret_cast<uint32_t*>(scratch + w.bound) : nullptr;
   cudaError_t e = launch_lora_forward(p, L->num_sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "adapter launch");
   return HMOE_OK;

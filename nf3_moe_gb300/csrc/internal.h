@@ -211,6 +211,7 @@ struct LoraParams {
   int* perm;
   float* u;
   float* part;
+  uint32_t* bound;        // NULL where u's rows have no power of two (lora.cu)
 };
 // Up to this many rows a batch is one launch that finds its groups itself and
 // keeps nothing outside it: no scratch but the (then unused) meta words.
@@ -218,12 +219,13 @@ constexpr int LORA_ONE_LAUNCH_ROWS = 128;
 // Scratch of a larger batch of T rows: the rows grouped by adapter (perm), cut
 // into tiles of up to LORA_TILE_ROWS rows (tiles: adapter or -1, first
 // position, rows, rank), A x of every position (u), and the sums of the pieces
-// of tiles, two for each CTA (part). meta: tiles with an adapter, all tiles.
+// of tiles, two for each CTA (part), a bound on |A x| of every position, in
+// bits (bound). meta: tiles with an adapter, all tiles.
 constexpr int LORA_TILE_ROWS = 128;
 constexpr int LORA_MIN_TILE_ROWS = 16;  // of the plan for the small kernel
 constexpr int LORA_MAX_CTAS = 160;
 struct LoraScratch {
-  size_t meta, tiles, perm, u, part, total;
+  size_t meta, tiles, perm, u, bound, part, total;
 };
 inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
   auto pad = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -233,7 +235,8 @@ inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
   s.tiles = s.meta + 256;
   s.perm = s.tiles + pad(most * 16);
   s.u = s.perm + pad((size_t)T * 4);
-  s.part = s.u + pad((size_t)T * g.max_r16 * 4);
+  s.bound = s.u + pad((size_t)T * g.max_r16 * 4);
+  s.part = s.bound + pad((size_t)T * 4);
   s.total = T <= LORA_ONE_LAUNCH_ROWS ? s.tiles : s.part + (size_t)LORA_MAX_CTAS * 2 * LORA_TILE_ROWS * g.max_r16 * 4;
   return s;
 }

@@ -223,6 +223,34 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
 
+// fp16's exponents are too few for u (x and A of a few 2^-10 each already give
+// a u whose low part is a subnormal, and |u| may pass 65504). So there each row
+// of u is multiplied by a power of two, exactly, that brings a bound on its
+// largest |u| to 2^14 .. 2^15, and the row's scale by the inverse: two values
+// then hold every u to 2^-22 of itself or 2^-39 of the bound. Infinities and
+// NaN, which any factor leaves as they are, have no part in the bound. Beside
+// bf16, which needs none of it, a row of rank 16 takes 3.9 to 4.1 us, 64 rows of 64
+// adapters of rank 64, 6144x6144, 14.5 to 15.1 (rank 128: 29.6 to 31.3), and in
+// tiles 2300 rows of 5, rank 64, 2048x2048, 28.5 to 30.6, 8192 of 8, rank 64,
+// 6144x6144, 72.2 to 73.4 (rank 128: 92.5 to 95.7).
+template <int ACT>
+constexpr bool ROW_POWERS = ACT == ACT_F16;
+// |u|, in bits (which order like the values), as far as it is finite.
+__device__ __forceinline__ uint32_t finite_bits(float u) {
+  const uint32_t b = __float_as_uint(u) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? b : 0u;
+}
+// From 2^-112 down the factor stays 2^126, so that its inverse is a normal number.
+__device__ __forceinline__ uint32_t row_exponent(uint32_t bound) { return max(bound >> 23, 15u); }
+__device__ __forceinline__ float row_power(uint32_t bound) { return __uint_as_float((268u - row_exponent(bound)) << 23); }
+// The scale times the inverse power, kept finite and, but for a scale of 0, away
+// from 0: beyond either end the products B u that it meets (0, at least 2^-48, at
+// most 2^38, or infinite) leave fp16's range to the same side as the exact ones.
+__device__ __forceinline__ float row_scale(float scale, uint32_t bound) {
+  const float s = fabsf(scale) * __uint_as_float((row_exponent(bound) - 14u) << 23);
+  return scale == 0.0f ? 0.0f : copysignf(fminf(fmaxf(s, 1.17549435e-38f), 3.40282347e38f), scale);
+}
+
 // u as a sum of two values of the activation type. An infinite u keeps its
 // value in the first.
 template <int ACT>
@@ -355,6 +383,7 @@ template <int ACT, int R, bool PLANNED>
 __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(LoraParams p) {
   extern __shared__ __align__(16) uint8_t ls_sm[];
   __shared__ int s_tok[LS_TOK], s_cnt[LS_WARPS];
+  __shared__ float s_scale[LS_TOK];  // of the group's rows, where each has a power of two
   __shared__ LsGroups<PLANNED> s_groups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = (int)ls_cluster_rank(), ctas = gridDim.x;  // one cluster a grid row
@@ -517,26 +546,52 @@ __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(Lo
     }
     cluster_arrive();
     cluster_wait();
-    for (int i = 4 * tid; i < n_tok * r16; i += 4 * LS_THREADS) {
+    // Four ranks of a row, from r on: their sums over the cluster (those past the
+    // rank, where A's zeros met whatever x held, are 0), and their two parts.
+    auto gather = [&](int row, int r, bool in) {
       float4 f[8], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) f[c] = c < ctas ? ld_cluster_f32x4(sum + i, c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c = 0; c < 8; ++c)
+        f[c] = in && c < ctas ? ld_cluster_f32x4(sum + row * r16 + r, c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int c = 0; c < 8; ++c) add4(v, f[c]);  // the same order in every CTA
-      const int row = i / r16, r = i - row * r16;
-      // past the rank A's zeros met whatever x held
-      const float u[4] = {r < rank ? v.x : 0.0f, r + 1 < rank ? v.y : 0.0f, r + 2 < rank ? v.z : 0.0f, r + 3 < rank ? v.w : 0.0f};
+      return make_float4(r < rank ? v.x : 0.0f, r + 1 < rank ? v.y : 0.0f, r + 2 < rank ? v.z : 0.0f, r + 3 < rank ? v.w : 0.0f);
+    };
+    auto put = [&](int row, int r, const float4& v) {
+      const float u[4] = {v.x, v.y, v.z, v.w};
       uint16_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) split_act<ACT>(u[e], hi + e, lo + e);
       *reinterpret_cast<uint2*>(u_hi + row * ur + r) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
       *reinterpret_cast<uint2*>(u_lo + row * ur + r) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+    };
+    if constexpr (!ROW_POWERS<ACT>) {
+      for (int i = 4 * tid; i < n_tok * r16; i += 4 * LS_THREADS) put(i / r16, i % r16, gather(i / r16, i % r16, true));
+    } else {  // a row's lanes side by side in a warp
+      constexpr int LANES = R <= 64 ? 16 : 32, ROWS = LS_TOK * LANES / LS_THREADS;
+      const int r = tid % LANES * 4;
+      float4 u[ROWS];
+#pragma unroll
+      for (int d = 0; d < ROWS; ++d) {
+        const int row = tid / LANES + d * (LS_TOK / ROWS);
+        u[d] = gather(row, r, row < n_tok && r < r16);
+      }
+#pragma unroll
+      for (int d = 0; d < ROWS; ++d) {
+        const int row = tid / LANES + d * (LS_TOK / ROWS);
+        uint32_t bound = max(max(finite_bits(u[d].x), finite_bits(u[d].y)), max(finite_bits(u[d].z), finite_bits(u[d].w)));
+        bound = __reduce_max_sync(LANES == 32 ? 0xffffffffu : 0xffffu << (lane & 16), bound);
+        const float power = row_power(bound);
+        if (r == 0) s_scale[row] = row_scale(scale, bound);
+        if (row < n_tok && r < r16) put(row, r, make_float4(power * u[d].x, power * u[d].y, power * u[d].z, power * u[d].w));
+      }
     }
     __syncthreads();
     cluster_arrive();  // this CTA has read the others' sums
 
     // ---- B u over this CTA's columns, 32 a step (rows of u past n_tok are not
     // set; they meet no other row, and their results are not stored)
+    const float by[2] = {ROW_POWERS<ACT> ? s_scale[g] : scale, ROW_POWERS<ACT> ? s_scale[g + 8] : scale};
     auto mma_b = [&](int n, const Cols& s, uint4* y) {
       float d[4][4];
 #pragma unroll
@@ -568,7 +623,7 @@ __global__ void __launch_bounds__(LS_THREADS, ls_per_sm(R)) lora_small_kernel(Lo
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 b = act_x2_to_f32<ACT>(yw[i]);
-            yw[i] = f32_to_act_x2<ACT>(fmaf(scale, d[i][2 * half], b.x), fmaf(scale, d[i][2 * half + 1], b.y));
+            yw[i] = f32_to_act_x2<ACT>(fmaf(by[half], d[i][2 * half], b.x), fmaf(by[half], d[i][2 * half + 1], b.y));
           }
           *reinterpret_cast<uint4*>(p.out + (size_t)t * p.ldout + c) = y[half];
         }
@@ -674,6 +729,8 @@ __global__ void __launch_bounds__(LP_THREADS) lora_plan_kernel(LoraParams p) {
   const int t0 = warp * rounds * 32 + lane;
   int* word = p.T <= LP_ROWS ? s_word : reinterpret_cast<int*>(p.u);
   int* mine = s_base + warp * G;
+  if (p.bound)
+    for (int t = tid; t < p.T; t += LP_THREADS) p.bound[t] = 0u;
   if (tid < G) s_rank[tid] = tid < p.g.slots ? __ldcg(reinterpret_cast<const int*>(p.packed) + tid) : 0;
   int bits = 1;  // of a group's number
   while (G > 1 << bits) ++bits;
@@ -922,7 +979,9 @@ struct LoraSpan {
 // A x of a tile's rows: to u[pos][r] where a CTA has the tile's whole K extent,
 // else a sum for each piece to part[slot][row][r], which the reader adds up
 // (letting the last CTA of a tile add them up here cost 10 us of this kernel's
-// tail at 8192 rows). HBM bounds it: 16 KB of x a unit, four MMAs of 128 x r x 16.
+// tail at 8192 rows). For fp16 also a bound on each row's |u|, to bound[pos]:
+// the row's largest, or its pieces' largest times their number. HBM bounds it:
+// 16 KB of x a unit, four MMAs of 128 x r x 16.
 template <int ACT>
 __global__ void __launch_bounds__(LA_THREADS, 1)
     lora_shrink_kernel(const __grid_constant__ LoraParams p) {
@@ -1038,15 +1097,26 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       // lane = row
       float* dst = nk == p.g.KB ? p.u + (size_t)(t.pos + row) * p.g.max_r16
                                 : p.part + ((size_t)(2 * blockIdx.x + (kb0 == 0)) * LORA_TILE_ROWS + row) * p.g.max_r16;
+      uint32_t bound = 0;
       for (int col = 0; col < t.r16; col += 16) {
         uint32_t w[16];
         tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)buf * acc_cols + col, w);
         tmem_wait_ld();
+        if constexpr (ROW_POWERS<ACT>) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) bound = max(bound, finite_bits(__uint_as_float(w[i])));
+        }
         if (row < t.n) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(dst + col + 4 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
+      }
+      if constexpr (ROW_POWERS<ACT>) {
+        const unsigned w0 = (unsigned)sp.tile * (unsigned)p.g.KB;
+        const unsigned pieces = shares.cta(w0 + p.g.KB - 1) - shares.cta(w0) + 1;
+        const float most = fminf(__uint_as_float(bound) * (float)pieces, 3.40282347e38f);
+        if (row < t.n) atomicMax(p.bound + t.pos + row, __float_as_uint(most));  // in any order the same
       }
       tc_fence_before();
       __syncwarp();
@@ -1092,6 +1162,7 @@ static_assert(LB_ACC % 2 == 0, "each epilogue group has accumulators of its own"
 struct LoraPieces {
   const float* first;
   const float* more;  // the second piece
+  const uint32_t* bound;  // of the rows, where each has a power of two
   int n;
 };
 template <int ACT, int Q>
@@ -1124,10 +1195,20 @@ __device__ __forceinline__ void lora_u_operand(const LoraTile& t, const LoraPiec
       for (int q = 0; q < Q; ++q)
         f[q] = make_float4(f[q].x + m[q].x, f[q].y + m[q].y, f[q].z + m[q].z, f[q].w + m[q].w);
     }
+    uint32_t bound[Q];  // asked for here: with the sums above it would be waited for before the walk
+    if constexpr (ROW_POWERS<ACT>) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) bound[q] = in[q] ? __ldcg(pc.bound + row[q]) : 0u;
+    }
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       if (i0 + q * nw >= items) break;
-      const float v[4] = {f[q].x, f[q].y, f[q].z, f[q].w};
+      const float power = ROW_POWERS<ACT> ? row_power(bound[q]) : 1.0f;
+      float v[4] = {f[q].x, f[q].y, f[q].z, f[q].w};
+      if constexpr (ROW_POWERS<ACT>) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= power;
+      }
       uint16_t h[4], l[4];
       // past the rank A's zeros met whatever x held
 #pragma unroll
@@ -1146,6 +1227,7 @@ __device__ __forceinline__ LoraPieces lora_pieces(const LoraParams& p, const Lor
   pc.first = b0 == b1 ? p.u + (size_t)t.pos * p.g.max_r16
                       : p.part + (size_t)(2 * b0 + 1) * LORA_TILE_ROWS * p.g.max_r16;
   pc.more = p.part + (size_t)(2 * b0 + 2) * LORA_TILE_ROWS * p.g.max_r16;
+  pc.bound = p.bound + t.pos;
   return pc;
 }
 
@@ -1349,6 +1431,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
                      ? __ldcs(reinterpret_cast<const uint4*>(p.base + (size_t)row[k] * p.ldbase + n))
                      : make_uint4(0, 0, 0, 0);
       };
+      float scales[ROW_POWERS<ACT> ? 4 : 1] = {scale};  // of the lane's rows
       // Unit i from its base values in y, which are then unit i + 4's.
       auto unit_of = [&](int i, uint4* y) {
         if (with) {
@@ -1367,8 +1450,8 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
               uint32_t* yw = reinterpret_cast<uint32_t*>(&y[2 * h + k]);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const float2 f = fma_x2(__uint_as_float(w[4 * j + 2 * k]), __uint_as_float(w[4 * j + 2 * k + 1]), scale,
-                                        act_x2_to_f32<ACT>(yw[j]));
+                const float2 f = fma_x2(__uint_as_float(w[4 * j + 2 * k]), __uint_as_float(w[4 * j + 2 * k + 1]),
+                                        scales[ROW_POWERS<ACT> ? 2 * h + k : 0], act_x2_to_f32<ACT>(yw[j]));
                 yw[j] = f32_to_act_x2<ACT>(f.x, f.y);
               }
             }
@@ -1392,6 +1475,16 @@ __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid
       load(i0, y0);
       load(i0 + 2, y1);
       if (v == v0 && with) first_u(t, sp.tile);
+      if constexpr (ROW_POWERS<ACT>) {  // after the A x kernel's end, which first_u waits for
+        uint32_t bound[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = quarter * 32 + (lane >> 2) + 8 * k;
+          bound[k] = with && r < t.n ? __ldcg(p.bound + t.pos + r) : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) scales[k] = row_scale(scale, bound[k]);
+      }
       for (int i = i0; i < sp.n && ok; i += 4) {
         unit_of(i, y0);
         if (i + 2 < sp.n && ok) unit_of(i + 2, y1);
@@ -1441,6 +1534,7 @@ template <int ACT>
 static cudaError_t forward_of(LoraParams p, int num_sms, cudaStream_t st) {
   if (p.T <= LS_MAX_T) return small_of<ACT, false>(p, st);
   if (lora_planned_small(p.g, p.T, num_sms)) {
+    p.bound = nullptr;  // the small kernel's rows have theirs in shared memory
     const cudaError_t e = p.T <= LS_COUNT_T ? cudaSuccess : launch_plan(p, LS_TOK, st);
     return e == cudaSuccess ? small_of<ACT, true>(p, st) : e;
   }
