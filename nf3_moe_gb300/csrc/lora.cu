@@ -7,13 +7,13 @@
 // the tensor cores do about 290 in a byte's time at HBM.
 //
 // u = A x is summed in fp32 and enters the second product as the sum of two
-// values of the activation type (split_act): u then keeps at least 16 bits, and
-// out has one rounding, its own. One 16-bit u would add an error as large as
-// that. No sum's order depends on the schedule.
+// values of the activation type (split_act): u then keeps 16 bits in bf16, 22 in
+// fp16 (ROW_POWERS), and out has one rounding, its own. One 16-bit u would add an
+// error as large as that. No sum's order depends on the schedule.
 //
 // Two ways, by what the host knows of the batch (lora_planned_small): a kernel
 // that serves 16 rows of one adapter with a small cluster, whose time is
-// latency (one launch up to 256 rows, two above), and a pair of persistent
+// latency (one launch up to 2048 rows, two above), and a pair of persistent
 // tensor-core kernels over tiles of 128 rows of one adapter (three launches).
 #include <math.h>
 
@@ -283,7 +283,7 @@ struct LsGroups {
   __device__ __forceinline__ void clear(const LoraParams& p, int tid) {
     for (int g = tid; g <= p.g.slots; g += LS_THREADS) n[g] = 0;
   }
-  // A warp's range of rows.
+  // A warp's rows, 32 at a time.
   __device__ __forceinline__ int rounds(const LoraParams& p) const { return (p.T + LS_THREADS - 1) / LS_THREADS; }
 
   // Returns the number of groups. wsum: scratch of LS_WARPS words.
@@ -700,8 +700,8 @@ static cudaError_t small_of(const LoraParams& p, cudaStream_t st) {
 // Three launches. The plan groups the rows by adapter and cuts the groups into
 // tiles of up to 128 rows; the rows of a tile sit on the M side of tcgen05.mma
 // and the adapter on its N side. 8192 rows of 12 requests, ranks up to 64,
-// 6144x6144 take 71.8 us, about 5 for the plan, 22 for A x (104 MB, at 6.9 TB/s
-// once its rings run) and 45 for B u (200 MB, 5.7 TB/s); the floor is 46.
+// 6144x6144 take 72.3 us, about 5 for the plan, 22 for A x (104 MB, 70% of HBM
+// with its start and end) and 45 for B u (201 MB, 67%); the floor is 46.
 
 // One CTA. Rows without an adapter (or with an empty slot) form the last group.
 // The rows of a group keep their order, so that the tiles, and with them the
@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     int j = 0;
     for (unsigned v = v0; v < v1 && ok; ++j) {
       const LoraSpan sp(v, v1, p.g.KB);
-      const int kb0 = sp.first, nk = sp.n;
+      const int nk = sp.n;
       const LoraTile t = lora_tile(p, sp.tile);
       v += nk;
       const int buf = j & 1;
@@ -1245,8 +1245,9 @@ __device__ __forceinline__ float2 fma_x2(float a, float b, float s, float2 c) {
 // out = base + scale B u. u enters as its two parts (split_act), whose products
 // with B add up in the same accumulator. An epilogue warp owns 32 rows and 32
 // columns of every second unit; a lane holds 16 bytes of 4 rows, whose base
-// values it has loaded two units ahead. HBM bounds it, 16 KB of base in and of
-// out a unit. Without B's permuted rows the results had to cross shared memory
+// values it has loaded two units ahead. It moves 16 KB of base in and of out a
+// unit, at 67% of HBM (8192 rows): its start and tail on 152 SMs and the epilogue
+// warps' issue of loads and stores take the rest. Without B's permuted rows the results had to cross shared memory
 // to reach 64 bytes of a row together: 54 against 44 us at 8192 rows.
 template <int ACT>
 __global__ void __launch_bounds__(LB_THREADS, 1) lora_expand_kernel(const __grid_constant__ LoraParams p) {

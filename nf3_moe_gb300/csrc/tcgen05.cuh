@@ -80,18 +80,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
 }
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart (SBO), version 1, base offset 0 (atoms 1024-aligned).
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
-  uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1u << 16;                 // leading byte offset (unused for swizzled K-major)
-  d |= (uint64_t)(1024u >> 4) << 32;       // stride byte offset
-  d |= (uint64_t)1u << 46;                 // descriptor version
-  d |= (uint64_t)2u << 61;                 // SWIZZLE_128B
-  return d;
-}
-// The descriptor above as (low word, high word). The low word holds the start
-// address (>> 4) and the leading byte offset; the high word is constant.
-// Advancing 32 bytes along K adds 2 to the low word.
+// 1024 bytes apart (SBO), version 1, base offset 0 (atoms 1024-aligned), as (low
+// word, high word). The low word holds the start address (>> 4) and the leading
+// byte offset (1, unused for swizzled K-major); the high word, with the stride
+// byte offset, the version and the swizzle, is constant. Advancing 32 bytes along
+// K adds 2 to the low word.
 constexpr uint32_t SW128_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t smem_desc_sw128_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
 __device__ __forceinline__ uint64_t desc_from_lo(uint32_t lo) {
