@@ -165,5 +165,5 @@ class LoraAdapters:
     def __call__(self, x, ids, base=None, out=None):
         if out is None:
             out = torch.empty((x.shape[0], self.N), dtype=self.dtype, device=x.device)
-        hmoe_lora_forward(self.lora, x, ids, out, self.ws, base=base)
+        hmoe_lora_forward(self.lora, x, ids, out, self.ws, base)
         return out
