@@ -56,7 +56,7 @@ class ExpertBranch:
         ids, gates, perm, offsets = routes
         rows, plan = self.rows_of.dispatch(x, perm, offsets)
         expert_of_row = ids.reshape(-1)[plan.row_slot.long()]      # no padding here (align=1): every row has a slot
-        z = self.adapters(rows.detach(), expert_of_row)
+        z = self.adapters(rows.detach(), expert_of_row)            # they have no gradient: constants up to here
         z.requires_grad_(logits.requires_grad)
         return self.rows_of.combine(z, plan, gates, ids=ids, logits=logits), z, plan
 

@@ -132,8 +132,8 @@ __device__ __forceinline__ int lora_slot(const LoraParams& p, int t) {
 // adapters of ranks 1 to 64, 6144x6144: 33 MB in 14.0 us, but two CTAs of rank 64
 // on one SM fetch 512 KB, at 30 to 36 KB a us however many loads are in flight:
 // rings of bulk copies took 16.7 us); below, a chain of waits does:
-// ids, A and x, the cluster's exchange, B (one row of rank 16, 2048x2048: 3.6 us,
-// of rank 64, 6144x6144: 6.1 us). So a CTA has the next step's operands on their
+// ids, A and x, the cluster's exchange, B (one row of rank 16, 2048x2048: 3.9 us,
+// of rank 64, 6144x6144, from L2: 8.0 us). So a CTA has the next step's operands on their
 // way, B's first ones and the base's before the exchange, and only the group's
 // own rows are exchanged. (Asking L2 for B at the start made 64 rows 2 us slower:
 // it delays A.)
