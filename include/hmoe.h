@@ -636,6 +636,47 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* lora, const void* x, int ldx, int
  *   No page defines it. */
 void hmoe_lora_destroy(hmoe_lora* lora);
 
+/* ------------------------------------------------------------ the whole layer for a few tokens
+ * A decode step from hidden states: the router's product, its top-k and
+ * gates, the experts and their sum, in two kernels.
+ *   logits[t][e] = sum_h x[t][h] * router[e][h] (+ bias[e])
+ *   ids, gates:  as hmoe_plan_routes gives them for these logits
+ *   out[t] = sum_j gates[t][j] * W2_e (silu(W1_e x_t) * W3_e x_t),  e = ids[t][j]
+ * Unlike hmoe_forward, h is not rounded to one value of the activation type
+ * between the products (it keeps 16 significant bits in bf16; in fp16 22, or
+ * 2^-38 of its token's largest where that is more), so that the result's own
+ * rounding is what remains. Sums are fp32 in a fixed order: the same call
+ * gives the same bits. A token whose x holds a NaN gets NaN and some experts;
+ * the other tokens do not see it.
+ *   These entry points have no counterpart on the pages; the weights and the
+ *   route geometry are the layer's ("quant: nvfp4_nf3_hybrid -- native serving
+ *   ...", How it works, an M<=8 decode path).
+ * Conventions as for the layer. Layers with act_quant are not supported. */
+#define HMOE_DECODE_MAX_TOKENS 8
+
+/* Workspace bytes for hmoe_decode at up to max_tokens tokens, 0..8. It may
+ * not be used by two calls that overlap on the GPU. Zero it once before its
+ * first use (hmoe_workspace_init), and again after a call reports
+ * HMOE_ERR_DEVICE_TIMEOUT. Host only.
+ *   No page defines it. Errors: the desc checks of hmoe_workspace_size;
+ *   HMOE_ERR_UNSUPPORTED_SHAPE (act_quant, max_tokens above 8, H above about
+ *   95000 or I above about 47000, which shared memory cannot hold);
+ *   HMOE_ERR_INVALID_ARG (bytes NULL, max_tokens < 0). */
+hmoe_status hmoe_decode_workspace_size(const hmoe_layer_desc* desc, int max_tokens, size_t* bytes);
+
+/* x: device [T][H], router: device [E][H], both of the activation type;
+ * bias: device fp32 [E], or NULL (an expert at -infinity is chosen only where
+ * too few others are left; NaN is not supported). out: device [T][H] of the
+ * activation type, fully overwritten, not x. ids int32 [T][topk], gates fp32
+ * [T][topk]: written where not NULL. x, router and out 16-byte aligned. T = 0
+ * is valid.
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
+ *   pointer, T < 0, out is x), HMOE_ERR_UNSUPPORTED_SHAPE (as for the
+ *   workspace), HMOE_ERR_WORKSPACE_TOO_SMALL, HMOE_ERR_CUDA; a bounded wait
+ *   that ran out is HMOE_ERR_DEVICE_TIMEOUT through hmoe_check_device_status. */
+hmoe_status hmoe_decode(const hmoe_layer* layer, const void* x, int T, const void* router, const float* bias, void* out,
+                        int32_t* ids, float* gates, void* ws, size_t ws_bytes, hmoe_stream_t stream);
+
 /* Message for the last failing call on this thread ("" if none). Part of
  * the error convention at the top of this file; no page defines it. */
 const char* hmoe_last_error(void);

@@ -39,6 +39,7 @@ EXPORTS = (
     "hmoe_combine_backward",
     "hmoe_lora_packed_size", "hmoe_lora_workspace_size", "hmoe_lora_create", "hmoe_lora_load", "hmoe_lora_forward",
     "hmoe_lora_destroy",
+    "hmoe_decode_workspace_size", "hmoe_decode",
 )
 
 
@@ -123,6 +124,8 @@ def load(path=LIB_PATH):
         "hmoe_lora_load": (i, [vp, i, vp, vp, i, ctypes.c_float, vp]),
         "hmoe_lora_forward": (i, [vp, vp, i, i, vp, vp, i, vp, i, vp, sz, vp]),
         "hmoe_lora_destroy": (None, [vp]),
+        "hmoe_decode_workspace_size": (i, [P(LayerDesc), i, P(sz)]),
+        "hmoe_decode": (i, [vp, vp, i, vp, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

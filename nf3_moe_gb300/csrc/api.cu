@@ -1305,3 +1305,109 @@ hmoe_status hmoe_lora_forward(const hmoe_lora* L, const void* x, int ldx, int T,
 void hmoe_lora_destroy(hmoe_lora* lora) { delete lora; }
 
 }  // extern "C"
+
+// ------------------------------------------------------------ the whole layer for a few tokens
+namespace {
+
+static_assert(HMOE_DECODE_MAX_TOKENS == DECODE_MAX_TOKENS, "the header's limit");
+
+struct DecodeWs {
+  size_t ctl, logits, hmax, h, y, total;
+};
+// The status word, then regions whose places do not depend on T before those that do.
+DecodeWs decode_ws(const hmoe_layer_desc& d, int T) {
+  DecodeWs w{};
+  const size_t S = (size_t)T * d.topk;
+  w.ctl = 256;
+  w.hmax = w.ctl + align256((size_t)(DK_CTL_ROWS + d.H / 128) * 4);
+  w.logits = w.hmax + align256((size_t)DECODE_MAX_TOKENS * MAX_TOPK * 4);
+  w.h = w.logits + align256((size_t)T * d.E * 4);
+  w.y = w.h + align256(S * d.I * 4);
+  w.total = w.y + align256(S * d.H * 4);
+  return w;
+}
+
+hmoe_status check_decode(const hmoe_layer_desc& d, int T) {
+  if (T < 0) return fail(HMOE_ERR_INVALID_ARG, "T=%d < 0", T);
+  if (T > DECODE_MAX_TOKENS)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d exceeds %d tokens", T, DECODE_MAX_TOKENS);
+  if (d.act_quant != HMOE_ACT_QUANT_NONE)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "layers with quantised activations (W4A4) are not supported");
+  const long long most = decode_act_cap();
+  if (2LL * d.H > most || 4LL * d.I > most)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "H=%d or I=%d exceeds what shared memory holds of one token (H <= %lld, I <= %lld)",
+                d.H, d.I, most / 2, most / 4);
+  return HMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+hmoe_status hmoe_decode_workspace_size(const hmoe_layer_desc* desc, int max_tokens, size_t* bytes) {
+  hmoe_status s = check_desc(desc);
+  if (s != HMOE_OK) return s;
+  if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  if ((s = check_decode(*desc, max_tokens)) != HMOE_OK) return s;
+  *bytes = decode_ws(*desc, max_tokens).total;
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_decode(const hmoe_layer* L, const void* x, int T, const void* router, const float* bias, void* out,
+                        int32_t* ids, float* gates, void* ws, size_t ws_bytes, hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_decode");
+  if (!L) return fail(HMOE_ERR_INVALID_ARG, "layer is NULL");
+  const hmoe_layer_desc& d = L->d;
+  hmoe_status s = check_decode(d, T);
+  if (s != HMOE_OK) return s;
+  if (T == 0) return HMOE_OK;
+  if (!x || !router || !out) return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
+  if (!aligned16(x) || !aligned16(router) || !aligned16(out))
+    return fail(HMOE_ERR_INVALID_ARG, "x, router and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(gates)) & 3)
+    return fail(HMOE_ERR_INVALID_ARG, "bias, ids and gates must be aligned to their elements");
+  if (x == out) return fail(HMOE_ERR_INVALID_ARG, "out must not be x");
+  if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
+  const DecodeWs w = decode_ws(d, T);
+  if (ws_bytes < w.total)
+    return fail(HMOE_ERR_WORKSPACE_TOO_SMALL, "workspace holds %zu bytes, T=%d needs %zu", ws_bytes, T, w.total);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  DecodeParams p{};
+  p.kept_buf = L->kept_buf;
+  p.nf3_buf = L->nf3_buf;
+  p.kept_fmt = d.kept_format;
+  p.act_type = d.act_dtype;
+  p.H = d.H;
+  p.I = d.I;
+  p.E = d.E;
+  p.topk = d.topk;
+  p.T = T;
+  p.act_cap = decode_act_cap();
+  p.group_tokens = std::min(DECODE_MAX_TOKENS, std::min(p.act_cap / (2 * d.H), p.act_cap / (4 * d.I)));
+  p.shares = L->num_sms;
+  const auto steps = [](int kb) { return (uint32_t)(kb % 2 == 0 ? kb / 2 : kb); };
+  p.by_shares = div_by_const((uint32_t)p.shares);
+  p.by_spu13 = div_by_const(steps(d.H / TILE_K));
+  p.by_spu2 = div_by_const(steps(d.I / TILE_K));
+  p.x = static_cast<const uint16_t*>(x);
+  p.logits = reinterpret_cast<float*>(b + w.logits);
+  p.ids = ids;
+  p.gates = gates;
+  p.h = reinterpret_cast<float*>(b + w.h);
+  p.hmax = reinterpret_cast<uint32_t*>(b + w.hmax);
+  p.y = reinterpret_cast<float*>(b + w.y);
+  p.out = static_cast<uint16_t*>(out);
+  p.ctl = reinterpret_cast<int*>(b + w.ctl);
+  p.status = reinterpret_cast<int*>(b);
+  p.wait_limit_ns = WAIT_LIMIT_NS;
+  p.kept_expert_bytes = L->gk.expert_bytes;
+  p.nf3_expert_bytes = L->gn.expert_bytes;
+  p.kept_w2_off = L->gk.w13_bytes;
+  p.nf3_w2_off = L->gn.w13_bytes;
+  p.tab = L->tab;
+  cudaError_t e = launch_decode(p, static_cast<const uint16_t*>(router), bias, L->num_sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+  return HMOE_OK;
+}
+
+}  // extern "C"

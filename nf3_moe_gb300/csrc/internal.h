@@ -242,6 +242,52 @@ inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
 }
 cudaError_t launch_lora_forward(const LoraParams& p, int num_sms, cudaStream_t st);
 
+// ---------------------------------------------------------------- the whole layer for a few tokens (decode.cu)
+constexpr int DECODE_MAX_TOKENS = 8;
+constexpr int DK_SMEM_LIMIT = 232448;    // dynamic shared memory of a CTA, 227 KB
+constexpr int DK_MAX_ROW_TILES = 1024;   // H / 128: above what the activations' shared memory admits
+// The counters of a call, in ints: claimed shares, CTAs that left, then the
+// W13 units done per group and the W2 units done per row tile.
+constexpr int DK_CTL_DONE = 64;
+constexpr int DK_CTL_ROWS = DK_CTL_DONE + DECODE_MAX_TOKENS * MAX_TOPK;
+// Division of 0 <= n < 2^31 by a constant: (umulhi(n, mul) + n) >> shift
+// (Granlund and Montgomery, Division by Invariant Integers using Multiplication).
+struct DivBy {
+  uint32_t mul;
+  int shift;
+};
+inline DivBy div_by_const(uint32_t d) {
+  int l = 0;
+  while ((1ull << l) < d) ++l;
+  return DivBy{(uint32_t)((((1ull << l) - d) << 32) / d + 1), l};
+}
+struct DecodeParams {
+  const uint8_t* kept_buf;
+  const uint8_t* nf3_buf;
+  int kept_fmt, act_type;
+  int H, I, E, topk, T;
+  int group_tokens;        // slots of a group, up to 8: as many as the activations' shared memory admits
+  int act_cap;             // bytes of that memory
+  int shares;              // of each product, one per SM
+  DivBy by_shares, by_spu13, by_spu2;  // division by the shares and by the steps of a unit
+  const uint16_t* x;       // [T][H]
+  float* logits;           // [T][E]
+  int* ids;                // [T][topk], or NULL
+  float* gates;            // [T][topk], or NULL
+  float* h;                // [T * topk][I]
+  uint32_t* hmax;          // fp16: bits of a slot's largest |h|; zero between calls
+  float* y;                // [T * topk][H]
+  uint16_t* out;           // [T][H]
+  int* ctl;                // zero between calls
+  int* status;
+  unsigned long long wait_limit_ns;
+  size_t kept_expert_bytes, nf3_expert_bytes, kept_w2_off, nf3_w2_off;
+  ExpertTable tab;
+};
+// Bytes for activations beside the kernel's tables.
+int decode_act_cap();
+cudaError_t launch_decode(const DecodeParams& p, const uint16_t* router, const float* bias, int num_sms, cudaStream_t st);
+
 // Raises a kernel's dynamic shared-memory limit once per device: the
 // attribute belongs to the current device, so a process that launches on
 // several GPUs sets it on each. done is the kernel's bit mask of devices
