@@ -677,6 +677,58 @@ hmoe_status hmoe_decode_workspace_size(const hmoe_layer_desc* desc, int max_toke
 hmoe_status hmoe_decode(const hmoe_layer* layer, const void* x, int T, const void* router, const float* bias, void* out,
                         int32_t* ids, float* gates, void* ws, size_t ws_bytes, hmoe_stream_t stream);
 
+/* ------------------------------------------------------------ 4-bit integer linear
+ * A weight matrix of 4-bit integers with a scale, and where wanted a zero
+ * point, per group along K, times few rows of x:
+ *   y[t][n] = sum_k x[t][k] * (q[n][k] - z[n][k / group]) * s[n][k / group] (+ bias[n])
+ * for the projections of a decode step; any number of rows is taken, 16 at
+ * most reading the weights once. The integers and their products with x are
+ * exact, a group's sum and all else are fp32 in a fixed order, rounded once to
+ * the activation type: the same call gives the same bits.
+ *   These entry points have no counterpart on the pages; beside the dense
+ *   linear above they take the integer formats' checkpoints.
+ * Conventions as for the layer. No workspace. */
+typedef struct {
+  int N;         /* output features, 1..2^20 */
+  int K;         /* input features, a multiple of group; a row must fit shared memory (about 60000) */
+  int group;     /* weights of one scale along K: 32, 64 or 128 */
+  int zeros;     /* 1: zero points are given; 0: all are 8 */
+  int act_dtype; /* hmoe_act_dtype of x, the scales, bias and out; 0 is bf16 */
+} hmoe_int4_desc;
+
+typedef struct hmoe_int4 hmoe_int4; /* opaque host handle: no device memory */
+
+/* Bytes of the packed matrix (the packed argument of hmoe_int4_pack). Host
+ * only.
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG,
+ *   HMOE_ERR_UNSUPPORTED_SHAPE (the limits above). */
+hmoe_status hmoe_int4_packed_size(const hmoe_int4_desc* desc, size_t* bytes);
+
+/* Repack W and create the handle. codes: device uint8 [N][K/2], element 2i in
+ * the low nibble, q in 0..15. scales: device [N][K/group] of act_dtype.
+ * zeros: device uint8 [N][K/group], of which the low 4 bits count, or NULL
+ * where the descriptor has none. packed: device buffer of
+ * hmoe_int4_packed_size bytes, 128-byte aligned, alive while the handle is
+ * used. The sources may be freed once the stream has passed this point.
+ *   No page defines it. Errors: as hmoe_int4_packed_size, HMOE_ERR_CUDA. */
+hmoe_status hmoe_int4_pack(const hmoe_int4_desc* desc, const void* codes, const void* scales, const void* zeros,
+                           void* packed, hmoe_stream_t stream, hmoe_int4** out);
+
+/* y = W x (+ bias). x: device [T] rows of K, ldx elements apart (a multiple of
+ * 8), 16-byte aligned, so column ranges of wider tensors serve; bias: device
+ * [N], or NULL; out: device [T] rows of N, ldout elements apart, fully
+ * overwritten, overlapping nothing else. All of the activation type. T = 0 is
+ * valid.
+ *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
+ *   pointer, T < 0, a bad stride), HMOE_ERR_UNSUPPORTED_SHAPE (more rows than
+ *   65535 passes), HMOE_ERR_CUDA. */
+hmoe_status hmoe_int4_forward(const hmoe_int4* linear, const void* x, int ldx, int T, const void* bias, void* out,
+                              int ldout, hmoe_stream_t stream);
+
+/* Free the handle (host memory only). NULL is ignored.
+ *   No page defines it. */
+void hmoe_int4_destroy(hmoe_int4* linear);
+
 /* Message for the last failing call on this thread ("" if none). Part of
  * the error convention at the top of this file; no page defines it. */
 const char* hmoe_last_error(void);

@@ -39,6 +39,7 @@ __all__ = [
     "LoraDesc", "hmoe_lora_packed_size", "hmoe_lora_workspace_size", "hmoe_lora_create", "hmoe_lora_load",
     "hmoe_lora_forward", "LoraAdapters",
     "hmoe_decode", "hmoe_decode_workspace_size", "DECODE_MAX_TOKENS",
+    "Int4Desc", "hmoe_int4_packed_size", "hmoe_int4_pack", "hmoe_int4_forward", "LinearInt4",
 ]
 
 
@@ -448,9 +449,10 @@ def hmoe_quantize_act_nvfp4(x, global_scale, codes, scales, stream=None):
 
 # ------------------------------------------------------------------ rows sorted by expert, low-rank adapters
 # These modules use the checks and helpers above.
-from ._lib import ROW_BF16, ROW_F16, ROW_F32, DispatchDesc, LoraDesc  # noqa: E402, F401
+from ._lib import ROW_BF16, ROW_F16, ROW_F32, DispatchDesc, Int4Desc, LoraDesc  # noqa: E402, F401
 from .rows import (ExpertRows, RowPlan, hmoe_combine, hmoe_combine_backward, hmoe_dispatch,  # noqa: E402, F401
                    hmoe_dispatch_backward, hmoe_dispatch_rows, hmoe_dispatch_workspace_size, row_torch_dtype)
 from .decode import DECODE_MAX_TOKENS, hmoe_decode, hmoe_decode_workspace_size  # noqa: E402, F401
 from .lora import (Lora, LoraAdapters, _no_gradient, hmoe_lora_create, hmoe_lora_forward, hmoe_lora_load,  # noqa: E402, F401
                    hmoe_lora_packed_size, hmoe_lora_workspace_size)
+from .int4 import Int4, LinearInt4, hmoe_int4_forward, hmoe_int4_pack, hmoe_int4_packed_size  # noqa: E402, F401

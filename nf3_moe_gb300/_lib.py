@@ -40,6 +40,7 @@ EXPORTS = (
     "hmoe_lora_packed_size", "hmoe_lora_workspace_size", "hmoe_lora_create", "hmoe_lora_load", "hmoe_lora_forward",
     "hmoe_lora_destroy",
     "hmoe_decode_workspace_size", "hmoe_decode",
+    "hmoe_int4_packed_size", "hmoe_int4_pack", "hmoe_int4_forward", "hmoe_int4_destroy",
 )
 
 
@@ -60,6 +61,11 @@ class DispatchDesc(ctypes.Structure):
 
 class LoraDesc(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int), ("N", ctypes.c_int), ("slots", ctypes.c_int), ("max_rank", ctypes.c_int),
+                ("act_dtype", ctypes.c_int)]
+
+
+class Int4Desc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("group", ctypes.c_int), ("zeros", ctypes.c_int),
                 ("act_dtype", ctypes.c_int)]
 
 
@@ -125,6 +131,10 @@ def load(path=LIB_PATH):
         "hmoe_lora_forward": (i, [vp, vp, i, i, vp, vp, i, vp, i, vp, sz, vp]),
         "hmoe_lora_destroy": (None, [vp]),
         "hmoe_decode_workspace_size": (i, [P(LayerDesc), i, P(sz)]),
+        "hmoe_int4_packed_size": (i, [P(Int4Desc), P(sz)]),
+        "hmoe_int4_pack": (i, [P(Int4Desc), vp, vp, vp, vp, vp, P(vp)]),
+        "hmoe_int4_forward": (i, [vp, vp, i, i, vp, vp, i, vp]),
+        "hmoe_int4_destroy": (None, [vp]),
         "hmoe_decode": (i, [vp, vp, i, vp, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():

@@ -1383,6 +1383,7 @@ hmoe_status hmoe_decode(const hmoe_layer* L, const void* x, int T, const void* r
   p.topk = d.topk;
   p.T = T;
   p.act_cap = decode_act_cap();
+  p.lut_stride = 128;
   p.group_tokens = std::min(DECODE_MAX_TOKENS, std::min(p.act_cap / (2 * d.H), p.act_cap / (4 * d.I)));
   p.shares = L->num_sms;
   const auto steps = [](int kb) { return (uint32_t)(kb % 2 == 0 ? kb / 2 : kb); };
@@ -1409,5 +1410,114 @@ hmoe_status hmoe_decode(const hmoe_layer* L, const void* x, int T, const void* r
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   return HMOE_OK;
 }
+
+}  // extern "C"
+
+// ------------------------------------------------------------ 4-bit integer linear
+struct hmoe_int4 {
+  hmoe_int4_desc d;
+  Int4Geom g;
+  uint8_t* packed;
+  int num_sms;
+};
+
+namespace {
+
+hmoe_status check_int4_desc(const hmoe_int4_desc* d) {
+  if (!d) return fail(HMOE_ERR_INVALID_ARG, "desc is NULL");
+  if (d->act_dtype != HMOE_ACT_BF16 && d->act_dtype != HMOE_ACT_F16)
+    return fail(HMOE_ERR_INVALID_ARG, "act_dtype must be HMOE_ACT_BF16 (0) or HMOE_ACT_F16 (1), got %d", d->act_dtype);
+  if (d->zeros != 0 && d->zeros != 1) return fail(HMOE_ERR_INVALID_ARG, "zeros must be 0 or 1, got %d", d->zeros);
+  if (d->N <= 0 || d->K <= 0) return fail(HMOE_ERR_INVALID_ARG, "N and K must be positive");
+  if (d->group != 32 && d->group != 64 && d->group != 128)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "group=%d must be 32, 64 or 128", d->group);
+  if (d->K % d->group != 0) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "K=%d must be a multiple of the group, %d", d->K, d->group);
+  if (d->N > INT4_MAX_DIM || d->K > INT4_MAX_DIM || int4_pass(int4_geom(d->N, d->K, d->group), 1) < 1)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "N=%d (up to %d) or K=%d (a row of x must fit shared memory) is too large", d->N,
+                INT4_MAX_DIM, d->K);
+  return HMOE_OK;
+}
+
+size_t int4_bytes(const hmoe_int4_desc& d) {
+  const Int4Geom g = int4_geom(d.N, d.K, d.group);
+  return (size_t)g.units * g.NB * i4_block_bytes(128 / d.group, d.zeros != 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+hmoe_status hmoe_int4_packed_size(const hmoe_int4_desc* desc, size_t* bytes) {
+  hmoe_status s = check_int4_desc(desc);
+  if (s != HMOE_OK) return s;
+  if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = int4_bytes(*desc);
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_int4_pack(const hmoe_int4_desc* desc, const void* codes, const void* scales, const void* zeros,
+                           void* packed, hmoe_stream_t stream, hmoe_int4** out) {
+  const NvtxRange nvtx("hmoe_int4_pack");
+  hmoe_status s = check_int4_desc(desc);
+  if (s != HMOE_OK) return s;
+  if (!codes || !scales || !packed || !out || (desc->zeros && !zeros))
+    return fail(HMOE_ERR_INVALID_ARG, "codes, scales, zeros, packed or out is NULL");
+  if (!desc->zeros && zeros) return fail(HMOE_ERR_INVALID_ARG, "zeros given, but the descriptor has none");
+  if (reinterpret_cast<uintptr_t>(packed) % 128 != 0)
+    return fail(HMOE_ERR_INVALID_ARG, "the packed buffer must be 128-byte aligned");
+  if (reinterpret_cast<uintptr_t>(scales) & 1) return fail(HMOE_ERR_INVALID_ARG, "scales must be aligned to their elements");
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HMOE_OK) return s;
+  hmoe_int4* L = new (std::nothrow) hmoe_int4();
+  if (!L) return fail(HMOE_ERR_INVALID_ARG, "out of host memory");
+  L->d = *desc;
+  L->g = int4_geom(desc->N, desc->K, desc->group);
+  L->packed = static_cast<uint8_t*>(packed);
+  L->num_sms = sms;
+  cudaError_t e = launch_int4_pack(L->g, static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
+                                   static_cast<const uint8_t*>(zeros), L->packed, (cudaStream_t)stream);
+  if (e != cudaSuccess) {
+    delete L;
+    return cuda_fail(e, "int4 pack launch");
+  }
+  *out = L;
+  return HMOE_OK;
+}
+
+hmoe_status hmoe_int4_forward(const hmoe_int4* L, const void* x, int ldx, int T, const void* bias, void* out, int ldout,
+                              hmoe_stream_t stream) {
+  const NvtxRange nvtx("hmoe_int4_forward");
+  if (!L) return fail(HMOE_ERR_INVALID_ARG, "linear is NULL");
+  if (T < 0) return fail(HMOE_ERR_INVALID_ARG, "T=%d < 0", T);
+  if (T == 0) return HMOE_OK;
+  if (!x || !out) return fail(HMOE_ERR_INVALID_ARG, "a buffer is NULL");
+  if (!aligned16(x) || ldx < L->d.K || ldx % 8 != 0)
+    return fail(HMOE_ERR_INVALID_ARG, "x must be 16-byte aligned, with a row stride of a multiple of 8 that holds a row (ldx=%d)", ldx);
+  if (((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(bias)) & 1) || ldout < L->d.N)
+    return fail(HMOE_ERR_INVALID_ARG, "out and bias must be aligned to their elements, and ldout hold a row (ldout=%d)", ldout);
+  Int4Params p{};
+  p.packed = L->packed;
+  p.zeros = L->d.zeros;
+  p.act_type = L->d.act_dtype;
+  p.N = L->g.N;
+  p.K = L->g.K;
+  p.units = L->g.units;
+  p.NB = L->g.NB;
+  p.pass = int4_pass(L->g, T);
+  if ((T + p.pass - 1) / p.pass > 65535)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d exceeds 65535 passes of %d rows", T, p.pass);
+  p.T = T;
+  p.x = static_cast<const uint16_t*>(x);
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.out = static_cast<uint16_t*>(out);
+  p.ldx = (size_t)ldx;
+  p.ldout = (size_t)ldout;
+  p.by_NB = div_by_const((uint32_t)p.NB);
+  cudaError_t e = launch_int4(p, 128 / L->d.group, L->num_sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "int4 launch");
+  return HMOE_OK;
+}
+
+void hmoe_int4_destroy(hmoe_int4* linear) { delete linear; }
 
 }  // extern "C"

@@ -57,7 +57,6 @@ template <int KEPT>
 __device__ __forceinline__ int by_unit_cost(int v, int fmt) {
   return fmt == FMT_NF3 ? v / UNIT_COST<FMT_NF3> : v / UNIT_COST<KEPT>;
 }
-__device__ __forceinline__ int div_by(int n, const DivBy& d) { return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift); }
 
 // ------------------------------------------------------------ kernel 1: router logits
 constexpr int RK_THREADS = 128;
@@ -173,13 +172,22 @@ __device__ __forceinline__ void warp_route_few(const float* __restrict__ row, in
   *my_gate = z / sum;
 }
 
+// nf3x8_lut (common.cuh) with the entries' distance as a value that the compiler does not know: a multiply-add, on the
+// FMA pipe, takes the place of a shift-and-add on the ALU, which the decoders fill.
+__device__ __forceinline__ void nf3x8_lut_at(uint32_t sel, uint32_t lut, uint32_t stride, uint32_t* p) {
+  p[0] = lds_u32(__byte_perm(sel, 0u, 0x4440) * stride + lut);
+  p[1] = lds_u32(__byte_perm(sel, 0u, 0x4441) * stride + lut);
+  p[2] = lds_u32(__byte_perm(sel, 0u, 0x4442) * stride + lut);
+  p[3] = lds_u32(__byte_perm(sel, 0u, 0x4443) * stride + lut);
+}
+
 // A lane's part of one k-block of one row group (half i of a unit, 16 rows x 64 K) from a ring slot, which holds the
 // unit's codes and scales in the order of the tile (common.cuh): its operand pairs r0 (row R0) and r1 (row R1), 16
 // values of K each. NF3 comes raw, with the two rows' scales as bf16 in the result; the others have their scales
 // applied.
 template <int FMT, int ACT>
 __device__ __forceinline__ uint32_t decode_kblock(const uint8_t* slot, int i, int lane, uint32_t* r0, uint32_t* r1,
-                                                  const uint32_t* s_e4m3, uint32_t nf3_lut) {
+                                                  const uint32_t* s_e4m3, uint32_t nf3_lut, uint32_t stride) {
   if constexpr (FMT == FMT_NF3) {
     const uint32_t* v = reinterpret_cast<const uint32_t*>(slot) + 32 * i + lane;
     uint32_t s[4];
@@ -187,7 +195,7 @@ __device__ __forceinline__ uint32_t decode_kblock(const uint8_t* slot, int i, in
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint32_t* p = (w < 2 ? r0 : r1) + 4 * (w & 1);
-      if (w < DK_NF3_LUT) nf3x8_lut(s[w], nf3_lut, p);
+      if (w < DK_NF3_LUT) nf3x8_lut_at(s[w], nf3_lut, stride, p);
       else if constexpr (ACT == ACT_F16) nf3x8_to_f16x2(s[w], p);
       else nf3x8_to_bf16x2(s[w], p);
     }
@@ -534,7 +542,7 @@ struct DkCtx {
         uint32_t r0[2][8], r1[2][8], sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          sc[i] = decode_kblock<FMT, ACT>(w + j * DK_SLOT, i, lane, r0[i], r1[i], s_e4m3, nf3_lut);
+          sc[i] = decode_kblock<FMT, ACT>(w + j * DK_SLOT, i, lane, r0[i], r1[i], s_e4m3, nf3_lut, p.lut_stride);
         load_x(on, x, half, xa, xb);
 #pragma unroll
         for (int i = 0; i < 2; ++i) mma_kblock<FMT, ACT>(r0[i], r1[i], sc[i], xa, xb, acc[i][0]);

@@ -1,0 +1,282 @@
+// int4.cu -- y = W x (+ bias) for few rows x and W of 4-bit integers with a scale (and a zero point) per group along K.
+//
+//   W[n][k] = (q[n][k] - z[n][k / G]) * s[n][k / G],  q, z in 0..15, G = 32, 64 or 128
+//
+// What bounds it is the bytes of W (0.516 a weight at G = 128), then, below some
+// megabytes, the chain launch, loads, sums. The work is a list of units, 16 rows
+// over the whole K; each CTA takes an even run of them, and its 16 warps even
+// parts of the run's k-blocks (128 of K), whole units or not. A warp streams its
+// blocks with cp.async into a ring of its own, decodes in registers and issues
+// m16n8k16 MMAs with x's rows as the N side; the sums of a unit that several
+// warps share are joined through shared memory in the order of K.
+//
+// Decoding costs 7 ALU operations for 8 weights and one exact subtraction a
+// pair: a nibble OR-ed into the low mantissa bits of 128 (bf16) or 1024 (fp16)
+// is 128 + q or 1024 + q, less 128 + z or 1024 + z. Products of those integers
+// and x are exact, the sums of a group are fp32, and the scale is applied to
+// them: nothing is rounded before the result.
+#include "act.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace hmoe {
+
+constexpr int I4_WARPS = 16;
+constexpr int I4_THREADS = I4_WARPS * 32;
+constexpr int I4_RING = 4;  // blocks of a warp's ring
+
+// ------------------------------------------------------------ packing
+// A block is 16 rows x 128 K. Codes: two halves of 64 K, each [32 lanes][4 words]: lane (g, q) holds rows g and g + 8
+// (words 0, 1 and 2, 3); word h covers the k16 steps 2h and 2h + 1 of the half, in which a lane's values are
+// k = 16 step + 4 q + 0..3: nibbles 0, 4 and 1, 5 are the first step's, 2, 6 and 3, 7 the second's. Then the scales,
+// [group of the block][g][row g, row g + 8], and in the same order the zero points, a byte each.
+__global__ void int4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
+                                 const uint8_t* __restrict__ zeros, int N, int K, int group, uint8_t* __restrict__ dst) {
+  const int NB = (K + 127) / 128, ng = 128 / group, groups = K / group;
+  const int unit = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  uint8_t* blk = dst + ((size_t)unit * NB + b) * i4_block_bytes(ng, zeros != nullptr);
+  {
+    const int half = tid >> 7, lane = (tid >> 2) & 31, word = tid & 3;
+    const int n = unit * 16 + (lane >> 2) + (word >> 1) * 8;
+    uint32_t v = 0;
+    if (n < N)
+      for (int i = 0; i < 8; ++i) {
+        const int step = 2 * (word & 1) + ((i >> 1) & 1), e = 2 * (i & 1) + (i >> 2);
+        const int k = b * 128 + half * 64 + step * 16 + (lane & 3) * 4 + e;
+        // nibble position of element e of the step: pairs (0, 4), (1, 5) for even steps, (2, 6), (3, 7) for odd ones
+        const int at = 2 * (step & 1) + (e >> 1) + 4 * (e & 1);
+        if (k < K) v |= (uint32_t)((codes[(size_t)n * (K / 2) + k / 2] >> (4 * (k & 1))) & 15u) << (4 * at);
+      }
+    reinterpret_cast<uint32_t*>(blk)[half * 128 + lane * 4 + word] = v;
+  }
+  if (tid < ng * 16) {
+    const int gr = tid >> 4, g = (tid >> 1) & 7, n = unit * 16 + g + (tid & 1) * 8, at = b * ng + gr;
+    const bool there = n < N && at < groups;
+    reinterpret_cast<uint16_t*>(blk + 1024)[tid] = there ? scales[(size_t)n * groups + at] : 0;
+    if (zeros) blk[1024 + ng * 32 + tid] = there ? (zeros[(size_t)n * groups + at] & 15) : 0;
+  }
+}
+
+cudaError_t launch_int4_pack(const Int4Geom& g, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                             uint8_t* dst, cudaStream_t st) {
+  int4_pack_kernel<<<dim3(g.units, g.NB), 256, 0, st>>>(codes, scales, zeros, g.N, g.K, g.group, dst);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------ product
+template <int ACT>
+__device__ __forceinline__ uint32_t sub_x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (ACT == ACT_F16) asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <int ACT>
+__device__ __forceinline__ float act_lo(uint32_t v) { return act_x2_to_f32<ACT>(v).x; }
+
+template <int ACT, int NT, int NG>
+__global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_constant__ Int4Params p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr uint32_t MAGIC = ACT == ACT_F16 ? 0x64006400u : 0x43004300u;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int BB = i4_block_bytes(NG, p.zeros != 0), NB = p.NB;
+  uint8_t* const ring = smem + warp * I4_RING * BB;
+  float* const part = reinterpret_cast<float*>(smem + I4_WARPS * I4_RING * BB);  // [warps][4 NT][32]
+  uint8_t* const xs = smem + I4_WARPS * I4_RING * BB + I4_WARPS * NT * 512;
+  const int t0 = blockIdx.y * p.pass, nt = min(p.pass, p.T - t0);
+
+  // This CTA's units and this warp's steps (blocks) of them.
+  const int u0 = div_by(p.units * (int)blockIdx.x, p.by_grid), u1 = div_by(p.units * ((int)blockIdx.x + 1), p.by_grid);
+  const int total = (u1 - u0) * NB;
+  auto border = [&](int w) { return (int)((long long)total * w / I4_WARPS); };
+  const int from = border(warp), to = border(warp + 1);
+  const uint8_t* at = p.packed + ((size_t)u0 * NB + from) * BB;  // a unit's blocks, and units, lie one after another
+  const int pieces = BB / 16 - 64;                               // of the scales and zero points
+  const uint32_t dst0 = smem_u32(ring) + lane * 16;
+  auto copy = [&](int slot) {
+    const uint8_t* src = at + lane * 16;
+    const uint32_t dst = dst0 + slot * BB;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(src + 512) : "memory");
+    if (lane < pieces) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 1024), "l"(src + 1024) : "memory");
+    at += BB;
+  };
+  // The first weights to L2 while the kernel before still runs; nothing is read before the wait.
+  for (int i = lane; i < min(I4_RING - 1, to - from) * (BB / 128); i += 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * 128));
+  pdl_wait();
+  pdl_trigger();
+  int ahead = from;
+#pragma unroll
+  for (int i = 0; i < I4_RING - 1; ++i) {
+    if (ahead < to) copy(i);
+    ++ahead;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps.
+  {
+    const int chunks = NB * 16;  // of 8 values
+    for (int c = 0; c < nt; ++c) {
+      const uint16_t* row = p.x + (size_t)(t0 + c) * p.ldx;
+      for (int i = tid; i < chunks; i += I4_THREADS) {
+        const uint4 v = i * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0, 0, 0, 0);
+        const int step = (i >> 1) & 3;
+        uint8_t* d = xs + (((i >> 3) * 2 + (step >> 1)) * nt + c) * 64 + (i & 1) * 32 + (step & 1) * 8;
+        *reinterpret_cast<uint2*>(d) = make_uint2(v.x, v.y);
+        *reinterpret_cast<uint2*>(d + 16) = make_uint2(v.z, v.w);
+      }
+    }
+  }
+  __syncthreads();
+
+  float acc[NT][4] = {};
+  auto emit = [&](int u) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = 8 * n + 2 * q + (i & 1), r = u * 16 + g + (i >> 1) * 8;
+        if (col < nt && r < p.N) {
+          const float b = p.bias ? act_lo<ACT>((uint32_t)p.bias[r]) : 0.0f;
+          p.out[(size_t)(t0 + col) * p.ldout + r] = f32_to_act<ACT>(acc[n][i] + b);
+        }
+      }
+  };
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] = 0.0f;
+  };
+  const int half = nt * 64;
+  const uint8_t* const x0 = xs + g * 64 + q * 16;
+  int unit = div_by(from, p.by_NB), st = from - unit * NB, slot = 0;
+  bool whole = st == 0;
+  for (int s = from; s < to; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(I4_RING - 2) : "memory");
+    __syncwarp();
+    if (ahead < to) copy(slot == 0 ? I4_RING - 1 : slot - 1);  // into the block of the step before, which all lanes have read
+    ++ahead;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint8_t* w = ring + slot * BB;
+    const uint8_t* x = x0 + (size_t)st * 4 * half;
+    float d[NT][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 c4 = reinterpret_cast<const uint4*>(w)[h * 32 + lane];
+      const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+      uint4 xv[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (8 * n + g < nt) {
+          xv[n][0] = *reinterpret_cast<const uint4*>(x + n * 512);
+          xv[n][1] = *reinterpret_cast<const uint4*>(x + n * 512 + half);
+        }
+      x += 2 * half;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // two k16 steps
+        const int gr = NG == 4 ? 2 * h + k : (NG == 2 ? h : 0);
+        uint32_t z0 = 8u * 0x00010001u + MAGIC, z1 = z0;
+        if (p.zeros) {
+          const uint32_t z = *reinterpret_cast<const uint16_t*>(w + 1024 + NG * 32 + gr * 16 + g * 2);
+          z0 = (z & 0xFFu) * 0x00010001u + MAGIC;
+          z1 = (z >> 8) * 0x00010001u + MAGIC;
+        }
+        uint32_t a[2][4];  // pairs of row g and of row g + 8
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            a[r][i] = sub_x2<ACT>(((cw[2 * r + k] >> (4 * i)) & 0x000F000Fu) | MAGIC, r ? z1 : z0);
+        const bool begin = NG == 4 || (k == 0 && (NG == 2 || h == 0)), end = NG == 4 || (k == 1 && (NG == 2 || h == 1));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4& xk = xv[n][k];
+          if (begin) mma_16816_zc<ACT>(d[n], a[0][0], a[1][0], a[0][1], a[1][1], xk.x, xk.y);
+          else mma_16816<ACT>(d[n], a[0][0], a[1][0], a[0][1], a[1][1], xk.x, xk.y);
+          mma_16816<ACT>(d[n], a[0][2], a[1][2], a[0][3], a[1][3], xk.z, xk.w);
+        }
+        if (end) {
+          const float2 sc = act_x2_to_f32<ACT>(*reinterpret_cast<const uint32_t*>(w + 1024 + gr * 32 + g * 4));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[n][0] = fmaf(sc.x, d[n][0], acc[n][0]);
+            acc[n][1] = fmaf(sc.x, d[n][1], acc[n][1]);
+            acc[n][2] = fmaf(sc.y, d[n][2], acc[n][2]);
+            acc[n][3] = fmaf(sc.y, d[n][3], acc[n][3]);
+          }
+        }
+      }
+    }
+    slot = slot == I4_RING - 1 ? 0 : slot + 1;
+    if (++st == NB) {
+      if (whole) {
+        emit(u0 + unit);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i) part[(warp * 4 * NT + i) * 32 + lane] = acc[i >> 2][i & 3];
+      }
+      clear();
+      whole = true;
+      st = 0;
+      ++unit;
+    }
+  }
+  __syncwarp();
+  float* const rest = reinterpret_cast<float*>(ring);  // the sums of a unit that another warp ends
+  if (st != 0 && from < to)
+#pragma unroll
+    for (int i = 0; i < 4 * NT; ++i) rest[i * 32 + lane] = acc[i >> 2][i & 3];
+  __syncthreads();
+  // The unit that this warp ended and others began, in the order of K.
+  const int mine = div_by(from, p.by_NB), begin = mine * NB;
+  if (from == begin || to < begin + NB) return;
+  int v = warp - 1;
+  while (border(v) > begin) --v;
+  clear();
+  for (; v < warp; ++v) {
+    if (border(v) == border(v + 1)) continue;  // a warp without work
+    const float* theirs = reinterpret_cast<const float*>(smem + v * I4_RING * BB);
+#pragma unroll
+    for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += theirs[i * 32 + lane];
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += part[(warp * 4 * NT + i) * 32 + lane];
+  emit(u0 + mine);
+}
+
+// ------------------------------------------------------------ launch
+// Rows of x that one pass takes: what shared memory holds beside the rings, up to 16, the passes evened out.
+int int4_pass(const Int4Geom& g, int T) {
+  const int fixed = I4_WARPS * (I4_RING * i4_block_bytes(128 / g.group, true) + 2 * 512);
+  const int most = (DK_SMEM_LIMIT - fixed) / (g.NB * 256);
+  const int cap = most < 16 ? most : 16;
+  if (cap < 1) return 0;
+  const int passes = (T + cap - 1) / cap;
+  return (T + passes - 1) / passes;
+}
+
+template <int ACT, int NT, int NG>
+static cudaError_t launch_as(const Int4Params& p, dim3 grid, int smem, cudaStream_t st) {
+  static std::atomic<unsigned long long> attr{0};
+  const cudaError_t e = ensure_smem_attr(int4_kernel<ACT, NT, NG>, DK_SMEM_LIMIT, attr);
+  return e != cudaSuccess ? e : launch_pdl(int4_kernel<ACT, NT, NG>, grid, dim3(I4_THREADS), (size_t)smem, st, p);
+}
+template <int ACT, int NT>
+static cudaError_t launch_by_group(const Int4Params& p, int ng, dim3 grid, int smem, cudaStream_t st) {
+  return ng == 1 ? launch_as<ACT, NT, 1>(p, grid, smem, st)
+                 : (ng == 2 ? launch_as<ACT, NT, 2>(p, grid, smem, st) : launch_as<ACT, NT, 4>(p, grid, smem, st));
+}
+
+cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st) {
+  const int nt = p.pass > 8 ? 2 : 1;
+  const int smem = I4_WARPS * (I4_RING * i4_block_bytes(ng, p.zeros != 0) + nt * 512) + p.NB * 256 * p.pass;
+  const dim3 grid((unsigned)(p.units < num_sms ? p.units : num_sms), (unsigned)((p.T + p.pass - 1) / p.pass));
+  p.by_grid = div_by_const(grid.x);
+  cudaError_t e;
+  if (p.act_type == ACT_F16) e = nt == 2 ? launch_by_group<ACT_F16, 2>(p, ng, grid, smem, st) : launch_by_group<ACT_F16, 1>(p, ng, grid, smem, st);
+  else e = nt == 2 ? launch_by_group<ACT_BF16, 2>(p, ng, grid, smem, st) : launch_by_group<ACT_BF16, 1>(p, ng, grid, smem, st);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace hmoe

@@ -242,14 +242,6 @@ inline LoraScratch lora_scratch(const LoraGeom& g, int T) {
 }
 cudaError_t launch_lora_forward(const LoraParams& p, int num_sms, cudaStream_t st);
 
-// ---------------------------------------------------------------- the whole layer for a few tokens (decode.cu)
-constexpr int DECODE_MAX_TOKENS = 8;
-constexpr int DK_SMEM_LIMIT = 232448;    // dynamic shared memory of a CTA, 227 KB
-constexpr int DK_MAX_ROW_TILES = 1024;   // H / 128: above what the activations' shared memory admits
-// The counters of a call, in ints: claimed shares, CTAs that left, then the
-// W13 units done per group and the W2 units done per row tile.
-constexpr int DK_CTL_DONE = 64;
-constexpr int DK_CTL_ROWS = DK_CTL_DONE + DECODE_MAX_TOKENS * MAX_TOPK;
 // Division of 0 <= n < 2^31 by a constant: (umulhi(n, mul) + n) >> shift
 // (Granlund and Montgomery, Division by Invariant Integers using Multiplication).
 struct DivBy {
@@ -261,6 +253,20 @@ inline DivBy div_by_const(uint32_t d) {
   while ((1ull << l) < d) ++l;
   return DivBy{(uint32_t)((((1ull << l) - d) << 32) / d + 1), l};
 }
+#ifdef __CUDACC__
+__device__ __forceinline__ int div_by(int n, const DivBy& d) {
+  return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift);
+}
+#endif
+
+// ---------------------------------------------------------------- the whole layer for a few tokens (decode.cu)
+constexpr int DECODE_MAX_TOKENS = 8;
+constexpr int DK_SMEM_LIMIT = 232448;    // dynamic shared memory of a CTA, 227 KB
+constexpr int DK_MAX_ROW_TILES = 1024;   // H / 128: above what the activations' shared memory admits
+// The counters of a call, in ints: claimed shares, CTAs that left, then the
+// W13 units done per group and the W2 units done per row tile.
+constexpr int DK_CTL_DONE = 64;
+constexpr int DK_CTL_ROWS = DK_CTL_DONE + DECODE_MAX_TOKENS * MAX_TOPK;
 struct DecodeParams {
   const uint8_t* kept_buf;
   const uint8_t* nf3_buf;
@@ -268,6 +274,7 @@ struct DecodeParams {
   int H, I, E, topk, T;
   int group_tokens;        // slots of a group, up to 8: as many as the activations' shared memory admits
   int act_cap;             // bytes of that memory
+  uint32_t lut_stride;     // 128, the distance of the NF3 pair table's entries
   int shares;              // of each product, one per SM
   DivBy by_shares, by_spu13, by_spu2;  // division by the shares and by the steps of a unit
   const uint16_t* x;       // [T][H]
@@ -287,6 +294,32 @@ struct DecodeParams {
 // Bytes for activations beside the kernel's tables.
 int decode_act_cap();
 cudaError_t launch_decode(const DecodeParams& p, const uint16_t* router, const float* bias, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- 4-bit integer linear (int4.cu)
+constexpr int INT4_MAX_DIM = 1 << 20;
+struct Int4Geom {
+  int N, K, group;
+  int units, NB;  // of 16 rows, and blocks of 128 K of each
+};
+inline Int4Geom int4_geom(int N, int K, int group) { return Int4Geom{N, K, group, (N + 15) / 16, (K + 127) / 128}; }
+__host__ __device__ constexpr int i4_block_bytes(int ng, bool zeros) { return 1024 + ng * (zeros ? 48 : 32); }
+cudaError_t launch_int4_pack(const Int4Geom& g, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                             uint8_t* dst, cudaStream_t st);
+struct Int4Params {
+  const uint8_t* packed;
+  int zeros;             // 1: the blocks hold zero points; 0: all are 8
+  int act_type;
+  int N, K, units, NB;
+  int T, pass;           // rows of x, and of one pass (int4_pass)
+  const uint16_t* x;
+  const uint16_t* bias;  // [N], or NULL
+  uint16_t* out;
+  size_t ldx, ldout;
+  DivBy by_NB, by_grid;
+};
+// Rows that one pass takes of T; 0: K is more than shared memory holds of one row.
+int int4_pass(const Int4Geom& g, int T);
+cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st);
 
 // Raises a kernel's dynamic shared-memory limit once per device: the
 // attribute belongs to the current device, so a process that launches on
