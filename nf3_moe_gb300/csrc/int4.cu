@@ -10,11 +10,15 @@
 // m16n8k16 MMAs with x's rows as the N side; the sums of a unit that several
 // warps share are joined through shared memory in the order of K.
 //
-// Decoding costs 7 ALU operations for 8 weights and one exact subtraction a
-// pair: a nibble OR-ed into the low mantissa bits of 128 (bf16) or 1024 (fp16)
-// is 128 + q or 1024 + q, less 128 + z or 1024 + z. Products of those integers
-// and x are exact, the sums of a group are fp32, and the scale is applied to
-// them: nothing is rounded before the result.
+// Decoding. A nibble OR-ed into the low mantissa bits of 128 (bf16) or 1024 (fp16)
+// is 128 + q or 1024 + q, exactly. bf16: those enter the products as they are,
+// 7 operations for 8 weights, and the group's sum of x times 128 + z is taken off
+// the group's sum of products (that leaves 2^-24 of sums up to 30 times the
+// result's, far below bf16's rounding). fp16, whose result keeps more bits and
+// whose offset is larger: 1024 + z is subtracted first, exactly, 11 operations.
+// What bounded it after the bytes was the issue of instructions: the offsets'
+// subtraction in bf16 and a wait for every block instead of every second cost
+// 36 against 26 us for 8 rows of 32768 x 6144.
 #include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -23,7 +27,7 @@ namespace hmoe {
 
 constexpr int I4_WARPS = 16;
 constexpr int I4_THREADS = I4_WARPS * 32;
-constexpr int I4_RING = 4;  // blocks of a warp's ring
+constexpr int I4_RING = 6;  // blocks of a warp's ring, in pairs
 
 // ------------------------------------------------------------ packing
 // A block is 16 rows x 128 K. Codes: two halves of 64 K, each [32 lanes][4 words]: lane (g, q) holds rows g and g + 8
@@ -83,7 +87,8 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
   const int BB = i4_block_bytes(NG, p.zeros != 0), NB = p.NB;
   uint8_t* const ring = smem + warp * I4_RING * BB;
   float* const part = reinterpret_cast<float*>(smem + I4_WARPS * I4_RING * BB);  // [warps][4 NT][32]
-  uint8_t* const xs = smem + I4_WARPS * I4_RING * BB + I4_WARPS * NT * 512;
+  float* const xsum = part + I4_WARPS * 4 * NT * 32;  // bf16: [groups][8 NT]
+  uint8_t* const xs = reinterpret_cast<uint8_t*>(xsum) + (ACT == ACT_F16 ? 0 : NB * NG * NT * 32);
   const int t0 = blockIdx.y * p.pass, nt = min(p.pass, p.T - t0);
 
   // This CTA's units and this warp's steps (blocks) of them.
@@ -103,28 +108,52 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
     at += BB;
   };
   // The first weights to L2 while the kernel before still runs; nothing is read before the wait.
-  for (int i = lane; i < min(I4_RING - 1, to - from) * (BB / 128); i += 32)
+  for (int i = lane; i < min(I4_RING - 2, to - from) * (BB / 128); i += 32)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * 128));
   pdl_wait();
   pdl_trigger();
   int ahead = from;
-#pragma unroll
-  for (int i = 0; i < I4_RING - 1; ++i) {
-    if (ahead < to) copy(i);
-    ++ahead;
+  auto copy2 = [&](int slot) {
+    if (ahead < to) copy(slot);
+    if (ahead + 1 < to) copy(slot + 1);
+    ahead += 2;
     asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps.
+  };
+#pragma unroll
+  for (int i = 0; i < I4_RING - 2; i += 2) copy2(i);
+  // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps. A thread
+  // has 8 values, the threads of a group of K are neighbours.
   {
-    const int chunks = NB * 16;  // of 8 values
-    for (int c = 0; c < nt; ++c) {
-      const uint16_t* row = p.x + (size_t)(t0 + c) * p.ldx;
-      for (int i = tid; i < chunks; i += I4_THREADS) {
-        const uint4 v = i * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0, 0, 0, 0);
-        const int step = (i >> 1) & 3;
-        uint8_t* d = xs + (((i >> 3) * 2 + (step >> 1)) * nt + c) * 64 + (i & 1) * 32 + (step & 1) * 8;
-        *reinterpret_cast<uint2*>(d) = make_uint2(v.x, v.y);
-        *reinterpret_cast<uint2*>(d + 16) = make_uint2(v.z, v.w);
+    constexpr int LOADS = 4, LANES = 16 / NG;
+    const int chunks = NB * 16, all = chunks * nt;
+    for (int i0 = tid; i0 - tid < all; i0 += LOADS * I4_THREADS) {  // whole warps: they shuffle
+      uint4 v[LOADS];
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) {
+        const int i = i0 + j * I4_THREADS, c = div_by(min(i, all - 1), p.by_NB) >> 4, k = i - c * chunks;
+        v[j] = i < all && k * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(t0 + c) * p.ldx) + k) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) {
+        const int i = i0 + j * I4_THREADS, c = div_by(min(i, all - 1), p.by_NB) >> 4, k = i - c * chunks;
+        if (ACT != ACT_F16) {
+          const uint32_t vv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+          float sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = act_x2_to_f32<ACT>(vv[e]);
+            sum += f.x + f.y;
+          }
+#pragma unroll
+          for (int off = 1; off < LANES; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          if (i < all && (k & (LANES - 1)) == 0) xsum[(k / LANES) * 8 * NT + c] = sum;
+        }
+        if (i < all) {
+          const int step = (k >> 1) & 3;
+          uint8_t* d = xs + (((k >> 3) * 2 + (step >> 1)) * nt + c) * 64 + (k & 1) * 32 + (step & 1) * 8;
+          *reinterpret_cast<uint2*>(d) = make_uint2(v[j].x, v[j].y);
+          *reinterpret_cast<uint2*>(d + 16) = make_uint2(v[j].z, v[j].w);
+        }
       }
     }
   }
@@ -151,14 +180,10 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
   const uint8_t* const x0 = xs + g * 64 + q * 16;
   int unit = div_by(from, p.by_NB), st = from - unit * NB, slot = 0;
   bool whole = st == 0;
-  for (int s = from; s < to; ++s) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(I4_RING - 2) : "memory");
-    __syncwarp();
-    if (ahead < to) copy(slot == 0 ? I4_RING - 1 : slot - 1);  // into the block of the step before, which all lanes have read
-    ++ahead;
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  auto block = [&]() {
     const uint8_t* w = ring + slot * BB;
     const uint8_t* x = x0 + (size_t)st * 4 * half;
+    const float* sums = xsum + st * NG * 8 * NT + 2 * q;
     float d[NT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -175,19 +200,17 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // two k16 steps
         const int gr = NG == 4 ? 2 * h + k : (NG == 2 ? h : 0);
-        uint32_t z0 = 8u * 0x00010001u + MAGIC, z1 = z0;
-        if (p.zeros) {
-          const uint32_t z = *reinterpret_cast<const uint16_t*>(w + 1024 + NG * 32 + gr * 16 + g * 2);
-          z0 = (z & 0xFFu) * 0x00010001u + MAGIC;
-          z1 = (z >> 8) * 0x00010001u + MAGIC;
-        }
+        const bool begin = NG == 4 || (k == 0 && (NG == 2 || h == 0)), end = NG == 4 || (k == 1 && (NG == 2 || h == 1));
+        uint32_t z = 0x0808u;  // of row g, and of row g + 8
+        if ((ACT == ACT_F16 || end) && p.zeros) z = *reinterpret_cast<const uint16_t*>(w + 1024 + NG * 32 + gr * 16 + g * 2);
         uint32_t a[2][4];  // pairs of row g and of row g + 8
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            a[r][i] = sub_x2<ACT>(((cw[2 * r + k] >> (4 * i)) & 0x000F000Fu) | MAGIC, r ? z1 : z0);
-        const bool begin = NG == 4 || (k == 0 && (NG == 2 || h == 0)), end = NG == 4 || (k == 1 && (NG == 2 || h == 1));
+          for (int i = 0; i < 4; ++i) {
+            a[r][i] = ((cw[2 * r + k] >> (4 * i)) & 0x000F000Fu) | MAGIC;
+            if (ACT == ACT_F16) a[r][i] = sub_x2<ACT>(a[r][i], (r ? z >> 8 : z & 0xFFu) * 0x00010001u + MAGIC);
+          }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint4& xk = xv[n][k];
@@ -197,8 +220,17 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
         }
         if (end) {
           const float2 sc = act_x2_to_f32<ACT>(*reinterpret_cast<const uint32_t*>(w + 1024 + gr * 32 + g * 4));
+          // 128 + z as fp32: z in the mantissa's upper bits
+          const float o0 = __uint_as_float(0x43000000u | (z & 0xFFu) << 16), o1 = __uint_as_float(0x43000000u | (z >> 8) << 16);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
+            if (ACT != ACT_F16) {
+              const float2 xsm = *reinterpret_cast<const float2*>(sums + gr * 8 * NT + 8 * n);
+              d[n][0] = fmaf(-o0, xsm.x, d[n][0]);
+              d[n][1] = fmaf(-o0, xsm.y, d[n][1]);
+              d[n][2] = fmaf(-o1, xsm.x, d[n][2]);
+              d[n][3] = fmaf(-o1, xsm.y, d[n][3]);
+            }
             acc[n][0] = fmaf(sc.x, d[n][0], acc[n][0]);
             acc[n][1] = fmaf(sc.x, d[n][1], acc[n][1]);
             acc[n][2] = fmaf(sc.y, d[n][2], acc[n][2]);
@@ -207,7 +239,7 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
         }
       }
     }
-    slot = slot == I4_RING - 1 ? 0 : slot + 1;
+    ++slot;
     if (++st == NB) {
       if (whole) {
         emit(u0 + unit);
@@ -220,6 +252,14 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
       st = 0;
       ++unit;
     }
+  };
+  for (int s = from; s < to; s += 2) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(I4_RING / 2 - 2) : "memory");
+    __syncwarp();
+    copy2(slot == 0 ? I4_RING - 2 : slot - 2);  // into the pair before, which all lanes have read
+    block();
+    if (s + 1 < to) block();
+    if (slot == I4_RING) slot = 0;
   }
   __syncwarp();
   float* const rest = reinterpret_cast<float*>(ring);  // the sums of a unit that another warp ends
@@ -247,7 +287,7 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
 // ------------------------------------------------------------ launch
 // Rows of x that one pass takes: what shared memory holds beside the rings, up to 16, the passes evened out.
 int int4_pass(const Int4Geom& g, int T) {
-  const int fixed = I4_WARPS * (I4_RING * i4_block_bytes(128 / g.group, true) + 2 * 512);
+  const int fixed = I4_WARPS * (I4_RING * i4_block_bytes(128 / g.group, true) + 2 * 512) + g.NB * (128 / g.group) * 64;
   const int most = (DK_SMEM_LIMIT - fixed) / (g.NB * 256);
   const int cap = most < 16 ? most : 16;
   if (cap < 1) return 0;
@@ -269,7 +309,8 @@ static cudaError_t launch_by_group(const Int4Params& p, int ng, dim3 grid, int s
 
 cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st) {
   const int nt = p.pass > 8 ? 2 : 1;
-  const int smem = I4_WARPS * (I4_RING * i4_block_bytes(ng, p.zeros != 0) + nt * 512) + p.NB * 256 * p.pass;
+  const int smem = I4_WARPS * (I4_RING * i4_block_bytes(ng, p.zeros != 0) + nt * 512) + p.NB * 256 * p.pass +
+                   (p.act_type == ACT_F16 ? 0 : p.NB * ng * nt * 32);
   const dim3 grid((unsigned)(p.units < num_sms ? p.units : num_sms), (unsigned)((p.T + p.pass - 1) / p.pass));
   p.by_grid = div_by_const(grid.x);
   cudaError_t e;
