@@ -68,6 +68,9 @@ __global__ void __launch_bounds__(RK_THREADS) router_kernel(const uint16_t* __re
                                                             float* __restrict__ logits) {
   __shared__ float s_part[RK_THREADS / 32][TM];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The row to L2 while the kernel before still runs; nothing is read before the wait.
+  for (int c = tid * 64; c < H; c += RK_THREADS * 64)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(router + (size_t)e * H + c));
   pdl_wait();
   pdl_trigger();
   float acc[TM];
@@ -267,7 +270,7 @@ __device__ __forceinline__ void load_x(bool on, uint32_t x, int half, uint4& xa,
 
 // A share's part of one group.
 struct Segment {
-  int e, fmt, n, p0;  // its expert, format, slots and first position
+  int g, loc, n, p0;  // its expert's place, slots and first position
   int a, b;           // units
   int act;            // byte offset of its activations
 };
@@ -278,20 +281,18 @@ struct DkShared {
   float part[DK_WARPS][16][32];               // partial sums of the unit that a warp ended and another began
   uint32_t e4m3[256];
   uint32_t nf3[NF3_LUT_WORDS];
-  uint16_t loc[MAX_E];         // the layer's table (ExpertTable)
-  float g13[MAX_E], g2[MAX_E];
   alignas(16) int id[DK_MAX_SLOTS];  // chosen experts by slot, then INT_MAX
   float gate[DK_MAX_SLOTS];
   int sorted[DK_MAX_SLOTS];    // slots by (expert, slot)
   int first[DK_MAX_SLOTS + 1]; // groups: first position in sorted
-  int expert[DK_MAX_SLOTS];
+  int loc[DK_MAX_SLOTS];       // groups: their expert's entries of the layer's table
+  float g13[DK_MAX_SLOTS], g2[DK_MAX_SLOTS];
   int cum[DK_MAX_SLOTS + 1];   // summed unit_cost of the groups before
   float hscale[DK_MAX_SLOTS];  // fp16: the power of two that a slot's h was divided by
   uint8_t head[DK_MAX_SLOTS];  // by position: a group begins
   uint32_t heads[DK_MAX_SLOTS / 32];
-  int a[DK_MAX_SLOTS], b[DK_MAX_SLOTS];  // by group: its units in the share
-  int2 border[DK_WARPS + 1];   // where a warp's part of the share's groups begins: a group and its step
-  int claim, abort, tiles;
+  int2 border[DK_WARPS + 1];   // where a warp's part of the groups worked on begins: a group and its step
+  int claim, abort, tiles, ends;  // ends: the group behind those worked on
   int tile[DK_MAX_ROW_TILES];  // row tiles this CTA brings together
 };
 
@@ -367,53 +368,48 @@ struct DkCtx {
   DkShared& s;
   uint8_t* act;
   int ph, upg, KB, S, spu, cols_per_slot;  // S: k-blocks of a step; spu: steps of a unit
-  int lo, hi;                              // the share, in costs
+  int2 lo, hi;                             // the share: from a group's unit to another's
 
-  __device__ __forceinline__ int fmt_of(int e) const { return (s.loc[e] & LOC_NF3) ? FMT_NF3 : KEPT; }
+  __device__ __forceinline__ int fmt_of(int g) const { return (s.loc[g] & LOC_NF3) ? FMT_NF3 : KEPT; }
 
+  // The part [lo, hi) of group g, of groups [g0, ...) worked on at once.
   __device__ __forceinline__ Segment segment(int g, int g0) const {
     Segment r;
-    r.e = s.expert[g];
-    r.fmt = fmt_of(r.e);
+    r.g = g;
+    r.loc = s.loc[g];
     r.p0 = s.first[g];
     r.n = s.first[g + 1] - r.p0;
-    r.a = s.a[g];
-    r.b = s.b[g];
+    r.a = g == lo.x ? lo.y : 0;
+    r.b = g == hi.x ? hi.y : upg;
     r.act = (r.p0 - s.first[g0]) * slot_bytes();
     return r;
   }
   __device__ __forceinline__ int slot_bytes() const { return cols_per_slot * KB * 128; }  // of a slot's activations
 
-  // All threads: the share's units, by group. Returns the first group and how many follow.
-  __device__ __forceinline__ int2 cut(int G) const {
-    const int g = threadIdx.x;
-    bool before = false, in = false;
-    if (g < G) {
-      const int fmt = fmt_of(s.expert[g]), w = unit_cost<KEPT>(fmt), base = s.cum[g] * upg;
-      const int a = lo > base ? by_unit_cost<KEPT>(lo - base + w - 1, fmt) : 0;
-      const int b = hi > base ? min(upg, by_unit_cost<KEPT>(hi - base + w - 1, fmt)) : 0;
-      s.a[g] = a;
-      s.b[g] = b;
-      before = a >= upg;
-      in = a < b;
-    }
-    const int first = __syncthreads_count(before);
-    return make_int2(first, __syncthreads_count(in));
+  // One warp: the group that holds the cost `at` (counted by `per` for each unit_cost of a group before it), or G.
+  __device__ __forceinline__ int find(int at, int per, int G, int lane) const {
+    int n = 0;
+    for (int g = lane; g < G; g += 32) n += s.cum[g + 1] * per <= at ? 1 : 0;
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
   }
-
-  // Threads 0..DK_WARPS: an even part of the cost of groups [g0, g1) for each warp.
-  __device__ __forceinline__ void set_borders(int g0, int g1) const {
-    const int w = threadIdx.x;
-    if (w > DK_WARPS) return;
-    auto at_unit = [&](int g, int u) {  // the cost before unit u of group g, in steps
-      return ((s.cum[g] - s.cum[g0]) * upg + u * (s.cum[g + 1] - s.cum[g])) * spu;
-    };
-    const int from = at_unit(g0, s.a[g0]), to = at_unit(g1 - 1, s.b[g1 - 1]);
+  // One warp: where share i begins: a group and its unit, the first whose cost begins at the share's or later.
+  __device__ __forceinline__ int2 share_border(int i, int G, int lane) const {
+    const int total = s.cum[G] * upg, each = div_by(total, p.by_shares);
+    const int at = each * i + div_by((total - each * p.shares) * i, p.by_shares);  // total * i / shares
+    const int g = find(at, upg, G, lane);
+    if (g == G) return make_int2(G, 0);
+    const int fmt = fmt_of(g), u = by_unit_cost<KEPT>(at - s.cum[g] * upg + unit_cost<KEPT>(fmt) - 1, fmt);
+    return u == upg ? make_int2(g + 1, 0) : make_int2(g, u);
+  }
+  // One warp: where warp w's part of groups [g0, g1) begins: an even part of their cost, in steps.
+  __device__ __forceinline__ int2 warp_border(int w, int g0, int g1, int G, int lane) const {
+    const int base = s.cum[g0] * upg;
+    auto cost = [&](int2 at) { return at.x == G ? (s.cum[G] * upg - base) * spu : (s.cum[at.x] * upg + at.y * (s.cum[at.x + 1] - s.cum[at.x]) - base) * spu; };
+    const int from = g0 == lo.x ? cost(lo) : 0, to = g1 > hi.x ? cost(hi) : cost(make_int2(g1, 0));
     const int at = from + (int)((long long)(to - from) * w / DK_WARPS);
-    int g = g0;
-    while (g + 1 < g1 && at_unit(g + 1, 0) <= at) ++g;
-    const int steps = by_unit_cost<KEPT>(at - at_unit(g, 0), fmt_of(s.expert[g])) - s.a[g] * spu;
-    s.border[w] = make_int2(g, max(0, min(steps, (s.b[g] - s.a[g]) * spu)));
+    if (w == DK_WARPS) return g1 > hi.x ? make_int2(hi.x, (hi.y - (hi.x == lo.x ? lo.y : 0)) * spu) : make_int2(g1, 0);
+    const int g = find(at + base * spu, upg * spu, G, lane);
+    return make_int2(g, by_unit_cost<KEPT>(at - cost(make_int2(g, 0)), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
   }
 
   // Activations of one segment as MMA fragments: [k-block][half][column][q], 16 bytes each: k = 16 q + 8 half + 0..7.
@@ -463,7 +459,7 @@ struct DkCtx {
 
   // Results of row group u: rows R0 = 16 u + g and R1 = R0 + 8 (tile order).
   __device__ __forceinline__ void emit(const Segment& r, int u, float (*acc)[4]) const {
-    const float gsc = (ph == 0 ? s.g13[r.e] : s.g2[r.e]) * (r.fmt == FMT_NVFP4 ? nvfp4_unscale<ACT>() : 1.0f);
+    const float gsc = (ph == 0 ? s.g13[r.g] : s.g2[r.g]) * (KEPT == FMT_NVFP4 && !(r.loc & LOC_NF3) ? nvfp4_unscale<ACT>() : 1.0f);
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     if (ph == 0) {
       const int ch = u * 8 + g;
@@ -501,7 +497,7 @@ struct DkCtx {
   __device__ __forceinline__ void begin(Loader& l, const Segment& r, int from, int to, int warp, int lane) const {
     constexpr bool nf3 = FMT == FMT_NF3;
     l.row = (nf3 ? p.nf3_buf : p.kept_buf) +
-            (size_t)(s.loc[r.e] & 0x7FFF) * (nf3 ? p.nf3_expert_bytes : p.kept_expert_bytes) +
+            (size_t)(r.loc & 0x7FFF) * (nf3 ? p.nf3_expert_bytes : p.kept_expert_bytes) +
             (ph == 0 ? 0 : (nf3 ? p.nf3_w2_off : p.kept_w2_off));
     l.ring = smem_u32(s.ring[warp]) + lane * 16;
     l.slot = 0;
@@ -579,9 +575,9 @@ struct DkCtx {
 
   // The unit that this warp ended and others began: their sums in the order of K.
   __device__ __forceinline__ void join(int2 from, int2 to, int g0, int warp, int lane) const {
-    const Segment r = segment(from.x, g0);
     const int u = spu_of(from.y), begin = u * spu;
-    if (from.y == begin || (to.x == from.x && to.y < begin + spu) || from.y >= (r.b - r.a) * spu) return;
+    if (from.x >= s.ends || from.y == begin || (to.x == from.x && to.y < begin + spu)) return;
+    const Segment r = segment(from.x, g0);
     int v = warp - 1;  // the warp that began it
     while (s.border[v].x == from.x && s.border[v].y > begin) --v;
     float acc[2][2][4] = {};
@@ -608,12 +604,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.T * p.topk;
   if (tid < 256) s.e4m3[tid] = e4m3_lut_entry<ACT>((uint32_t)tid);
-  nf3_lut_fill<ACT>(s.nf3, tid, DK_THREADS);
-  for (int e = tid; e < p.E; e += DK_THREADS) {
-    s.loc[e] = p.tab.loc[e];
-    s.g13[e] = p.tab.g13[e];
-    s.g2[e] = p.tab.g2[e];
-  }
+  if (p.has_nf3) nf3_lut_fill<ACT>(s.nf3, tid, DK_THREADS);
   if (tid < DK_MAX_SLOTS) {
     s.id[tid] = INT_MAX;
     s.head[tid] = 0;
@@ -665,8 +656,11 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
     }
     if (tid < S && s.head[tid]) {
       const int g = before + __popc(ballot & ((1u << lane) - 1u));
+      const int e = s.id[s.sorted[tid]];
       s.first[g] = tid;
-      s.expert[g] = s.id[s.sorted[tid]];
+      s.loc[g] = p.tab.loc[e];
+      s.g13[g] = p.tab.g13[e];
+      s.g2[g] = p.tab.g2[e];
     }
     if (tid == 0) s.first[G] = S;
   }
@@ -675,8 +669,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
     int run = 0;
     for (int g0 = 0; g0 < G; g0 += 32) {
       const int g = g0 + lane;
-      const int e = s.expert[min(g, G - 1)];
-      const int w = g < G ? unit_cost<KEPT>((s.loc[e] & LOC_NF3) ? FMT_NF3 : KEPT) : 0;
+      const int w = g < G ? unit_cost<KEPT>((s.loc[g] & LOC_NF3) ? FMT_NF3 : KEPT) : 0;
       int incl = w;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -706,23 +699,25 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
     c.S = c.KB % 2 == 0 ? 2 : 1;
     c.spu = c.KB / c.S;
     c.cols_per_slot = c.ph == 0 ? 1 : 2;
-    const int total = s.cum[G] * c.upg, share = c.ph == 0 ? claim : claim - C;
-    const int each = div_by(total, p.by_shares), over = total - each * C;  // share i begins at total * i / C
-    c.lo = each * share + div_by(over * share, p.by_shares);
-    c.hi = each * (share + 1) + div_by(over * (share + 1), p.by_shares);
-    const int2 groups = c.cut(G);
-    int g0 = groups.x;
-    const int gend = groups.x + groups.y;
+    const int share = c.ph == 0 ? claim : claim - C;
+    c.lo = c.share_border(share, G, lane);
+    c.hi = c.share_border(share + 1, G, lane);
+    int g0 = c.lo.x;
+    const int gend = c.lo.x == c.hi.x && c.lo.y == c.hi.y ? g0 : (c.hi.y > 0 ? c.hi.x + 1 : c.hi.x);
     while (g0 < gend) {
       // As many groups of the share as their activations fit at once (nearly always all).
       int g1 = g0 + 1;
       while (g1 < gend && (s.first[g1 + 1] - s.first[g0]) * c.slot_bytes() <= p.act_cap) ++g1;
-      c.set_borders(g0, g1);
-      __syncthreads();
-      const int2 from = s.border[warp], to = s.border[warp + 1];
+      const int2 from = c.warp_border(warp, g0, g1, G, lane), to = c.warp_border(warp + 1, g0, g1, G, lane);
+      if (lane == 0) {
+        s.border[warp] = from;
+        if (warp == DK_WARPS - 1) s.border[DK_WARPS] = to;
+      }
+      if (tid == 0) s.ends = g1;
       Loader l;
       auto range = [&](int g) {
-        return make_int2(g == from.x ? from.y : 0, g == to.x ? to.y : (s.b[g] - s.a[g]) * c.spu);
+        const int all = g >= g1 ? 0 : ((g == c.hi.x ? c.hi.y : c.upg) - (g == c.lo.x ? c.lo.y : 0)) * c.spu;
+        return make_int2(g == from.x ? from.y : 0, g == to.x ? to.y : all);
       };
       // f(format, k-blocks of a step) of a segment, as types
       auto as = [&](const Segment& r, auto f) {
@@ -731,7 +726,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
           if (c.S == 2) f(fmt, integral_constant<int, 2>());
           else f(fmt, integral_constant<int, 1>());
         };
-        if (r.fmt == FMT_NF3) by_step(integral_constant<int, FMT_NF3>());
+        if (r.loc & LOC_NF3) by_step(integral_constant<int, FMT_NF3>());
         else by_step(integral_constant<int, KEPT>());
       };
       auto start = [&](const Segment& r, int2 steps) {
@@ -757,7 +752,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
       }
       for (int g = g0; g < g1; ++g) c.fill(c.segment(g, g0));
       __syncthreads();
-      for (; i <= to.x; ++i) {
+      for (; i <= to.x && i < g1; ++i) {
         const int2 r = range(i);
         if (r.x >= r.y) continue;
         const Segment g = c.segment(i, g0);
@@ -770,11 +765,15 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
       if (tid == 0) s.tiles = 0;
       __syncthreads();
       if (c.ph == 0) {
-        for (int g = g0 + tid; g < g1; g += DK_THREADS) atomicAdd(done13 + g, s.b[g] - s.a[g]);
+        for (int g = g0 + tid; g < g1; g += DK_THREADS) {
+          const Segment r = c.segment(g, g0);
+          atomicAdd(done13 + g, r.b - r.a);
+        }
       } else {
         // Row tiles whose last units were these: their tokens' slots are summed here.
         for (int g = g0; g < g1; ++g) {
-          const int a = s.a[g], b = s.b[g];
+          const Segment r = c.segment(g, g0);
+          const int a = r.a, b = r.b;
           for (int rt = (a >> 2) + tid; rt <= (b - 1) >> 2; rt += DK_THREADS) {
             const int cnt = min(b, 4 * rt + 4) - max(a, 4 * rt);
             if (atomicAdd(rows_done + rt, cnt) + cnt == 4 * G) s.tile[atomicAdd(&s.tiles, 1)] = rt;

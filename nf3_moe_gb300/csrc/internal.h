@@ -272,6 +272,7 @@ struct DecodeParams {
   const uint8_t* nf3_buf;
   int kept_fmt, act_type;
   int H, I, E, topk, T;
+  int has_nf3;             // 1: some expert is in the NF3 tier
   int group_tokens;        // slots of a group, up to 8: as many as the activations' shared memory admits
   int act_cap;             // bytes of that memory
   uint32_t lut_stride;     // 128, the distance of the NF3 pair table's entries
