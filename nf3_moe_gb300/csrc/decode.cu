@@ -292,6 +292,7 @@ struct DkShared {
   uint8_t head[DK_MAX_SLOTS];  // by position: a group begins
   uint32_t heads[DK_MAX_SLOTS / 32];
   int2 border[DK_WARPS + 1];   // where a warp's part of the groups worked on begins: a group and its step
+  int2 lo, hi;                 // the share
   int claim, abort, tiles, ends;  // ends: the group behind those worked on
   int tile[DK_MAX_ROW_TILES];  // row tiles this CTA brings together
 };
@@ -401,15 +402,22 @@ struct DkCtx {
     const int fmt = fmt_of(g), u = by_unit_cost<KEPT>(at - s.cum[g] * upg + unit_cost<KEPT>(fmt) - 1, fmt);
     return u == upg ? make_int2(g + 1, 0) : make_int2(g, u);
   }
-  // One warp: where warp w's part of groups [g0, g1) begins: an even part of their cost, in steps.
-  __device__ __forceinline__ int2 warp_border(int w, int g0, int g1, int G, int lane) const {
-    const int base = s.cum[g0] * upg;
-    auto cost = [&](int2 at) { return at.x == G ? (s.cum[G] * upg - base) * spu : (s.cum[at.x] * upg + at.y * (s.cum[at.x + 1] - s.cum[at.x]) - base) * spu; };
-    const int from = g0 == lo.x ? cost(lo) : 0, to = g1 > hi.x ? cost(hi) : cost(make_int2(g1, 0));
-    const int at = from + (int)((long long)(to - from) * w / DK_WARPS);
-    if (w == DK_WARPS) return g1 > hi.x ? make_int2(hi.x, (hi.y - (hi.x == lo.x ? lo.y : 0)) * spu) : make_int2(g1, 0);
-    const int g = find(at + base * spu, upg * spu, G, lane);
-    return make_int2(g, by_unit_cost<KEPT>(at - cost(make_int2(g, 0)), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
+  // One warp: the groups from g0 on that are worked on at once, as many of the share as their activations fit (nearly
+  // always all), and where each warp's part of them begins, an even part of their cost, in steps.
+  __device__ __forceinline__ void plan(int g0, int lane) const {
+    const int end = hi.y > 0 ? hi.x + 1 : hi.x;
+    int g1 = g0 + 1;
+    while (g1 < end && (s.first[g1 + 1] - s.first[g0]) * slot_bytes() <= p.act_cap) ++g1;
+    if (lane <= DK_WARPS) {
+      const int base = s.cum[g0];
+      auto cost = [&](int g, int u) { return ((s.cum[g] - base) * upg + (u ? u * (s.cum[g + 1] - s.cum[g]) : 0)) * spu; };
+      const int from = g0 == lo.x ? cost(g0, lo.y) : 0, to = g1 > hi.x ? cost(hi.x, hi.y) : cost(g1, 0);
+      const int at = from + (int)((long long)(to - from) * lane / DK_WARPS);
+      int g = g0;
+      while (g + 1 < g1 && cost(g + 1, 0) <= at) ++g;
+      s.border[lane] = make_int2(g, by_unit_cost<KEPT>(at - cost(g, 0), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
+    }
+    if (lane == 0) s.ends = g1;
   }
 
   // Activations of one segment as MMA fragments: [k-block][half][column][q], 16 bytes each: k = 16 q + 8 half + 0..7.
@@ -700,20 +708,23 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
     c.spu = c.KB / c.S;
     c.cols_per_slot = c.ph == 0 ? 1 : 2;
     const int share = c.ph == 0 ? claim : claim - C;
-    c.lo = c.share_border(share, G, lane);
-    c.hi = c.share_border(share + 1, G, lane);
+    if (warp == 0) {
+      c.lo = c.share_border(share, G, lane);
+      c.hi = c.share_border(share + 1, G, lane);
+      if (lane == 0) {
+        s.lo = c.lo;
+        s.hi = c.hi;
+      }
+      if (c.lo.x != c.hi.x || c.lo.y != c.hi.y) c.plan(c.lo.x, lane);
+    }
+    __syncthreads();
+    c.lo = s.lo;
+    c.hi = s.hi;
     int g0 = c.lo.x;
     const int gend = c.lo.x == c.hi.x && c.lo.y == c.hi.y ? g0 : (c.hi.y > 0 ? c.hi.x + 1 : c.hi.x);
     while (g0 < gend) {
-      // As many groups of the share as their activations fit at once (nearly always all).
-      int g1 = g0 + 1;
-      while (g1 < gend && (s.first[g1 + 1] - s.first[g0]) * c.slot_bytes() <= p.act_cap) ++g1;
-      const int2 from = c.warp_border(warp, g0, g1, G, lane), to = c.warp_border(warp + 1, g0, g1, G, lane);
-      if (lane == 0) {
-        s.border[warp] = from;
-        if (warp == DK_WARPS - 1) s.border[DK_WARPS] = to;
-      }
-      if (tid == 0) s.ends = g1;
+      const int g1 = s.ends;
+      const int2 from = s.border[warp], to = s.border[warp + 1];
       Loader l;
       auto range = [&](int g) {
         const int all = g >= g1 ? 0 : ((g == c.hi.x ? c.hi.y : c.upg) - (g == c.lo.x ? c.lo.y : 0)) * c.spu;
@@ -796,8 +807,12 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
           *reinterpret_cast<uint32_t*>(p.out + (size_t)t * p.H + col) = f32x2_to_act<ACT>(a, b);
         }
       }
-      __syncthreads();
       g0 = g1;
+      if (g0 < gend) {
+        __syncthreads();
+        if (warp == 0) c.plan(g0, lane);
+      }
+      __syncthreads();
     }
     __syncthreads();
   }
