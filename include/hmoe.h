@@ -690,7 +690,7 @@ hmoe_status hmoe_decode(const hmoe_layer* layer, const void* x, int T, const voi
  * Conventions as for the layer. No workspace. */
 typedef struct {
   int N;         /* output features, 1..2^20 */
-  int K;         /* input features, a multiple of group; a row must fit shared memory (about 60000) */
+  int K;         /* input features, a multiple of group up to 2^20 */
   int group;     /* weights of one scale along K: 32, 64 or 128 */
   int zeros;     /* 1: zero points are given; 0: all are 8 */
   int act_dtype; /* hmoe_act_dtype of x, the scales, bias and out; 0 is bf16 */
@@ -720,8 +720,8 @@ hmoe_status hmoe_int4_pack(const hmoe_int4_desc* desc, const void* codes, const 
  * overwritten, overlapping nothing else. All of the activation type. T = 0 is
  * valid.
  *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
- *   pointer, T < 0, a bad stride), HMOE_ERR_UNSUPPORTED_SHAPE (more rows than
- *   65535 passes), HMOE_ERR_CUDA. */
+ *   pointer, T < 0, a bad stride), HMOE_ERR_UNSUPPORTED_SHAPE (T above 2^19),
+ *   HMOE_ERR_CUDA. */
 hmoe_status hmoe_int4_forward(const hmoe_int4* linear, const void* x, int ldx, int T, const void* bias, void* out,
                               int ldout, hmoe_stream_t stream);
 

@@ -1437,9 +1437,8 @@ hmoe_status check_int4_desc(const hmoe_int4_desc* d) {
   if (d->group != 32 && d->group != 64 && d->group != 128)
     return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "group=%d must be 32, 64 or 128", d->group);
   if (d->K % d->group != 0) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "K=%d must be a multiple of the group, %d", d->K, d->group);
-  if (d->N > INT4_MAX_DIM || d->K > INT4_MAX_DIM || int4_pass(int4_geom(d->N, d->K, d->group), 1) < 1)
-    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "N=%d (up to %d) or K=%d (a row of x must fit shared memory) is too large", d->N,
-                INT4_MAX_DIM, d->K);
+  if (d->N > INT4_MAX_DIM || d->K > INT4_MAX_DIM)
+    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "N=%d and K=%d must be at most %d", d->N, d->K, INT4_MAX_DIM);
   return HMOE_OK;
 }
 
@@ -1508,16 +1507,13 @@ hmoe_status hmoe_int4_forward(const hmoe_int4* L, const void* x, int ldx, int T,
   p.K = L->g.K;
   p.units = L->g.units;
   p.NB = L->g.NB;
-  p.pass = int4_pass(L->g, T);
-  if ((T + p.pass - 1) / p.pass > 65535)
-    return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d exceeds 65535 passes of %d rows", T, p.pass);
+  if (T > INT4_MAX_ROWS) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d exceeds %d rows", T, INT4_MAX_ROWS);
   p.T = T;
   p.x = static_cast<const uint16_t*>(x);
   p.bias = static_cast<const uint16_t*>(bias);
   p.out = static_cast<uint16_t*>(out);
   p.ldx = (size_t)ldx;
   p.ldout = (size_t)ldout;
-  p.by_NB = div_by_const((uint32_t)p.NB);
   cudaError_t e = launch_int4(p, 128 / L->d.group, L->num_sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "int4 launch");
   return HMOE_OK;

@@ -5,7 +5,10 @@
 // What bounds it is the bytes of W (0.516 a weight at G = 128), then, below some
 // megabytes, the chain launch, loads, sums. The work is a list of units, 16 rows
 // over the whole K; each CTA takes an even run of them, and its 16 warps even
-// parts of the run's k-blocks (128 of K), whole units or not. A warp streams its
+// parts of the run's k-blocks (128 of K), whole units or not. Where shared memory
+// does not hold x's rows over all of K, K is taken in parts and the units' sums
+// wait in shared memory (16 rows of K = 6144 in two parts: 25 us for 12288 x 6144,
+// against 30 with two passes of 8 rows over the weights). A warp streams its
 // blocks with cp.async into a ring of its own, decodes in registers and issues
 // m16n8k16 MMAs with x's rows as the N side; the sums of a unit that several
 // warps share are joined through shared memory in the order of K.
@@ -28,6 +31,8 @@ namespace hmoe {
 constexpr int I4_WARPS = 16;
 constexpr int I4_THREADS = I4_WARPS * 32;
 constexpr int I4_RING = 6;  // blocks of a warp's ring, in pairs
+constexpr int I4_ROWS = 16; // rows of x of a pass
+constexpr int I4_UNITS = 16;  // units worked on at once where K is taken in parts
 
 // ------------------------------------------------------------ packing
 // A block is 16 rows x 128 K. Codes: two halves of 64 K, each [32 lanes][4 words]: lane (g, q) holds rows g and g + 8
@@ -87,99 +92,86 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
   const int BB = i4_block_bytes(NG, p.zeros != 0), NB = p.NB;
   uint8_t* const ring = smem + warp * I4_RING * BB;
   float* const part = reinterpret_cast<float*>(smem + I4_WARPS * I4_RING * BB);  // [warps][4 NT][32]
-  float* const xsum = part + I4_WARPS * 4 * NT * 32;  // bf16: [groups][8 NT]
-  uint8_t* const xs = reinterpret_cast<uint8_t*>(xsum) + (ACT == ACT_F16 ? 0 : NB * NG * NT * 32);
+  float* const kept = part + I4_WARPS * 4 * NT * 32;  // K in parts: [I4_UNITS][4 NT][32]
+  float* const xsum = kept + (p.parts > 1 ? I4_UNITS * 4 * NT * 32 : 0);  // bf16: [groups][8 NT]
+  uint8_t* const xs = reinterpret_cast<uint8_t*>(xsum) + (ACT == ACT_F16 ? 0 : p.kc * NG * NT * 32);
   const int t0 = blockIdx.y * p.pass, nt = min(p.pass, p.T - t0);
-
-  // This CTA's units and this warp's steps (blocks) of them.
   const int u0 = div_by(p.units * (int)blockIdx.x, p.by_grid), u1 = div_by(p.units * ((int)blockIdx.x + 1), p.by_grid);
-  const int total = (u1 - u0) * NB;
-  auto border = [&](int w) { return (int)((long long)total * w / I4_WARPS); };
-  const int from = border(warp), to = border(warp + 1);
-  const uint8_t* at = p.packed + ((size_t)u0 * NB + from) * BB;  // a unit's blocks, and units, lie one after another
-  const int pieces = BB / 16 - 64;                               // of the scales and zero points
+  const int pieces = BB / 16 - 64;  // of a block's scales and zero points
   const uint32_t dst0 = smem_u32(ring) + lane * 16;
-  auto copy = [&](int slot) {
+  const int half = nt * 64;
+  const uint8_t* const x0 = xs + g * 64 + q * 16;
+
+  // Now: units [ub, ub + nu), part c of K, nb blocks from block c * kc on; this warp's steps (blocks) of them.
+  int ub = u0, c = 0, nu = p.parts > 1 ? min(I4_UNITS, u1 - u0) : u1 - u0, nb = p.parts > 1 ? p.kc : NB;
+  auto by_nb = [&](int n) { return c == p.parts - 1 ? div_by(n, p.by_last) : div_by(n, p.by_kc); };
+  auto border = [&](int w) { return (int)((long long)(nu * nb) * w / I4_WARPS); };
+  int from = 0, to = 0, unit = 0, st = 0, slot = 0, ahead = 0, left = 0;
+  const uint8_t* at = p.packed;  // the next block to copy: a unit's blocks, and units, lie one after another
+  bool whole = true;
+  auto copy = [&](int s) {
     const uint8_t* src = at + lane * 16;
-    const uint32_t dst = dst0 + slot * BB;
+    const uint32_t dst = dst0 + s * BB;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(src + 512) : "memory");
     if (lane < pieces) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 1024), "l"(src + 1024) : "memory");
     at += BB;
+    if (--left == 0) {  // the unit's blocks of this part of K
+      left = nb;
+      at += (size_t)(NB - nb) * BB;
+    }
   };
-  // The first weights to L2 while the kernel before still runs; nothing is read before the wait.
-  for (int i = lane; i < min(I4_RING - 2, to - from) * (BB / 128); i += 32)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * 128));
-  pdl_wait();
-  pdl_trigger();
-  int ahead = from;
-  auto copy2 = [&](int slot) {
-    if (ahead < to) copy(slot);
-    if (ahead + 1 < to) copy(slot + 1);
+  auto copy2 = [&](int s) {
+    if (ahead < to) copy(s);
+    if (ahead + 1 < to) copy(s + 1);
     ahead += 2;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
-  for (int i = 0; i < I4_RING - 2; i += 2) copy2(i);
-  // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps. A thread
-  // has 8 values, the threads of a group of K are neighbours.
-  {
-    constexpr int LOADS = 4, LANES = 16 / NG;
-    const int chunks = NB * 16, all = chunks * nt;
-    for (int i0 = tid; i0 - tid < all; i0 += LOADS * I4_THREADS) {  // whole warps: they shuffle
-      uint4 v[LOADS];
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        const int i = i0 + j * I4_THREADS, c = div_by(min(i, all - 1), p.by_NB) >> 4, k = i - c * chunks;
-        v[j] = i < all && k * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(t0 + c) * p.ldx) + k) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        const int i = i0 + j * I4_THREADS, c = div_by(min(i, all - 1), p.by_NB) >> 4, k = i - c * chunks;
-        if (ACT != ACT_F16) {
-          const uint32_t vv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-          float sum = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = act_x2_to_f32<ACT>(vv[e]);
-            sum += f.x + f.y;
-          }
-#pragma unroll
-          for (int off = 1; off < LANES; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          if (i < all && (k & (LANES - 1)) == 0) xsum[(k / LANES) * 8 * NT + c] = sum;
-        }
-        if (i < all) {
-          const int step = (k >> 1) & 3;
-          uint8_t* d = xs + (((k >> 3) * 2 + (step >> 1)) * nt + c) * 64 + (k & 1) * 32 + (step & 1) * 8;
-          *reinterpret_cast<uint2*>(d) = make_uint2(v[j].x, v[j].y);
-          *reinterpret_cast<uint2*>(d + 16) = make_uint2(v[j].z, v[j].w);
-        }
-      }
-    }
-  }
-  __syncthreads();
+  auto place = [&]() {
+    from = border(warp);
+    to = border(warp + 1);
+    unit = by_nb(from);
+    st = from - unit * nb;
+    slot = 0;
+    ahead = from;
+    left = nb - st;
+    whole = st == 0;
+    at = p.packed + ((size_t)(ub + unit) * NB + (size_t)c * p.kc + st) * BB;
+  };
+  place();
+  // The first weights to L2 while the kernel before still runs; nothing is read before the wait.
+  for (int i = lane; i < min(I4_RING - 2, min(to - from, left)) * (BB / 128); i += 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * 128));
+  pdl_wait();
+  pdl_trigger();
 
   float acc[NT][4] = {};
-  auto emit = [&](int u) {
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] = 0.0f;
+  };
+  // The sums of unit ub + u over this part of K: kept for the next part, or the result.
+  auto finish = [&](int u) {
+    if (p.parts > 1) {
+      float* k = kept + (u * 4 * NT) * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < 4 * NT; ++i) {
+        if (c > 0) acc[i >> 2][i & 3] += k[i * 32];
+        if (c < p.parts - 1) k[i * 32] = acc[i >> 2][i & 3];
+      }
+      if (c < p.parts - 1) return;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int col = 8 * n + 2 * q + (i & 1), r = u * 16 + g + (i >> 1) * 8;
+        const int col = 8 * n + 2 * q + (i & 1), r = (ub + u) * 16 + g + (i >> 1) * 8;
         if (col < nt && r < p.N) {
           const float b = p.bias ? act_lo<ACT>((uint32_t)p.bias[r]) : 0.0f;
           p.out[(size_t)(t0 + col) * p.ldout + r] = f32_to_act<ACT>(acc[n][i] + b);
         }
       }
   };
-  auto clear = [&]() {
-#pragma unroll
-    for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] = 0.0f;
-  };
-  const int half = nt * 64;
-  const uint8_t* const x0 = xs + g * 64 + q * 16;
-  int unit = div_by(from, p.by_NB), st = from - unit * NB, slot = 0;
-  bool whole = st == 0;
   auto block = [&]() {
     const uint8_t* w = ring + slot * BB;
     const uint8_t* x = x0 + (size_t)st * 4 * half;
@@ -240,9 +232,9 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
       }
     }
     ++slot;
-    if (++st == NB) {
+    if (++st == nb) {
       if (whole) {
-        emit(u0 + unit);
+        finish(unit);
       } else {
 #pragma unroll
         for (int i = 0; i < 4 * NT; ++i) part[(warp * 4 * NT + i) * 32 + lane] = acc[i >> 2][i & 3];
@@ -253,47 +245,97 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
       ++unit;
     }
   };
-  for (int s = from; s < to; s += 2) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(I4_RING / 2 - 2) : "memory");
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < I4_RING - 2; i += 2) copy2(i);
+    // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps. A thread
+    // has 8 values, the threads of a group of K are neighbours.
+    {
+      constexpr int LOADS = 4, LANES = 16 / NG;
+      const int chunks = nb * 16, all = chunks * nt, k0 = c * p.kc * 16;
+      for (int i0 = tid; i0 - tid < all; i0 += LOADS * I4_THREADS) {  // whole warps: they shuffle
+        uint4 v[LOADS];
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+          const int i = i0 + j * I4_THREADS, r = by_nb(min(i, all - 1)) >> 4, k = k0 + i - r * chunks;
+          v[j] = i < all && k * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(t0 + r) * p.ldx) + k) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+          const int i = i0 + j * I4_THREADS, r = by_nb(min(i, all - 1)) >> 4, k = i - r * chunks;
+          if (ACT != ACT_F16) {
+            const uint32_t vv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = act_x2_to_f32<ACT>(vv[e]);
+              sum += f.x + f.y;
+            }
+#pragma unroll
+            for (int off = 1; off < LANES; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (i < all && (k & (LANES - 1)) == 0) xsum[(k / LANES) * 8 * NT + r] = sum;
+          }
+          if (i < all) {
+            const int step = (k >> 1) & 3;
+            uint8_t* d = xs + (((k >> 3) * 2 + (step >> 1)) * nt + r) * 64 + (k & 1) * 32 + (step & 1) * 8;
+            *reinterpret_cast<uint2*>(d) = make_uint2(v[j].x, v[j].y);
+            *reinterpret_cast<uint2*>(d + 16) = make_uint2(v[j].z, v[j].w);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    for (int s = from; s < to; s += 2) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(I4_RING / 2 - 2) : "memory");
+      __syncwarp();
+      copy2(slot == 0 ? I4_RING - 2 : slot - 2);  // into the pair before, which all lanes have read
+      block();
+      if (s + 1 < to) block();
+      if (slot == I4_RING) slot = 0;
+    }
     __syncwarp();
-    copy2(slot == 0 ? I4_RING - 2 : slot - 2);  // into the pair before, which all lanes have read
-    block();
-    if (s + 1 < to) block();
-    if (slot == I4_RING) slot = 0;
+    float* const rest = reinterpret_cast<float*>(ring);  // the sums of a unit that another warp ends
+    if (st != 0 && from < to)
+#pragma unroll
+      for (int i = 0; i < 4 * NT; ++i) rest[i * 32 + lane] = acc[i >> 2][i & 3];
+    __syncthreads();
+    // The unit that this warp ended and others began, in the order of K.
+    const int mine = by_nb(from), begin = mine * nb;
+    if (from != begin && to >= begin + nb) {
+      int v = warp - 1;
+      while (border(v) > begin) --v;
+      clear();
+      for (; v < warp; ++v) {
+        if (border(v) == border(v + 1)) continue;  // a warp without work
+        const float* theirs = reinterpret_cast<const float*>(smem + v * I4_RING * BB);
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += theirs[i * 32 + lane];
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += part[(warp * 4 * NT + i) * 32 + lane];
+      finish(mine);
+    }
+    if (p.parts == 1) return;
+    if (++c == p.parts) {
+      c = 0;
+      ub += nu;
+      if (ub >= u1) return;
+      nu = min(I4_UNITS, u1 - ub);
+    }
+    nb = c == p.parts - 1 ? NB - c * p.kc : p.kc;
+    clear();
+    place();
+    __syncthreads();  // the rings, the sums and x are free
   }
-  __syncwarp();
-  float* const rest = reinterpret_cast<float*>(ring);  // the sums of a unit that another warp ends
-  if (st != 0 && from < to)
-#pragma unroll
-    for (int i = 0; i < 4 * NT; ++i) rest[i * 32 + lane] = acc[i >> 2][i & 3];
-  __syncthreads();
-  // The unit that this warp ended and others began, in the order of K.
-  const int mine = div_by(from, p.by_NB), begin = mine * NB;
-  if (from == begin || to < begin + NB) return;
-  int v = warp - 1;
-  while (border(v) > begin) --v;
-  clear();
-  for (; v < warp; ++v) {
-    if (border(v) == border(v + 1)) continue;  // a warp without work
-    const float* theirs = reinterpret_cast<const float*>(smem + v * I4_RING * BB);
-#pragma unroll
-    for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += theirs[i * 32 + lane];
-  }
-#pragma unroll
-  for (int i = 0; i < 4 * NT; ++i) acc[i >> 2][i & 3] += part[(warp * 4 * NT + i) * 32 + lane];
-  emit(u0 + mine);
 }
 
 // ------------------------------------------------------------ launch
-// Rows of x that one pass takes: what shared memory holds beside the rings, up to 16, the passes evened out.
-int int4_pass(const Int4Geom& g, int T) {
-  const int fixed = I4_WARPS * (I4_RING * i4_block_bytes(128 / g.group, true) + 2 * 512) + g.NB * (128 / g.group) * 64;
-  const int most = (DK_SMEM_LIMIT - fixed) / (g.NB * 256);
-  const int cap = most < 16 ? most : 16;
-  if (cap < 1) return 0;
-  const int passes = (T + cap - 1) / cap;
-  return (T + passes - 1) / passes;
+// Bytes of shared memory beside x for passes of `pass` rows, and of x and its sums for each block of K.
+static int i4_fixed(int ng, int pass, bool parts) {
+  const int nt = pass > 8 ? 2 : 1;
+  return I4_WARPS * (I4_RING * i4_block_bytes(ng, true) + nt * 512) + (parts ? I4_UNITS * nt * 512 : 0);
 }
+static int i4_per_block(int ng, int pass) { return pass * 256 + ng * (pass > 8 ? 2 : 1) * 32; }
 
 template <int ACT, int NT, int NG>
 static cudaError_t launch_as(const Int4Params& p, dim3 grid, int smem, cudaStream_t st) {
@@ -308,10 +350,20 @@ static cudaError_t launch_by_group(const Int4Params& p, int ng, dim3 grid, int s
 }
 
 cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st) {
-  const int nt = p.pass > 8 ? 2 : 1;
-  const int smem = I4_WARPS * (I4_RING * i4_block_bytes(ng, p.zeros != 0) + nt * 512) + p.NB * 256 * p.pass +
-                   (p.act_type == ACT_F16 ? 0 : p.NB * ng * nt * 32);
-  const dim3 grid((unsigned)(p.units < num_sms ? p.units : num_sms), (unsigned)((p.T + p.pass - 1) / p.pass));
+  const int passes = (p.T + I4_ROWS - 1) / I4_ROWS;
+  p.pass = (p.T + passes - 1) / passes;  // the passes evened out
+  const int nt = p.pass > 8 ? 2 : 1, per = i4_per_block(ng, p.pass);
+  p.parts = 1;
+  if (p.NB * per > DK_SMEM_LIMIT - i4_fixed(ng, p.pass, false)) {
+    const int most = (DK_SMEM_LIMIT - i4_fixed(ng, p.pass, true)) / per;
+    p.parts = (p.NB + most - 1) / most;
+  }
+  p.kc = (p.NB + p.parts - 1) / p.parts;
+  p.parts = (p.NB + p.kc - 1) / p.kc;  // none empty
+  p.by_kc = div_by_const((uint32_t)p.kc);
+  p.by_last = div_by_const((uint32_t)(p.NB - (p.parts - 1) * p.kc));
+  const int smem = i4_fixed(ng, p.pass, p.parts > 1) + p.kc * per;
+  const dim3 grid((unsigned)(p.units < num_sms ? p.units : num_sms), (unsigned)passes);
   p.by_grid = div_by_const(grid.x);
   cudaError_t e;
   if (p.act_type == ACT_F16) e = nt == 2 ? launch_by_group<ACT_F16, 2>(p, ng, grid, smem, st) : launch_by_group<ACT_F16, 1>(p, ng, grid, smem, st);

@@ -298,6 +298,7 @@ cudaError_t launch_decode(const DecodeParams& p, const uint16_t* router, const f
 
 // ---------------------------------------------------------------- 4-bit integer linear (int4.cu)
 constexpr int INT4_MAX_DIM = 1 << 20;
+constexpr int INT4_MAX_ROWS = 1 << 19;
 struct Int4Geom {
   int N, K, group;
   int units, NB;  // of 16 rows, and blocks of 128 K of each
@@ -311,15 +312,14 @@ struct Int4Params {
   int zeros;             // 1: the blocks hold zero points; 0: all are 8
   int act_type;
   int N, K, units, NB;
-  int T, pass;           // rows of x, and of one pass (int4_pass)
+  int T;                 // rows of x
+  int pass, parts, kc;   // set by launch_int4: rows of a pass, parts of K and their blocks
   const uint16_t* x;
   const uint16_t* bias;  // [N], or NULL
   uint16_t* out;
   size_t ldx, ldout;
-  DivBy by_NB, by_grid;
+  DivBy by_kc, by_last, by_grid;
 };
-// Rows that one pass takes of T; 0: K is more than shared memory holds of one row.
-int int4_pass(const Int4Geom& g, int T);
 cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st);
 
 // Raises a kernel's dynamic shared-memory limit once per device: the

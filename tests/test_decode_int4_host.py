@@ -85,7 +85,7 @@ def test_int4_sizes(lib):
 
 @pytest.mark.parametrize("bad,status", [((0, 128, 128, 0, 0), -1), ((16, 0, 128, 0, 0), -1), ((16, 128, 128, 2, 0), -1), ((16, 128, 128, 0, 2), -1),
                                         ((16, 128, 16, 0, 0), -2), ((16, 128, 96, 0, 0), -2), ((16, 160, 64, 0, 0), -2),
-                                        ((16, 1 << 19, 128, 0, 0), -2), (((1 << 20) + 1, 128, 128, 0, 0), -2), ((16, (1 << 31) - 128, 128, 0, 0), -2)])
+                                        ((16, (1 << 20) + 128, 128, 0, 0), -2), (((1 << 20) + 1, 128, 128, 0, 0), -2), ((16, (1 << 31) - 128, 128, 0, 0), -2)])
 def test_int4_bad_descriptors(lib, bad, status):
     with pytest.raises(hm.HmoeError) as ei:
         hm.hmoe_int4_packed_size(hm.Int4Desc(*bad))

@@ -61,10 +61,13 @@ def test_k_that_ends_inside_a_block(T, N, K, group, act):
 
 
 @pytest.mark.parametrize("T,N,K,group,act", [(1, 6144, 6144, 128, "bf16"), (5, 4096, 6144, 64, "f16"), (16, 2048, 6144, 128, "bf16"),
-                                             (8, 12000, 1024, 32, "bf16"), (2, 200, 32768, 128, "f16"), (9, 100, 16384, 64, "bf16")])
+                                             (8, 12000, 1024, 32, "bf16"), (2, 200, 32768, 128, "f16"), (9, 100, 16384, 64, "bf16"),
+                                             # K in parts: many units a CTA, an uneven last part, a K of one row that does not fit
+                                             (16, 40000, 4224, 128, "bf16"), (12, 3000, 6176, 32, "f16"), (1, 33, 131072, 128, "bf16"),
+                                             (33, 64, 9216, 64, "bf16")])
 def test_larger(T, N, K, group, act):
-    linear, x, made = make(T, N, K, group, act, True)
-    check(linear(x), x, made, group, act)
+    linear, x, made = make(T, N, K, group, act, True, True)
+    check(linear(x, bias=made[3]), x, made, group, act)
 
 
 def test_column_ranges_and_one_row_of_any_stride():
