@@ -81,6 +81,12 @@ __device__ __forceinline__ uint32_t sub_x2(uint32_t a, uint32_t b) {
   else asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// (v & mask) | bits in one operation: both as registers, since as constants the compiler takes an operation for each.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+  return d;
+}
 template <int ACT>
 __device__ __forceinline__ float act_lo(uint32_t v) { return act_x2_to_f32<ACT>(v).x; }
 
@@ -90,6 +96,8 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
   constexpr uint32_t MAGIC = ACT == ACT_F16 ? 0x64006400u : 0x43004300u;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int BB = i4_block_bytes(NG, p.zeros != 0), NB = p.NB;
+  // not constants to the compiler
+  const uint32_t mask = p.mask, magic = p.magic;
   uint8_t* const ring = smem + warp * I4_RING * BB;
   float* const part = reinterpret_cast<float*>(smem + I4_WARPS * I4_RING * BB);  // [warps][4 NT][32]
   float* const kept = part + I4_WARPS * 4 * NT * 32;  // K in parts: [I4_UNITS][4 NT][32]
@@ -107,14 +115,13 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
   auto by_nb = [&](int n) { return c == p.parts - 1 ? div_by(n, p.by_last) : div_by(n, p.by_kc); };
   auto border = [&](int w) { return (int)((long long)(nu * nb) * w / I4_WARPS); };
   int from = 0, to = 0, unit = 0, st = 0, slot = 0, ahead = 0, left = 0;
-  const uint8_t* at = p.packed;  // the next block to copy: a unit's blocks, and units, lie one after another
+  const uint8_t* at = p.packed;  // this lane's 16 bytes of the next block to copy: a unit's blocks, and units, lie one after another
   bool whole = true;
   auto copy = [&](int s) {
-    const uint8_t* src = at + lane * 16;
     const uint32_t dst = dst0 + s * BB;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(src + 512) : "memory");
-    if (lane < pieces) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 1024), "l"(src + 1024) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(at) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(at + 512) : "memory");
+    if (lane < pieces) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 1024), "l"(at + 1024) : "memory");
     at += BB;
     if (--left == 0) {  // the unit's blocks of this part of K
       left = nb;
@@ -136,12 +143,12 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
     ahead = from;
     left = nb - st;
     whole = st == 0;
-    at = p.packed + ((size_t)(ub + unit) * NB + (size_t)c * p.kc + st) * BB;
+    at = p.packed + ((size_t)(ub + unit) * NB + (size_t)c * p.kc + st) * BB + lane * 16;
   };
   place();
   // The first weights to L2 while the kernel before still runs; nothing is read before the wait.
   for (int i = lane; i < min(I4_RING - 2, min(to - from, left)) * (BB / 128); i += 32)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * 128));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at - lane * 16 + i * 128));
   pdl_wait();
   pdl_trigger();
 
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            a[r][i] = ((cw[2 * r + k] >> (4 * i)) & 0x000F000Fu) | MAGIC;
+            a[r][i] = and_or(cw[2 * r + k] >> (4 * i), mask, magic);
             if (ACT == ACT_F16) a[r][i] = sub_x2<ACT>(a[r][i], (r ? z >> 8 : z & 0xFFu) * 0x00010001u + MAGIC);
           }
 #pragma unroll
@@ -365,6 +372,8 @@ cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st) {
   const int smem = i4_fixed(ng, p.pass, p.parts > 1) + p.kc * per;
   const dim3 grid((unsigned)(p.units < num_sms ? p.units : num_sms), (unsigned)passes);
   p.by_grid = div_by_const(grid.x);
+  p.mask = 0x000F000Fu;
+  p.magic = p.act_type == ACT_F16 ? 0x64006400u : 0x43004300u;
   cudaError_t e;
   if (p.act_type == ACT_F16) e = nt == 2 ? launch_by_group<ACT_F16, 2>(p, ng, grid, smem, st) : launch_by_group<ACT_F16, 1>(p, ng, grid, smem, st);
   else e = nt == 2 ? launch_by_group<ACT_BF16, 2>(p, ng, grid, smem, st) : launch_by_group<ACT_BF16, 1>(p, ng, grid, smem, st);

@@ -319,6 +319,7 @@ struct Int4Params {
   uint16_t* out;
   size_t ldx, ldout;
   DivBy by_kc, by_last, by_grid;
+  uint32_t mask, magic;  // of the decoder (and_or)
 };
 cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st);
 
