@@ -520,13 +520,13 @@ struct DkCtx {
 
   // This warp's steps [from, to) of a segment, whose first copies are under way. Whole units are emitted; the sums of
   // one that another warp began go to s.part, of one that another ends to the ring.
-  template <int FMT, int STEP>
+  template <int FMT, int STEP, bool TWO>
   __device__ __forceinline__ void run(Loader& l, const Segment& r, int from, int to, int warp, int lane) const {
     constexpr int SLOTS = DK_RING / STEP;
     const int g = lane >> 2, q = lane & 3;
     const uint32_t nf3_lut = smem_u32(s.nf3) + 4u * (uint32_t)lane;
     const int cols = r.n * cols_per_slot, half = cols * 64;
-    const bool on = g < cols, two = cols > 8, on2 = g + 8 < cols;
+    const bool on = g < cols, on2 = g + 8 < cols;
     const uint32_t x0 = smem_u32(act) + r.act + g * 64 + q * 16;
     const uint32_t* const s_e4m3 = s.e4m3;
     const uint8_t* const ring = s.ring[warp];
@@ -550,7 +550,7 @@ struct DkCtx {
         load_x(on, x, half, xa, xb);
 #pragma unroll
         for (int i = 0; i < 2; ++i) mma_kblock<FMT, ACT>(r0[i], r1[i], sc[i], xa, xb, acc[i][0]);
-        if (two) {
+        if constexpr (TWO) {  // more than 8 columns
           load_x(on2, x + 512, half, xa, xb);
 #pragma unroll
           for (int i = 0; i < 2; ++i) mma_kblock<FMT, ACT>(r0[i], r1[i], sc[i], xa, xb, acc[i][1]);
@@ -768,7 +768,10 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
         if (r.x >= r.y) continue;
         const Segment g = c.segment(i, g0);
         if (i != first) start(g, r);
-        as(g, [&](auto fmt, auto step) { c.template run<fmt(), step()>(l, g, r.x, r.y, warp, lane); });
+        as(g, [&](auto fmt, auto step) {
+          if (g.n * c.cols_per_slot > 8) c.template run<fmt(), step(), true>(l, g, r.x, r.y, warp, lane);
+          else c.template run<fmt(), step(), false>(l, g, r.x, r.y, warp, lane);
+        });
       }
       __syncthreads();
       c.join(from, to, g0, warp, lane);
