@@ -48,14 +48,18 @@ constexpr int DK_SLOT = 1152;    // bytes of a ring slot: a unit's k-block in th
 constexpr int DK_MAX_SLOTS = DECODE_MAX_TOKENS * MAX_TOPK;
 constexpr int DK_NF3_LUT = 3;    // selector words of an NF3 slot through the pair table (of 4)
 
-// Relative time of a unit's k-block, by format, and the division by it.
-template <int FMT>
-constexpr int UNIT_COST = FMT == FMT_NF3 ? 13 : (FMT == FMT_NVFP4 ? 18 : 17);
-template <int KEPT>
-__device__ __forceinline__ int unit_cost(int fmt) { return fmt == FMT_NF3 ? UNIT_COST<FMT_NF3> : UNIT_COST<KEPT>; }
-template <int KEPT>
+// Relative time of a unit's k-block, by format and type: what bounds the warps is their instructions, not the bytes
+// (layers of one format, 2 and 4 tokens, 6144 x 2048: NF3 40, NVFP4 42, in fp16 47, MXFP4 45 clocks an SM for 16 rows x
+// 64 K, where the bytes are as 13 : 18 : 17).
+template <int FMT, int ACT>
+constexpr int UNIT_COST = FMT == FMT_NF3 ? 20 : (FMT == FMT_NVFP4 ? (ACT == ACT_F16 ? 23 : 21) : 22);
+template <int KEPT, int ACT>
+__device__ __forceinline__ int unit_cost(int fmt) {
+  return fmt == FMT_NF3 ? UNIT_COST<FMT_NF3, ACT> : UNIT_COST<KEPT, ACT>;
+}
+template <int KEPT, int ACT>
 __device__ __forceinline__ int by_unit_cost(int v, int fmt) {
-  return fmt == FMT_NF3 ? v / UNIT_COST<FMT_NF3> : v / UNIT_COST<KEPT>;
+  return fmt == FMT_NF3 ? v / UNIT_COST<FMT_NF3, ACT> : v / UNIT_COST<KEPT, ACT>;
 }
 
 // ------------------------------------------------------------ kernel 1: router logits
@@ -190,7 +194,7 @@ __device__ __forceinline__ void nf3x8_lut_at(uint32_t sel, uint32_t lut, uint32_
 // applied.
 template <int FMT, int ACT>
 __device__ __forceinline__ uint32_t decode_kblock(const uint8_t* slot, int i, int lane, uint32_t* r0, uint32_t* r1,
-                                                  const uint32_t* s_e4m3, uint32_t nf3_lut, uint32_t stride) {
+                                                  const uint32_t* s_scale, uint32_t nf3_lut, uint32_t stride) {
   if constexpr (FMT == FMT_NF3) {
     const uint32_t* v = reinterpret_cast<const uint32_t*>(slot) + 32 * i + lane;
     uint32_t s[4];
@@ -209,12 +213,12 @@ __device__ __forceinline__ uint32_t decode_kblock(const uint8_t* slot, int i, in
     uint32_t s0, s1;
     if constexpr (FMT == FMT_NVFP4) {
       const uint32_t sc = reinterpret_cast<const uint16_t*>(slot + 1024)[32 * i + lane];
-      s0 = s_e4m3[sc & 0xFFu];
-      s1 = s_e4m3[sc >> 8];
+      s0 = s_scale[sc & 0xFFu];
+      s1 = s_scale[sc >> 8];
     } else {
       const uint32_t sc = reinterpret_cast<const uint16_t*>(slot + 1024)[16 * i + (lane >> 1)];
-      s0 = bf16_bcast(ACT == ACT_F16 ? e8m0_to_f16(sc & 0xFFu) : e8m0_to_bf16(sc & 0xFFu));
-      s1 = bf16_bcast(ACT == ACT_F16 ? e8m0_to_f16(sc >> 8) : e8m0_to_bf16(sc >> 8));
+      s0 = s_scale[sc & 0xFFu];
+      s1 = s_scale[sc >> 8];
     }
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -279,7 +283,7 @@ struct Segment {
 struct DkShared {
   uint8_t ring[DK_WARPS][DK_RING * DK_SLOT];  // codes in flight; after a warp's last k-block its partial sums
   float part[DK_WARPS][16][32];               // partial sums of the unit that a warp ended and another began
-  uint32_t e4m3[256];
+  uint32_t scale[256];                        // scale byte of the kept format -> pair of the operand type
   uint32_t nf3[NF3_LUT_WORDS];
   alignas(16) int id[DK_MAX_SLOTS];  // chosen experts by slot, then INT_MAX
   float gate[DK_MAX_SLOTS];
@@ -399,7 +403,7 @@ struct DkCtx {
     const int at = each * i + div_by((total - each * p.shares) * i, p.by_shares);  // total * i / shares
     const int g = find(at, upg, G, lane);
     if (g == G) return make_int2(G, 0);
-    const int fmt = fmt_of(g), u = by_unit_cost<KEPT>(at - s.cum[g] * upg + unit_cost<KEPT>(fmt) - 1, fmt);
+    const int fmt = fmt_of(g), u = by_unit_cost<KEPT, ACT>(at - s.cum[g] * upg + unit_cost<KEPT, ACT>(fmt) - 1, fmt);
     return u == upg ? make_int2(g + 1, 0) : make_int2(g, u);
   }
   // One warp: the groups from g0 on that are worked on at once, as many of the share as their activations fit (nearly
@@ -415,7 +419,7 @@ struct DkCtx {
       const int at = from + (int)((long long)(to - from) * lane / DK_WARPS);
       int g = g0;
       while (g + 1 < g1 && cost(g + 1, 0) <= at) ++g;
-      s.border[lane] = make_int2(g, by_unit_cost<KEPT>(at - cost(g, 0), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
+      s.border[lane] = make_int2(g, by_unit_cost<KEPT, ACT>(at - cost(g, 0), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
     }
     if (lane == 0) s.ends = g1;
   }
@@ -528,7 +532,7 @@ struct DkCtx {
     const int cols = r.n * cols_per_slot, half = cols * 64;
     const bool on = g < cols, on2 = g + 8 < cols;
     const uint32_t x0 = smem_u32(act) + r.act + g * 64 + q * 16;
-    const uint32_t* const s_e4m3 = s.e4m3;
+    const uint32_t* const s_scale = s.scale;
     const uint8_t* const ring = s.ring[warp];
     const uint8_t* w = ring;
     int u = spu_of(from), st = from - u * spu;
@@ -546,7 +550,7 @@ struct DkCtx {
         uint32_t r0[2][8], r1[2][8], sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          sc[i] = decode_kblock<FMT, ACT>(w + j * DK_SLOT, i, lane, r0[i], r1[i], s_e4m3, nf3_lut, p.lut_stride);
+          sc[i] = decode_kblock<FMT, ACT>(w + j * DK_SLOT, i, lane, r0[i], r1[i], s_scale, nf3_lut, p.lut_stride);
         load_x(on, x, half, xa, xb);
 #pragma unroll
         for (int i = 0; i < 2; ++i) mma_kblock<FMT, ACT>(r0[i], r1[i], sc[i], xa, xb, acc[i][0]);
@@ -611,7 +615,9 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
   uint8_t* act = smem + DK_SHARED_BYTES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.T * p.topk;
-  if (tid < 256) s.e4m3[tid] = e4m3_lut_entry<ACT>((uint32_t)tid);
+  if (tid < 256)
+    s.scale[tid] = KEPT == FMT_NVFP4 ? e4m3_lut_entry<ACT>((uint32_t)tid)
+                                     : bf16_bcast(ACT == ACT_F16 ? e8m0_to_f16((uint32_t)tid) : e8m0_to_bf16((uint32_t)tid));
   if (p.has_nf3) nf3_lut_fill<ACT>(s.nf3, tid, DK_THREADS);
   if (tid < DK_MAX_SLOTS) {
     s.id[tid] = INT_MAX;
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
     int run = 0;
     for (int g0 = 0; g0 < G; g0 += 32) {
       const int g = g0 + lane;
-      const int w = g < G ? unit_cost<KEPT>((s.loc[g] & LOC_NF3) ? FMT_NF3 : KEPT) : 0;
+      const int w = g < G ? unit_cost<KEPT, ACT>((s.loc[g] & LOC_NF3) ? FMT_NF3 : KEPT) : 0;
       int incl = w;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -696,7 +702,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
   int* rows_done = p.ctl + DK_CTL_ROWS;
   for (;;) {
     const int claim = s.claim;
-    if (claim >= 2 * C) break;
+    if ((unsigned)claim >= 2u * (unsigned)C) break;  // all taken (or a workspace that was not zeroed)
     __syncthreads();
     if (tid == DK_THREADS - 1) s.claim = atomicAdd(p.ctl, 1);  // the next one's way to L2 and back under this one's work
     DkCtx<ACT, KEPT> c{p, s, act};
@@ -790,12 +796,15 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
           const int a = r.a, b = r.b;
           for (int rt = (a >> 2) + tid; rt <= (b - 1) >> 2; rt += DK_THREADS) {
             const int cnt = min(b, 4 * rt + 4) - max(a, 4 * rt);
-            if (atomicAdd(rows_done + rt, cnt) + cnt == 4 * G) s.tile[atomicAdd(&s.tiles, 1)] = rt;
+            if (atomicAdd(rows_done + rt, cnt) + cnt == 4 * G) {
+              const int at = atomicAdd(&s.tiles, 1);
+              if (at < DK_MAX_ROW_TILES) s.tile[at] = rt;
+            }
           }
         }
         __syncthreads();
         __threadfence();
-        const int pairs = s.tiles * p.T * 64;  // of columns
+        const int pairs = min(s.tiles, DK_MAX_ROW_TILES) * p.T * 64;  // of columns
         for (int j = tid; j < pairs; j += DK_THREADS) {
           const int tile = j / (p.T * 64), t = (j >> 6) % p.T, col = s.tile[tile] * 128 + 2 * (j & 63);
           const float* y = p.y + (size_t)t * p.topk * p.H + col;
