@@ -126,8 +126,8 @@ __device__ __forceinline__ void warp_route_few(const float* __restrict__ row, in
   uint32_t key[MAX_E / 32];
 #pragma unroll
   for (int j = 0; j < MAX_E / 32; ++j) key[j] = j < per && lane + 32 * j < E ? route_key(__ldcg(row + lane + 32 * j)) : 0u;
-  uint32_t taken = 0, k1, k2;
-  int j1, j2;
+  uint32_t taken = 0, k1 = 0, k2 = 0;
+  int j1 = 0, j2 = 0;
   auto scan = [&]() {  // j ascending: the first of equal keys has the lowest id
     k1 = k2 = 0;
     j1 = j2 = 0;
@@ -146,8 +146,7 @@ __device__ __forceinline__ void warp_route_few(const float* __restrict__ row, in
       }
     }
   };
-  scan();
-  bool spent = false;
+  bool spent = true;
   int rid = 0;
   uint32_t rkey = 0;
   for (int r = 0; r < k; ++r) {
@@ -518,7 +517,7 @@ struct DkCtx {
     l.in_unit = spu - rest;
     l.steps = to - from;
     loader_unit<FMT>(l, KB, rest * STEP, lane);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < DK_RING / STEP - 1; ++i) loader_issue<FMT, STEP>(l, KB, lane);
   }
 
@@ -841,6 +840,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------ launch
+static_assert((DK_SMEM_LIMIT - DK_SHARED_BYTES) / 256 <= DK_MAX_ROW_TILES, "row tiles of the largest H");
 int decode_act_cap() { return DK_SMEM_LIMIT - DK_SHARED_BYTES; }
 
 template <int ACT, int TM>
