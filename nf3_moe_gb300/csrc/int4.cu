@@ -4,7 +4,7 @@
 //
 // What bounds it is the bytes of W (0.516 a weight at G = 128), then, below some
 // megabytes, the chain launch, loads, sums. The work is a list of units, 16 rows
-// over the whole K; each CTA takes an even run of them, and its 16 warps even
+// over the whole K; each CTA takes an even run of them, and its warps even
 // parts of the run's k-blocks (128 of K), whole units or not. Where shared memory
 // does not hold x's rows over all of K, K is taken in parts and the units' sums
 // wait in shared memory (16 rows of K = 6144 in two parts: 25 us for 12288 x 6144,
@@ -28,8 +28,10 @@
 
 namespace hmoe {
 
-constexpr int I4_WARPS = 16;
-constexpr int I4_THREADS = I4_WARPS * 32;
+// Warps of a CTA: 16, or 8 where a CTA has few blocks, whose time is the start, the
+// joining and the fetch of the code (one row of 2048 x 2048: 4.2 against 3.6 us;
+// of 6144 x 6144, 144 blocks a CTA: 8.4 against 8.9; 8 rows of 32768 x 6144: 26 against 36).
+constexpr int I4_WARPS = 16, I4_FEW_WARPS = 8, I4_FEW_BLOCKS = 32;
 constexpr int I4_RING = 6;  // blocks of a warp's ring, in pairs
 constexpr int I4_ROWS = 16; // rows of x of a pass
 constexpr int I4_UNITS = 16;  // units worked on at once where K is taken in parts
@@ -90,8 +92,8 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
 template <int ACT>
 __device__ __forceinline__ float act_lo(uint32_t v) { return act_x2_to_f32<ACT>(v).x; }
 
-template <int ACT, int NT, int NG>
-__global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_constant__ Int4Params p) {
+template <int ACT, int NT, int NG, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_constant__ Int4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr uint32_t MAGIC = ACT == ACT_F16 ? 0x64006400u : 0x43004300u;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
@@ -99,8 +101,8 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
   // not constants to the compiler
   const uint32_t mask = p.mask, magic = p.magic;
   uint8_t* const ring = smem + warp * I4_RING * BB;
-  float* const part = reinterpret_cast<float*>(smem + I4_WARPS * I4_RING * BB);  // [warps][4 NT][32]
-  float* const kept = part + I4_WARPS * 4 * NT * 32;  // K in parts: [I4_UNITS][4 NT][32]
+  float* const part = reinterpret_cast<float*>(smem + WARPS * I4_RING * BB);  // [warps][4 NT][32]
+  float* const kept = part + WARPS * 4 * NT * 32;  // K in parts: [I4_UNITS][4 NT][32]
   float* const xsum = kept + (p.parts > 1 ? I4_UNITS * 4 * NT * 32 : 0);  // bf16: [groups][8 NT]
   uint8_t* const xs = reinterpret_cast<uint8_t*>(xsum) + (ACT == ACT_F16 ? 0 : p.kc * NG * NT * 32);
   const int t0 = blockIdx.y * p.pass, nt = min(p.pass, p.T - t0);
@@ -109,11 +111,12 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
   const uint32_t dst0 = smem_u32(ring) + lane * 16;
   const int half = nt * 64;
   const uint8_t* const x0 = xs + g * 64 + q * 16;
+  const bool on0 = g < nt, on1 = 8 + g < nt;
 
   // Now: units [ub, ub + nu), part c of K, nb blocks from block c * kc on; this warp's steps (blocks) of them.
   int ub = u0, c = 0, nu = p.parts > 1 ? min(I4_UNITS, u1 - u0) : u1 - u0, nb = p.parts > 1 ? p.kc : NB;
   auto by_nb = [&](int n) { return c == p.parts - 1 ? div_by(n, p.by_last) : div_by(n, p.by_kc); };
-  auto border = [&](int w) { return (int)((long long)(nu * nb) * w / I4_WARPS); };
+  auto border = [&](int w) { return (int)((long long)(nu * nb) * w / WARPS); };
   int from = 0, to = 0, unit = 0, st = 0, slot = 0, ahead = 0, left = 0;
   const uint8_t* at = p.packed;  // this lane's 16 bytes of the next block to copy: a unit's blocks, and units, lie one after another
   bool whole = true;
@@ -179,10 +182,9 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
         }
       }
   };
+  const uint8_t *x = x0, *w = ring;
+  const float* sums = xsum + 2 * q;
   auto block = [&]() {
-    const uint8_t* w = ring + slot * BB;
-    const uint8_t* x = x0 + (size_t)st * 4 * half;
-    const float* sums = xsum + st * NG * 8 * NT + 2 * q;
     float d[NT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
       uint4 xv[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (8 * n + g < nt) {
+        if (n ? on1 : on0) {
           xv[n][0] = *reinterpret_cast<const uint4*>(x + n * 512);
           xv[n][1] = *reinterpret_cast<const uint4*>(x + n * 512 + half);
         }
@@ -238,7 +240,8 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
         }
       }
     }
-    ++slot;
+    sums += NG * 8 * NT;
+    w += BB;
     if (++st == nb) {
       if (whole) {
         finish(unit);
@@ -249,27 +252,29 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
       clear();
       whole = true;
       st = 0;
+      x = x0;
+      sums = xsum + 2 * q;
       ++unit;
     }
   };
   for (;;) {
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < I4_RING - 2; i += 2) copy2(i);
     // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps. A thread
     // has 8 values, the threads of a group of K are neighbours.
     {
-      constexpr int LOADS = 4, LANES = 16 / NG;
+      constexpr int LOADS = 2, LANES = 16 / NG;
       const int chunks = nb * 16, all = chunks * nt, k0 = c * p.kc * 16;
-      for (int i0 = tid; i0 - tid < all; i0 += LOADS * I4_THREADS) {  // whole warps: they shuffle
+      for (int i0 = tid; i0 - tid < all; i0 += LOADS * (WARPS * 32)) {  // whole warps: they shuffle
         uint4 v[LOADS];
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-          const int i = i0 + j * I4_THREADS, r = by_nb(min(i, all - 1)) >> 4, k = k0 + i - r * chunks;
+          const int i = i0 + j * (WARPS * 32), r = by_nb(min(i, all - 1)) >> 4, k = k0 + i - r * chunks;
           v[j] = i < all && k * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(t0 + r) * p.ldx) + k) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-          const int i = i0 + j * I4_THREADS, r = by_nb(min(i, all - 1)) >> 4, k = i - r * chunks;
+          const int i = i0 + j * (WARPS * 32), r = by_nb(min(i, all - 1)) >> 4, k = i - r * chunks;
           if (ACT != ACT_F16) {
             const uint32_t vv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
             float sum = 0.0f;
@@ -292,13 +297,20 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
       }
     }
     __syncthreads();
+    x = x0 + st * 4 * half;
+    sums = xsum + st * NG * 8 * NT + 2 * q;
+    w = ring;
     for (int s = from; s < to; s += 2) {
       asm volatile("cp.async.wait_group %0;" ::"n"(I4_RING / 2 - 2) : "memory");
       __syncwarp();
       copy2(slot == 0 ? I4_RING - 2 : slot - 2);  // into the pair before, which all lanes have read
       block();
       if (s + 1 < to) block();
-      if (slot == I4_RING) slot = 0;
+      slot += 2;
+      if (slot == I4_RING) {
+        slot = 0;
+        w = ring;
+      }
     }
     __syncwarp();
     float* const rest = reinterpret_cast<float*>(ring);  // the sums of a unit that another warp ends
@@ -338,45 +350,52 @@ __global__ void __launch_bounds__(I4_THREADS, 1) int4_kernel(const __grid_consta
 
 // ------------------------------------------------------------ launch
 // Bytes of shared memory beside x for passes of `pass` rows, and of x and its sums for each block of K.
-static int i4_fixed(int ng, int pass, bool parts) {
+static int i4_fixed(int ng, int pass, bool parts, int warps) {
   const int nt = pass > 8 ? 2 : 1;
-  return I4_WARPS * (I4_RING * i4_block_bytes(ng, true) + nt * 512) + (parts ? I4_UNITS * nt * 512 : 0);
+  return warps * (I4_RING * i4_block_bytes(ng, true) + nt * 512) + (parts ? I4_UNITS * nt * 512 : 0);
 }
 static int i4_per_block(int ng, int pass) { return pass * 256 + ng * (pass > 8 ? 2 : 1) * 32; }
 
-template <int ACT, int NT, int NG>
+template <int ACT, int NT, int NG, int WARPS>
 static cudaError_t launch_as(const Int4Params& p, dim3 grid, int smem, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
-  const cudaError_t e = ensure_smem_attr(int4_kernel<ACT, NT, NG>, DK_SMEM_LIMIT, attr);
-  return e != cudaSuccess ? e : launch_pdl(int4_kernel<ACT, NT, NG>, grid, dim3(I4_THREADS), (size_t)smem, st, p);
+  const cudaError_t e = ensure_smem_attr(int4_kernel<ACT, NT, NG, WARPS>, DK_SMEM_LIMIT, attr);
+  return e != cudaSuccess ? e : launch_pdl(int4_kernel<ACT, NT, NG, WARPS>, grid, dim3(WARPS * 32), (size_t)smem, st, p);
 }
-template <int ACT, int NT>
+template <int ACT, int NT, int WARPS>
 static cudaError_t launch_by_group(const Int4Params& p, int ng, dim3 grid, int smem, cudaStream_t st) {
-  return ng == 1 ? launch_as<ACT, NT, 1>(p, grid, smem, st)
-                 : (ng == 2 ? launch_as<ACT, NT, 2>(p, grid, smem, st) : launch_as<ACT, NT, 4>(p, grid, smem, st));
+  return ng == 1 ? launch_as<ACT, NT, 1, WARPS>(p, grid, smem, st)
+                 : (ng == 2 ? launch_as<ACT, NT, 2, WARPS>(p, grid, smem, st) : launch_as<ACT, NT, 4, WARPS>(p, grid, smem, st));
+}
+template <int ACT>
+static cudaError_t launch_by_size(const Int4Params& p, int nt, bool few, int ng, dim3 grid, int smem, cudaStream_t st) {
+  if (few) return nt == 2 ? launch_by_group<ACT, 2, I4_FEW_WARPS>(p, ng, grid, smem, st) : launch_by_group<ACT, 1, I4_FEW_WARPS>(p, ng, grid, smem, st);
+  return nt == 2 ? launch_by_group<ACT, 2, I4_WARPS>(p, ng, grid, smem, st) : launch_by_group<ACT, 1, I4_WARPS>(p, ng, grid, smem, st);
 }
 
 cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st) {
   const int passes = (p.T + I4_ROWS - 1) / I4_ROWS;
   p.pass = (p.T + passes - 1) / passes;  // the passes evened out
   const int nt = p.pass > 8 ? 2 : 1, per = i4_per_block(ng, p.pass);
+  const unsigned ctas = (unsigned)(p.units < num_sms ? p.units : num_sms);
+  const bool few = (long long)((p.units + (int)ctas - 1) / (int)ctas) * p.NB <= I4_FEW_BLOCKS;
+  const int warps = few ? I4_FEW_WARPS : I4_WARPS;
   p.parts = 1;
-  if (p.NB * per > DK_SMEM_LIMIT - i4_fixed(ng, p.pass, false)) {
-    const int most = (DK_SMEM_LIMIT - i4_fixed(ng, p.pass, true)) / per;
+  if (p.NB * per > DK_SMEM_LIMIT - i4_fixed(ng, p.pass, false, warps)) {
+    const int most = (DK_SMEM_LIMIT - i4_fixed(ng, p.pass, true, warps)) / per;
     p.parts = (p.NB + most - 1) / most;
   }
   p.kc = (p.NB + p.parts - 1) / p.parts;
   p.parts = (p.NB + p.kc - 1) / p.kc;  // none empty
   p.by_kc = div_by_const((uint32_t)p.kc);
   p.by_last = div_by_const((uint32_t)(p.NB - (p.parts - 1) * p.kc));
-  const int smem = i4_fixed(ng, p.pass, p.parts > 1) + p.kc * per;
-  const dim3 grid((unsigned)(p.units < num_sms ? p.units : num_sms), (unsigned)passes);
+  const int smem = i4_fixed(ng, p.pass, p.parts > 1, warps) + p.kc * per;
+  const dim3 grid(ctas, (unsigned)passes);
   p.by_grid = div_by_const(grid.x);
   p.mask = 0x000F000Fu;
   p.magic = p.act_type == ACT_F16 ? 0x64006400u : 0x43004300u;
-  cudaError_t e;
-  if (p.act_type == ACT_F16) e = nt == 2 ? launch_by_group<ACT_F16, 2>(p, ng, grid, smem, st) : launch_by_group<ACT_F16, 1>(p, ng, grid, smem, st);
-  else e = nt == 2 ? launch_by_group<ACT_BF16, 2>(p, ng, grid, smem, st) : launch_by_group<ACT_BF16, 1>(p, ng, grid, smem, st);
+  const cudaError_t e = p.act_type == ACT_F16 ? launch_by_size<ACT_F16>(p, nt, few, ng, grid, smem, st)
+                                              : launch_by_size<ACT_BF16>(p, nt, few, ng, grid, smem, st);
   count_launches(1);
   return e;
 }
