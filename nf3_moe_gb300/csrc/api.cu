@@ -1337,9 +1337,9 @@ hmoe_status check_decode(const hmoe_layer_desc& d, int T) {
   if (2LL * d.H > most || 4LL * d.I > most)
     return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "H=%d or I=%d exceeds what shared memory holds of one token (H <= %lld, I <= %lld)",
                 d.H, d.I, most / 2, most / 4);
-  // The kernel cuts its work by cost in 32-bit steps (of a k-block or two; a unit's k-block costs up to 23).
+  // The kernel cuts its work by cost in 32-bit steps (of a k-block or two; a unit's k-block costs up to 24).
   const long long steps13 = (2LL * d.I / 32) * (d.H / 128), steps2 = (d.H / 32LL) * (d.I / (d.I % 128 == 0 ? 128 : 64));
-  if ((long long)T * d.topk * 23 * std::max(steps13, steps2) > (long long)INT_MAX)
+  if ((long long)T * d.topk * 24 * std::max(steps13, steps2) > (long long)INT_MAX)
     return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d, topk=%d, H=%d, I=%d exceed the 32-bit cost of a call", T, d.topk, d.H, d.I);
   return HMOE_OK;
 }
@@ -1387,7 +1387,6 @@ hmoe_status hmoe_decode(const hmoe_layer* L, const void* x, int T, const void* r
   p.topk = d.topk;
   p.T = T;
   p.act_cap = decode_act_cap();
-  p.lut_stride = 128;
   p.has_nf3 = L->n_nf3 > 0 ? 1 : 0;
   p.group_tokens = std::min(DECODE_MAX_TOKENS, std::min(p.act_cap / (2 * d.H), p.act_cap / (4 * d.I)));
   p.shares = L->num_sms;

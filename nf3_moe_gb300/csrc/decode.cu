@@ -9,18 +9,35 @@
 // takes the top-k of the few logits itself, which costs less than a kernel or a
 // wait between CTAs, and finds the chosen experts (at most T * topk) with their
 // tokens. Then the work of W13, and after it that of W2, is cut into one
-// share per SM of equal cost: a run of units, 16 weight rows of one expert over
+// share per SM of equal cost: a run of units, 32 weight rows of one expert over
 // the whole K, in the order (expert, rows). Shares are claimed from a counter,
 // every W13 share before any W2 share, and only W2 shares wait (for the W13
 // units of their experts, bounded), so every wait ends whatever runs beside
 // this kernel.
 //
-// A warp streams its units' packed codes from HBM straight into registers,
-// DK_DEPTH k-blocks ahead and across unit borders, decodes there and issues
-// m16n8k16 MMAs with the tokens as the N side; the activations are in shared
-// memory, laid out as the MMAs' fragments. Nothing but activations and the
-// decoders' tables passes through shared memory, and warps of a share never
-// wait for one another.
+// A share's steps (one or two k-blocks of a unit) are cut evenly among the CTA's
+// warps, wherever in K that falls. A warp copies its steps' packed bytes into a
+// ring of its own with asynchronous 16-byte copies, DK_RING k-blocks deep and
+// across unit borders, decodes them into MMA operands and issues m16n8k16 MMAs
+// with the tokens as the N side; the activations are in shared memory, laid
+// out as the MMAs' fragments. Warps do not wait for one another within a
+// share; afterwards the warp that ends a unit adds the sums of those that
+// began it, in the order of K. The CTA whose units complete a tile of 128
+// output rows adds its tokens' slots by their gates.
+//
+// What bounds it. With one or two tokens an expert the MMAs use a quarter of
+// their columns at most, so decoding the codes costs more than their bytes: a
+// k-block of 16 rows takes about 40 clocks an SM, of which the copies and the
+// loop alone are 26, and the bytes at the copy rate 13 (NF3). 152 SMs at that
+// pace stream 3.7 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 261 us,
+// 968.6 MB; the bytes alone would take 143 us). The ALU is 49% busy, issue
+// 48%, shared memory 41%: the warps wait on each other's pipes and on their
+// own chains. More warps (20, 24, 32), deeper rings, L2 prefetch ahead of them,
+// codes loaded into registers without a ring (355 us, its waits at every use)
+// and one bulk copy a warp and step (379) were all slower or equal. A
+// small call is bounded by its chain of waits instead, 14 to 15 us of logits,
+// top-k, the plan, first copies, W13's counts and cold instruction fetches
+// (one token of 128 experts, 2048 x 768, top-8: 21.9 us, 21.8 MB).
 //
 // Rounding. h stays fp32 between the products and enters W2 as the sum of two
 // values of the activation type (hi + lo, 16 significant bits in bf16, 22 in
@@ -40,19 +57,27 @@
 
 namespace hmoe {
 
+// 16 warps keep the pipes busy (8 tokens of the 256-expert layer: 265 us, with 8 warps 306). Where a CTA has few steps
+// of W13 (of two k-blocks) the barriers of fewer warps and their longer parts count more: 40 steps take 23.5 us with 16
+// warps and 21.9 with 8, 81 steps 28.8 and 27.9, 121 steps 34.3 and 34.1, 162 steps 38.9 and 41.0, 323 steps 53.7 and
+// 55.1. The rule counts every slot as an expert of its own, which the host knows.
 constexpr int DK_WARPS = 16;
-constexpr int DK_THREADS = DK_WARPS * 32;
+constexpr int DK_FEW_WARPS = 8;
+constexpr int DK_FEW_STEPS = 100;  // at most
 constexpr int DK_UNIT = 32;      // weight rows of a unit: two row groups of a tile
 constexpr int DK_RING = 6;       // k-blocks of a warp's ring
 constexpr int DK_SLOT = 1152;    // bytes of a ring slot: a unit's k-block in the widest format
 constexpr int DK_MAX_SLOTS = DECODE_MAX_TOKENS * MAX_TOPK;
-constexpr int DK_NF3_LUT = 3;    // selector words of an NF3 slot through the pair table (of 4)
+// Selector words of an NF3 slot through the pair table, of 4; the others by byte permutes. Each way loads one pipe; 2 and
+// 4 measured the same within 1%.
+constexpr int DK_NF3_LUT = 3;
 
 // Relative time of a unit's k-block, by format and type: what bounds the warps is their instructions, not the bytes
-// (layers of one format, 2 and 4 tokens, 6144 x 2048: NF3 40, NVFP4 42, in fp16 47, MXFP4 45 clocks an SM for 16 rows x
-// 64 K, where the bytes are as 13 : 18 : 17).
+// (layers of one format, 2 and 4 tokens, 6144 x 2048: NF3 40, NVFP4 42, in fp16 47, MXFP4 47 to 49 clocks an SM for 16
+// rows x 64 K, where the bytes are as 13 : 18 : 17). Shares by bytes took 285 us where these take 261 (8 tokens of the
+// 256-expert layer, bf16), 167 where they take 156 (4 tokens, MXFP4, fp16).
 template <int FMT, int ACT>
-constexpr int UNIT_COST = FMT == FMT_NF3 ? 20 : (FMT == FMT_NVFP4 ? (ACT == ACT_F16 ? 23 : 21) : 22);
+constexpr int UNIT_COST = FMT == FMT_NF3 ? 20 : (FMT == FMT_NVFP4 ? (ACT == ACT_F16 ? 23 : 21) : 24);
 template <int KEPT, int ACT>
 __device__ __forceinline__ int unit_cost(int fmt) {
   return fmt == FMT_NF3 ? UNIT_COST<FMT_NF3, ACT> : UNIT_COST<KEPT, ACT>;
@@ -178,22 +203,13 @@ __device__ __forceinline__ void warp_route_few(const float* __restrict__ row, in
   *my_gate = z / sum;
 }
 
-// nf3x8_lut (common.cuh) with the entries' distance as a value that the compiler does not know: a multiply-add, on the
-// FMA pipe, takes the place of a shift-and-add on the ALU, which the decoders fill.
-__device__ __forceinline__ void nf3x8_lut_at(uint32_t sel, uint32_t lut, uint32_t stride, uint32_t* p) {
-  p[0] = lds_u32(__byte_perm(sel, 0u, 0x4440) * stride + lut);
-  p[1] = lds_u32(__byte_perm(sel, 0u, 0x4441) * stride + lut);
-  p[2] = lds_u32(__byte_perm(sel, 0u, 0x4442) * stride + lut);
-  p[3] = lds_u32(__byte_perm(sel, 0u, 0x4443) * stride + lut);
-}
-
 // A lane's part of one k-block of one row group (half i of a unit, 16 rows x 64 K) from a ring slot, which holds the
 // unit's codes and scales in the order of the tile (common.cuh): its operand pairs r0 (row R0) and r1 (row R1), 16
 // values of K each. NF3 comes raw, with the two rows' scales as bf16 in the result; the others have their scales
 // applied.
 template <int FMT, int ACT>
 __device__ __forceinline__ uint32_t decode_kblock(const uint8_t* slot, int i, int lane, uint32_t* r0, uint32_t* r1,
-                                                  const uint32_t* s_scale, uint32_t nf3_lut, uint32_t stride) {
+                                                  const uint32_t* s_scale, uint32_t nf3_lut) {
   if constexpr (FMT == FMT_NF3) {
     const uint32_t* v = reinterpret_cast<const uint32_t*>(slot) + 32 * i + lane;
     uint32_t s[4];
@@ -201,7 +217,7 @@ __device__ __forceinline__ uint32_t decode_kblock(const uint8_t* slot, int i, in
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint32_t* p = (w < 2 ? r0 : r1) + 4 * (w & 1);
-      if (w < DK_NF3_LUT) nf3x8_lut_at(s[w], nf3_lut, stride, p);
+      if (w < DK_NF3_LUT) nf3x8_lut(s[w], nf3_lut, p);
       else if constexpr (ACT == ACT_F16) nf3x8_to_f16x2(s[w], p);
       else nf3x8_to_bf16x2(s[w], p);
     }
@@ -279,9 +295,10 @@ struct Segment {
 };
 
 // Shared memory of decode_kernel.
+template <int WARPS>
 struct DkShared {
-  uint8_t ring[DK_WARPS][DK_RING * DK_SLOT];  // codes in flight; after a warp's last k-block its partial sums
-  float part[DK_WARPS][16][32];               // partial sums of the unit that a warp ended and another began
+  uint8_t ring[WARPS][DK_RING * DK_SLOT];  // codes in flight; after a warp's last k-block its partial sums
+  float part[WARPS][16][32];               // partial sums of the unit that a warp ended and another began
   uint32_t scale[256];                        // scale byte of the kept format -> pair of the operand type
   uint32_t nf3[NF3_LUT_WORDS];
   alignas(16) int id[DK_MAX_SLOTS];  // chosen experts by slot, then INT_MAX
@@ -294,13 +311,13 @@ struct DkShared {
   float hscale[DK_MAX_SLOTS];  // fp16: the power of two that a slot's h was divided by
   uint8_t head[DK_MAX_SLOTS];  // by position: a group begins
   uint32_t heads[DK_MAX_SLOTS / 32];
-  int2 border[DK_WARPS + 1];   // where a warp's part of the groups worked on begins: a group and its step
+  int2 border[WARPS + 1];      // where a warp's part of the groups worked on begins: a group and its step
   int2 lo, hi;                 // the share
   int claim, abort, tiles, ends;  // ends: the group behind those worked on
   int tile[DK_MAX_ROW_TILES];  // row tiles this CTA brings together
 };
 
-constexpr int DK_SHARED_BYTES = (int)((sizeof(DkShared) + 127) / 128 * 128);
+constexpr int DK_SHARED_BYTES = (int)((sizeof(DkShared<DK_WARPS>) + 127) / 128 * 128);
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -366,10 +383,10 @@ __device__ __forceinline__ void loader_issue(Loader& l, int KB, int lane) {
   cp_async_commit();
 }
 
-template <int ACT, int KEPT>
+template <int ACT, int KEPT, int WARPS>
 struct DkCtx {
   const DecodeParams& p;
-  DkShared& s;
+  DkShared<WARPS>& s;
   uint8_t* act;
   int ph, upg, KB, S, spu, cols_per_slot;  // S: k-blocks of a step; spu: steps of a unit
   int2 lo, hi;                             // the share: from a group's unit to another's
@@ -411,11 +428,11 @@ struct DkCtx {
     const int end = hi.y > 0 ? hi.x + 1 : hi.x;
     int g1 = g0 + 1;
     while (g1 < end && (s.first[g1 + 1] - s.first[g0]) * slot_bytes() <= p.act_cap) ++g1;
-    if (lane <= DK_WARPS) {
+    if (lane <= WARPS) {
       const int base = s.cum[g0];
       auto cost = [&](int g, int u) { return ((s.cum[g] - base) * upg + (u ? u * (s.cum[g + 1] - s.cum[g]) : 0)) * spu; };
       const int from = g0 == lo.x ? cost(g0, lo.y) : 0, to = g1 > hi.x ? cost(hi.x, hi.y) : cost(g1, 0);
-      const int at = from + (int)((long long)(to - from) * lane / DK_WARPS);
+      const int at = from + (int)((long long)(to - from) * lane / WARPS);
       int g = g0;
       while (g + 1 < g1 && cost(g + 1, 0) <= at) ++g;
       s.border[lane] = make_int2(g, by_unit_cost<KEPT, ACT>(at - cost(g, 0), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
@@ -431,7 +448,7 @@ struct DkCtx {
       const int pieces = p.H / 8;
       for (int c = 0; c < r.n; ++c) {
         const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(s.sorted[r.p0 + c] / p.topk) * p.H);
-        for (int i = tid; i < pieces; i += DK_THREADS)
+        for (int i = tid; i < pieces; i += WARPS * 32)
           *reinterpret_cast<uint4*>(dst + (((i >> 3) * 2 + (i & 1)) * r.n + c) * 64 + ((i >> 1) & 3) * 16) = __ldg(src + i);
       }
     } else {
@@ -448,7 +465,7 @@ struct DkCtx {
           down = __uint_as_float((uint32_t)(127 + by) << 23);
           if (tid == 0) s.hscale[r.p0 + c] = __uint_as_float((uint32_t)(127 - by) << 23);
         }
-        for (int i = tid; i < pieces; i += DK_THREADS) {
+        for (int i = tid; i < pieces; i += WARPS * 32) {
           const float4 v0 = __ldcg(src + 2 * i), v1 = __ldcg(src + 2 * i + 1);
           const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
           uint32_t hi4[4], lo4[4];
@@ -549,7 +566,7 @@ struct DkCtx {
         uint32_t r0[2][8], r1[2][8], sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          sc[i] = decode_kblock<FMT, ACT>(w + j * DK_SLOT, i, lane, r0[i], r1[i], s_scale, nf3_lut, p.lut_stride);
+          sc[i] = decode_kblock<FMT, ACT>(w + j * DK_SLOT, i, lane, r0[i], r1[i], s_scale, nf3_lut);
         load_x(on, x, half, xa, xb);
 #pragma unroll
         for (int i = 0; i < 2; ++i) mma_kblock<FMT, ACT>(r0[i], r1[i], sc[i], xa, xb, acc[i][0]);
@@ -607,17 +624,19 @@ struct DkCtx {
   }
 };
 
-template <int ACT, int KEPT>
-__global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
+template <int ACT, int KEPT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  DkShared& s = *reinterpret_cast<DkShared*>(smem);
+  constexpr int THREADS = WARPS * 32;
+  static_assert(THREADS >= DK_MAX_SLOTS && WARPS >= DECODE_MAX_TOKENS && WARPS < 32, "a thread a slot, a warp a token");
+  DkShared<WARPS>& s = *reinterpret_cast<DkShared<WARPS>*>(smem);
   uint8_t* act = smem + DK_SHARED_BYTES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.T * p.topk;
   if (tid < 256)
     s.scale[tid] = KEPT == FMT_NVFP4 ? e4m3_lut_entry<ACT>((uint32_t)tid)
                                      : bf16_bcast(ACT == ACT_F16 ? e8m0_to_f16((uint32_t)tid) : e8m0_to_bf16((uint32_t)tid));
-  if (p.has_nf3) nf3_lut_fill<ACT>(s.nf3, tid, DK_THREADS);
+  if (p.has_nf3) nf3_lut_fill<ACT>(s.nf3, tid, THREADS);
   if (tid < DK_MAX_SLOTS) {
     s.id[tid] = INT_MAX;
     s.head[tid] = 0;
@@ -626,7 +645,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
   __syncthreads();
   pdl_wait();  // the router's logits; also the last use of the workspace
   pdl_trigger();
-  if (tid == DK_THREADS - 1) s.claim = atomicAdd(p.ctl, 1);
+  if (tid == THREADS - 1) s.claim = atomicAdd(p.ctl, 1);
   if (warp < p.T) {
     int id;
     float gt;
@@ -703,8 +722,8 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
     const int claim = s.claim;
     if ((unsigned)claim >= 2u * (unsigned)C) break;  // all taken (or a workspace that was not zeroed)
     __syncthreads();
-    if (tid == DK_THREADS - 1) s.claim = atomicAdd(p.ctl, 1);  // the next one's way to L2 and back under this one's work
-    DkCtx<ACT, KEPT> c{p, s, act};
+    if (tid == THREADS - 1) s.claim = atomicAdd(p.ctl, 1);  // the next one's way to L2 and back under this one's work
+    DkCtx<ACT, KEPT, WARPS> c{p, s, act};
     c.ph = claim >= C ? 1 : 0;
     const int upg13 = 2 * p.I / DK_UNIT;
     c.upg = c.ph == 0 ? upg13 : p.H / DK_UNIT;
@@ -784,7 +803,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
       if (tid == 0) s.tiles = 0;
       __syncthreads();
       if (c.ph == 0) {
-        for (int g = g0 + tid; g < g1; g += DK_THREADS) {
+        for (int g = g0 + tid; g < g1; g += THREADS) {
           const Segment r = c.segment(g, g0);
           atomicAdd(done13 + g, r.b - r.a);
         }
@@ -793,7 +812,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
         for (int g = g0; g < g1; ++g) {
           const Segment r = c.segment(g, g0);
           const int a = r.a, b = r.b;
-          for (int rt = (a >> 2) + tid; rt <= (b - 1) >> 2; rt += DK_THREADS) {
+          for (int rt = (a >> 2) + tid; rt <= (b - 1) >> 2; rt += THREADS) {
             const int cnt = min(b, 4 * rt + 4) - max(a, 4 * rt);
             if (atomicAdd(rows_done + rt, cnt) + cnt == 4 * G) {
               const int at = atomicAdd(&s.tiles, 1);
@@ -804,7 +823,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
         __syncthreads();
         __threadfence();
         const int pairs = min(s.tiles, DK_MAX_ROW_TILES) * p.T * 64;  // of columns
-        for (int j = tid; j < pairs; j += DK_THREADS) {
+        for (int j = tid; j < pairs; j += THREADS) {
           const int tile = j / (p.T * 64), t = (j >> 6) % p.T, col = s.tile[tile] * 128 + 2 * (j & 63);
           const float* y = p.y + (size_t)t * p.topk * p.H + col;
           float a = 0.0f, b = 0.0f;
@@ -831,10 +850,10 @@ __global__ void __launch_bounds__(DK_THREADS, 1) decode_kernel(const __grid_cons
   if (tid == 0) s.tiles = atomicAdd(p.ctl + 1, 1) == (int)gridDim.x - 1 ? 1 : 0;
   __syncthreads();
   if (s.tiles) {
-    for (int i = tid; i < G; i += DK_THREADS) done13[i] = 0;
-    for (int i = tid; i < p.H / 128; i += DK_THREADS) rows_done[i] = 0;
+    for (int i = tid; i < G; i += THREADS) done13[i] = 0;
+    for (int i = tid; i < p.H / 128; i += THREADS) rows_done[i] = 0;
     if (ACT == ACT_F16)
-      for (int i = tid; i < S; i += DK_THREADS) p.hmax[i] = 0;
+      for (int i = tid; i < S; i += THREADS) p.hmax[i] = 0;
     if (tid < 2) p.ctl[tid] = 0;
   }
 }
@@ -849,17 +868,25 @@ static cudaError_t launch_router(const DecodeParams& p, const uint16_t* router, 
                     p.logits);
 }
 
+template <int ACT, int KEPT, int WARPS>
+static cudaError_t launch_decode_warps(const DecodeParams& p, int num_sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> attr{0};
+  cudaError_t e = ensure_smem_attr(decode_kernel<ACT, KEPT, WARPS>, DK_SMEM_LIMIT, attr);
+  if (e == cudaSuccess) e = launch_pdl(decode_kernel<ACT, KEPT, WARPS>, dim3(num_sms), dim3(WARPS * 32), DK_SMEM_LIMIT, st, p);
+  return e;
+}
+
 template <int ACT, int KEPT>
 static cudaError_t launch_decode_as(const DecodeParams& p, const uint16_t* router, const float* bias, int num_sms,
                                      cudaStream_t st) {
-  static std::atomic<unsigned long long> attr{0};
-  cudaError_t e = ensure_smem_attr(decode_kernel<ACT, KEPT>, DK_SMEM_LIMIT, attr);
-  if (e == cudaSuccess)
-    e = p.T == 1 ? launch_router<ACT, 1>(p, router, bias, st)
+  cudaError_t e =
+      p.T == 1 ? launch_router<ACT, 1>(p, router, bias, st)
                  : (p.T == 2 ? launch_router<ACT, 2>(p, router, bias, st)
                              : (p.T <= 4 ? launch_router<ACT, 4>(p, router, bias, st) : launch_router<ACT, 8>(p, router, bias, st)));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_kernel<ACT, KEPT>, dim3(num_sms), dim3(DK_THREADS), DK_SMEM_LIMIT, st, p);
+  const long long steps = (long long)p.T * p.topk * (2 * p.I / DK_UNIT) * (p.H / (2 * TILE_K));  // of W13, at most
+  e = steps <= (long long)DK_FEW_STEPS * num_sms ? launch_decode_warps<ACT, KEPT, DK_FEW_WARPS>(p, num_sms, st)
+                                                 : launch_decode_warps<ACT, KEPT, DK_WARPS>(p, num_sms, st);
   count_launches(2);
   return e;
 }

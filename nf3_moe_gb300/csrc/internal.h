@@ -275,7 +275,6 @@ struct DecodeParams {
   int has_nf3;             // 1: some expert is in the NF3 tier
   int group_tokens;        // slots of a group, up to 8: as many as the activations' shared memory admits
   int act_cap;             // bytes of that memory
-  uint32_t lut_stride;     // 128, the distance of the NF3 pair table's entries
   int shares;              // of each product, one per SM
   DivBy by_shares, by_spu13, by_spu2;  // division by the shares and by the steps of a unit
   const uint16_t* x;       // [T][H]

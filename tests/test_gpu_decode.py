@@ -67,6 +67,13 @@ CASES = [
     (8, 8192, 64, 2, 1, synth.FMT_NVFP4, 1, "bf16"),              # activations that fit a few tokens at a time
     (6, 128, 4096, 2, 2, synth.FMT_NVFP4, 1, "f16"),
     (4, 640, 1088, 9, 5, synth.FMT_MXFP4, 0, "bf16"),
+    # more work a CTA than the 8 warps of the small calls are taken for
+    (8, 1024, 512, 40, 8, synth.FMT_NVFP4, 20, "bf16"),
+    (8, 640, 576, 12, 12, synth.FMT_MXFP4, 6, "f16"),             # every token to every expert, odd k-blocks of W2
+    (1, 4096, 1024, 10, 10, synth.FMT_NVFP4, 5, "bf16"),
+    (7, 1152, 640, 33, 9, synth.FMT_MXFP4, 16, "bf16"),
+    (8, 8192, 256, 16, 4, synth.FMT_NVFP4, 8, "f16"),
+    (6, 128, 8192, 6, 6, synth.FMT_NVFP4, 3, "f16"),
 ]
 
 
