@@ -668,11 +668,11 @@ hmoe_status hmoe_decode_workspace_size(const hmoe_layer_desc* desc, int max_toke
 /* x: device [T][H], router: device [E][H], both of the activation type;
  * bias: device fp32 [E], or NULL (an expert at -infinity is chosen only where
  * too few others are left; NaN is not supported). out: device [T][H] of the
- * activation type, fully overwritten, not x. ids int32 [T][topk], gates fp32
+ * activation type, fully overwritten, not over x. ids int32 [T][topk], gates fp32
  * [T][topk]: written where not NULL. x, router and out 16-byte aligned. T = 0
  * is valid.
  *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
- *   pointer, T < 0, out is x), HMOE_ERR_UNSUPPORTED_SHAPE (as for the
+ *   pointer, T < 0, out overlaps x), HMOE_ERR_UNSUPPORTED_SHAPE (as for the
  *   workspace), HMOE_ERR_WORKSPACE_TOO_SMALL, HMOE_ERR_CUDA; a bounded wait
  *   that ran out is HMOE_ERR_DEVICE_TIMEOUT through hmoe_check_device_status. */
 hmoe_status hmoe_decode(const hmoe_layer* layer, const void* x, int T, const void* router, const float* bias, void* out,
@@ -685,7 +685,10 @@ hmoe_status hmoe_decode(const hmoe_layer* layer, const void* x, int T, const voi
  * for the projections of a decode step; any number of rows is taken, 16 at
  * most reading the weights once. The integers and their products with x are
  * exact, a group's sum and all else are fp32 in a fixed order, rounded once to
- * the activation type: the same call gives the same bits.
+ * the activation type: the same call gives the same bits. In bf16 a group's
+ * sum is taken of (128 + q) x, and (128 + z) sum x off it: that adds an error
+ * of some 2^-16 of sum |x s|, a row of x that holds an infinity gives NaN where
+ * fp16 may give infinities, and |x| above 2^112 is not supported.
  *   These entry points have no counterpart on the pages; beside the dense
  *   linear above they take the integer formats' checkpoints.
  * Conventions as for the layer. No workspace. */
@@ -718,10 +721,10 @@ hmoe_status hmoe_int4_pack(const hmoe_int4_desc* desc, const void* codes, const 
 /* y = W x (+ bias). x: device [T] rows of K, ldx elements apart (a multiple of
  * 8), 16-byte aligned, so column ranges of wider tensors serve; bias: device
  * [N], or NULL; out: device [T] rows of N, ldout elements apart, fully
- * overwritten, overlapping nothing else. All of the activation type. T = 0 is
- * valid.
+ * overwritten, overlapping nothing else (x and out may be column ranges of one
+ * tensor). All of the activation type. T = 0 is valid.
  *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
- *   pointer, T < 0, a bad stride), HMOE_ERR_UNSUPPORTED_SHAPE (T above 2^19),
+ *   pointer, T < 0, a bad stride, out overlaps x), HMOE_ERR_UNSUPPORTED_SHAPE (T above 2^19),
  *   HMOE_ERR_CUDA. */
 hmoe_status hmoe_int4_forward(const hmoe_int4* linear, const void* x, int ldx, int T, const void* bias, void* out,
                               int ldout, hmoe_stream_t stream);

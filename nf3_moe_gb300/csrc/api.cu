@@ -1370,7 +1370,9 @@ hmoe_status hmoe_decode(const hmoe_layer* L, const void* x, int T, const void* r
     return fail(HMOE_ERR_INVALID_ARG, "x, router and out must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(gates)) & 3)
     return fail(HMOE_ERR_INVALID_ARG, "bias, ids and gates must be aligned to their elements");
-  if (x == out) return fail(HMOE_ERR_INVALID_ARG, "out must not be x");
+  const size_t bytes = (size_t)T * d.H * 2;
+  const uintptr_t xp = reinterpret_cast<uintptr_t>(x), op = reinterpret_cast<uintptr_t>(out);
+  if (xp < op + bytes && op < xp + bytes) return fail(HMOE_ERR_INVALID_ARG, "out must not overlap x");
   if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
   const DecodeWs w = decode_ws(d, T);
   if (ws_bytes < w.total)
@@ -1441,6 +1443,16 @@ hmoe_status check_int4_desc(const hmoe_int4_desc* d) {
   return HMOE_OK;
 }
 
+// Rows of K at x and of N at out share memory: other than as column ranges of one wider tensor.
+bool int4_overlap(const void* x, int ldx, int K, const void* out, int ldout, int N, int T) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(out);
+  const size_t of_x = ((size_t)(T - 1) * ldx + K) * 2, of_out = ((size_t)(T - 1) * ldout + N) * 2;
+  if (a + of_x <= b || b + of_out <= a) return false;
+  if (ldx != ldout) return true;
+  const size_t pitch = (size_t)ldx * 2, at = b >= a ? (b - a) % pitch : (pitch - (a - b) % pitch) % pitch;  // out's column behind x's
+  return at < (size_t)K * 2 || at + (size_t)N * 2 > pitch;
+}
+
 size_t int4_bytes(const hmoe_int4_desc& d) {
   const Int4Geom g = int4_geom(d.N, d.K, d.group);
   return (size_t)g.units * g.NB * i4_block_bytes(128 / d.group, d.zeros != 0);
@@ -1498,6 +1510,8 @@ hmoe_status hmoe_int4_forward(const hmoe_int4* L, const void* x, int ldx, int T,
     return fail(HMOE_ERR_INVALID_ARG, "x must be 16-byte aligned, with a row stride of a multiple of 8 that holds a row (ldx=%d)", ldx);
   if (((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(bias)) & 1) || ldout < L->d.N)
     return fail(HMOE_ERR_INVALID_ARG, "out and bias must be aligned to their elements, and ldout hold a row (ldout=%d)", ldout);
+  if (T > INT4_MAX_ROWS) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d exceeds %d rows", T, INT4_MAX_ROWS);
+  if (int4_overlap(x, ldx, L->d.K, out, ldout, L->d.N, T)) return fail(HMOE_ERR_INVALID_ARG, "out must not overlap x");
   Int4Params p{};
   p.packed = L->packed;
   p.zeros = L->d.zeros;
@@ -1506,7 +1520,6 @@ hmoe_status hmoe_int4_forward(const hmoe_int4* L, const void* x, int ldx, int T,
   p.K = L->g.K;
   p.units = L->g.units;
   p.NB = L->g.NB;
-  if (T > INT4_MAX_ROWS) return fail(HMOE_ERR_UNSUPPORTED_SHAPE, "T=%d exceeds %d rows", T, INT4_MAX_ROWS);
   p.T = T;
   p.x = static_cast<const uint16_t*>(x);
   p.bias = static_cast<const uint16_t*>(bias);

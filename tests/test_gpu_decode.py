@@ -250,6 +250,18 @@ def test_a_wait_that_runs_out_is_reported():
     check(L, moe, x, router, moe.decode(x, router))
 
 
+def test_results_over_x_are_refused():
+    L, moe, x, router = make(2, 256, 128, 4, 2, kept=2)
+    flat = torch.zeros(2 * 512, dtype=x.dtype, device="cuda")
+    flat[256:768] = x.flatten()
+    for lo in (0, 256, 264, 504):
+        with pytest.raises(hm.HmoeError, match="overlap"):
+            moe.decode(flat[256:768].view(2, 256), router, out=flat[lo:lo + 512].view(2, 256))
+    token = torch.stack([x[0], x[0]])
+    moe.decode(token[:1], router, out=token[1:])                   # beside it
+    assert torch.equal(token[1:], moe.decode(x[:1], router)[0])
+
+
 def test_refusals():
     L, moe, x, router = make(2, 256, 128, 4, 2, kept=2)
     with pytest.raises(hm.HmoeError) as ei:                        # more tokens than the entry point takes

@@ -177,3 +177,25 @@ def test_refusals():
     before = out._version
     linear(x, out=out)
     assert out._version > before
+
+
+def test_results_over_x_are_refused_and_beside_it_taken():
+    linear, x, made = make(3, 40, 256, 64, "bf16")
+    want, wide = linear(x), torch.zeros((3, 400), dtype=x.dtype, device="cuda")
+    ranges = {lo: torch.as_strided(wide, (3, 40), (400, 1), lo) for lo in (0, 100, 217, 255, 256, 300, 360)}
+    for lo in (0, 100, 217, 255):
+        with pytest.raises(hm.HmoeError, match="overlap"):
+            linear(wide[:, :256], out=ranges[lo])
+    for lo in (256, 300, 360):                                     # columns behind x's
+        wide[:, :256] = x
+        linear(wide[:, :256], out=ranges[lo])
+        assert torch.equal(ranges[lo], want) and torch.equal(wide[:, :256], x)
+    wide.zero_()
+    wide[:, 144:] = x                                              # columns before x's, and in the next row's end
+    linear(wide[:, 144:], out=wide[:, 104:144])
+    assert torch.equal(wide[:, 104:144], want)
+    with pytest.raises(hm.HmoeError, match="overlap"):             # a row stride of its own over the same memory
+        linear(wide[:, 144:], out=torch.as_strided(wide, (3, 40), (80, 1), 120))
+    square, y, _ = make(1, 256, 256, 64, "f16")
+    with pytest.raises(hm.HmoeError, match="overlap"):
+        square(y, out=y)
