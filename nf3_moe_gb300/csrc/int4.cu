@@ -19,9 +19,11 @@
 // the group's sum of products (that leaves 2^-24 of sums up to 30 times the
 // result's, far below bf16's rounding). fp16, whose result keeps more bits and
 // whose offset is larger: 1024 + z is subtracted first, exactly, 11 operations.
-// What bounded it after the bytes was the issue of instructions: the offsets'
-// subtraction in bf16 and a wait for every block instead of every second cost
-// 36 against 26 us for 8 rows of 32768 x 6144.
+// What bounds it after the bytes is the issue of instructions and the ALU (58%
+// busy, with DRAM at 46%): the offsets' subtraction in bf16 and a wait for every
+// block instead of every second cost 36 against 29 us for 8 rows of 32768 x 6144
+// (105 MB), a mask and an OR apart in the decoder 29.6 against 25.1. More warps
+// (20, 24) were slower, as were 8.
 #include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -29,8 +31,8 @@
 namespace hmoe {
 
 // Warps of a CTA: 16, or 8 where a CTA has few blocks, whose time is the start, the
-// joining and the fetch of the code (one row of 2048 x 2048: 4.2 against 3.6 us;
-// of 6144 x 6144, 144 blocks a CTA: 8.4 against 8.9; 8 rows of 32768 x 6144: 26 against 36).
+// joining and the fetch of the code (16 warps against 8: one row of 2048 x 2048, 16 blocks a
+// CTA, 4.2 and 3.6 us; of 6144 x 6144, 144 blocks, 8.4 and 8.9; 8 rows of 32768 x 6144 26 and 36).
 constexpr int I4_WARPS = 16, I4_FEW_WARPS = 8, I4_FEW_BLOCKS = 32;
 constexpr int I4_RING = 6;  // blocks of a warp's ring, in pairs
 constexpr int I4_ROWS = 16; // rows of x of a pass
@@ -261,9 +263,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
 #pragma unroll 1
     for (int i = 0; i < I4_RING - 2; i += 2) copy2(i);
     // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps. A thread
-    // has 8 values, the threads of a group of K are neighbours.
+    // has 8 values, the threads of a group of K are neighbours. Few blocks: less code to fetch (one row of 2048 x 2048:
+    // 3.2 us with two loads in flight, 3.4 with four; 8 rows of 32768 x 6144: 26.4 and 25.0).
     {
-      constexpr int LOADS = 2, LANES = 16 / NG;
+      constexpr int LOADS = WARPS == I4_FEW_WARPS ? 2 : 4, LANES = 16 / NG;
       const int chunks = nb * 16, all = chunks * nt, k0 = c * p.kc * 16;
       for (int i0 = tid; i0 - tid < all; i0 += LOADS * (WARPS * 32)) {  // whole warps: they shuffle
         uint4 v[LOADS];
