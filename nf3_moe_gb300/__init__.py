@@ -14,7 +14,9 @@ Typical use (see ``HybridMoELayer`` for the same thing with owned buffers):
 
 Beside the layer: rows sorted by expert and back with their gradients (rows.py,
 ``ExpertRows``) and low-rank adapters of many requests (lora.py, ``LoraAdapters``);
-examples/adapters.py runs them together.
+examples/adapters.py runs them together. For a decode step: the whole layer from
+hidden states (decode.py, ``HybridMoELayer.decode``) and linears of 4-bit integer
+weights (int4.py, ``LinearInt4``); examples/decode_step.py runs them in a graph.
 """
 
 import ctypes
