@@ -198,6 +198,29 @@ def test_graph_and_other_streams():
         check(L, moe, x, router, (out, ids, gates))
 
 
+def test_two_graphs_share_a_workspace():
+    """Graphs of one layer with different numbers of tokens (and warps a CTA), replayed in turn on one stream."""
+    L, moe, x, router = make(8, 1024, 512, 20, 8, kept=10, act="f16")
+    big, small = [t.clone() for t in moe.decode(x, router)], [t.clone() for t in moe.decode(x[:1], router)]
+    outs, graphs, st = [[torch.empty_like(t) for t in w] for w in (big, small)], [], torch.cuda.Stream()
+    st.wait_stream(torch.cuda.default_stream())
+    with torch.cuda.stream(st):
+        for o, v in zip(outs, (x, x[:1])):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                moe.decode(v, router, out=o[0], ids=o[1], gates=o[2])
+            graphs.append(g)
+        for _ in range(3):
+            for o, g, want in zip(outs, graphs, (big, small)):
+                o[0].fill_(7.0)
+                g.replay()
+                g.replay()
+                st.synchronize()
+                assert all(torch.equal(p, q) for p, q in zip(o, want))
+    hm.hmoe_check_device_status(moe.decode_ws)
+    check(L, moe, x, router, big)
+
+
 def test_two_layers_at_once():
     """Two calls that share the GPU: neither may wait for a place the other holds."""
     made = [make(8, 1024, 512, 16, 4, kept=8, seed=s) for s in (1, 2)]

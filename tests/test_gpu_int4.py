@@ -199,3 +199,14 @@ def test_results_over_x_are_refused_and_beside_it_taken():
     square, y, _ = make(1, 256, 256, 64, "f16")
     with pytest.raises(hm.HmoeError, match="overlap"):
         square(y, out=y)
+
+
+def test_too_many_rows_are_refused():
+    linear, x, _ = make(1, 16, 64, 64, "bf16")
+    rows = (1 << 19) + 1
+    many, out = x.new_zeros((rows, 64)), x.new_zeros((rows, 16))
+    with pytest.raises(hm.HmoeError) as ei:
+        linear(many, out=out)
+    assert ei.value.status == -2
+    many[-2] = x[0]
+    assert torch.equal(linear(many[:-1])[-1:], linear(x)) and not bool(linear(many[:-1])[:-1].any())
