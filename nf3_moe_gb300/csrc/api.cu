@@ -1319,7 +1319,7 @@ DecodeWs decode_ws(const hmoe_layer_desc& d, int T) {
   DecodeWs w{};
   const size_t S = (size_t)T * d.topk;
   w.ctl = 256;
-  w.hmax = w.ctl + align256((size_t)(DK_CTL_ROWS + d.H / 128) * 4);
+  w.hmax = w.ctl + align256((size_t)DK_CTL_INTS * 4);
   w.logits = w.hmax + align256((size_t)DECODE_MAX_TOKENS * MAX_TOPK * 4);
   w.h = w.logits + align256((size_t)T * d.E * 4);
   w.y = w.h + align256(S * d.I * 4);

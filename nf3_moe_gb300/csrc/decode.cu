@@ -12,8 +12,8 @@
 // share per SM of equal cost: a run of units, 32 weight rows of one expert over
 // the whole K, in the order (expert, rows). Shares are claimed from a counter,
 // every W13 share before any W2 share, and only W2 shares wait (for the W13
-// units of their experts, bounded), so every wait ends whatever runs beside
-// this kernel.
+// units of their experts, bounded) and CTAs that find none left (for all of
+// W2), so every wait is for CTAs that run, whatever runs beside this kernel.
 //
 // A share's steps (one or two k-blocks of a unit) are cut evenly among the CTA's
 // warps, wherever in K that falls. A warp copies its steps' packed bytes into a
@@ -22,22 +22,24 @@
 // with the tokens as the N side; the activations are in shared memory, laid
 // out as the MMAs' fragments. Warps do not wait for one another within a
 // share; afterwards the warp that ends a unit adds the sums of those that
-// began it, in the order of K. The CTA whose units complete a tile of 128
-// output rows adds its tokens' slots by their gates.
+// began it, in the order of K. When all W2 units are done, each CTA adds the
+// slots of an even part of the output by their gates. (Left to the CTA that
+// completes a tile of 128 output rows, that falls to the few with the last
+// expert, which then took 20 us more than the others for 8 tokens of 6144.)
 //
 // What bounds it. With one or two tokens an expert the MMAs use a quarter of
 // their columns at most, so decoding the codes costs more than their bytes: a
 // k-block of 16 rows takes about 40 clocks an SM, of which the copies and the
 // loop alone are 26, and the bytes at the copy rate 13 (NF3). 152 SMs at that
-// pace stream 3.7 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 261 us,
+// pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 247 us,
 // 968.6 MB; the bytes alone would take 143 us). The ALU is 49% busy, issue
 // 48%, shared memory 41%: the warps wait on each other's pipes and on their
 // own chains. More warps (20, 24, 32), deeper rings, L2 prefetch ahead of them,
 // codes loaded into registers without a ring (355 us, its waits at every use)
 // and one bulk copy a warp and step (379) were all slower or equal. A
-// small call is bounded by its chain of waits instead, 14 to 15 us of logits,
+// small call is bounded by its chain of waits instead, about 14 us of logits,
 // top-k, the plan, first copies, W13's counts and cold instruction fetches
-// (one token of 128 experts, 2048 x 768, top-8: 21.9 us, 21.8 MB).
+// (one token of 128 experts, 2048 x 768, top-8: 21.3 us, 21.8 MB).
 //
 // Rounding. h stays fp32 between the products and enters W2 as the sum of two
 // values of the activation type (hi + lo, 16 significant bits in bf16, 22 in
@@ -313,8 +315,7 @@ struct DkShared {
   uint32_t heads[DK_MAX_SLOTS / 32];
   int2 border[WARPS + 1];      // where a warp's part of the groups worked on begins: a group and its step
   int2 lo, hi;                 // the share
-  int claim, abort, tiles, ends;  // ends: the group behind those worked on
-  int tile[DK_MAX_ROW_TILES];  // row tiles this CTA brings together
+  int claim, abort, last, ends;  // ends: the group behind those worked on
 };
 
 constexpr int DK_SHARED_BYTES = (int)((sizeof(DkShared<DK_WARPS>) + 127) / 128 * 128);
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
 
   const int C = p.shares;
   int* done13 = p.ctl + DK_CTL_DONE;
-  int* rows_done = p.ctl + DK_CTL_ROWS;
+  int* done2 = p.ctl + DK_CTL_DONE2;
   for (;;) {
     const int claim = s.claim;
     if ((unsigned)claim >= 2u * (unsigned)C) break;  // all taken (or a workspace that was not zeroed)
@@ -800,42 +801,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
       __syncthreads();
       c.join(from, to, g0, warp, lane);
       __threadfence();  // this thread's h or y values, before their counts
-      if (tid == 0) s.tiles = 0;
       __syncthreads();
       if (c.ph == 0) {
         for (int g = g0 + tid; g < g1; g += THREADS) {
           const Segment r = c.segment(g, g0);
           atomicAdd(done13 + g, r.b - r.a);
         }
-      } else {
-        // Row tiles whose last units were these: their tokens' slots are summed here.
+      } else if (tid == 0) {
+        int units = 0;
         for (int g = g0; g < g1; ++g) {
           const Segment r = c.segment(g, g0);
-          const int a = r.a, b = r.b;
-          for (int rt = (a >> 2) + tid; rt <= (b - 1) >> 2; rt += THREADS) {
-            const int cnt = min(b, 4 * rt + 4) - max(a, 4 * rt);
-            if (atomicAdd(rows_done + rt, cnt) + cnt == 4 * G) {
-              const int at = atomicAdd(&s.tiles, 1);
-              if (at < DK_MAX_ROW_TILES) s.tile[at] = rt;
-            }
-          }
+          units += r.b - r.a;
         }
-        __syncthreads();
-        __threadfence();
-        const int pairs = min(s.tiles, DK_MAX_ROW_TILES) * p.T * 64;  // of columns
-        for (int j = tid; j < pairs; j += THREADS) {
-          const int tile = j / (p.T * 64), t = (j >> 6) % p.T, col = s.tile[tile] * 128 + 2 * (j & 63);
-          const float* y = p.y + (size_t)t * p.topk * p.H + col;
-          float a = 0.0f, b = 0.0f;
-#pragma unroll 8
-          for (int k = 0; k < p.topk; ++k) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(y + (size_t)k * p.H));
-            const float gt = s.gate[t * p.topk + k];
-            a = fmaf(gt, v.x, a);
-            b = fmaf(gt, v.y, b);
-          }
-          *reinterpret_cast<uint32_t*>(p.out + (size_t)t * p.H + col) = f32x2_to_act<ACT>(a, b);
-        }
+        atomicAdd(done2, units);
       }
       g0 = g1;
       if (g0 < gend) {
@@ -846,20 +824,40 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
     }
     __syncthreads();
   }
-  // The last CTA to leave brings the workspace's counters back to zero.
-  if (tid == 0) s.tiles = atomicAdd(p.ctl + 1, 1) == (int)gridDim.x - 1 ? 1 : 0;
+  // Every share is taken, by CTAs that run: when their units are done, each CTA sums the slots of its part of the columns.
+  if (tid == 0 && !wait_count_at_least(done2, G * (p.H / DK_UNIT), &s.abort, p.wait_limit_ns)) {
+    *(volatile int*)&s.abort = 1;
+    set_status(p.status, DEV_TIMEOUT);
+  }
   __syncthreads();
-  if (s.tiles) {
+  if (*(volatile int*)&s.abort) return;
+  const int half = p.H / 2, pairs = p.T * half, each = (pairs + (int)gridDim.x - 1) / (int)gridDim.x;  // pairs of columns
+  for (int j = (int)blockIdx.x * each + tid; j < min(pairs, ((int)blockIdx.x + 1) * each); j += THREADS) {
+    const int t = j / half, col = 2 * (j - t * half);
+    const float* y = p.y + (size_t)t * p.topk * p.H + col;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < p.topk; ++k) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(y + (size_t)k * p.H));
+      const float gt = s.gate[t * p.topk + k];
+      a = fmaf(gt, v.x, a);
+      b = fmaf(gt, v.y, b);
+    }
+    *reinterpret_cast<uint32_t*>(p.out + (size_t)t * p.H + col) = f32x2_to_act<ACT>(a, b);
+  }
+  // The last CTA to leave brings the workspace's counters back to zero.
+  if (tid == 0) s.last = atomicAdd(p.ctl + 1, 1) == (int)gridDim.x - 1 ? 1 : 0;
+  __syncthreads();
+  if (s.last) {
     for (int i = tid; i < G; i += THREADS) done13[i] = 0;
-    for (int i = tid; i < p.H / 128; i += THREADS) rows_done[i] = 0;
     if (ACT == ACT_F16)
       for (int i = tid; i < S; i += THREADS) p.hmax[i] = 0;
     if (tid < 2) p.ctl[tid] = 0;
+    if (tid == 2) *done2 = 0;
   }
 }
 
 // ------------------------------------------------------------ launch
-static_assert((DK_SMEM_LIMIT - DK_SHARED_BYTES) / 256 <= DK_MAX_ROW_TILES, "row tiles of the largest H");
 int decode_act_cap() { return DK_SMEM_LIMIT - DK_SHARED_BYTES; }
 
 template <int ACT, int TM>

@@ -262,11 +262,11 @@ __device__ __forceinline__ int div_by(int n, const DivBy& d) {
 // ---------------------------------------------------------------- the whole layer for a few tokens (decode.cu)
 constexpr int DECODE_MAX_TOKENS = 8;
 constexpr int DK_SMEM_LIMIT = 232448;    // dynamic shared memory of a CTA, 227 KB
-constexpr int DK_MAX_ROW_TILES = 256;    // H / 128: above what the activations' shared memory admits
-// The counters of a call, in ints: claimed shares, CTAs that left, then the
-// W13 units done per group and the W2 units done per row tile.
+// The counters of a call, in ints: claimed shares, CTAs that left, then W2
+// units done, then the W13 units done per group.
+constexpr int DK_CTL_DONE2 = 32;
 constexpr int DK_CTL_DONE = 64;
-constexpr int DK_CTL_ROWS = DK_CTL_DONE + DECODE_MAX_TOKENS * MAX_TOPK;
+constexpr int DK_CTL_INTS = DK_CTL_DONE + DECODE_MAX_TOKENS * MAX_TOPK;
 struct DecodeParams {
   const uint8_t* kept_buf;
   const uint8_t* nf3_buf;

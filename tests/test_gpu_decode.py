@@ -93,9 +93,8 @@ def test_every_token_count_in_one_workspace(act):
         assert out.shape == (T, 256) and ids.shape == gates.shape == (T, 4)
         if T:
             check(L, moe, x[:T], router, (out, ids, gates))
-    # the status word, the counters (64 + 256 + H / 128 ints) and the largest |h| (256) are back at zero: what a later
-    # call relies on
-    counters = 256 + -(-(64 + 256 + 256 // 128) * 4 // 256) * 256 + 1024
+    # the status word, the counters (64 + 256 ints) and the largest |h| (256) are back at zero: what a later call relies on
+    counters = 256 + (64 + 256) * 4 + 1024
     assert int(moe.decode_ws[:counters].count_nonzero()) == 0
 
 
