@@ -1391,7 +1391,7 @@ hmoe_status hmoe_decode(const hmoe_layer* L, const void* x, int T, const void* r
   p.act_cap = decode_act_cap();
   p.has_nf3 = L->n_nf3 > 0 ? 1 : 0;
   p.group_tokens = std::min(DECODE_MAX_TOKENS, std::min(p.act_cap / (2 * d.H), p.act_cap / (4 * d.I)));
-  p.shares = L->num_sms;
+  p.shares = std::min(L->num_sms, DK_MAX_SHARES);
   const auto steps = [](int kb) { return (uint32_t)(kb % 2 == 0 ? kb / 2 : kb); };
   p.by_shares = div_by_const((uint32_t)p.shares);
   p.by_spu13 = div_by_const(steps(d.H / TILE_K));

@@ -11,9 +11,9 @@
 // tokens. Then the work of W13, and after it that of W2, is cut into one
 // share per SM of equal cost: a run of units, 32 weight rows of one expert over
 // the whole K, in the order (expert, rows). Shares are claimed from a counter,
-// every W13 share before any W2 share, and only W2 shares wait (for the W13
-// units of their experts, bounded) and CTAs that find none left (for all of
-// W2), so every wait is for CTAs that run, whatever runs beside this kernel.
+// every W13 share before any W2 share. W2 shares wait for the W13 units of
+// their experts, and CTAs that find no share left for all of W2: every wait is
+// for CTAs that run, whatever runs beside this kernel, and bounded.
 //
 // A share's steps (one or two k-blocks of a unit) are cut evenly among the CTA's
 // warps, wherever in K that falls. A warp copies its steps' packed bytes into a
@@ -22,24 +22,27 @@
 // with the tokens as the N side; the activations are in shared memory, laid
 // out as the MMAs' fragments. Warps do not wait for one another within a
 // share; afterwards the warp that ends a unit adds the sums of those that
-// began it, in the order of K. When all W2 units are done, each CTA adds the
-// slots of an even part of the output by their gates. (Left to the CTA that
-// completes a tile of 128 output rows, that falls to the few with the last
-// expert, which then took 20 us more than the others for 8 tokens of 6144.)
+// began it, in the order of K. Every thread finds the borders of some shares at
+// the start and every warp its own part of a share, so that nothing waits for a
+// plan between W13 and W2 (a warp that planned each share for all: 21.1 us where
+// this takes 20.6, one token of 128 experts). When all W2 units are done, each
+// CTA adds the slots of an even part of the output by their gates. (Left to the
+// CTA that completes a tile of 128 output rows, that falls to the few with the
+// last expert, which then took 20 us more than the others for 8 tokens of 6144.)
 //
 // What bounds it. With one or two tokens an expert the MMAs use a quarter of
 // their columns at most, so decoding the codes costs more than their bytes: a
 // k-block of 16 rows takes about 40 clocks an SM, of which the copies and the
 // loop alone are 26, and the bytes at the copy rate 13 (NF3). 152 SMs at that
-// pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 247 us,
+// pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 250 us,
 // 968.6 MB; the bytes alone would take 143 us). The ALU is 49% busy, issue
 // 48%, shared memory 41%: the warps wait on each other's pipes and on their
 // own chains. More warps (20, 24, 32), deeper rings, L2 prefetch ahead of them,
 // codes loaded into registers without a ring (355 us, its waits at every use)
 // and one bulk copy a warp and step (379) were all slower or equal. A
-// small call is bounded by its chain of waits instead, about 14 us of logits,
+// small call is bounded by its chain of waits instead, about 13 us of logits,
 // top-k, the plan, first copies, W13's counts and cold instruction fetches
-// (one token of 128 experts, 2048 x 768, top-8: 21.3 us, 21.8 MB).
+// (one token of 128 experts, 2048 x 768, top-8: 20.6 us, 21.8 MB).
 //
 // Rounding. h stays fp32 between the products and enters W2 as the sum of two
 // values of the activation type (hi + lo, 16 significant bits in bf16, 22 in
@@ -313,9 +316,10 @@ struct DkShared {
   float hscale[DK_MAX_SLOTS];  // fp16: the power of two that a slot's h was divided by
   uint8_t head[DK_MAX_SLOTS];  // by position: a group begins
   uint32_t heads[DK_MAX_SLOTS / 32];
+  int2 share[2][DK_MAX_SHARES + 1];  // of each product: where a share begins, a group and its unit
   int2 border[WARPS + 1];      // where a warp's part of the groups worked on begins: a group and its step
-  int2 lo, hi;                 // the share
-  int claim, abort, last, ends;  // ends: the group behind those worked on
+  int claim[2];                // the share worked on and the next one
+  int abort, last;
 };
 
 constexpr int DK_SHARED_BYTES = (int)((sizeof(DkShared<DK_WARPS>) + 127) / 128 * 128);
@@ -331,7 +335,6 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // Where a warp's copies into its ring stand: a step is STEP k-blocks of the segment's units, in their order.
 struct Loader {
-  const uint8_t* row;      // the matrix
   const uint8_t* at;       // this lane's pieces of the next step
   const uint8_t* at2;
   uint32_t ring;           // shared address of the ring, at this lane's 16 bytes
@@ -343,8 +346,8 @@ struct Loader {
 // scales: 52 pieces of 16 bytes, a lane's at `at` and `at2`) and two in the kept formats (1024 bytes of codes, 128 or
 // 64 of scales: a lane's two pieces at `at`, its third at `at2`).
 template <int FMT>
-__device__ __forceinline__ void loader_unit(Loader& l, int KB, int kb, int lane) {
-  const uint8_t* tile = l.row + ((size_t)(l.u >> 2) * KB + kb) * tile_bytes(FMT);
+__device__ __forceinline__ void loader_unit(Loader& l, const uint8_t* matrix, int KB, int kb, int lane) {
+  const uint8_t* tile = matrix + ((size_t)(l.u >> 2) * KB + kb) * tile_bytes(FMT);
   const int i = l.u & 3;
   if constexpr (FMT == FMT_NF3) {
     l.at = tile + i * 256 + (lane >> 4) * 1024 + (lane & 15) * 16;
@@ -372,13 +375,15 @@ __device__ __forceinline__ void loader_issue(Loader& l, int KB, int lane) {
       for (int j = 0; j < STEP; ++j) cp_async16(dst + j * DK_SLOT + (FMT == FMT_NF3 ? 512 : 1024), l.at2 + j * TB);
     }
     l.slot = l.slot == (DK_RING - STEP) * DK_SLOT ? 0 : l.slot + STEP * DK_SLOT;
+    l.at += STEP * TB;
+    l.at2 += STEP * TB;
     if (--l.in_unit == 0) {
+      // the next quarter of the same tiles, or the first of those that follow
+      const bool same = (++l.u & 3) != 0;
+      const int codes = FMT == FMT_NF3 ? 256 : 1024, rest = FMT == FMT_NF3 ? (lane < 16 ? 256 : 64) : (FMT == FMT_NVFP4 ? 128 : 64);
+      l.at += same ? codes - KB * TB : -3 * codes;
+      l.at2 += same ? rest - KB * TB : -3 * rest;
       l.in_unit = KB / STEP;
-      ++l.u;
-      loader_unit<FMT>(l, KB, 0, lane);
-    } else {
-      l.at += STEP * TB;
-      l.at2 += STEP * TB;
     }
   }
   cp_async_commit();
@@ -391,6 +396,15 @@ struct DkCtx {
   uint8_t* act;
   int ph, upg, KB, S, spu, cols_per_slot;  // S: k-blocks of a step; spu: steps of a unit
   int2 lo, hi;                             // the share: from a group's unit to another's
+
+  __device__ __forceinline__ void set(int phase) {
+    ph = phase;
+    upg = (ph == 0 ? 2 * p.I : p.H) / DK_UNIT;
+    KB = (ph == 0 ? p.H : p.I) / TILE_K;
+    S = KB % 2 == 0 ? 2 : 1;
+    spu = KB / S;
+    cols_per_slot = ph == 0 ? 1 : 2;
+  }
 
   __device__ __forceinline__ int fmt_of(int g) const { return (s.loc[g] & LOC_NF3) ? FMT_NF3 : KEPT; }
 
@@ -408,37 +422,37 @@ struct DkCtx {
   }
   __device__ __forceinline__ int slot_bytes() const { return cols_per_slot * KB * 128; }  // of a slot's activations
 
-  // One warp: the group that holds the cost `at` (counted by `per` for each unit_cost of a group before it), or G.
-  __device__ __forceinline__ int find(int at, int per, int G, int lane) const {
-    int n = 0;
-    for (int g = lane; g < G; g += 32) n += s.cum[g + 1] * per <= at ? 1 : 0;
-    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
-  }
-  // One warp: where share i begins: a group and its unit, the first whose cost begins at the share's or later.
-  __device__ __forceinline__ int2 share_border(int i, int G, int lane) const {
+  // Where share i begins: a group and its unit, the first whose cost begins at the share's or later.
+  __device__ __forceinline__ int2 share_border(int i, int G) const {
     const int total = s.cum[G] * upg, each = div_by(total, p.by_shares);
     const int at = each * i + div_by((total - each * p.shares) * i, p.by_shares);  // total * i / shares
-    const int g = find(at, upg, G, lane);
+    int g = 0;
+    for (int n = G; n > 0;) {  // the groups that end at `at` or before
+      const int m = n >> 1;
+      const bool ends = s.cum[g + m + 1] * upg <= at;
+      g = ends ? g + m + 1 : g;
+      n = ends ? n - m - 1 : m;
+    }
     if (g == G) return make_int2(G, 0);
     const int fmt = fmt_of(g), u = by_unit_cost<KEPT, ACT>(at - s.cum[g] * upg + unit_cost<KEPT, ACT>(fmt) - 1, fmt);
     return u == upg ? make_int2(g + 1, 0) : make_int2(g, u);
   }
-  // One warp: the groups from g0 on that are worked on at once, as many of the share as their activations fit (nearly
-  // always all), and where each warp's part of them begins, an even part of their cost, in steps.
-  __device__ __forceinline__ void plan(int g0, int lane) const {
-    const int end = hi.y > 0 ? hi.x + 1 : hi.x;
+  // The group behind those that are worked on at once from g0 on: as many of the share as their activations fit, nearly
+  // always all.
+  __device__ __forceinline__ int end_of(int g0, int end) const {
     int g1 = g0 + 1;
     while (g1 < end && (s.first[g1 + 1] - s.first[g0]) * slot_bytes() <= p.act_cap) ++g1;
-    if (lane <= WARPS) {
-      const int base = s.cum[g0];
-      auto cost = [&](int g, int u) { return ((s.cum[g] - base) * upg + (u ? u * (s.cum[g + 1] - s.cum[g]) : 0)) * spu; };
-      const int from = g0 == lo.x ? cost(g0, lo.y) : 0, to = g1 > hi.x ? cost(hi.x, hi.y) : cost(g1, 0);
-      const int at = from + (int)((long long)(to - from) * lane / WARPS);
-      int g = g0;
-      while (g + 1 < g1 && cost(g + 1, 0) <= at) ++g;
-      s.border[lane] = make_int2(g, by_unit_cost<KEPT, ACT>(at - cost(g, 0), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
-    }
-    if (lane == 0) s.ends = g1;
+    return g1;
+  }
+  // Where warp w's part of the groups [g0, g1) begins, an even part of their cost: a group and its step.
+  __device__ __forceinline__ int2 part_border(int w, int g0, int g1) const {
+    const int base = s.cum[g0];
+    auto cost = [&](int g, int u) { return ((s.cum[g] - base) * upg + (u ? u * (s.cum[g + 1] - s.cum[g]) : 0)) * spu; };
+    const int from = g0 == lo.x ? cost(g0, lo.y) : 0, to = g1 > hi.x ? cost(hi.x, hi.y) : cost(g1, 0);
+    const int at = from + (int)((long long)(to - from) * w / WARPS);
+    int g = g0;
+    while (g + 1 < g1 && cost(g + 1, 0) <= at) ++g;
+    return make_int2(g, by_unit_cost<KEPT, ACT>(at - cost(g, 0), fmt_of(g)) - (g == lo.x ? lo.y * spu : 0));
   }
 
   // Activations of one segment as MMA fragments: [k-block][half][column][q], 16 bytes each: k = 16 q + 8 half + 0..7.
@@ -525,7 +539,7 @@ struct DkCtx {
   template <int FMT, int STEP>
   __device__ __forceinline__ void begin(Loader& l, const Segment& r, int from, int to, int warp, int lane) const {
     constexpr bool nf3 = FMT == FMT_NF3;
-    l.row = (nf3 ? p.nf3_buf : p.kept_buf) +
+    const uint8_t* matrix = (nf3 ? p.nf3_buf : p.kept_buf) +
             (size_t)(r.loc & 0x7FFF) * (nf3 ? p.nf3_expert_bytes : p.kept_expert_bytes) +
             (ph == 0 ? 0 : (nf3 ? p.nf3_w2_off : p.kept_w2_off));
     l.ring = smem_u32(s.ring[warp]) + lane * 16;
@@ -534,7 +548,7 @@ struct DkCtx {
     l.u = r.a + whole;
     l.in_unit = spu - rest;
     l.steps = to - from;
-    loader_unit<FMT>(l, KB, rest * STEP, lane);
+    loader_unit<FMT>(l, matrix, KB, rest * STEP, lane);
 #pragma unroll 1
     for (int i = 0; i < DK_RING / STEP - 1; ++i) loader_issue<FMT, STEP>(l, KB, lane);
   }
@@ -603,9 +617,9 @@ struct DkCtx {
   }
 
   // The unit that this warp ended and others began: their sums in the order of K.
-  __device__ __forceinline__ void join(int2 from, int2 to, int g0, int warp, int lane) const {
+  __device__ __forceinline__ void join(int2 from, int2 to, int g0, int g1, int warp, int lane) const {
     const int u = spu_of(from.y), begin = u * spu;
-    if (from.x >= s.ends || from.y == begin || (to.x == from.x && to.y < begin + spu)) return;
+    if (from.x >= g1 || from.y == begin || (to.x == from.x && to.y < begin + spu)) return;
     const Segment r = segment(from.x, g0);
     int v = warp - 1;  // the warp that began it
     while (s.border[v].x == from.x && s.border[v].y > begin) --v;
@@ -643,10 +657,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
     s.head[tid] = 0;
   }
   if (tid == 0) s.abort = 0;
+  // The layer's table while the router still runs: constants at an index of each thread's own are read one by one.
+  ExpertTable& tab = *reinterpret_cast<ExpertTable*>(s.ring);  // which the weights take later
+  static_assert(sizeof(ExpertTable) <= sizeof(s.ring), "the table in the rings");
+  for (int e = tid; e < p.E; e += THREADS) {
+    tab.loc[e] = p.tab.loc[e];
+    tab.g13[e] = p.tab.g13[e];
+    tab.g2[e] = p.tab.g2[e];
+  }
   __syncthreads();
   pdl_wait();  // the router's logits; also the last use of the workspace
   pdl_trigger();
-  if (tid == THREADS - 1) s.claim = atomicAdd(p.ctl, 1);
+  if (tid == THREADS - 1) s.claim[0] = atomicAdd(p.ctl, 1);
   if (warp < p.T) {
     int id;
     float gt;
@@ -691,9 +713,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
       const int g = before + __popc(ballot & ((1u << lane) - 1u));
       const int e = s.id[s.sorted[tid]];
       s.first[g] = tid;
-      s.loc[g] = p.tab.loc[e];
-      s.g13[g] = p.tab.g13[e];
-      s.g2[g] = p.tab.g2[e];
+      s.loc[g] = tab.loc[e];
+      s.g13[g] = tab.g13[e];
+      s.g2[g] = tab.g2[e];
     }
     if (tid == 0) s.first[G] = S;
   }
@@ -719,37 +741,33 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
   const int C = p.shares;
   int* done13 = p.ctl + DK_CTL_DONE;
   int* done2 = p.ctl + DK_CTL_DONE2;
-  for (;;) {
-    const int claim = s.claim;
-    if ((unsigned)claim >= 2u * (unsigned)C) break;  // all taken (or a workspace that was not zeroed)
-    __syncthreads();
-    if (tid == THREADS - 1) s.claim = atomicAdd(p.ctl, 1);  // the next one's way to L2 and back under this one's work
+  const int upg13 = 2 * p.I / DK_UNIT;
+  for (int i = tid; i <= 2 * C + 1; i += THREADS) {
     DkCtx<ACT, KEPT, WARPS> c{p, s, act};
-    c.ph = claim >= C ? 1 : 0;
-    const int upg13 = 2 * p.I / DK_UNIT;
-    c.upg = c.ph == 0 ? upg13 : p.H / DK_UNIT;
-    c.KB = (c.ph == 0 ? p.H : p.I) / TILE_K;
-    c.S = c.KB % 2 == 0 ? 2 : 1;
-    c.spu = c.KB / c.S;
-    c.cols_per_slot = c.ph == 0 ? 1 : 2;
-    const int share = c.ph == 0 ? claim : claim - C;
-    if (warp == 0) {
-      c.lo = c.share_border(share, G, lane);
-      c.hi = c.share_border(share + 1, G, lane);
-      if (lane == 0) {
-        s.lo = c.lo;
-        s.hi = c.hi;
-      }
-      if (c.lo.x != c.hi.x || c.lo.y != c.hi.y) c.plan(c.lo.x, lane);
-    }
-    __syncthreads();
-    c.lo = s.lo;
-    c.hi = s.hi;
+    const int ph = i > C ? 1 : 0;
+    c.set(ph);
+    s.share[ph][i - ph * (C + 1)] = c.share_border(i - ph * (C + 1), G);
+  }
+  __syncthreads();
+  for (int place = 0;; place ^= 1) {
+    const int claim = s.claim[place];
+    if ((unsigned)claim >= 2u * (unsigned)C) break;  // all taken (or a workspace that was not zeroed)
+    DkCtx<ACT, KEPT, WARPS> c{p, s, act};
+    c.set(claim >= C ? 1 : 0);
+    c.lo = s.share[c.ph][claim - c.ph * C];
+    c.hi = s.share[c.ph][claim - c.ph * C + 1];
     int g0 = c.lo.x;
     const int gend = c.lo.x == c.hi.x && c.lo.y == c.hi.y ? g0 : (c.hi.y > 0 ? c.hi.x + 1 : c.hi.x);
+    if (g0 == gend) {  // a share without units
+      if (tid == THREADS - 1) s.claim[place ^ 1] = atomicAdd(p.ctl, 1);
+      __syncthreads();
+    }
     while (g0 < gend) {
-      const int g1 = s.ends;
-      const int2 from = s.border[warp], to = s.border[warp + 1];
+      const int g1 = c.end_of(g0, gend);
+      const int2 mine = c.part_border(warp + (lane & 1), g0, g1);
+      if (lane < 2) s.border[warp + lane] = mine;  // for join (the next warp writes the same)
+      const int2 from = make_int2(__shfl_sync(0xffffffffu, mine.x, 0), __shfl_sync(0xffffffffu, mine.y, 0));
+      const int2 to = make_int2(__shfl_sync(0xffffffffu, mine.x, 1), __shfl_sync(0xffffffffu, mine.y, 1));
       Loader l;
       auto range = [&](int g) {
         const int all = g >= g1 ? 0 : ((g == c.hi.x ? c.hi.y : c.upg) - (g == c.lo.x ? c.lo.y : 0)) * c.spu;
@@ -772,6 +790,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
       while (i < to.x && range(i).x >= range(i).y) ++i;
       const int first = i;
       if (range(first).x < range(first).y) start(c.segment(first, g0), range(first));
+      // the next share's way to L2 and back under this one's work
+      if (g0 == c.lo.x && tid == THREADS - 1) s.claim[place ^ 1] = atomicAdd(p.ctl, 1);
       if (c.ph == 1) {
         // every W13 unit of these groups written, by any CTA
         if (warp == 0)
@@ -799,7 +819,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
         });
       }
       __syncthreads();
-      c.join(from, to, g0, warp, lane);
+      c.join(from, to, g0, g1, warp, lane);
       __threadfence();  // this thread's h or y values, before their counts
       __syncthreads();
       if (c.ph == 0) {
@@ -816,13 +836,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
         atomicAdd(done2, units);
       }
       g0 = g1;
-      if (g0 < gend) {
-        __syncthreads();
-        if (warp == 0) c.plan(g0, lane);
-      }
-      __syncthreads();
     }
-    __syncthreads();
   }
   // Every share is taken, by CTAs that run: when their units are done, each CTA sums the slots of its part of the columns.
   if (tid == 0 && !wait_count_at_least(done2, G * (p.H / DK_UNIT), &s.abort, p.wait_limit_ns)) {

@@ -261,6 +261,7 @@ __device__ __forceinline__ int div_by(int n, const DivBy& d) {
 
 // ---------------------------------------------------------------- the whole layer for a few tokens (decode.cu)
 constexpr int DECODE_MAX_TOKENS = 8;
+constexpr int DK_MAX_SHARES = 192;       // of a product: one per SM, up to these
 constexpr int DK_SMEM_LIMIT = 232448;    // dynamic shared memory of a CTA, 227 KB
 // The counters of a call, in ints: claimed shares, CTAs that left, then W2
 // units done, then the W13 units done per group.
