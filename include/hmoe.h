@@ -659,8 +659,8 @@ void hmoe_lora_destroy(hmoe_lora* lora);
  * first use (hmoe_workspace_init), and again after a call reports
  * HMOE_ERR_DEVICE_TIMEOUT. Host only.
  *   No page defines it. Errors: the desc checks of hmoe_workspace_size;
- *   HMOE_ERR_UNSUPPORTED_SHAPE (act_quant, max_tokens above 8, H above 29952
- *   or I above 14976, of which shared memory does not hold one token, or a
+ *   HMOE_ERR_UNSUPPORTED_SHAPE (act_quant, max_tokens above 8, H above 39680
+ *   or I above 19840, of which shared memory does not hold one token, or a
  *   batch whose work the kernel's 32-bit costs do not hold);
  *   HMOE_ERR_INVALID_ARG (bytes NULL, max_tokens < 0). */
 hmoe_status hmoe_decode_workspace_size(const hmoe_layer_desc* desc, int max_tokens, size_t* bytes);

@@ -17,7 +17,7 @@
 //
 // A share's steps (one or two k-blocks of a unit) are cut evenly among the CTA's
 // warps, wherever in K that falls. A warp copies its steps' packed bytes into a
-// ring of its own with asynchronous 16-byte copies, DK_RING k-blocks deep and
+// ring of its own with asynchronous 16-byte copies, some k-blocks ahead and
 // across unit borders, decodes them into MMA operands and issues m16n8k16 MMAs
 // with the tokens as the N side; the activations are in shared memory, laid
 // out as the MMAs' fragments. Warps do not wait for one another within a
@@ -34,7 +34,7 @@
 // their columns at most, so decoding the codes costs more than their bytes: a
 // k-block of 16 rows takes about 40 clocks an SM, of which the copies and the
 // loop alone are 26, and the bytes at the copy rate 13 (NF3). 152 SMs at that
-// pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 250 us,
+// pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 248 us,
 // 968.6 MB; the bytes alone would take 143 us). The ALU is 49% busy, issue
 // 48%, shared memory 41%: the warps wait on each other's pipes and on their
 // own chains. More warps (20, 24, 32), deeper rings, L2 prefetch ahead of them,
@@ -63,19 +63,23 @@
 namespace hmoe {
 
 // 16 warps keep the pipes busy (8 tokens of the 256-expert layer: 265 us, with 8 warps 306). Where a CTA has few steps
-// of W13 (of two k-blocks) the barriers of fewer warps and their longer parts count more: 40 steps take 23.5 us with 16
-// warps and 21.9 with 8, 81 steps 28.8 and 27.9, 121 steps 34.3 and 34.1, 162 steps 38.9 and 41.0, 323 steps 53.7 and
-// 55.1. The rule counts every slot as an expert of its own, which the host knows.
+// of W13 (of two k-blocks) the barriers of fewer warps and their longer parts count more: 40 steps take 22.3 us with 16
+// warps and 20.7 with 8, 81 steps 29.4 and 28.4, 121 steps 33.3 and 32.7, 162 steps 35.4 and 35.9, 323 steps 51.7 and
+// 53.3. The rule counts every slot as an expert of its own, which the host knows.
 constexpr int DK_WARPS = 16;
 constexpr int DK_FEW_WARPS = 8;
-constexpr int DK_FEW_STEPS = 100;  // at most
+constexpr int DK_FEW_STEPS = 140;  // at most
 constexpr int DK_UNIT = 32;      // weight rows of a unit: two row groups of a tile
-constexpr int DK_RING = 6;       // k-blocks of a warp's ring
+// K-blocks of a warp's ring: with 16 warps 4 keep as much in flight as the loop uses, and leave room for more activations
+// (8 tokens of the 128-expert layer in fp16: 53.8 us, 55.0 with 6).
+__host__ __device__ constexpr int dk_ring(int warps) { return warps == DK_FEW_WARPS ? 6 : 4; }
 constexpr int DK_SLOT = 1152;    // bytes of a ring slot: a unit's k-block in the widest format
 constexpr int DK_MAX_SLOTS = DECODE_MAX_TOKENS * MAX_TOPK;
-// Selector words of an NF3 slot through the pair table, of 4; the others by byte permutes. Each way loads one pipe; 2 and
-// 4 measured the same within 1%.
-constexpr int DK_NF3_LUT = 3;
+// Of a slot's four NF3 words three go through a pair table and one through byte permutes, each of which loads one pipe (two
+// and four words measured the same within 1%). The table (common.cuh) is indexed by the code words' bytes as they are: bits
+// 3 and 7, which belong to other codes, make no difference to the entry. That saves a mask a word (one token of the
+// 256-expert layer: 51.3 -> 50.8 us, 8 tokens: 250 -> 248).
+constexpr int DK_NF3_ENTRIES = 256;
 
 // Relative time of a unit's k-block, by format and type: what bounds the warps is their instructions, not the bytes
 // (layers of one format, 2 and 4 tokens, 6144 x 2048: NF3 40, NVFP4 42, in fp16 47, MXFP4 47 to 49 clocks an SM for 16
@@ -219,13 +223,11 @@ __device__ __forceinline__ uint32_t decode_kblock(const uint8_t* slot, int i, in
     const uint32_t* v = reinterpret_cast<const uint32_t*>(slot) + 32 * i + lane;
     uint32_t s[4];
     nf3_selectors(v[0], v[64], v[128], s);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t* p = (w < 2 ? r0 : r1) + 4 * (w & 1);
-      if (w < DK_NF3_LUT) nf3x8_lut(s[w], nf3_lut, p);
-      else if constexpr (ACT == ACT_F16) nf3x8_to_f16x2(s[w], p);
-      else nf3x8_to_bf16x2(s[w], p);
-    }
+    nf3x8_lut(v[0], nf3_lut, r0);
+    nf3x8_lut(v[64], nf3_lut, r0 + 4);
+    nf3x8_lut(v[128], nf3_lut, r1);
+    if constexpr (ACT == ACT_F16) nf3x8_to_f16x2(s[3], r1 + 4);
+    else nf3x8_to_bf16x2(s[3], r1 + 4);
     return reinterpret_cast<const uint32_t*>(slot)[192 + 8 * i + (lane >> 2)];
   } else {
     const uint4 v = reinterpret_cast<const uint4*>(slot)[32 * i + lane];
@@ -302,10 +304,10 @@ struct Segment {
 // Shared memory of decode_kernel.
 template <int WARPS>
 struct DkShared {
-  uint8_t ring[WARPS][DK_RING * DK_SLOT];  // codes in flight; after a warp's last k-block its partial sums
+  uint8_t ring[WARPS][dk_ring(WARPS) * DK_SLOT];  // codes in flight; after a warp's last k-block its partial sums
   float part[WARPS][16][32];               // partial sums of the unit that a warp ended and another began
   uint32_t scale[256];                        // scale byte of the kept format -> pair of the operand type
-  uint32_t nf3[NF3_LUT_WORDS];
+  uint32_t nf3[DK_NF3_ENTRIES * 32];
   alignas(16) int id[DK_MAX_SLOTS];  // chosen experts by slot, then INT_MAX
   float gate[DK_MAX_SLOTS];
   int sorted[DK_MAX_SLOTS];    // slots by (expert, slot)
@@ -359,7 +361,7 @@ __device__ __forceinline__ void loader_unit(Loader& l, const uint8_t* matrix, in
 }
 
 // Starts the next step's copies, if there is one; one commit group either way.
-template <int FMT, int STEP>
+template <int FMT, int STEP, int RING>
 __device__ __forceinline__ void loader_issue(Loader& l, int KB, int lane) {
   constexpr int TB = tile_bytes(FMT);
   if (l.steps > 0) {
@@ -374,7 +376,7 @@ __device__ __forceinline__ void loader_issue(Loader& l, int KB, int lane) {
 #pragma unroll
       for (int j = 0; j < STEP; ++j) cp_async16(dst + j * DK_SLOT + (FMT == FMT_NF3 ? 512 : 1024), l.at2 + j * TB);
     }
-    l.slot = l.slot == (DK_RING - STEP) * DK_SLOT ? 0 : l.slot + STEP * DK_SLOT;
+    l.slot = l.slot == (RING - STEP) * DK_SLOT ? 0 : l.slot + STEP * DK_SLOT;
     l.at += STEP * TB;
     l.at2 += STEP * TB;
     if (--l.in_unit == 0) {
@@ -394,6 +396,7 @@ struct DkCtx {
   const DecodeParams& p;
   DkShared<WARPS>& s;
   uint8_t* act;
+  static constexpr int RING = dk_ring(WARPS);
   int ph, upg, KB, S, spu, cols_per_slot;  // S: k-blocks of a step; spu: steps of a unit
   int2 lo, hi;                             // the share: from a group's unit to another's
 
@@ -550,14 +553,14 @@ struct DkCtx {
     l.steps = to - from;
     loader_unit<FMT>(l, matrix, KB, rest * STEP, lane);
 #pragma unroll 1
-    for (int i = 0; i < DK_RING / STEP - 1; ++i) loader_issue<FMT, STEP>(l, KB, lane);
+    for (int i = 0; i < RING / STEP - 1; ++i) loader_issue<FMT, STEP, RING>(l, KB, lane);
   }
 
   // This warp's steps [from, to) of a segment, whose first copies are under way. Whole units are emitted; the sums of
   // one that another warp began go to s.part, of one that another ends to the ring.
   template <int FMT, int STEP, bool TWO>
   __device__ __forceinline__ void run(Loader& l, const Segment& r, int from, int to, int warp, int lane) const {
-    constexpr int SLOTS = DK_RING / STEP;
+    constexpr int SLOTS = RING / STEP;
     const int g = lane >> 2, q = lane & 3;
     const uint32_t nf3_lut = smem_u32(s.nf3) + 4u * (uint32_t)lane;
     const int cols = r.n * cols_per_slot, half = cols * 64;
@@ -575,7 +578,7 @@ struct DkCtx {
     for (int left = to - from; left > 0; --left) {
       cp_async_wait<SLOTS - 2>();
       __syncwarp();
-      loader_issue<FMT, STEP>(l, KB, lane);  // into the slot of the step before, which every lane has read
+      loader_issue<FMT, STEP, RING>(l, KB, lane);  // into the slot of the step before, which every lane has read
 #pragma unroll
       for (int j = 0; j < STEP; ++j) {
         uint32_t r0[2][8], r1[2][8], sc[2];
@@ -592,7 +595,7 @@ struct DkCtx {
         }
         x += 2 * half;
       }
-      w = w == ring + (DK_RING - STEP) * DK_SLOT ? ring : w + STEP * DK_SLOT;
+      w = w == ring + (RING - STEP) * DK_SLOT ? ring : w + STEP * DK_SLOT;
       if (++st == spu) {
         if (whole) {
 #pragma unroll
@@ -644,6 +647,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int THREADS = WARPS * 32;
   static_assert(THREADS >= DK_MAX_SLOTS && WARPS >= DECODE_MAX_TOKENS && WARPS < 32, "a thread a slot, a warp a token");
+  static_assert(sizeof(DkShared<WARPS>) <= DK_SHARED_BYTES, "what the activations leave");
   DkShared<WARPS>& s = *reinterpret_cast<DkShared<WARPS>*>(smem);
   uint8_t* act = smem + DK_SHARED_BYTES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -651,7 +655,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_kernel(const __grid_cons
   if (tid < 256)
     s.scale[tid] = KEPT == FMT_NVFP4 ? e4m3_lut_entry<ACT>((uint32_t)tid)
                                      : bf16_bcast(ACT == ACT_F16 ? e8m0_to_f16((uint32_t)tid) : e8m0_to_bf16((uint32_t)tid));
-  if (p.has_nf3) nf3_lut_fill<ACT>(s.nf3, tid, THREADS);
+  if (p.has_nf3)
+    for (int w = tid; w < DK_NF3_ENTRIES * 32; w += THREADS) {
+      uint32_t v[4];
+      if constexpr (ACT == ACT_F16) nf3x8_to_f16x2((uint32_t)(w >> 5) & 0x77u, v);
+      else nf3x8_to_bf16x2((uint32_t)(w >> 5) & 0x77u, v);
+      s.nf3[w] = v[0];
+    }
   if (tid < DK_MAX_SLOTS) {
     s.id[tid] = INT_MAX;
     s.head[tid] = 0;

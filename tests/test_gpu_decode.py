@@ -74,6 +74,14 @@ CASES = [
     (7, 1152, 640, 33, 9, synth.FMT_MXFP4, 16, "bf16"),
     (8, 8192, 256, 16, 4, synth.FMT_NVFP4, 8, "f16"),
     (6, 128, 8192, 6, 6, synth.FMT_NVFP4, 3, "f16"),
+    (8, 1024, 704, 40, 8, synth.FMT_NVFP4, 20, "bf16"),
+    (8, 640, 832, 12, 12, synth.FMT_MXFP4, 6, "f16"),
+    (1, 4096, 1216, 10, 10, synth.FMT_NVFP4, 5, "bf16"),
+    (6, 128, 9792, 6, 6, synth.FMT_NVFP4, 3, "f16"),
+    # the limits: activations of one token fill shared memory
+    (3, 39680, 64, 2, 1, synth.FMT_NVFP4, 1, "bf16"),
+    (3, 128, 19840, 2, 2, synth.FMT_MXFP4, 1, "f16"),
+    (8, 39680, 320, 4, 2, synth.FMT_NVFP4, 2, "f16"),             # with 16 warps
 ]
 
 
@@ -296,6 +304,10 @@ def test_refusals():
     with pytest.raises(hm.HmoeError) as ei:
         moe.decode(x, router, out=x)
     assert ei.value.status == -1
+    for H, I in ((39680 + 128, 64), (128, 19840 + 64)):            # activations of a token above shared memory
+        with pytest.raises(hm.HmoeError) as ei:
+            hm.hmoe_decode_workspace_size(hm.LayerDesc(H, I, 4, 2, hm.FMT_NVFP4), 1)
+        assert ei.value.status == -2
     flat = torch.zeros(2 * 256 + 8, dtype=x.dtype, device="cuda")
     with pytest.raises(hm.HmoeError) as ei:
         moe.decode(flat[1:513].view(2, 256), router)
