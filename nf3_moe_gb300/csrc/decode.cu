@@ -35,8 +35,8 @@
 // k-block of 16 rows takes about 40 clocks an SM, of which the copies and the
 // loop alone are 26, and the bytes at the copy rate 13 (NF3). 152 SMs at that
 // pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 248 us,
-// 968.6 MB; the bytes alone would take 143 us). The ALU is 49% busy, issue
-// 48%, shared memory 41%: the warps wait on each other's pipes and on their
+// 968.6 MB; the bytes alone would take 143 us). The ALU is 50% busy, issue
+// 57%, shared memory 47%: the warps wait on each other's pipes and on their
 // own chains. More warps (20, 24, 32), deeper rings, L2 prefetch ahead of them,
 // codes loaded into registers without a ring (355 us, its waits at every use)
 // and one bulk copy a warp and step (379) were all slower or equal. A
