@@ -353,7 +353,7 @@ __device__ __forceinline__ void loader_unit(Loader& l, const uint8_t* matrix, in
   const int i = l.u & 3;
   if constexpr (FMT == FMT_NF3) {
     l.at = tile + i * 256 + (lane >> 4) * 1024 + (lane & 15) * 16;
-    l.at2 = tile + (lane < 16 ? 2048 + i * 256 + lane * 16 : 3072 + i * 64 + (lane & 3) * 16);
+    l.at2 = tile + (lane < 16 ? 2 * 1024 + i * 256 + lane * 16 : 3 * 1024 + i * 64 + (lane & 3) * 16);
   } else {
     l.at = tile + i * 1024 + lane * 16;
     l.at2 = tile + 4096 + i * (FMT == FMT_NVFP4 ? 128 : 64) + (lane & 7) * 16;
