@@ -685,10 +685,8 @@ hmoe_status hmoe_decode(const hmoe_layer* layer, const void* x, int T, const voi
  * for the projections of a decode step; any number of rows is taken, 16 at
  * most reading the weights once. The integers and their products with x are
  * exact, a group's sum and all else are fp32 in a fixed order, rounded once to
- * the activation type: the same call gives the same bits. In bf16 a group's
- * sum is taken of (128 + q) x, and (128 + z) sum x off it: that adds an error
- * of some 2^-16 of sum |x s|, a row of x that holds an infinity gives NaN where
- * fp16 may give infinities, and |x| above 2^112 is not supported.
+ * the activation type: the same call gives the same bits. A group's sum is
+ * taken before its scale: in bf16, |x| above 2^116 may exceed fp32 there.
  *   These entry points have no counterpart on the pages; beside the dense
  *   linear above they take the integer formats' checkpoints.
  * Conventions as for the layer. No workspace. */

@@ -14,16 +14,17 @@
 // warps share are joined through shared memory in the order of K.
 //
 // Decoding. A nibble OR-ed into the low mantissa bits of 128 (bf16) or 1024 (fp16)
-// is 128 + q or 1024 + q, exactly. bf16: those enter the products as they are,
-// 7 operations for 8 weights, and the group's sum of x times 128 + z is taken off
-// the group's sum of products (that leaves 2^-24 of sums up to 30 times the
-// result's, far below bf16's rounding). fp16, whose result keeps more bits and
-// whose offset is larger: 1024 + z is subtracted first, exactly, 11 operations.
-// What bounds it after the bytes is the issue of instructions and the ALU (58%
-// busy, with DRAM at 46%): the offsets' subtraction in bf16 and a wait for every
-// block instead of every second cost 36 against 29 us for 8 rows of 32768 x 6144
-// (105 MB), a mask and an OR apart in the decoder 29.6 against 25.1. More warps
-// (20, 24) were slower, as were 8.
+// is 128 + q or 1024 + q, exactly (the magic-number conversion of Kim et al., Who
+// Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale
+// Production, 2022); 128 + z or 1024 + z is subtracted, exactly, before the
+// product, 11 operations for 8 weights. The products are of (q - z) x alone, so
+// that a large x on a weight of zero adds nothing. (bf16 products of 128 + q with
+// the group's sum of x times 128 + z taken off afterwards are 7 operations, 25.2
+// against 27.4 us for 8 rows of 32768 x 6144, 105 MB, but leave 2^-17 of the
+// sum of |x s|: one x 10^6 times the others cost 13% of a result it has no part in.)
+// What bounds it after the bytes is the issue of instructions and the ALU. A mask and
+// an OR apart in the decoder cost 29.6 against 25.1, when that was all of it. More
+// warps (20, 24) were slower, as were 8.
 #include "act.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -105,8 +106,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
   uint8_t* const ring = smem + warp * I4_RING * BB;
   float* const part = reinterpret_cast<float*>(smem + WARPS * I4_RING * BB);  // [warps][4 NT][32]
   float* const kept = part + WARPS * 4 * NT * 32;  // K in parts: [I4_UNITS][4 NT][32]
-  float* const xsum = kept + (p.parts > 1 ? I4_UNITS * 4 * NT * 32 : 0);  // bf16: [groups][8 NT]
-  uint8_t* const xs = reinterpret_cast<uint8_t*>(xsum) + (ACT == ACT_F16 ? 0 : p.kc * NG * NT * 32);
+  uint8_t* const xs = reinterpret_cast<uint8_t*>(kept + (p.parts > 1 ? I4_UNITS * 4 * NT * 32 : 0));
   const int t0 = blockIdx.y * p.pass, nt = min(p.pass, p.T - t0);
   const int u0 = div_by(p.units * (int)blockIdx.x, p.by_grid), u1 = div_by(p.units * ((int)blockIdx.x + 1), p.by_grid);
   const int pieces = BB / 16 - 64;  // of a block's scales and zero points
@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
       }
   };
   const uint8_t *x = x0, *w = ring;
-  const float* sums = xsum + 2 * q;
   auto block = [&]() {
     float d[NT][4];
 #pragma unroll
@@ -205,15 +204,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
         const int gr = NG == 4 ? 2 * h + k : (NG == 2 ? h : 0);
         const bool begin = NG == 4 || (k == 0 && (NG == 2 || h == 0)), end = NG == 4 || (k == 1 && (NG == 2 || h == 1));
         uint32_t z = 0x0808u;  // of row g, and of row g + 8
-        if ((ACT == ACT_F16 || end) && p.zeros) z = *reinterpret_cast<const uint16_t*>(w + 1024 + NG * 32 + gr * 16 + g * 2);
+        if (p.zeros) z = *reinterpret_cast<const uint16_t*>(w + 1024 + NG * 32 + gr * 16 + g * 2);
         uint32_t a[2][4];  // pairs of row g and of row g + 8
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[r][i] = and_or(cw[2 * r + k] >> (4 * i), mask, magic);
-            if (ACT == ACT_F16) a[r][i] = sub_x2<ACT>(a[r][i], (r ? z >> 8 : z & 0xFFu) * 0x00010001u + MAGIC);
-          }
+          for (int i = 0; i < 4; ++i)
+            a[r][i] = sub_x2<ACT>(and_or(cw[2 * r + k] >> (4 * i), mask, magic), (r ? z >> 8 : z & 0xFFu) * 0x00010001u + MAGIC);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint4& xk = xv[n][k];
@@ -223,17 +220,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
         }
         if (end) {
           const float2 sc = act_x2_to_f32<ACT>(*reinterpret_cast<const uint32_t*>(w + 1024 + gr * 32 + g * 4));
-          // 128 + z as fp32: z in the mantissa's upper bits
-          const float o0 = __uint_as_float(0x43000000u | (z & 0xFFu) << 16), o1 = __uint_as_float(0x43000000u | (z >> 8) << 16);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            if (ACT != ACT_F16) {
-              const float2 xsm = *reinterpret_cast<const float2*>(sums + gr * 8 * NT + 8 * n);
-              d[n][0] = fmaf(-o0, xsm.x, d[n][0]);
-              d[n][1] = fmaf(-o0, xsm.y, d[n][1]);
-              d[n][2] = fmaf(-o1, xsm.x, d[n][2]);
-              d[n][3] = fmaf(-o1, xsm.y, d[n][3]);
-            }
             acc[n][0] = fmaf(sc.x, d[n][0], acc[n][0]);
             acc[n][1] = fmaf(sc.x, d[n][1], acc[n][1]);
             acc[n][2] = fmaf(sc.y, d[n][2], acc[n][2]);
@@ -242,7 +230,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
         }
       }
     }
-    sums += NG * 8 * NT;
     w += BB;
     if (++st == nb) {
       if (whole) {
@@ -255,7 +242,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
       whole = true;
       st = 0;
       x = x0;
-      sums = xsum + 2 * q;
       ++unit;
     }
   };
@@ -263,12 +249,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
 #pragma unroll 1
     for (int i = 0; i < I4_RING - 2; i += 2) copy2(i);
     // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps. A thread
-    // has 8 values, the threads of a group of K are neighbours. Few blocks: less code to fetch (one row of 2048 x 2048:
+    // has 8 values. Few blocks: less code to fetch (one row of 2048 x 2048:
     // 3.2 us with two loads in flight, 3.4 with four; 8 rows of 32768 x 6144: 26.4 and 25.0).
     {
-      constexpr int LOADS = WARPS == I4_FEW_WARPS ? 2 : 4, LANES = 16 / NG;
+      constexpr int LOADS = WARPS == I4_FEW_WARPS ? 2 : 4;
       const int chunks = nb * 16, all = chunks * nt, k0 = c * p.kc * 16;
-      for (int i0 = tid; i0 - tid < all; i0 += LOADS * (WARPS * 32)) {  // whole warps: they shuffle
+      for (int i0 = tid; i0 < all; i0 += LOADS * (WARPS * 32)) {
         uint4 v[LOADS];
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
@@ -278,18 +264,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
           const int i = i0 + j * (WARPS * 32), r = by_nb(min(i, all - 1)) >> 4, k = i - r * chunks;
-          if (ACT != ACT_F16) {
-            const uint32_t vv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-            float sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = act_x2_to_f32<ACT>(vv[e]);
-              sum += f.x + f.y;
-            }
-#pragma unroll
-            for (int off = 1; off < LANES; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (i < all && (k & (LANES - 1)) == 0) xsum[(k / LANES) * 8 * NT + r] = sum;
-          }
           if (i < all) {
             const int step = (k >> 1) & 3;
             uint8_t* d = xs + (((k >> 3) * 2 + (step >> 1)) * nt + r) * 64 + (k & 1) * 32 + (step & 1) * 8;
@@ -301,7 +275,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
     }
     __syncthreads();
     x = x0 + st * 4 * half;
-    sums = xsum + st * NG * 8 * NT + 2 * q;
     w = ring;
     for (int s = from; s < to; s += 2) {
       asm volatile("cp.async.wait_group %0;" ::"n"(I4_RING / 2 - 2) : "memory");
@@ -352,12 +325,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------ launch
-// Bytes of shared memory beside x for passes of `pass` rows, and of x and its sums for each block of K.
+// Bytes of shared memory beside x for passes of `pass` rows.
 static int i4_fixed(int ng, int pass, bool parts, int warps) {
   const int nt = pass > 8 ? 2 : 1;
   return warps * (I4_RING * i4_block_bytes(ng, true) + nt * 512) + (parts ? I4_UNITS * nt * 512 : 0);
 }
-static int i4_per_block(int ng, int pass) { return pass * 256 + ng * (pass > 8 ? 2 : 1) * 32; }
 
 template <int ACT, int NT, int NG, int WARPS>
 static cudaError_t launch_as(const Int4Params& p, dim3 grid, int smem, cudaStream_t st) {
@@ -379,7 +351,7 @@ static cudaError_t launch_by_size(const Int4Params& p, int nt, bool few, int ng,
 cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st) {
   const int passes = (p.T + I4_ROWS - 1) / I4_ROWS;
   p.pass = (p.T + passes - 1) / passes;  // the passes evened out
-  const int nt = p.pass > 8 ? 2 : 1, per = i4_per_block(ng, p.pass);
+  const int nt = p.pass > 8 ? 2 : 1, per = p.pass * 256;  // bytes of x for each block of K
   const unsigned ctas = (unsigned)(p.units < num_sms ? p.units : num_sms);
   const bool few = (long long)((p.units + (int)ctas - 1) / (int)ctas) * p.NB <= I4_FEW_BLOCKS;
   const int warps = few ? I4_FEW_WARPS : I4_WARPS;

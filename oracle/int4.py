@@ -32,3 +32,13 @@ def bound(x, codes, scales, zeros, group, bias=None, act="bf16"):
     off = (143.0 * (2 * group + 16) if act == "bf16" else 15.0 * (group + 16)) * u * (per @ s.T)
     size = x @ np.abs(weights(codes, scales, zeros, group)).T
     return off + (2 * groups + 48) * u * (size + (0 if bias is None else np.abs(np.asarray(bias, dtype=np.float64))))
+
+
+def sum_bound(x, codes, scales, zeros, group, bias=None):
+    """A bound on the error of fp32 sums of the exact terms (q - z) x, whatever their offsets cost: with u = 2^-23 the
+    largest error of one (truncating) fp32 addition, a group's sum of at most group + 16 additions, then as in bound().
+    A weight of zero adds nothing, however large its x."""
+    x = np.abs(np.asarray(x, dtype=np.float64))
+    size = x @ np.abs(weights(codes, scales, zeros, group)).T
+    groups = x.shape[1] // group
+    return 2.0 ** -23 * ((group + 16 + 2 * groups + 48) * size + (2 * groups + 48) * (0 if bias is None else np.abs(np.asarray(bias, dtype=np.float64))))
