@@ -303,12 +303,10 @@ class HybridMoELayer:
         self.max_tokens = max_tokens
         self.ws = torch.empty(hmoe_workspace_size(self.desc, max_tokens), dtype=torch.uint8, device=device)
         hmoe_workspace_init(self.ws)
-        try:
-            self.decode_ws = torch.empty(hmoe_decode_workspace_size(self.desc, min(max_tokens, DECODE_MAX_TOKENS)),
-                                         dtype=torch.uint8, device=device)
+        self.decode_ws, nbytes = None, _owned_workspace_size(self.desc, max_tokens)
+        if nbytes is not None:
+            self.decode_ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
             hmoe_workspace_init(self.decode_ws)
-        except HmoeError:                                # a layer that decode() does not take
-            self.decode_ws = None
         self.topk = topk
         self.E = E
         self.H = H
@@ -331,11 +329,12 @@ class HybridMoELayer:
         return out
 
     def decode(self, x, router, bias=None, out=None, ids=None, gates=None):
-        """The whole layer for up to 8 tokens (and max_tokens) from hidden states, in two kernels: out, ids and gates of
-        x [T, H] with the router's matrix [E, H] of the activation type and its bias (fp32 [E]; None: zeros). No
-        gradient. The calls of one layer share a workspace: they may not overlap on the GPU."""
+        """The whole layer for up to 8 tokens (max_tokens, or what hmoe_decode admits of these sizes, where less) from
+        hidden states, in two kernels: out, ids and gates of x [T, H] with the router's matrix [E, H] of the activation
+        type and its bias (fp32 [E]; None: zeros). No gradient. The calls of one layer share a workspace: they may not
+        overlap on the GPU."""
         if self.decode_ws is None:
-            hmoe_decode_workspace_size(self.desc, 1)     # raises what the layer lacks
+            hmoe_decode_workspace_size(self.desc, 0)     # raises what the layer lacks
         T, dev = x.shape[0], x.device
         if out is None:
             out = torch.empty((T, self.H), dtype=self.dtype, device=dev)
@@ -454,7 +453,7 @@ def hmoe_quantize_act_nvfp4(x, global_scale, codes, scales, stream=None):
 from ._lib import ROW_BF16, ROW_F16, ROW_F32, DispatchDesc, Int4Desc, LoraDesc  # noqa: E402, F401
 from .rows import (ExpertRows, RowPlan, hmoe_combine, hmoe_combine_backward, hmoe_dispatch,  # noqa: E402, F401
                    hmoe_dispatch_backward, hmoe_dispatch_rows, hmoe_dispatch_workspace_size, row_torch_dtype)
-from .decode import DECODE_MAX_TOKENS, hmoe_decode, hmoe_decode_workspace_size  # noqa: E402, F401
+from .decode import DECODE_MAX_TOKENS, _owned_workspace_size, hmoe_decode, hmoe_decode_workspace_size  # noqa: E402, F401
 from .lora import (Lora, LoraAdapters, _no_gradient, hmoe_lora_create, hmoe_lora_forward, hmoe_lora_load,  # noqa: E402, F401
                    hmoe_lora_packed_size, hmoe_lora_workspace_size)
 from .int4 import Int4, LinearInt4, hmoe_int4_forward, hmoe_int4_pack, hmoe_int4_packed_size  # noqa: E402, F401

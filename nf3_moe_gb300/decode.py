@@ -22,6 +22,18 @@ def hmoe_decode_workspace_size(desc, max_tokens):
     return b.value
 
 
+def _owned_workspace_size(desc, max_tokens):
+    """Bytes of a workspace for up to max_tokens tokens (and 8), or for as many as the layer's sizes admit where that is
+    less; None for a layer that hmoe_decode does not take."""
+    for tokens in range(min(max_tokens, DECODE_MAX_TOKENS), -1, -1):
+        try:
+            return hmoe_decode_workspace_size(desc, tokens)
+        except _lib.HmoeError as e:
+            if _lib.STATUS_NAMES[e.status] != "HMOE_ERR_UNSUPPORTED_SHAPE":
+                raise
+    return None
+
+
 def _check_decode(desc, x, router, out, ids, gates, ws, bias, cuda=True):
     """Returns T and the device index."""
     dt, H, E = _TORCH[desc.act_dtype], desc.H, desc.E
