@@ -10,7 +10,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import _lib, _need
-from .rows import _int32, _is, _is_ws, _raw, _raw_stream
+from .rows import _int32, _is, _is_ws, _need_constants, _raw, _raw_stream
 
 DECODE_MAX_TOKENS = 8
 _TORCH = {_lib.ACT_BF16: torch.bfloat16, _lib.ACT_F16: torch.float16}
@@ -57,9 +57,7 @@ def _check_decode(desc, x, router, out, ids, gates, ws, bias, cuda=True):
 
 def _no_gradient(**tensors):
     """The call has no gradient: one that would lose it in silence is refused."""
-    for name, t in tensors.items():
-        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
-            raise RuntimeError(f"{name} requires a gradient, and hmoe_decode has none: detach it, or call under torch.no_grad()")
+    _need_constants("hmoe_decode has none", **tensors)
 
 
 def hmoe_decode(layer, x, router, out, ws, bias=None, ids=None, gates=None, stream=None):

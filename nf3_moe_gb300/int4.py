@@ -12,7 +12,7 @@ from torch.autograd.graph import increment_version
 from . import _lib, _need, act_torch_dtype
 from ._lib import ACT_BF16, Int4Desc
 from .lora import _need_rows, _no_gradient as _no_adapter_gradient
-from .rows import _INT_MAX, _is, _raw, _raw_stream
+from .rows import _INT_MAX, _forward_mode, _is, _need_constants, _raw, _raw_stream
 
 _TORCH = {_lib.ACT_BF16: torch.bfloat16, _lib.ACT_F16: torch.float16}
 
@@ -80,16 +80,14 @@ def _check_int4_forward(desc, x, out, bias, cuda=True):
 
 
 def _no_gradient(x, out, bias):
-    for name, t in (("x", x), ("out", out), ("bias", bias)):
-        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
-            raise RuntimeError(f"{name} requires a gradient, and the 4-bit integer linear has none: detach it, or call under torch.no_grad()")
+    _need_constants("the 4-bit integer linear has none", x=x, out=out, bias=bias)
 
 
 def hmoe_int4_forward(linear, x, out, bias=None, stream=None):
     """out[t] = W x[t] (+ bias) for rows x [T, K] (a column range of a wider tensor serves) and out [T, N]. No gradient:
     x, out and bias may not require one (outside torch.no_grad())."""
     T, ldx, ldo, dev = _check_int4_forward(linear.desc, x, out, bias)
-    if x.requires_grad or out.requires_grad or bias is not None and bias.requires_grad:
+    if x.requires_grad or out.requires_grad or bias is not None and bias.requires_grad or _forward_mode():
         _no_gradient(x, out, bias)
     increment_version(out)                               # autograd does not see the library's writes
     status = _lib.lib().hmoe_int4_forward(linear.handle, x.data_ptr(), ldx, T, _raw(bias), out.data_ptr(), ldo, _raw_stream(stream, dev))

@@ -13,7 +13,7 @@ from torch.autograd.graph import increment_version
 
 from . import _lib, _need, act_torch_dtype, hmoe_workspace_init
 from ._lib import ACT_BF16, ACT_F16, LoraDesc
-from .rows import _INT_MAX, _int32, _is, _is_ws, _raw_stream
+from .rows import _INT_MAX, _forward_mode, _int32, _is, _is_ws, _need_constants, _raw_stream
 
 _TORCH = {ACT_BF16: torch.bfloat16, ACT_F16: torch.float16}
 
@@ -72,9 +72,7 @@ def _check_lora_forward(desc, x, ids, base, out, ws, cuda=True):
 
 def _no_gradient(x, base, out):
     """The adapters have no gradient: a call that would lose one in silence is refused."""
-    for name, t in (("x", x), ("base", base), ("out", out)):
-        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
-            raise RuntimeError(f"{name} requires a gradient, and the adapters have none: detach it, or call under torch.no_grad()")
+    _need_constants("the adapters have none", x=x, base=base, out=out)
 
 
 def hmoe_lora_packed_size(desc):
@@ -129,7 +127,7 @@ def hmoe_lora_forward(lora, x, ids, out, ws, base=None, stream=None):
     """out[t] = base[t] + scale_a B_a (A_a x[t]), a = ids[t]; base None: zeros; base may be out. No gradient: x, base
     and out may not require one (outside torch.no_grad())."""
     T, ldx, ldb, ldo, dev = _check_lora_forward(lora.desc, x, ids, base, out, ws)
-    if x.requires_grad or out.requires_grad or base is not None and base.requires_grad:
+    if x.requires_grad or out.requires_grad or base is not None and base.requires_grad or _forward_mode():
         _no_gradient(x, base, out)
     increment_version(out)                               # autograd does not see the library's writes
     status = _lib.lib().hmoe_lora_forward(lora.handle, x.data_ptr(), ldx, T, ids.data_ptr(),
