@@ -61,8 +61,19 @@ def forward(x, ids, gates, get_expert, H, I, act="bf16"):
     return out, off
 
 
+def rms_tolerance(H, I, act="bf16"):
+    """rms(error) / rms(result) of a token, of weights and x of random signs, where every sum, slot and digit of h is there.
+
+    The result's rounding: half a step at most. A product of n terms: n / 16 MMAs and up to 32 joins and additions, each off
+    by at most u = 2^-23 of a partial sum, whose rms is no larger than the whole sum's. W13's reaches h through silu'(a) b
+    <= 1.1 |b| and silu(a), by up to 4 times itself (rms(a) / rms(silu(a)) <= 2). Then h's digits, expf and the gates."""
+    u, half = 2.0 ** -23, 2.0 ** -8 if act == "bf16" else 2.0 ** -11
+    split = 2.0 ** -17 if act == "bf16" else 2.0 ** -21
+    return half + (4 * (H / 16 + 32) + I / 16 + 32) * u + split + 2.0 ** -18
+
+
 def route_of(x, router, k, bias=None):
     return choose(logits(x, router, bias), k)
 
 
-__all__ = ["weights", "logits", "choose", "forward", "route_of", "route"]
+__all__ = ["weights", "logits", "choose", "forward", "rms_tolerance", "route_of", "route"]
