@@ -22,9 +22,10 @@ def forward(x, codes, scales, zeros, group, bias=None):
 
 
 def bound(x, codes, scales, zeros, group, bias=None, act="bf16"):
-    """A bound on the error of the sums alone. With u = 2^-23 the largest error of one fp32 addition: a group's sum of
-    products, of terms up to 143 |x| in bf16 (128 + q; the offset's share is taken off, from a sum of x with its own
-    error) and 15 |x| in fp16; then the sum over the groups of terms s |sum|, joined by up to 16 warps."""
+    """A wide bound on the error of the sums alone. With u = 2^-23 the largest error of one fp32 addition: a group's sum of
+    products, of terms up to 15 |x| in fp16 and 143 |x| in bf16 (room for products of 128 + q with the offset's share
+    taken off the sum); then the sum over the groups of terms s |sum|, joined by up to 16 warps. sum_bound is what sums
+    of the exact (q - z) x keep to."""
     x, s = np.abs(np.asarray(x, dtype=np.float64)), np.abs(np.asarray(scales, dtype=np.float64))
     T, K = x.shape
     u, groups = 2.0 ** -23, K // group
