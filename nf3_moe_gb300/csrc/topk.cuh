@@ -1,4 +1,4 @@
-// topk.cuh -- one warp's softmax top-k of a token's logits, shared by the routing and the decode kernels.
+// topk.cuh -- the order of logits that the routing and the few-token layer choose by, and the routing's choice for one token.
 #pragma once
 #include "common.cuh"
 
