@@ -667,7 +667,9 @@ hmoe_status hmoe_decode_workspace_size(const hmoe_layer_desc* desc, int max_toke
 
 /* x: device [T][H], router: device [E][H], both of the activation type;
  * bias: device fp32 [E], or NULL (an expert at -infinity is chosen only where
- * too few others are left; NaN is not supported). out: device [T][H] of the
+ * too few others are left, the lower ids first, with a gate of zero; a token
+ * whose experts are all at -infinity gets the lowest ids, NaN gates and a NaN
+ * result, as from hmoe_plan_routes; NaN is not supported). out: device [T][H] of the
  * activation type, fully overwritten, not over x. ids int32 [T][topk], gates fp32
  * [T][topk]: written where not NULL. x, router and out 16-byte aligned. T = 0
  * is valid.
