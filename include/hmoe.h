@@ -670,11 +670,12 @@ hmoe_status hmoe_decode_workspace_size(const hmoe_layer_desc* desc, int max_toke
  * too few others are left, the lower ids first, with a gate of zero; a token
  * whose experts are all at -infinity gets the lowest ids, NaN gates and a NaN
  * result, as from hmoe_plan_routes; NaN is not supported). out: device [T][H] of the
- * activation type, fully overwritten, not over x. ids int32 [T][topk], gates fp32
- * [T][topk]: written where not NULL. x, router and out 16-byte aligned. T = 0
+ * activation type, fully overwritten. ids int32 [T][topk], gates fp32
+ * [T][topk]: written where not NULL. The results overlap neither x nor one
+ * another, nor the workspace. x, router and out 16-byte aligned. T = 0
  * is valid.
  *   No page defines it. Errors: HMOE_ERR_INVALID_ARG (NULL or misaligned
- *   pointer, T < 0, out overlaps x), HMOE_ERR_UNSUPPORTED_SHAPE (as for the
+ *   pointer, T < 0, results over x or one another), HMOE_ERR_UNSUPPORTED_SHAPE (as for the
  *   workspace), HMOE_ERR_WORKSPACE_TOO_SMALL, HMOE_ERR_CUDA; a bounded wait
  *   that ran out is HMOE_ERR_DEVICE_TIMEOUT through hmoe_check_device_status. */
 hmoe_status hmoe_decode(const hmoe_layer* layer, const void* x, int T, const void* router, const float* bias, void* out,

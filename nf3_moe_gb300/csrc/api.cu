@@ -1327,6 +1327,12 @@ DecodeWs decode_ws(const hmoe_layer_desc& d, int T) {
   return w;
 }
 
+// NULL overlaps nothing.
+bool overlap(const void* a, size_t of_a, const void* b, size_t of_b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && p < q + of_b && q < p + of_a;
+}
+
 hmoe_status check_decode(const hmoe_layer_desc& d, int T) {
   if (T < 0) return fail(HMOE_ERR_INVALID_ARG, "T=%d < 0", T);
   if (T > DECODE_MAX_TOKENS)
@@ -1370,9 +1376,11 @@ hmoe_status hmoe_decode(const hmoe_layer* L, const void* x, int T, const void* r
     return fail(HMOE_ERR_INVALID_ARG, "x, router and out must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(gates)) & 3)
     return fail(HMOE_ERR_INVALID_ARG, "bias, ids and gates must be aligned to their elements");
-  const size_t bytes = (size_t)T * d.H * 2;
-  const uintptr_t xp = reinterpret_cast<uintptr_t>(x), op = reinterpret_cast<uintptr_t>(out);
-  if (xp < op + bytes && op < xp + bytes) return fail(HMOE_ERR_INVALID_ARG, "out must not overlap x");
+  const size_t bytes = (size_t)T * d.H * 2, small = (size_t)T * d.topk * 4;
+  if (overlap(x, bytes, out, bytes)) return fail(HMOE_ERR_INVALID_ARG, "out must not overlap x");
+  if (overlap(x, bytes, ids, small) || overlap(x, bytes, gates, small) || overlap(out, bytes, ids, small) ||
+      overlap(out, bytes, gates, small) || overlap(ids, small, gates, small))
+    return fail(HMOE_ERR_INVALID_ARG, "ids and gates must not overlap x, out or each other");
   if ((s = check_status_ws(ws, ws_bytes)) != HMOE_OK) return s;
   const DecodeWs w = decode_ws(d, T);
   if (ws_bytes < w.total)
