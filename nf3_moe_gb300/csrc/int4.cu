@@ -31,10 +31,17 @@
 
 namespace hmoe {
 
-// Warps of a CTA: 16, or 8 where a CTA has few blocks, whose time is the start, the
-// joining and the fetch of the code (16 warps against 8: one row of 2048 x 2048, 16 blocks a
-// CTA, 4.2 and 3.6 us; of 6144 x 6144, 144 blocks, 8.4 and 8.9; 8 rows of 32768 x 6144 26 and 36).
-constexpr int I4_WARPS = 16, I4_FEW_WARPS = 8, I4_FEW_BLOCKS = 32;
+// Warps of a CTA: 16, or 8 where a CTA has few blocks, whose time is the start, the joining and the fetch of the code, and,
+// with more than two rows, filling x. us with 16 warps and with 8, by the blocks of a CTA:
+//   1 row:   16: 3.9, 3.2   32: 4.5, 4.2   48: 5.5, 5.3   64: 6.3, 6.1   96: 6.9, 7.1   144: 8.6, 9.0   288: 13.1, 14.9
+//   2 rows:  16: 4.0, 3.3   32: 4.7, 4.6   48: 5.8, 5.6   64: 5.8, 5.9   96: 7.0, 7.5
+//   3 rows:  16: 4.0, 3.7   25: 4.6, 4.8   32: 4.7, 5.0   48: 6.1, 6.3
+//   8 rows:   8: 3.7, 3.3   16: 4.4, 4.4   25: 5.4, 6.1   48: 7.5, 8.5   96: 8.8, 10.4
+// The rings of 8 warps also leave room for twice the x. Where those of 16 do not leave it all of K:
+//   12 rows: 48: 13.8, 10.8   96: 14.3, 12.9   128: 20.0, 18.7
+//   16 rows: 32: 11.5, 9.4   48: 16.9, 14.9   64: 11.3, 10.8   96: 16.6, 16.8   128: 21.5, 21.3   144: 17.9, 19.6
+constexpr int I4_WARPS = 16, I4_FEW_WARPS = 8;
+constexpr int I4_FEW_BLOCKS = 16, I4_FEW_BLOCKS_2ROWS = 48, I4_FEW_BLOCKS_PARTS = 128;  // at most
 constexpr int I4_RING = 6;  // blocks of a warp's ring, in pairs
 constexpr int I4_ROWS = 16; // rows of x of a pass
 constexpr int I4_UNITS = 16;  // units worked on at once where K is taken in parts
@@ -353,10 +360,12 @@ cudaError_t launch_int4(Int4Params p, int ng, int num_sms, cudaStream_t st) {
   p.pass = (p.T + passes - 1) / passes;  // the passes evened out
   const int nt = p.pass > 8 ? 2 : 1, per = p.pass * 256;  // bytes of x for each block of K
   const unsigned ctas = (unsigned)(p.units < num_sms ? p.units : num_sms);
-  const bool few = (long long)((p.units + (int)ctas - 1) / (int)ctas) * p.NB <= I4_FEW_BLOCKS;
+  const auto in_parts = [&](int w) { return p.NB * per > DK_SMEM_LIMIT - i4_fixed(ng, p.pass, false, w); };
+  const int most_few = in_parts(I4_WARPS) ? I4_FEW_BLOCKS_PARTS : (p.pass <= 2 ? I4_FEW_BLOCKS_2ROWS : I4_FEW_BLOCKS);
+  const bool few = (long long)((p.units + (int)ctas - 1) / (int)ctas) * p.NB <= most_few;
   const int warps = few ? I4_FEW_WARPS : I4_WARPS;
   p.parts = 1;
-  if (p.NB * per > DK_SMEM_LIMIT - i4_fixed(ng, p.pass, false, warps)) {
+  if (in_parts(warps)) {
     const int most = (DK_SMEM_LIMIT - i4_fixed(ng, p.pass, true, warps)) / per;
     p.parts = (p.NB + most - 1) / most;
   }

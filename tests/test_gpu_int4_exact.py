@@ -24,6 +24,14 @@ def test_exact_inputs_bit_for_bit(T, N, K, group, zeros, act):
     assert np.array_equal(f64(linear(x[T // 2:T // 2 + 1], bias=bias)), want[T // 2:T // 2 + 1])
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 2432, 6144), (1, 2432, 6272), (2, 2432, 6144), (3, 2432, 2048), (3, 2432, 2176), (8, 2448, 2048),
+                                   (16, 2432, 2048), (16, 2432, 4096), (16, 4864, 8192), (16, 4880, 8192), (12, 2432, 6144)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_both_warp_counts_around_their_border(T, N, K, act):
+    """152 units (or twice, and one more) of 16, 17, 48 or 49 blocks and up to 128: eight warps a CTA, or sixteen, with K whole or in parts."""
+    test_exact_inputs_bit_for_bit(T, N, K, 128, True, act)
+
+
 @pytest.mark.parametrize("T,K", [(1, 131072), (3, 32768), (16, 6144)])
 def test_one_value_of_x_at_the_ends_of_each_block(T, K):
     """Rows of x with a single one: the weight there, wherever K is cut."""
