@@ -99,7 +99,9 @@ __device__ __forceinline__ int by_unit_cost(int v, int fmt) {
 // ------------------------------------------------------------ kernel 1: router logits
 constexpr int RK_THREADS = 128;
 // One CTA an expert: logits[t][e] for T <= TM tokens. fp32 sums in a fixed
-// order (a thread's own values, the warp's tree, the warps in turn).
+// order (a thread's own values, the warp's tree, the warps in turn). Inputs that
+// the kernel before may still write when this one starts are read by coherent
+// loads: those of the read-only path are for what nobody writes meanwhile.
 template <int ACT, int TM>
 __global__ void __launch_bounds__(RK_THREADS) router_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ router,
                                                             const float* __restrict__ bias, int T, int H, int E,
@@ -117,11 +119,11 @@ __global__ void __launch_bounds__(RK_THREADS) router_kernel(const uint16_t* __re
   const uint16_t* row = router + (size_t)e * H;
 #pragma unroll 2
   for (int c = tid * 8; c < H; c += RK_THREADS * 8) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + c));
+    const uint4 w = __ldca(reinterpret_cast<const uint4*>(row + c));
     uint4 v[TM];
 #pragma unroll
     for (int t = 0; t < TM; ++t)
-      v[t] = t < T ? __ldg(reinterpret_cast<const uint4*>(x + (size_t)t * H + c)) : make_uint4(0, 0, 0, 0);
+      v[t] = t < T ? __ldca(reinterpret_cast<const uint4*>(x + (size_t)t * H + c)) : make_uint4(0, 0, 0, 0);
     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(RK_THREADS) router_kernel(const uint16_t* __re
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < RK_THREADS / 32; ++w) s += s_part[w][tid];
-    if (bias) s += bias[e];
+    if (bias) s += __ldca(bias + e);
     logits[(size_t)tid * E + e] = isnan(s) ? __int_as_float(0x7FFFFFFF) : s;  // one NaN, which the top-k takes as the largest
   }
 }
@@ -467,7 +469,7 @@ struct DkCtx {
       for (int c = 0; c < r.n; ++c) {
         const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(s.sorted[r.p0 + c] / p.topk) * p.H);
         for (int i = tid; i < pieces; i += WARPS * 32)
-          *reinterpret_cast<uint4*>(dst + (((i >> 3) * 2 + (i & 1)) * r.n + c) * 64 + ((i >> 1) & 3) * 16) = __ldg(src + i);
+          *reinterpret_cast<uint4*>(dst + (((i >> 3) * 2 + (i & 1)) * r.n + c) * 64 + ((i >> 1) & 3) * 16) = __ldca(src + i);
       }
     } else {
       const int pieces = p.I / 8, cols = 2 * r.n;

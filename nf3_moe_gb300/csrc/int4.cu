@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
 #pragma unroll 1
     for (int i = 0; i < I4_RING - 2; i += 2) copy2(i);
     // x as fragments: [64 of K][half][row][q], 16 bytes: the q-th four values of the half's two k16 steps. A thread
-    // has 8 values. Few blocks: less code to fetch (one row of 2048 x 2048:
+    // has 8 values. The loads are coherent ones, since the kernel before may write x while this one starts. Few blocks: less code to fetch (one row of 2048 x 2048:
     // 3.2 us with two loads in flight, 3.4 with four; 8 rows of 32768 x 6144: 26.4 and 25.0).
     {
       constexpr int LOADS = WARPS == I4_FEW_WARPS ? 2 : 4;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) int4_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
           const int i = i0 + j * (WARPS * 32), r = by_nb(min(i, all - 1)) >> 4, k = k0 + i - r * chunks;
-          v[j] = i < all && k * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(t0 + r) * p.ldx) + k) : make_uint4(0, 0, 0, 0);
+          v[j] = i < all && k * 8 < p.K ? __ldca(reinterpret_cast<const uint4*>(p.x + (size_t)(t0 + r) * p.ldx) + k) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
