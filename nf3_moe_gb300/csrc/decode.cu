@@ -34,10 +34,10 @@
 // their columns at most, so decoding the codes costs more than their bytes: a
 // k-block of 16 rows takes about 40 clocks an SM, of which the copies and the
 // loop alone are 26, and the bytes at the copy rate 13 (NF3). 152 SMs at that
-// pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 248 us,
-// 968.6 MB; the bytes alone would take 143 us). The ALU is 50% busy, issue
-// 57%, shared memory 47%: the warps wait on each other's pipes and on their
-// own chains. More warps (20, 24, 32), deeper rings, L2 prefetch ahead of them,
+// pace stream 3.9 TB/s (8 tokens of 256 experts, 6144 x 2048, top-8: 245 us,
+// 968.6 MB; the bytes alone would take 143 us). In 4 tokens of 16 experts, 12 of
+// them NF3, the ALU is 49% busy, issue 57%, shared memory 37%: the warps wait
+// on each other's pipes and on their own chains. More warps (20, 24, 32), deeper rings, L2 prefetch ahead of them,
 // codes loaded into registers without a ring (355 us, its waits at every use)
 // and one bulk copy a warp and step (379) were all slower or equal. A
 // small call is bounded by its chain of waits instead, about 13 us of logits,
@@ -82,7 +82,7 @@ constexpr int DK_MAX_SLOTS = DECODE_MAX_TOKENS * MAX_TOPK;
 constexpr int DK_NF3_ENTRIES = 256;
 
 // Relative time of a unit's k-block, by format and type: what bounds the warps is their instructions, not the bytes
-// (layers of one format, 2 and 4 tokens, 6144 x 2048: NF3 40, NVFP4 42, in fp16 47, MXFP4 47 to 49 clocks an SM for 16
+// (layers of one format and of this one shape, 2 and 4 tokens, 6144 x 2048: NF3 40, NVFP4 42, in fp16 47, MXFP4 47 to 49 clocks an SM for 16
 // rows x 64 K, where the bytes are as 13 : 18 : 17). Shares by bytes took 285 us where these take 261 (8 tokens of the
 // 256-expert layer, bf16), 167 where they take 156 (4 tokens, MXFP4, fp16).
 template <int FMT, int ACT>

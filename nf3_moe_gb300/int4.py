@@ -100,7 +100,8 @@ class LinearInt4:
 
     codes uint8 [N, K/2] (element 2i in the low nibble), scales [N, K/group] of the activation type, zeros uint8
     [N, K/group] or None (all 8): W = (q - z) s, group 32, 64 or 128. For serving: no gradient goes through it.
-    max_tokens is there as in LinearW4A16; without a workspace it sizes nothing, and any batch is taken.
+    max_tokens is there as in LinearW4A16; without a workspace it sizes nothing, and any batch is taken, in passes of 16
+    rows that each read the weights (16 rows of 6144 x 6144 take 17 us, 4096 rows 4.2 ms).
     """
 
     def __init__(self, N, K, group, codes, scales, zeros=None, max_tokens=8, act_dtype=ACT_BF16, device="cuda"):

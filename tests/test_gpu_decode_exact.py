@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 
 # the benchmark's two layers and a batch of one, beside the cases that the CPU checks too
 LARGER = [(8, 6144, 2048, 32, 8, synth.FMT_NVFP4, 8, "bf16"), (1, 2048, 768, 128, 8, synth.FMT_NVFP4, None, "bf16"),
+          (8, 128, 64, 512, 32, synth.FMT_NVFP4, 100, "bf16"),  # 256 slots of more experts than there are shares
           (8, 2048, 768, 64, 8, synth.FMT_NVFP4, None, "f16"), (4, 6144, 2048, 16, 8, synth.FMT_MXFP4, 4, "f16")]
 
 
