@@ -74,10 +74,11 @@ def _forward_mode():
 def _need_constants(what, **tensors):
     """A call without a derivative would lose one in silence: reverse mode's outside torch.no_grad(), forward mode's
     wherever a tensor has a tangent (which does not make it require a gradient, and torch.no_grad() does not stop)."""
+    dual = _forward_mode()
     for name, t in tensors.items():
         if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
             raise RuntimeError(f"{name} requires a gradient, and {what}: detach it, or call under torch.no_grad()")
-        if isinstance(t, torch.Tensor) and _forward_mode() and forward_ad.unpack_dual(t).tangent is not None:
+        if dual and isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
             raise RuntimeError(f"{name} carries a forward-mode derivative, and {what}: give its primal (forward_ad.unpack_dual)")
 
 
